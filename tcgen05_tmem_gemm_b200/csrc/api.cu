@@ -256,7 +256,7 @@ bool gemv_applicable(const Views &v, int64_t M, int64_t N, int64_t K, int kind) 
         // stride (a TMA map); each block's slice of x fits in shared memory
         if (!(v.b.col.n == 1 && v.b.col.stride[0] == 2 && v.b.row.n <= 1)) return false;
         if (N % 8) return false;
-        if (v.b.row.n == 1 && v.b.row.stride[0] % 16) return false;
+        if (v.b.row.n == 1 && (v.b.row.stride[0] <= 0 || v.b.row.stride[0] % 16)) return false;
         if ((K + kMaxCluster - 1) / kMaxCluster * r_inst > 16384) return false;
         return true;
     }

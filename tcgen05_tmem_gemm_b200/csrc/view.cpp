@@ -144,14 +144,15 @@ dg_status analyse(const dg_view *v, bool is_output, ViewInfo *info) {
     }
 
     // One 2-D TMA map: a unit-stride dim, the other group a single dim whose
-    // stride is a multiple of 16 bytes, a 16-byte aligned base and extents
-    // that fit the map's 32-bit dims.
+    // stride is a positive multiple of 16 bytes (a map has no stride of 0, so
+    // a broadcast dim is left to the thread loads), a 16-byte aligned base and
+    // extents that fit the map's 32-bit dims.
     if (r.unit_dim != 0 && !empty) {
         const Axis &o = (r.unit_dim == 1) ? r.row : r.col;
         const int64_t inner_ext = (r.unit_dim == 1) ? cols : rows;
         const int64_t outer_ext = (r.unit_dim == 1) ? rows : cols;
         bool ok = (reinterpret_cast<uintptr_t>(v->ptr) % 16) == 0;
-        if (o.n == 1) ok = ok && (o.stride[0] % 16 == 0) && o.stride[0] < (int64_t(1) << 40);
+        if (o.n == 1) ok = ok && o.stride[0] > 0 && (o.stride[0] % 16 == 0) && o.stride[0] < (int64_t(1) << 40);
         ok = ok && inner_ext < (int64_t(1) << 31) && outer_ext < (int64_t(1) << 31);
         r.tma_ok = ok && o.n <= 1;
     }
