@@ -174,14 +174,144 @@ dg_status dg_gemm_ex(const dg_view *A, const dg_view *B, const dg_view *C,
 dg_status dg_gemv(const dg_view *x, const dg_view *W, const dg_view *y,
                   float alpha, float beta, void *stream);
 
+/*
+ * A weight matrix held in 4 bits, with one scale (and one zero point) per
+ * group of `group` consecutive k of a column:
+ *
+ *     W[k][n] = scale[n][k / group] * (code[n][k] - zero[n][k / group])
+ *
+ * The codes of one column n are contiguous along k, two per byte, the even k
+ * in the low four bits (the layout of GEMV_K: a [N x K] weight of a linear
+ * layer, read as K^T).
+ *  codes        device uint8; column n starts at codes + n * code_stride and
+ *               has ceil(K / 2) bytes (K odd: the last byte's high four bits
+ *               are not used)
+ *  scales       device, `scale_dtype` (F32, F16 or BF16); column n's
+ *               ceil(K / group) scales start at scales + n * scale_stride
+ *  zeros        device uint8, one per scale, only the low four bits count;
+ *               column n's start at zeros + n * zero_stride.  NULL: every
+ *               zero point is 8
+ *  K, N         sizes of W; at most 2^31 - 1
+ *  *_stride     BYTES between columns, >= 0 (zero_stride is not read when
+ *               zeros is NULL)
+ *  group        a positive multiple of 32; the last group of a column may be
+ *               shorter, and group >= K is one scale per column
+ * Only the bytes named here are read, whatever the strides.  Any alignment of
+ * the codes is accepted; columns that start at multiples of 16 bytes are read
+ * fastest.
+ */
+typedef struct {
+    const void *codes;
+    const void *scales;
+    const void *zeros;
+    int64_t K, N;
+    int64_t code_stride, scale_stride, zero_stride;
+    int32_t group;
+    int32_t scale_dtype;
+    int32_t reserved[2]; /* set to 0 */
+} dg_w4;
+
+/*
+ * dg_gemv_w4 — y = act(alpha * x W + beta * y + bias) for up to 8 rows of
+ * activations and 4-bit weights: dg_gemv for a quantised layer, which reads a
+ * quarter of the bytes.  x is [R x K] (F16 or BF16), y is [R x N] (F32, F16 or
+ * BF16; read only when beta != 0), any strided views; epilogue as in
+ * dg_gemm_ex, or NULL.
+ *  Arithmetic: code - zero is an exact small integer, its products with x are
+ *  summed in FP32 over each group, and the group's sum is multiplied by its
+ *  scale in FP32; nothing is rounded to fewer bits before y is stored.
+ *  Partial sums are added in a fixed order: runs are bit-identical.  A NaN or
+ *  infinity in x meets every weight (infinity times a weight of 0 is NaN).
+ *  alpha == 0 or K == 0 reads neither x nor W.
+ * Errors: DG_ERR_UNSUPPORTED if R > 8, DG_ERR_VALUE for a group that is not a
+ * positive multiple of 32, a reserved field that is not 0 or a non-finite
+ * alpha or beta, DG_ERR_SHAPE, DG_ERR_STRIDE, DG_ERR_ALIGN (scales),
+ * DG_ERR_DTYPE and DG_ERR_POINTER as dg_gemm.
+ */
+dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y,
+                     float alpha, float beta, const dg_epilogue *epilogue,
+                     void *stream);
+
+/*
+ * Linear cross entropy — the loss of an output layer straight from its input,
+ * without keeping the logits:
+ *
+ *     z[t][v]  = alpha * sum_d X[t][d] W[d][v]
+ *     lse[t]   = log sum_v exp z[t][v]
+ *     loss[t]  = lse[t] - z[t][target[t]]      (0 where target[t] == ignore_index)
+ *
+ * The logits exist one piece of the vocabulary at a time: in the tensor
+ * core's accumulators, where the epilogue reduces each row of a tile to its
+ * maximum and its sum of exponentials, or, for few rows and for operands that
+ * the paired tensor-core tiles do not take, in a piece of the workspace.
+ *
+ *  X [T x D], W [D x V]: views of one type, F16 or BF16 (tensor cores) or F32
+ *    (CUDA cores).  X may be any view of up to 4 dims (e.g. all tokens but
+ *    each sequence's last); W's rows and columns are one dim each (either
+ *    order: a [V x D] weight is passed transposed), else DG_ERR_UNSUPPORTED.
+ *  target  device int64[T].  A target outside [0, V) that is not ignore_index
+ *    makes its row's loss NaN, keeps the row out of the gradients and is
+ *    reported by dg_sync_status as DG_ERR_VALUE.
+ *  loss, lse  device float32[T], all written (lse for ignored rows too).
+ *  workspace  device memory, 256-byte aligned, for this call alone until it
+ *    has run; at least dg_linear_ce_workspace's `least` bytes.  More bytes
+ *    mean fewer and larger pieces.
+ *  A row whose logits hold a NaN or +infinity has loss and lse NaN; the rows
+ *  that are ignored never reach the loss or a gradient, whatever they hold.
+ *  Sums are FP32 and in a fixed order.
+ * Errors: as dg_gemm; DG_ERR_SHAPE also when V == 0 with T > 0, or for a
+ * workspace that is too small; DG_ERR_ALIGN for a misaligned array.
+ */
+dg_status dg_linear_ce(const dg_view *X, const dg_view *W,
+                       const int64_t *target, int64_t ignore_index,
+                       float alpha, float *loss, float *lse,
+                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * dg_linear_ce_grad — the gradients of sum_t dloss[t] * loss[t], from the lse
+ * that dg_linear_ce wrote:
+ *
+ *     G[t][v] = dloss[t] * (exp(z[t][v] - lse[t]) - (v == target[t]))
+ *     dX = alpha * G W^T,   dW = alpha * X^T G
+ *
+ * with G zero in rows that are ignored (or whose target is out of range).
+ *  dloss  device float32, dloss[t] at byte offset t * dloss_stride: 4, or 0
+ *    for one value that every row shares (the gradient of a mean or a sum).
+ *  dX [T x D] and dW [D x V]: views of F32, F16 or BF16, overwritten; either
+ *    may be NULL.  dW's rows and columns are one dim each.  Neither may
+ *    overlap X, W or the other.
+ *  workspace as above, from dg_linear_ce_grad_workspace.
+ * G is held one piece of the vocabulary at a time, rounded to the type of X
+ * (as the gradient of logits of that type would be; F16 pieces are scaled by a
+ * power of two found on the device, so that neither small probabilities nor a
+ * loss scale leave F16's range), and the products are summed in FP32 over all
+ * pieces; dX and dW are rounded once.
+ */
+dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W,
+                            const int64_t *target, int64_t ignore_index,
+                            float alpha, const float *lse,
+                            const float *dloss, int64_t dloss_stride,
+                            const dg_view *dX, const dg_view *dW,
+                            void *workspace, int64_t workspace_bytes,
+                            void *stream);
+
+/* Workspace of dg_linear_ce / dg_linear_ce_grad for these views: the least
+ * that the call takes and what it is fastest with (host only). */
+dg_status dg_linear_ce_workspace(const dg_view *X, const dg_view *W,
+                                 int64_t *least, int64_t *best);
+dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W,
+                                      const dg_view *dX, const dg_view *dW,
+                                      int64_t *least, int64_t *best);
+
 /* Human-readable name of a status code (static storage). */
 const char *dg_status_string(dg_status s);
 
 /*
  * dg_sync_status — synchronise `stream`, then return and clear the device
  * error word of the current device: DG_ERR_TIMEOUT if a kernel's bounded wait
- * gave up since the last check (its output is then undefined), DG_ERR_CUDA if
- * the synchronisation failed, DG_OK otherwise.
+ * gave up since the last check (its output is then undefined), DG_ERR_VALUE if
+ * a target of dg_linear_ce was out of range, DG_ERR_CUDA if the
+ * synchronisation failed, DG_OK otherwise.
  */
 dg_status dg_sync_status(void *stream);
 

@@ -96,6 +96,16 @@ class dg_tune_result(ctypes.Structure):
     ]
 
 
+class dg_w4(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+        ("K", ctypes.c_int64), ("N", ctypes.c_int64),
+        ("code_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("zero_stride", ctypes.c_int64),
+        ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32 * 2),
+    ]
+
+
 class DgError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -116,6 +126,19 @@ def _load():
     L.dg_gemm_ex.restype = ctypes.c_int
     L.dg_gemv.argtypes = [V, V, V, ctypes.c_float, ctypes.c_float, ctypes.c_void_p]
     L.dg_gemv.restype = ctypes.c_int
+    L.dg_gemv_w4.argtypes = [V, P(dg_w4), V, ctypes.c_float, ctypes.c_float, P(dg_epilogue), ctypes.c_void_p]
+    L.dg_gemv_w4.restype = ctypes.c_int
+    I64 = ctypes.c_int64
+    L.dg_linear_ce.argtypes = [V, V, ctypes.c_void_p, I64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                               ctypes.c_void_p, I64, ctypes.c_void_p]
+    L.dg_linear_ce.restype = ctypes.c_int
+    L.dg_linear_ce_grad.argtypes = [V, V, ctypes.c_void_p, I64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, I64,
+                                    V, V, ctypes.c_void_p, I64, ctypes.c_void_p]
+    L.dg_linear_ce_grad.restype = ctypes.c_int
+    L.dg_linear_ce_workspace.argtypes = [V, V, P(I64), P(I64)]
+    L.dg_linear_ce_workspace.restype = ctypes.c_int
+    L.dg_linear_ce_grad_workspace.argtypes = [V, V, V, V, P(I64), P(I64)]
+    L.dg_linear_ce_grad_workspace.restype = ctypes.c_int
     L.dg_status_string.argtypes = [ctypes.c_int]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_sync_status.argtypes = [ctypes.c_void_p]
@@ -246,6 +269,48 @@ def dg_gemv(x: dg_view, W: dg_view, y: dg_view, alpha: float, beta: float, strea
                        _stream_ptr(stream))
 
 
+def dg_gemv_w4(x: dg_view, W: dg_w4, y: dg_view, alpha: float, beta: float, epi=None, stream=None) -> int:
+    """y = act(alpha * x W + beta * y + bias) for at most 8 rows and 4-bit weights; returns the status."""
+    return lib.dg_gemv_w4(ctypes.byref(x), ctypes.byref(W), ctypes.byref(y), float(alpha), float(beta),
+                          None if epi is None else ctypes.byref(epi), _stream_ptr(stream))
+
+
+def dg_linear_ce(X: dg_view, W: dg_view, target, ignore_index: int, alpha: float, loss, lse, workspace,
+                 workspace_bytes: int, stream=None) -> int:
+    """loss and lse of the logits alpha * X W, which are not kept; returns the status."""
+    return lib.dg_linear_ce(ctypes.byref(X), ctypes.byref(W), _ptr(target), int(ignore_index), float(alpha),
+                            _ptr(loss), _ptr(lse), _ptr(workspace), int(workspace_bytes), _stream_ptr(stream))
+
+
+def dg_linear_ce_grad(X: dg_view, W: dg_view, target, ignore_index: int, alpha: float, lse, dloss, dloss_stride: int,
+                      dX, dW, workspace, workspace_bytes: int, stream=None) -> int:
+    """dX and dW (dg_view or None) of sum_t dloss[t] * loss[t]; returns the status."""
+    return lib.dg_linear_ce_grad(ctypes.byref(X), ctypes.byref(W), _ptr(target), int(ignore_index), float(alpha),
+                                 _ptr(lse), _ptr(dloss), int(dloss_stride), None if dX is None else ctypes.byref(dX),
+                                 None if dW is None else ctypes.byref(dW), _ptr(workspace), int(workspace_bytes),
+                                 _stream_ptr(stream))
+
+
+def dg_linear_ce_workspace(X: dg_view, W: dg_view):
+    """(least, best): bytes of workspace dg_linear_ce needs and is fastest with."""
+    least, best = ctypes.c_int64(), ctypes.c_int64()
+    st = lib.dg_linear_ce_workspace(ctypes.byref(X), ctypes.byref(W), ctypes.byref(least), ctypes.byref(best))
+    if st != DG_OK:
+        raise DgError(st, "dg_linear_ce_workspace")
+    return least.value, best.value
+
+
+def dg_linear_ce_grad_workspace(X: dg_view, W: dg_view, dX=None, dW=None):
+    """(least, best): bytes of workspace dg_linear_ce_grad needs and is fastest with."""
+    least, best = ctypes.c_int64(), ctypes.c_int64()
+    st = lib.dg_linear_ce_grad_workspace(ctypes.byref(X), ctypes.byref(W), None if dX is None else ctypes.byref(dX),
+                                         None if dW is None else ctypes.byref(dW), ctypes.byref(least),
+                                         ctypes.byref(best))
+    if st != DG_OK:
+        raise DgError(st, "dg_linear_ce_grad_workspace")
+    return least.value, best.value
+
+
 def dg_sync_status(stream=None) -> int:
     return lib.dg_sync_status(_stream_ptr(stream))
 
@@ -320,3 +385,118 @@ def gemv(x, W, y, alpha: float = 1.0, beta: float = 0.0, stream=None):
     if st != DG_OK:
         raise DgError(st, "dg_gemv")
     return y
+
+
+def w4(codes, scales, zeros=None, group: int = 128, K: int | None = None) -> dg_w4:
+    """A dg_w4 of torch tensors in place: codes uint8 [N, ceil(K / 2)], two codes
+    per byte along k (even k in the low four bits), scales [N, ceil(K / group)],
+    zeros uint8 of the same shape or None (every zero point is 8).  K defaults
+    to two per byte.  The last dim of each tensor must be contiguous."""
+    import torch
+
+    n, nbytes = codes.shape
+    K = 2 * nbytes if K is None else int(K)
+    groups = -(-K // group) if group > 0 else -1
+    if codes.dtype != torch.uint8 or (zeros is not None and zeros.dtype != torch.uint8):
+        raise TypeError("codes and zeros must be uint8")
+    if nbytes != (K + 1) // 2:
+        raise ValueError(f"codes must have ceil(K / 2) = {(K + 1) // 2} bytes a row, not {nbytes}")
+    for t in (scales, zeros):
+        if t is not None and tuple(t.shape) != (n, groups):
+            raise ValueError(f"scales and zeros must be [{n}, {groups}]")
+    for t in (codes, scales, zeros):
+        if t is not None and t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError("codes, scales and zeros must be contiguous along their last dim")
+    w = dg_w4()
+    w.codes, w.scales = codes.data_ptr(), scales.data_ptr()
+    w.K, w.N, w.group, w.scale_dtype = K, n, int(group), _torch_dtype_code(scales)
+    w.code_stride, w.scale_stride = codes.stride(0), scales.stride(0) * scales.element_size()
+    if zeros is not None:
+        w.zeros, w.zero_stride = zeros.data_ptr(), zeros.stride(0)
+    return w
+
+
+def gemv_w4(x, codes, scales, y, zeros=None, group: int = 128, alpha: float = 1.0, beta: float = 0.0,
+            stream=None, bias=None, act="none"):
+    """dg_gemv_w4 on torch tensors: y = act(alpha * x W + beta * y + bias), W [K x N]
+    given by its codes, scales and zeros (see w4); x is [R, K] or [K], R <= 8.
+    Raises DgError on a bad status."""
+    xv = view(x, 1 if x.dim() > 1 else 0)
+    yv = view(y, 1 if y.dim() > 1 else 0)
+    W = w4(codes, scales, zeros, group, x.shape[-1])
+    epi = None if bias is None and act in ("none", DG_ACT_NONE) else epilogue(bias, act)
+    st = dg_gemv_w4(xv, W, yv, alpha, beta, epi, stream)
+    if st != DG_OK:
+        raise DgError(st, "dg_gemv_w4")
+    return y
+
+
+def _vector(t, name, dtype, n):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+    return t
+
+
+def _workspace(nbytes: int, stream):
+    """Device bytes of torch's pool, allocated on the stream that uses them."""
+    import torch
+
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def linear_ce(x, w, target, loss, lse, alpha: float = 1.0, ignore_index: int = -100, stream=None, workspace=None,
+              x_row_dims: int | None = None):
+    """dg_linear_ce on torch tensors: the cross entropy of the logits alpha * x w
+    against `target`, without keeping the logits.  x is [..., D] (x_row_dims
+    defaults to all dims but the last), w [D, V] (a [V, D] weight is passed as
+    weight.t()), target int64, loss and lse float32, one per row.  `workspace`
+    is a uint8 tensor (at least dg_linear_ce_workspace's bytes); None takes one
+    from torch's pool.  Raises DgError on a bad status; returns (loss, lse)."""
+    import torch
+
+    xv, wv = view(x, x.dim() - 1 if x_row_dims is None else x_row_dims), view(w)
+    rows = x.numel() // x.shape[-1] if x.shape[-1] else target.numel()
+    _vector(target, "target", torch.int64, rows)
+    _vector(loss, "loss", torch.float32, rows)
+    _vector(lse, "lse", torch.float32, rows)
+    if workspace is None:
+        workspace = _workspace(dg_linear_ce_workspace(xv, wv)[1], stream)
+    st = dg_linear_ce(xv, wv, target, ignore_index, alpha, loss, lse, workspace, workspace.numel(), stream)
+    if st != DG_OK:
+        raise DgError(st, "dg_linear_ce")
+    return loss, lse
+
+
+def linear_ce_grad(x, w, target, lse, dloss, dx=None, dw=None, alpha: float = 1.0, ignore_index: int = -100,
+                   stream=None, workspace=None, x_row_dims: int | None = None):
+    """dg_linear_ce_grad on torch tensors: the gradients of sum(dloss * loss) into
+    dx (like x) and dw (like w), either of which may be None.  dloss is float32,
+    one per row, or one value for all rows (one element, or expanded from one);
+    lse is what linear_ce wrote.  Raises DgError on a bad status; returns
+    (dx, dw)."""
+    import torch
+
+    rd = x.dim() - 1 if x_row_dims is None else x_row_dims
+    xv, wv = view(x, rd), view(w)
+    dxv = None if dx is None else view(dx, rd)
+    dwv = None if dw is None else view(dw)
+    rows = x.numel() // x.shape[-1] if x.shape[-1] else target.numel()
+    _vector(target, "target", torch.int64, rows)
+    _vector(lse, "lse", torch.float32, rows)
+    shared = dloss.numel() == 1 or all(s == 0 for s, n in zip(dloss.stride(), dloss.shape) if n > 1)
+    if not shared:
+        _vector(dloss, "dloss", torch.float32, rows)
+    elif dloss.dtype != torch.float32 or dloss.numel() not in (1, rows):
+        raise ValueError(f"dloss must be a float32 tensor of 1 or {rows} elements")
+    if workspace is None:
+        workspace = _workspace(dg_linear_ce_grad_workspace(xv, wv, dxv, dwv)[1], stream)
+    st = dg_linear_ce_grad(xv, wv, target, ignore_index, alpha, lse, dloss, 0 if shared else 4, dxv, dwv, workspace,
+                           workspace.numel(), stream)
+    if st != DG_OK:
+        raise DgError(st, "dg_linear_ce_grad")
+    return dx, dw

@@ -1073,6 +1073,22 @@ std::vector<Override> tune_candidates(const dg_plan_info &base) {
 }
 
 }  // namespace
+
+bool device_pointer(const void *p) { return device_accessible(p); }
+
+dg_status device_info(int *num_sms, int **err_word) {
+    DeviceState *ds = nullptr;
+    const dg_status st = device_state(&ds);
+    if (st != DG_OK) return st;
+    *num_sms = ds->num_sms;
+    *err_word = ds->err_word;
+    return DG_OK;
+}
+
+int early_launch_mode() { return g_pdl.load(); }
+
+void count_launch() { g_launches.fetch_add(1); }
+
 }  // namespace dg
 
 using namespace dg;
@@ -1374,6 +1390,84 @@ dg_status dg_gemv(const dg_view *x, const dg_view *W, const dg_view *y, float al
     return dg_gemm(x, W, y, alpha, beta, nullptr, nullptr, stream);
 }
 
+dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y, float alpha, float beta,
+                     const dg_epilogue *epilogue, void *stream) {
+    if (!x || !W || !y) return DG_ERR_NULL;
+    const float *bias = nullptr;
+    int act = DG_ACT_NONE;
+    if (epilogue) {
+        if (epilogue->activation < DG_ACT_NONE || epilogue->activation > DG_ACT_GELU_TANH || epilogue->reserved != 0)
+            return DG_ERR_VALUE;
+        bias = epilogue->bias;
+        act = epilogue->activation;
+    }
+    ViewInfo xi, yi;
+    dg_status st;
+    if ((st = analyse(x, false, &xi)) != DG_OK) return st;
+    if ((st = analyse(y, true, &yi)) != DG_OK) return st;
+    if (W->reserved[0] != 0 || W->reserved[1] != 0) return DG_ERR_VALUE;
+    if (W->K < 0 || W->N < 0 || xi.cols != W->K || yi.rows != xi.rows || yi.cols != W->N) return DG_ERR_SHAPE;
+    if (x->dtype != DG_F16 && x->dtype != DG_BF16) return DG_ERR_DTYPE;
+    if (y->dtype == DG_E4M3) return DG_ERR_DTYPE;
+    if (W->scale_dtype != DG_F32 && W->scale_dtype != DG_F16 && W->scale_dtype != DG_BF16) return DG_ERR_DTYPE;
+    if (W->group <= 0 || W->group % 32 != 0) return DG_ERR_VALUE;
+    if (!std::isfinite(alpha) || !std::isfinite(beta)) return DG_ERR_VALUE;
+    if (xi.rows > 8 || W->K > INT32_MAX || W->N > INT32_MAX) return DG_ERR_UNSUPPORTED;
+    if (xi.rows == 0 || W->N == 0) return DG_OK;
+    const bool product = alpha != 0.f && W->K > 0;
+    if (W->code_stride < 0 || W->scale_stride < 0 || (W->zeros && W->zero_stride < 0)) return DG_ERR_STRIDE;
+    const int ses = elem_size(W->scale_dtype);
+    if (W->K > 0) {
+        if (!W->codes || !W->scales) return DG_ERR_NULL;
+        if (reinterpret_cast<uintptr_t>(W->scales) % ses || (W->N > 1 && W->scale_stride % ses)) return DG_ERR_ALIGN;
+        const int64_t groups = (W->K + W->group - 1) / W->group;
+        const struct {
+            int64_t stride, bytes;
+        } extent[3] = {{W->code_stride, (W->K + 1) / 2},
+                       {W->scale_stride, groups * ses},
+                       {W->zeros ? W->zero_stride : 0, groups}};
+        for (const auto &e : extent) {
+            int64_t t;
+            if (__builtin_mul_overflow(W->N - 1, e.stride, &t) || __builtin_add_overflow(t, e.bytes, &t))
+                return DG_ERR_STRIDE;
+        }
+    }
+    if (product && (!device_accessible(x->ptr) || !device_accessible(W->codes) || !device_accessible(W->scales) ||
+                    (W->zeros && !device_accessible(W->zeros))))
+        return DG_ERR_POINTER;
+    if (!device_accessible(y->ptr) || (bias && !device_accessible(bias))) return DG_ERR_POINTER;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int pdl = g_pdl.load() != 0;
+    cudaError_t err;
+    if (!product) {
+        err = launch_scale_c(dev_view(y, yi), xi.rows, W->N, beta, bias, act, pdl, s);
+    } else {
+        GemvW4Params p{};
+        p.x = dev_view(x, xi);
+        p.y = dev_view(y, yi);
+        p.codes = static_cast<const uint8_t *>(W->codes);
+        p.scales = static_cast<const char *>(W->scales);
+        p.zeros = static_cast<const uint8_t *>(W->zeros);
+        p.code_stride = W->code_stride;
+        p.scale_stride = W->scale_stride;
+        p.zero_stride = W->zero_stride;
+        p.R = (int32_t)xi.rows;
+        p.K = (int32_t)W->K;
+        p.N = (int32_t)W->N;
+        p.group = W->group;
+        p.scale_dtype = W->scale_dtype;
+        p.alpha = alpha;
+        p.beta = beta;
+        p.bias = bias;
+        p.act = act;
+        p.pdl = pdl;
+        err = launch_gemv_w4(p, s);
+    }
+    if (err != cudaSuccess) return DG_ERR_CUDA;
+    g_launches.fetch_add(1);
+    return DG_OK;
+}
+
 const char *dg_status_string(dg_status s) {
     switch (s) {
     case DG_OK: return "ok";
@@ -1402,7 +1496,7 @@ dg_status dg_sync_status(void *stream) {
     if (word != 0) {
         if (cudaMemset(ds->err_word, 0, sizeof(int)) != cudaSuccess) return DG_ERR_CUDA;
         if (cudaDeviceSynchronize() != cudaSuccess) return DG_ERR_CUDA;
-        return word == DG_ERR_TIMEOUT ? DG_ERR_TIMEOUT : DG_ERR_CUDA;
+        return word == DG_ERR_TIMEOUT || word == DG_ERR_VALUE ? (dg_status)word : DG_ERR_CUDA;
     }
     return DG_OK;
 }

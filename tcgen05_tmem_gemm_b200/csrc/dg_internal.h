@@ -160,6 +160,22 @@ struct GemvParams {
     int32_t pdl;             // 0 off, 1 release dependents at start, 2 near the end
 };
 
+// 4-bit weights (see dg_w4), x [R x K], y [R x N].
+struct GemvW4Params {
+    DevView x, y;
+    const uint8_t *codes;
+    const char *scales;
+    const uint8_t *zeros;    // null: every zero point is 8
+    int64_t code_stride, scale_stride, zero_stride;
+    int32_t R, K, N;
+    int32_t group;
+    int32_t scale_dtype;
+    float alpha, beta;
+    const float *bias;
+    int32_t act;
+    int32_t pdl;
+};
+
 struct SimtParams {
     DevView a, b;            // a: rows m, cols k;  b: rows k, cols n
     DevView c;               // rows m, cols n
@@ -189,8 +205,16 @@ int umma_pair_max_stages(int bn, bool epi_tma, int ksub);
 cudaError_t launch_gemv_n(const GemvParams &p, const CUtensorMap *tmap_w, cudaStream_t s, int *grid_out);
 size_t gemv_n_smem_bytes(int r_inst, int kper);
 cudaError_t launch_gemv_k(const GemvParams &p, cudaStream_t s, int *grid_out);
+cudaError_t launch_gemv_w4(const GemvW4Params &p, cudaStream_t s);
 cudaError_t launch_simt(const SimtParams &p, cudaStream_t s);
 cudaError_t launch_scale_c(const DevView &c, int64_t M, int64_t N, float beta, const float *bias, int act, int pdl,
                            cudaStream_t s);
+
+// --------------------------------------------- what the entry points share
+// (api.cu; used by the entry points that have a file of their own)
+bool device_pointer(const void *p);                       // device memory of the current device
+dg_status device_info(int *num_sms, int **err_word);      // the current device's, set up on first use
+int early_launch_mode();                                  // DG_OPT_EARLY_LAUNCH
+void count_launch();                                      // one kernel enqueued (dg_launch_count)
 
 }  // namespace dg

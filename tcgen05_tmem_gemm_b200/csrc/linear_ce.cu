@@ -1,0 +1,565 @@
+// Linear cross entropy: the loss of an output layer from its input X and
+// weight W without keeping the logits, and its gradient.
+//
+//   z[t][v] = alpha x_t w_v,   lse[t] = log sum_v exp z[t][v],
+//   loss[t] = lse[t] - z[t][target],
+//   G[t][v] = dloss[t] (exp(z[t][v] - lse[t]) - (v == target)),
+//   dX = alpha G W^T,  dW = alpha X^T G.
+//
+// The vocabulary is walked in pieces.  A row's logits of one piece are reduced
+// to a pair (m, s): their maximum and sum_v exp(z - m); two pairs join as
+//   m = max(m1, m2),  s = s1 exp(m1 - m) + s2 exp(m2 - m),
+// so one pass over the logits is enough and none of them has to be kept.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+
+namespace dg {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kStatCols = 2048;                    // logits per block of ce_stats_kernel
+constexpr int64_t kForwardPiece = int64_t(256) << 20;  // most bytes of one piece of logits (forward)
+constexpr int64_t kGradPiece = int64_t(512) << 20;     // most bytes of one piece of G
+constexpr int kPieceCols = 256;                    // pieces are whole multiples of this many columns
+
+// What a row's target means.
+constexpr int kIgnored = -1, kInvalid = -2;
+
+__device__ __forceinline__ int read_target(const int64_t *target, int64_t ignore_index, int64_t V, int64_t t) {
+    const int64_t y = target[t];
+    if (y == ignore_index) return kIgnored;
+    return (y < 0 || y >= V) ? kInvalid : (int)y;
+}
+
+// exp(x) = 2^(x log2 e) with the hardware's power of two (relative error
+// about 2^-22, below the FP32 sums it goes into).
+__device__ __forceinline__ float exp_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+    return y;
+}
+
+// The pair (m, s) with one more; m == -inf means an empty pair.  A NaN or
+// +infinity among the logits ends as s = NaN.
+__device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
+    const float mx = fmaxf(m, m2);
+    const float a = m == -INFINITY ? (s != s ? s : 0.f) : s * exp_fast(m - mx);
+    const float b = m2 == -INFINITY ? (s2 != s2 ? s2 : 0.f) : s2 * exp_fast(m2 - mx);
+    m = mx;
+    s = a + b;
+}
+
+// One block per row and run of kStatCols columns of a piece of FP32 logits:
+// the run's (m, s), and the target's logit if it lies in the run.
+__global__ void __launch_bounds__(256)
+    ce_stats_kernel(const float *z, int64_t ldz, int64_t T, int64_t V, int v0, int cols, int chunks,
+                    const int64_t *target, int64_t ignore_index, float2 *part, float *ztarget) {
+    pdl_wait_then_release();
+    __shared__ float2 red[8];
+    const int64_t t = blockIdx.x / chunks;
+    const int chunk = (int)(blockIdx.x - t * chunks);
+    const float *row = z + t * ldz;
+    const int c0 = chunk * kStatCols, c1 = min(cols, c0 + kStatCols);
+    float v[kStatCols / 256];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kStatCols / 256; ++i) {
+        const int c = c0 + threadIdx.x + 256 * i;
+        v[i] = c < c1 ? row[c] : -INFINITY;
+        m = fmaxf(m, v[i]);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kStatCols / 256; ++i)
+        s += v[i] == -INFINITY ? 0.f : exp_fast(v[i] - m);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, off), s2 = __shfl_xor_sync(0xffffffffu, s, off);
+        join(m, s, m2, s2);
+    }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) join(m, s, red[w].x, red[w].y);
+        part[(int64_t)chunk * T + t] = make_float2(m, s);
+        const int y = read_target(target, ignore_index, V, t);
+        if (y >= v0 + c0 && y < v0 + c1) ztarget[t] = row[y - v0];
+    }
+}
+
+// Joins the `slots` pairs of each row of a piece, in slot order, with the
+// row's pair of the earlier pieces; the last piece writes lse and loss.
+// 32 rows per block, eight warps walk the slots.
+__global__ void __launch_bounds__(256)
+    ce_join_kernel(const float2 *part, int slots, int64_t T, int64_t V, bool first, bool last, float2 *run,
+                   const int64_t *target, int64_t ignore_index, const float *ztarget, float *loss, float *lse,
+                   int *err_word) {
+    pdl_wait_then_release();
+    __shared__ float2 red[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.f;
+    if (t < T)
+        for (int i = warp; i < slots; i += 8) {
+            const float2 q = part[(int64_t)i * T + t];
+            join(m, s, q.x, q.y);
+        }
+    red[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp != 0 || t >= T) return;
+    for (int w = 1; w < 8; ++w) join(m, s, red[w][lane].x, red[w][lane].y);
+    if (!first) join(m, s, run[t].x, run[t].y);
+    if (!last) {
+        run[t] = make_float2(m, s);
+        return;
+    }
+    const float ls = logf(s);
+    lse[t] = m + ls;
+    const int y = read_target(target, ignore_index, V, t);
+    if (y == kInvalid) {
+        loss[t] = NAN;
+        if (err_word) atomicCAS(err_word, 0, (int)DG_ERR_VALUE);
+    } else {
+        // m - z first: exact when the target is near the maximum
+        loss[t] = y == kIgnored ? 0.f : (m - ztarget[t]) + ls;
+    }
+}
+
+// What the gradient's kernels need of a row.
+struct RowGrad {
+    float lse, scale;  // G = scale * (exp(z - lse) - 1[v == target])
+    int32_t target;    // negative: the row of G is zero
+    int32_t pad_;
+};
+
+// F16 only: the power of two that brings the largest |dloss| of a row that
+// counts to [2^9, 2^10), and its inverse in `undo` (n entries, a constant
+// scale array for the products).  One block.
+__global__ void __launch_bounds__(1024)
+    ce_norm_kernel(const char *dloss, int64_t dloss_stride, const int64_t *target, int64_t ignore_index, int64_t T,
+                   int64_t V, float *norm, float *undo, int64_t n) {
+    pdl_wait_then_release();
+    __shared__ float red[32];
+    float big = 0.f;
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+        if (read_target(target, ignore_index, V, t) < 0) continue;
+        const float g = fabsf(*reinterpret_cast<const float *>(dloss + t * dloss_stride));
+        if (g < INFINITY) big = fmaxf(big, g);
+    }
+    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = big;
+    __syncthreads();
+    big = red[threadIdx.x & 31];
+    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    int e = 0;
+    if (big > 0.f) frexpf(big, &e);  // big = f 2^e, f in [1/2, 1)
+    e = 10 - e;
+    e = min(max(e, -126), 126);      // both powers stay normal
+    if (threadIdx.x == 0) *norm = ldexpf(1.f, e);
+    for (int64_t i = threadIdx.x; i < n; i += 1024) undo[i] = ldexpf(1.f, -e);
+}
+
+// Per row: its RowGrad, and (xc != null) a copy of X's row, zero in rows that
+// take no part, so that whatever those rows hold stays out of dW.
+__global__ void __launch_bounds__(256)
+    ce_rows_kernel(const DevView x, int D, int64_t T, int64_t V, const int64_t *target, int64_t ignore_index,
+                   const float *lse, const char *dloss, int64_t dloss_stride, const float *norm, RowGrad *rows,
+                   char *xc, int64_t ldx, int *err_word) {
+    pdl_wait_then_release();
+    const int64_t t = blockIdx.x;
+    const int y = target ? read_target(target, ignore_index, V, t) : 0;
+    if (rows && threadIdx.x == 0) {
+        RowGrad r;
+        r.lse = lse[t];
+        r.scale = y < 0 ? 0.f : *reinterpret_cast<const float *>(dloss + t * dloss_stride) * (norm ? *norm : 1.f);
+        r.target = y;
+        r.pad_ = 0;
+        rows[t] = r;
+        if (y == kInvalid && err_word) atomicCAS(err_word, 0, (int)DG_ERR_VALUE);
+    }
+    if (!xc) return;
+    const char *src = x.ptr + axis_offset(x.row, t);
+    char *dst = xc + t * ldx;
+    if (x.dtype == DG_F32) {
+        for (int d = threadIdx.x; d < D; d += 256)
+            reinterpret_cast<float *>(dst)[d] =
+                y < 0 ? 0.f : *reinterpret_cast<const float *>(src + axis_offset(x.col, d));
+    } else {
+        for (int d = threadIdx.x; d < D; d += 256)
+            reinterpret_cast<uint16_t *>(dst)[d] =
+                y < 0 ? 0 : *reinterpret_cast<const uint16_t *>(src + axis_offset(x.col, d));
+    }
+}
+
+// A piece of FP32 logits to the piece of G.
+__global__ void __launch_bounds__(256)
+    ce_grad_kernel(const float *z, int64_t ldz, int64_t T, int v0, int cols, const RowGrad *rows, char *g, int64_t ldg,
+                   int dtype) {
+    pdl_wait_then_release();
+    const int chunks = (cols + 1023) / 1024;
+    const int64_t t = blockIdx.x / chunks;
+    const int c0 = (int)(blockIdx.x - t * chunks) * 1024;
+    const RowGrad r = rows[t];
+    const int es = elem_bytes(dtype);
+    for (int c = c0 + threadIdx.x; c < min(cols, c0 + 1024); c += 256) {
+        float v = 0.f;
+        if (r.target >= 0) v = r.scale * (exp_fast(z[t * ldz + c] - r.lse) - (v0 + c == r.target ? 1.f : 0.f));
+        store_elem(g + t * ldg + (int64_t)c * es, dtype, v);
+    }
+}
+
+// dX = the FP32 sum over all pieces, rounded once.
+__global__ void __launch_bounds__(256) ce_round_kernel(const float *acc, int64_t ld, const DevView out, int D) {
+    pdl_wait_then_release();
+    const int64_t t = blockIdx.x;
+    char *row = const_cast<char *>(out.ptr) + axis_offset(out.row, t);
+    for (int d = threadIdx.x; d < D; d += 256) store_elem(row + axis_offset(out.col, d), out.dtype, acc[t * ld + d]);
+}
+
+// ------------------------------------------------------------------- host side
+
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+
+dg_view view2(const void *ptr, int64_t rows, int64_t cols, int64_t rs, int64_t cs, int dtype) {
+    dg_view v;
+    std::memset(&v, 0, sizeof(v));
+    v.ptr = const_cast<void *>(ptr);
+    v.ndim = 2;
+    v.row_dims = 1;
+    v.shape[0] = rows;
+    v.shape[1] = cols;
+    v.stride[0] = rs;
+    v.stride[1] = cs;
+    v.dtype = dtype;
+    return v;
+}
+
+// One merged dim's stride, or any legal one for an extent of 1.
+int64_t stride_of(const Axis &a, int es) { return a.n == 1 ? a.stride[0] : es; }
+
+// A matrix given by its two strides: W and dW.
+struct Mat {
+    char *ptr = nullptr;
+    int64_t rs = 0, cs = 0;
+    int dtype = 0;
+};
+
+struct Problem {
+    int64_t T = 0, D = 0, V = 0;
+    int es = 0;
+    ViewInfo x, w, dx, dw;
+    Mat wm, dwm;
+    bool tensor = false;   // 16-bit operands
+};
+
+dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
+    dg_status st;
+    if (!X || !W) return DG_ERR_NULL;
+    if ((st = analyse(X, false, &p->x)) != DG_OK) return st;
+    if ((st = analyse(W, false, &p->w)) != DG_OK) return st;
+    p->T = p->x.rows;
+    p->D = p->x.cols;
+    p->V = p->w.cols;
+    if (p->w.rows != p->D || (p->V == 0 && p->T > 0)) return DG_ERR_SHAPE;
+    if (X->dtype != W->dtype || X->dtype == DG_E4M3) return DG_ERR_DTYPE;
+    p->es = elem_size(X->dtype);
+    p->tensor = X->dtype != DG_F32;
+    // the products put T and V on a grid dimension of the CUDA-core kernel
+    const int64_t most = int64_t(65535) * 64;
+    if (p->T > most || p->V > most || p->D > most) return DG_ERR_UNSUPPORTED;
+    if (p->w.row.n > 1 || p->w.col.n > 1) return DG_ERR_UNSUPPORTED;
+    p->wm = Mat{static_cast<char *>(W->ptr), stride_of(p->w.row, p->es), stride_of(p->w.col, p->es), W->dtype};
+    return DG_OK;
+}
+
+// The workspace's parts, each 256-byte aligned, for pieces of `piece` columns.
+struct Layout {
+    int64_t xc = 0, part = 0, run = 0, ztarget = 0, z = 0, rows = 0, norm = 0, undo = 0, g = 0, acc = 0;
+    int64_t ldx = 0, ldz = 0, ldg = 0;
+    int64_t total = 0;
+};
+
+int64_t take(Layout *l, int64_t bytes) {
+    const int64_t at = l->total;
+    l->total += align256(bytes);
+    return at;
+}
+
+// X is copied when the tensor cores could not read it in place through TMA
+// (a copy costs T D elements, a gathered operand slows every tile).
+bool forward_copies_x(const Problem &p) { return p.tensor && !p.x.tma_ok; }
+
+int64_t stat_slots(int64_t piece) { return (piece + kStatCols - 1) / kStatCols; }
+
+Layout forward_layout(const Problem &p, int64_t piece) {
+    Layout l;
+    l.ldx = align256(p.D * p.es);
+    l.ldz = align256(piece * 4);
+    l.xc = take(&l, forward_copies_x(p) ? p.T * l.ldx : 0);
+    l.part = take(&l, stat_slots(piece) * p.T * 8);
+    l.run = take(&l, p.T * 8);
+    l.ztarget = take(&l, p.T * 4);
+    l.z = take(&l, p.T * l.ldz);
+    return l;
+}
+
+Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int dx_dtype) {
+    Layout l;
+    l.ldx = align256(p.D * p.es);
+    l.ldz = align256(piece * 4);
+    l.ldg = align256(piece * p.es);
+    l.xc = take(&l, need_dw || forward_copies_x(p) ? p.T * l.ldx : 0);
+    l.rows = take(&l, p.T * (int64_t)sizeof(RowGrad));
+    l.norm = take(&l, 256);
+    l.undo = take(&l, p.es == 2 ? std::max(p.T, std::max(p.D, p.V)) * 4 : 0);
+    l.acc = take(&l, need_dx && piece < p.V && dx_dtype != DG_F32 ? p.T * p.D * 4 : 0);
+    l.g = take(&l, p.T * l.ldg);
+    l.z = take(&l, p.T * l.ldz);
+    return l;
+}
+
+int64_t piece_min(const Problem &p) { return std::min<int64_t>(std::max<int64_t>(p.V, 1), kPieceCols); }
+
+// Pieces of equal size, whole multiples of kPieceCols: as many columns as
+// `bytes` of `per_col` bytes each allow.
+int64_t piece_for(const Problem &p, int64_t bytes, int64_t per_col) {
+    int64_t cols = per_col > 0 ? bytes / per_col : p.V;
+    if (cols >= p.V) return std::max<int64_t>(p.V, 1);
+    cols = std::max<int64_t>(cols / kPieceCols * kPieceCols, kPieceCols);
+    const int64_t n = (p.V + cols - 1) / cols;
+    const int64_t even = ((p.V + n - 1) / n + kPieceCols - 1) / kPieceCols * kPieceCols;
+    return std::min(cols, even);
+}
+
+dg_status launched(cudaError_t e) {
+    if (e != cudaSuccess) return DG_ERR_CUDA;
+    count_launch();
+    return DG_OK;
+}
+
+DevView dev_of(const dg_view *v, const ViewInfo &vi) {
+    DevView d{};
+    d.ptr = static_cast<const char *>(v->ptr);
+    d.row = vi.row;
+    d.col = vi.col;
+    d.dtype = v->dtype;
+    return d;
+}
+
+// The largest piece whose layout fits `bytes` (0: not even the smallest).
+template <typename LayoutOf>
+int64_t fit_piece(const Problem &p, int64_t bytes, int64_t best, LayoutOf layout_of) {
+    int64_t piece = best;
+    while (layout_of(piece).total > bytes) {
+        if (piece <= piece_min(p)) return 0;
+        const int64_t half = (piece / 2 + kPieceCols - 1) / kPieceCols * kPieceCols;
+        piece = std::max(piece_min(p), std::min(half, piece - 1));
+    }
+    return piece;
+}
+
+}  // namespace
+
+}  // namespace dg
+
+using namespace dg;
+
+#define DG_TRY(call)                         \
+    do {                                     \
+        const dg_status st_ = (call);        \
+        if (st_ != DG_OK) return st_;        \
+    } while (0)
+
+extern "C" {
+
+dg_status dg_linear_ce_workspace(const dg_view *X, const dg_view *W, int64_t *least, int64_t *best) {
+    if (!least || !best) return DG_ERR_NULL;
+    Problem p;
+    DG_TRY(check_problem(X, W, &p));
+    *least = forward_layout(p, piece_min(p)).total;
+    *best = forward_layout(p, piece_for(p, kForwardPiece, p.T * 4)).total;
+    return DG_OK;
+}
+
+dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target, int64_t ignore_index, float alpha,
+                       float *loss, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
+    Problem p;
+    DG_TRY(check_problem(X, W, &p));
+    if (!std::isfinite(alpha)) return DG_ERR_VALUE;
+    if (p.T == 0) return DG_OK;
+    if (!target || !loss || !lse || !workspace) return DG_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(target) % 8 || reinterpret_cast<uintptr_t>(loss) % 4 ||
+        reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256)
+        return DG_ERR_ALIGN;
+    auto layout_of = [&](int64_t piece) { return forward_layout(p, piece); };
+    const int64_t piece = fit_piece(p, workspace_bytes, piece_for(p, kForwardPiece, p.T * 4), layout_of);
+    if (piece == 0) return DG_ERR_SHAPE;
+    int num_sms = 0, *err_word = nullptr;
+    DG_TRY(device_info(&num_sms, &err_word));
+    if ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
+        !device_pointer(loss) || !device_pointer(lse) || !device_pointer(workspace))
+        return DG_ERR_POINTER;
+    const Layout l = layout_of(piece);
+    char *ws = static_cast<char *>(workspace);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int pdl = early_launch_mode() != 0;
+    const dim3 one(1, 1, 1);
+    dg_view xv = *X;
+    if (forward_copies_x(p)) {
+        DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x),
+                                  (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
+                                  (const char *)nullptr, (int64_t)0, (const float *)nullptr, (RowGrad *)nullptr,
+                                  ws + l.xc, l.ldx, (int *)nullptr)));
+        xv = view2(ws + l.xc, p.T, p.D, l.ldx, p.es, X->dtype);
+    }
+    float2 *part = reinterpret_cast<float2 *>(ws + l.part), *run = reinterpret_cast<float2 *>(ws + l.run);
+    float *ztarget = reinterpret_cast<float *>(ws + l.ztarget), *z = reinterpret_cast<float *>(ws + l.z);
+    for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
+        const int64_t cols = std::min(piece, p.V - v0);
+        const dg_view wv = view2(p.wm.ptr + v0 * p.wm.cs, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
+        const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
+        DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
+        const int chunks = (int)stat_slots(cols);
+        DG_TRY(launched(launch_ex(ce_stats_kernel, dim3((unsigned)(p.T * chunks)), dim3(256), 0, s, one, pdl,
+                                  (const float *)z, l.ldz / 4, p.T, p.V, (int)v0, (int)cols, chunks, target,
+                                  ignore_index, part, ztarget)));
+        DG_TRY(launched(launch_ex(ce_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, s, one, pdl,
+                                  (const float2 *)part, chunks, p.T, p.V, v0 == 0, v0 + cols == p.V, run, target,
+                                  ignore_index, (const float *)ztarget, loss, lse, err_word)));
+    }
+    return DG_OK;
+}
+
+}  // extern "C"
+
+namespace dg {
+namespace {
+
+dg_status check_grad(const dg_view *X, const dg_view *W, const dg_view *dX, const dg_view *dW, Problem *p) {
+    DG_TRY(check_problem(X, W, p));
+    if (dX) {
+        DG_TRY(analyse(dX, true, &p->dx));
+        if (p->dx.rows != p->T || p->dx.cols != p->D) return DG_ERR_SHAPE;
+        if (dX->dtype == DG_E4M3) return DG_ERR_DTYPE;
+    }
+    if (dW) {
+        DG_TRY(analyse(dW, true, &p->dw));
+        if (p->dw.rows != p->D || p->dw.cols != p->V) return DG_ERR_SHAPE;
+        if (dW->dtype == DG_E4M3) return DG_ERR_DTYPE;
+        if (p->dw.row.n > 1 || p->dw.col.n > 1) return DG_ERR_UNSUPPORTED;
+        const int es = elem_size(dW->dtype);
+        p->dwm = Mat{static_cast<char *>(dW->ptr), stride_of(p->dw.row, es), stride_of(p->dw.col, es), dW->dtype};
+    }
+    return DG_OK;
+}
+
+int64_t grad_piece(const Problem &p) { return piece_for(p, kGradPiece, p.T * p.es); }
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W, const dg_view *dX, const dg_view *dW,
+                                      int64_t *least, int64_t *best) {
+    if (!least || !best) return DG_ERR_NULL;
+    Problem p;
+    DG_TRY(check_grad(X, W, dX, dW, &p));
+    const int dxt = dX ? dX->dtype : DG_F32;
+    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt).total;
+    *best = grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt).total;
+    return DG_OK;
+}
+
+dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *target, int64_t ignore_index,
+                            float alpha, const float *lse, const float *dloss, int64_t dloss_stride, const dg_view *dX,
+                            const dg_view *dW, void *workspace, int64_t workspace_bytes, void *stream) {
+    Problem p;
+    DG_TRY(check_grad(X, W, dX, dW, &p));
+    if (!std::isfinite(alpha)) return DG_ERR_VALUE;
+    if (!dX && !dW) return DG_ERR_NULL;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int pdl = early_launch_mode() != 0;
+    const dim3 one(1, 1, 1);
+    int num_sms = 0, *err_word = nullptr;
+    if (p.T > 0) {
+        if (!target || !lse || !dloss || !workspace) return DG_ERR_NULL;
+        if (dloss_stride != 0 && dloss_stride != 4) return DG_ERR_STRIDE;
+        if (reinterpret_cast<uintptr_t>(target) % 8 || reinterpret_cast<uintptr_t>(dloss) % 4 ||
+            reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256)
+            return DG_ERR_ALIGN;
+    }
+    const int dxt = dX ? dX->dtype : DG_F32;
+    auto layout_of = [&](int64_t piece) { return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt); };
+    const int64_t piece = p.T > 0 ? fit_piece(p, workspace_bytes, grad_piece(p), layout_of) : p.V;
+    if (p.T > 0 && piece == 0) return DG_ERR_SHAPE;
+    DG_TRY(device_info(&num_sms, &err_word));
+    if (p.T > 0 && ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
+                    !device_pointer(lse) || !device_pointer(dloss) || !device_pointer(workspace)))
+        return DG_ERR_POINTER;
+    if (p.D > 0 && p.T > 0 && dX && !device_pointer(dX->ptr)) return DG_ERR_POINTER;
+    if (p.D > 0 && p.V > 0 && dW && !device_pointer(dW->ptr)) return DG_ERR_POINTER;
+    if (p.D == 0 || p.V == 0) return DG_OK;  // no gradient has an element
+    if (p.T == 0) {
+        if (!dW) return DG_OK;
+        return launched(launch_scale_c(dev_of(dW, p.dw), p.D, p.V, 0.f, nullptr, DG_ACT_NONE, pdl, s));
+    }
+    const Layout l = layout_of(piece);
+    char *ws = static_cast<char *>(workspace);
+    RowGrad *rows = reinterpret_cast<RowGrad *>(ws + l.rows);
+    float *norm = nullptr, *undo = nullptr;
+    if (X->dtype == DG_F16) {
+        norm = reinterpret_cast<float *>(ws + l.norm);
+        undo = reinterpret_cast<float *>(ws + l.undo);
+        DG_TRY(launched(launch_ex(ce_norm_kernel, one, dim3(1024), 0, s, one, pdl,
+                                  reinterpret_cast<const char *>(dloss), dloss_stride, target, ignore_index, p.T, p.V,
+                                  norm, undo, std::max(p.T, std::max(p.D, p.V)))));
+    }
+    const bool copy = dW != nullptr || forward_copies_x(p);
+    DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
+                              p.T, p.V, target, ignore_index, lse, reinterpret_cast<const char *>(dloss), dloss_stride,
+                              (const float *)norm, rows, copy ? ws + l.xc : (char *)nullptr, l.ldx, err_word)));
+    // a row that takes no part has no use for its logits, so the copy serves them too
+    const dg_view xv = copy ? view2(ws + l.xc, p.T, p.D, l.ldx, p.es, X->dtype) : *X;
+    const dg_view xt = view2(ws + l.xc, p.D, p.T, p.es, l.ldx, X->dtype);
+    char *g = ws + l.g;
+    float *z = reinterpret_cast<float *>(ws + l.z);
+    const bool sum = dX && piece < p.V;                        // dX is summed over several pieces
+    const bool own_acc = sum && dxt != DG_F32;                 // in the workspace, rounded at the end
+    const dg_view accv = own_acc ? view2(ws + l.acc, p.T, p.D, p.D * 4, 4, DG_F32) : (dX ? *dX : xv);
+    for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
+        const int64_t cols = std::min(piece, p.V - v0);
+        char *wp = p.wm.ptr + v0 * p.wm.cs;
+        const dg_view wv = view2(wp, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
+        const dg_view wt = view2(wp, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
+        const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
+        DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
+        const int64_t blocks = p.T * ((cols + 1023) / 1024);
+        DG_TRY(launched(launch_ex(ce_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, s, one, pdl, (const float *)z,
+                                  l.ldz / 4, p.T, (int)v0, (int)cols, (const RowGrad *)rows, g, l.ldg, X->dtype)));
+        const dg_view gv = view2(g, p.T, cols, l.ldg, p.es, X->dtype);
+        const dg_view gt = view2(g, cols, p.T, p.es, l.ldg, X->dtype);
+        if (dX) DG_TRY(dg_gemm(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, undo, nullptr, stream));
+        if (dW) {
+            // the product in the order that gives dW's unit stride to the columns of the output
+            char *op = p.dwm.ptr + v0 * p.dwm.cs;
+            if (p.dw.unit_dim == 2) {
+                const dg_view ov = view2(op, cols, p.D, p.dwm.cs, p.dwm.rs, p.dwm.dtype);
+                DG_TRY(dg_gemm(&gt, &xv, &ov, alpha, 0.f, undo, nullptr, stream));
+            } else {
+                const dg_view ov = view2(op, p.D, cols, p.dwm.rs, p.dwm.cs, p.dwm.dtype);
+                DG_TRY(dg_gemm(&xt, &gv, &ov, alpha, 0.f, undo, nullptr, stream));
+            }
+        }
+    }
+    if (own_acc)
+        DG_TRY(launched(launch_ex(ce_round_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl,
+                                  reinterpret_cast<const float *>(ws + l.acc), p.D, dev_of(dX, p.dx), (int)p.D)));
+    return DG_OK;
+}
+
+}  // extern "C"
