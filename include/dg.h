@@ -191,7 +191,7 @@ dg_status dg_gemv(const dg_view *x, const dg_view *W, const dg_view *y,
  *  zeros        device uint8, one per scale, only the low four bits count;
  *               column n's start at zeros + n * zero_stride.  NULL: every
  *               zero point is 8
- *  K, N         sizes of W; at most 2^31 - 1
+ *  K, N         sizes of W; at most 2^31 - 2^13
  *  *_stride     BYTES between columns, >= 0 (zero_stride is not read when
  *               zeros is NULL)
  *  group        a positive multiple of 32; the last group of a column may be

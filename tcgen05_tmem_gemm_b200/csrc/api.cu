@@ -1412,7 +1412,8 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y, float a
     if (W->scale_dtype != DG_F32 && W->scale_dtype != DG_F16 && W->scale_dtype != DG_BF16) return DG_ERR_DTYPE;
     if (W->group <= 0 || W->group % 32 != 0) return DG_ERR_VALUE;
     if (!std::isfinite(alpha) || !std::isfinite(beta)) return DG_ERR_VALUE;
-    if (xi.rows > 8 || W->K > INT32_MAX || W->N > INT32_MAX) return DG_ERR_UNSUPPORTED;
+    constexpr int64_t most = (int64_t(1) << 31) - (1 << 13);  // the kernel rounds k and n up to its tiles in 32 bits
+    if (xi.rows > 8 || W->K > most || W->N > most) return DG_ERR_UNSUPPORTED;
     if (xi.rows == 0 || W->N == 0) return DG_OK;
     const bool product = alpha != 0.f && W->K > 0;
     if (W->code_stride < 0 || W->scale_stride < 0 || (W->zeros && W->zero_stride < 0)) return DG_ERR_STRIDE;
@@ -1436,6 +1437,8 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y, float a
                     (W->zeros && !device_accessible(W->zeros))))
         return DG_ERR_POINTER;
     if (!device_accessible(y->ptr) || (bias && !device_accessible(bias))) return DG_ERR_POINTER;
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds)) != DG_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int pdl = g_pdl.load() != 0;
     cudaError_t err;
@@ -1456,12 +1459,16 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y, float a
         p.N = (int32_t)W->N;
         p.group = W->group;
         p.scale_dtype = W->scale_dtype;
+        p.in_dtype = x->dtype;
+        p.x_vec16 = xi.col.n <= 1 && (xi.col.n == 0 || xi.col.stride[0] == 2) &&
+                    reinterpret_cast<uintptr_t>(x->ptr) % 16 == 0;
+        for (int d = 0; d < xi.row.n; ++d) p.x_vec16 = p.x_vec16 && xi.row.stride[d] % 16 == 0;
         p.alpha = alpha;
         p.beta = beta;
         p.bias = bias;
         p.act = act;
         p.pdl = pdl;
-        err = launch_gemv_w4(p, s);
+        err = launch_gemv_w4(p, ds->num_sms, s);
     }
     if (err != cudaSuccess) return DG_ERR_CUDA;
     g_launches.fetch_add(1);

@@ -170,6 +170,9 @@ struct GemvW4Params {
     int32_t R, K, N;
     int32_t group;
     int32_t scale_dtype;
+    int32_t in_dtype;
+    int32_t x_vec16;         // x unit-stride along k, rows at multiples of 16 bytes
+    int32_t steps;           // blocks of k per warp and round (set by the launcher)
     float alpha, beta;
     const float *bias;
     int32_t act;
@@ -205,7 +208,7 @@ int umma_pair_max_stages(int bn, bool epi_tma, int ksub);
 cudaError_t launch_gemv_n(const GemvParams &p, const CUtensorMap *tmap_w, cudaStream_t s, int *grid_out);
 size_t gemv_n_smem_bytes(int r_inst, int kper);
 cudaError_t launch_gemv_k(const GemvParams &p, cudaStream_t s, int *grid_out);
-cudaError_t launch_gemv_w4(const GemvW4Params &p, cudaStream_t s);
+cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s);
 cudaError_t launch_simt(const SimtParams &p, cudaStream_t s);
 cudaError_t launch_scale_c(const DevView &c, int64_t M, int64_t N, float beta, const float *bias, int act, int pdl,
                            cudaStream_t s);
