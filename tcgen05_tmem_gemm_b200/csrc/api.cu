@@ -1461,8 +1461,12 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y, float a
         p.scale_dtype = W->scale_dtype;
         p.in_dtype = x->dtype;
         p.x_vec16 = xi.col.n <= 1 && (xi.col.n == 0 || xi.col.stride[0] == 2) &&
-                    reinterpret_cast<uintptr_t>(x->ptr) % 16 == 0;
-        for (int d = 0; d < xi.row.n; ++d) p.x_vec16 = p.x_vec16 && xi.row.stride[d] % 16 == 0;
+                    reinterpret_cast<uintptr_t>(x->ptr) % 16 == 0 && xi.row.n <= 1;
+        p.x_ld = axis_stride(xi.row);
+        p.x_vec16 = p.x_vec16 && p.x_ld % 16 == 0;
+        p.y_plain = yi.row.n <= 1 && yi.col.n <= 1;
+        p.y_rs = axis_stride(yi.row);
+        p.y_cs = axis_stride(yi.col);
         p.alpha = alpha;
         p.beta = beta;
         p.bias = bias;

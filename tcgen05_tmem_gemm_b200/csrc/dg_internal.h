@@ -172,7 +172,13 @@ struct GemvW4Params {
     int32_t scale_dtype;
     int32_t in_dtype;
     int32_t x_vec16;         // x unit-stride along k, rows at multiples of 16 bytes
-    int32_t steps;           // blocks of k per warp and round (set by the launcher)
+    int64_t x_ld;            // bytes between rows of x (x_vec16 only)
+    int32_t y_plain;         // y's rows and columns are one dim each, strides y_rs and y_cs
+    int64_t y_rs, y_cs;
+    // set by the launcher: a block is `tiles` tiles of 16 columns x `kw` warps along k, which take
+    // `steps` blocks of k each per round
+    int32_t tiles, kw, steps;
+    int32_t group_shift;     // log2(group), or -1
     float alpha, beta;
     const float *bias;
     int32_t act;

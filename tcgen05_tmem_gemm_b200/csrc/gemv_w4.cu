@@ -17,17 +17,24 @@
 // 0x000F000F are the codes of k+j and k+j+4 in the low bits of two 16-bit
 // halves.  OR-ed into the significand of 128 (BF16) or 1024 (F16) they read
 // as 128 + code or 1024 + code, and one packed add of -(128 + zero) leaves
-// code - zero exactly.  The pairs (k+j, k+j+4) fix the order in which a
-// thread meets k; x is staged in shared memory in the same order.
+// code - zero exactly.  F16's longer significand also takes the codes of odd
+// j four bits higher (1024 + 16 code), where a packed multiply-add by 1/16
+// leaves the same and saves the shift: the shifts and masks run on the
+// half-rate integer pipe, which bounds the kernel next to HBM.  The pairs
+// (k+j, k+j+4) fix the order in which a thread meets k; x is staged in shared
+// memory in the same order.
 //
 // Work split.  It streams W once and is bound by HBM, so what counts is bytes
-// in flight.  A block owns 16 * MT columns; its eight warps (and the blocks of
-// its cluster) share k in blocks of 128.  A lane loads 16 bytes of a column's
-// codes at a time, all loads of up to kBatch blocks of k at once, before x is
-// staged, so the two trips to memory overlap.  Partial sums meet in shared
-// memory and, across a cluster, in distributed shared memory, in a fixed
-// order.
-#include <atomic>
+// in flight and few instructions per byte.  A warp owns 16 columns and a share
+// of k, in steps of 128 k; every lane copies the 16 bytes of each of its two
+// columns that it will itself unpack into a ring of kStages steps in shared
+// memory (cp.async: no registers, no synchronisation between lanes, bytes past
+// a column's end arrive as zeros).  A block is column tiles x warps along k
+// over one staged slice of x; blocks of a cluster share k further where there
+// are few columns.  Partial sums meet in shared memory and, across a cluster,
+// in distributed shared memory, in a fixed order.
+#include <algorithm>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "sm100.cuh"
@@ -36,45 +43,75 @@ namespace dg {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kBlockK = 128;   // k per step of a warp: 16 bytes of codes per lane and column
-constexpr int kBatch = 4;      // steps whose loads are in flight together
+constexpr int kStages = 8;     // steps of a warp in flight: two batches
+constexpr uint32_t kStageBytes = 32 * 2 * 16;
+constexpr uint32_t kRingBytes = kStages * kStageBytes;  // per warp
+
+constexpr int kBatch = 4;      // steps between waits
+
+// (w & mask) | bits in one instruction (two literals would take two).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+    return r;
+}
 
 template <typename T>
 struct Pair;  // packed 16-bit arithmetic of x's type
 
 template <>
 struct Pair<__nv_bfloat16> {
-    static constexpr uint32_t kMagic = 0x43004300u;     // 128, 128
-    static constexpr uint32_t kNegMagic = 0xC300C300u;  // -128, -128
+    struct Zero {  // -(128 + zero), twice
+        uint32_t lo;
+        __device__ __forceinline__ Zero from(int src) const { return Zero{__shfl_sync(0xffffffffu, lo, src)}; }
+    };
+    static __device__ __forceinline__ Zero zero(uint32_t z) { return Zero{z * 0x00010001u | 0xC300C300u}; }
     static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
         uint32_t r;
-        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        asm("fma.rn.bf16x2 %0, %1, %3, %2;" : "=r"(r) : "r"(a), "r"(b), "r"(0x3F803F80u));
         return r;
     }
-    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    // the pairs j = 0..3 of code - zero
+    static __device__ __forceinline__ void unpack(uint32_t (&a)[4], uint32_t w, Zero z) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = add(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), z.lo);
+    }
+    static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1, const float (&c)[4]) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     }
 };
 
 template <>
 struct Pair<__half> {
-    static constexpr uint32_t kMagic = 0x64006400u;     // 1024, 1024
-    static constexpr uint32_t kNegMagic = 0xE400E400u;  // -1024, -1024
-    static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
+    struct Zero {  // -(1024 + zero) and -(64 + zero), twice each
+        uint32_t lo, hi;
+        __device__ __forceinline__ Zero from(int src) const {
+            return Zero{__shfl_sync(0xffffffffu, lo, src), __shfl_sync(0xffffffffu, hi, src)};
+        }
+    };
+    static __device__ __forceinline__ Zero zero(uint32_t z) {
+        return Zero{z * 0x00010001u | 0xE400E400u, z * 0x00100010u | 0xD400D400u};
     }
-    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    static __device__ __forceinline__ void unpack(uint32_t (&a)[4], uint32_t w, Zero z) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t v = w >> (8 * h);
+            const uint32_t even = and_or(v, 0x000F000Fu, 0x64006400u), odd = and_or(v, 0x00F000F0u, 0x64006400u);
+            asm("fma.rn.f16x2 %0, %1, %3, %2;" : "=r"(a[2 * h]) : "r"(even), "r"(z.lo), "r"(0x3C003C00u));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(a[2 * h + 1]) : "r"(odd), "r"(0x2C002C00u), "r"(z.hi));
+        }
+    }
+    static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1, const float (&c)[4]) {
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     }
 };
 
@@ -101,236 +138,298 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
     }
 }
 
-// The codes of k .. k+7 (k a multiple of 8) of a column, bytes at or past
-// `nbytes` as zero.
-__device__ __forceinline__ uint32_t load_word_bytes(const uint8_t *row, int k, int nbytes) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (k / 2 + i < nbytes) w |= (uint32_t)__ldg(row + k / 2 + i) << (8 * i);
-    return w;
-}
-
-// One step's words of one column.  VEC: the alignment of every column's codes.
+// Copies one step's 16 bytes of one column into this lane's slot, zeros past
+// the column's `nbytes`.  VEC: the alignment of every column's codes.
 template <int VEC, Order O>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t *row, int k0, int t, int nbytes) {
-    if (VEC == 16) {  // as the lane's 16 bytes; a word-major kernel transposes them before use
-        const int b = k0 / 2 + 16 * t;
-        if (b + 16 <= nbytes) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + b));
-            w[0] = v.x;
-            w[1] = v.y;
-            w[2] = v.z;
-            w[3] = v.w;
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) w[c] = load_word_bytes(row, k0 + 32 * t + 8 * c, nbytes);
-        }
+__device__ __forceinline__ void copy_codes(uint32_t slot, const uint8_t *row, int k0, int t, int nbytes) {
+    if (VEC == 16) {  // the lane's 16 bytes; a word-major kernel transposes them after the read
+        const int b = k0 / 2 + 16 * t, n = min(max(nbytes - b, 0), 16);
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(slot), "l"(row + (n > 0 ? b : 0)),
+                     "r"(n)
+                     : "memory");
     } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const int k = k0 + order_k(O, c, t);
-            if (VEC == 4 && k / 2 + 4 <= nbytes) w[c] = __ldcs(reinterpret_cast<const uint32_t *>(row + k / 2));
-            else w[c] = load_word_bytes(row, k, nbytes);
-        }
-    }
-}
-
-// One word's eight codes of two columns (16-row halves of the M side) times
-// x: two tensor instructions.
-template <typename T>
-__device__ __forceinline__ void word_mma(float (&d)[4], uint32_t lo, uint32_t hi, uint32_t zlo, uint32_t zhi,
-                                         const uint4 &x) {
-    uint32_t a[4];
+            const int b = (k0 + order_k(O, c, t)) / 2;
+            if (VEC == 4) {
+                const int n = min(max(nbytes - b, 0), 4);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + 4 * c),
+                             "l"(row + (n > 0 ? b : 0)), "r"(n)
+                             : "memory");
+            } else {
+                uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            a[2 * q] = Pair<T>::add(((lo >> (4 * (j + q))) & 0x000F000Fu) | Pair<T>::kMagic, zlo);
-            a[2 * q + 1] = Pair<T>::add(((hi >> (4 * (j + q))) & 0x000F000Fu) | Pair<T>::kMagic, zhi);
-        }
-        Pair<T>::mma(d, a, j == 0 ? x.x : x.z, j == 0 ? x.y : x.w);
-    }
-}
-
-// Eight consecutive x of one row as the four pairs (k+j, k+j+4).
-__device__ __forceinline__ uint4 x_pairs(const GemvW4Params &p, int r, int k, bool vec) {
-    uint32_t h[4];
-    if (vec && k + 8 <= p.K) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p.x.ptr + axis_offset(p.x.row, r) + (int64_t)k * 2);
-        h[0] = v.x;
-        h[1] = v.y;
-        h[2] = v.z;
-        h[3] = v.w;
-    } else {
-        const char *row = p.x.ptr + axis_offset(p.x.row, r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t e[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int kk = k + 2 * i + q;
-                e[q] = kk < p.K ? *reinterpret_cast<const uint16_t *>(row + axis_offset(p.x.col, kk)) : 0u;
+                for (int i = 0; i < 4; ++i)
+                    if (b + i < nbytes) w |= (uint32_t)__ldg(row + b + i) << (8 * i);
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + 4 * c), "r"(w) : "memory");
             }
-            h[i] = e[0] | (e[1] << 16);
         }
     }
-    return make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
-                      __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632));
 }
 
-struct W4Layout {
-    uint32_t pitch, red, part, total;  // x: pitch bytes per row; red: the warps' sums; part: the block's
+__device__ __forceinline__ void copy16(uint32_t slot, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// One word's eight codes of two columns (g and g + 8 of the M side) times x:
+// d = c + two tensor instructions.
+template <typename T>
+__device__ __forceinline__ void word_mma(float (&d)[4], const float (&c)[4], uint32_t w0, uint32_t w1,
+                                         typename Pair<T>::Zero z0, typename Pair<T>::Zero z1, const uint4 &x) {
+    uint32_t a[4], b[4];
+    Pair<T>::unpack(a, w0, z0);
+    Pair<T>::unpack(b, w1, z1);
+    Pair<T>::mma(d, a[0], b[0], a[1], b[1], x.x, x.y, c);
+    Pair<T>::mma(d, a[2], b[2], a[3], b[3], x.z, x.w, d);
+}
+
+// Eight 16-bit x, h = k .. k+7, as the four pairs (k+j, k+j+4).
+__device__ __forceinline__ uint4 x_pairs(const uint4 &h) {
+    return make_uint4(__byte_perm(h.x, h.z, 0x5410), __byte_perm(h.x, h.z, 0x7632), __byte_perm(h.y, h.w, 0x5410),
+                      __byte_perm(h.y, h.w, 0x7632));
+}
+
+// x of k .. k+7 of row r, element by element, zeros at and past K.
+__device__ __forceinline__ uint4 x_elements(const DevView &x, int r, int k, int K) {
+    const char *row = x.ptr + axis_offset(x.row, r);
+    uint32_t h[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int i = 7; i >= 0; --i) {  // shifted in from the top, so no index into h varies
+        const uint32_t v =
+            k + i < K ? *reinterpret_cast<const uint16_t *>(row + axis_offset(x.col, k + i)) : (uint16_t)0;
+        h[3] = (h[3] << 16) | (h[2] >> 16);
+        h[2] = (h[2] << 16) | (h[1] >> 16);
+        h[1] = (h[1] << 16) | (h[0] >> 16);
+        h[0] = (h[0] << 16) | v;
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// The raw bits of a scale, converted where it is used, so that the load can
+// be in flight until then.
+__device__ __forceinline__ uint32_t scale_bits(const char *row, int grp, int dtype) {
+    if (dtype == DG_F32) return __ldg(reinterpret_cast<const uint32_t *>(row) + grp);
+    return __ldg(reinterpret_cast<const uint16_t *>(row) + grp);
+}
+__device__ __forceinline__ float scale_value(uint32_t bits, int dtype) {
+    if (dtype == DG_F32) return __uint_as_float(bits);
+    if (dtype == DG_BF16) return __uint_as_float(bits << 16);
+    return __half2float(__ushort_as_half((unsigned short)bits));
+}
+
+// The scales and zero points of this lane's two columns for one batch of
+// steps, as loaded.  !FINE: lane t of a quad holds those of the t-th step;
+// FINE: of every step's t-th run of 32 k.  The quad shares them by shuffles.
+template <bool FINE>
+struct Scales {
+    static constexpr int kN = FINE ? kBatch : 1;
+    uint32_t s0[kN], s1[kN], z0[kN], z1[kN];
 };
 
-// steps: the most steps of k any warp takes in one round.
-__host__ __device__ inline W4Layout w4_layout(int R, int steps, int mt) {
+struct W4Layout {
+    uint32_t pitch, zero, ring, red, part, total;  // x: pitch bytes per row, then a step of zeros; the ring;
+                                                    // red: the warps' sums; part: the block's
+};
+
+// A block of `tiles` column tiles and `kw` warps along k, each taking `steps`
+// steps per round.
+__host__ __device__ inline W4Layout w4_layout(int R, int tiles, int kw, int steps) {
     W4Layout L;
-    L.pitch = (uint32_t)(kWarps * steps * kBlockK * 2 + 64);  // rows 64 bytes apart modulo 128: no bank conflicts
-    L.red = (uint32_t)R * L.pitch;
-    const uint32_t red_bytes = (uint32_t)(kWarps * mt * 128 * 4);
-    L.part = L.red + red_bytes;
-    L.total = L.part + (uint32_t)(mt * 128 * 4);
+    L.pitch = (uint32_t)(kw * steps * kBlockK * 2 + 64);  // rows 64 bytes apart modulo 128: no bank conflicts
+    L.zero = (uint32_t)R * L.pitch;
+    L.ring = (L.zero + 256 + 127) / 128 * 128;
+    const uint32_t ring_bytes = (uint32_t)(tiles * kw) * kRingBytes;
+    L.red = L.ring;  // the sums take the ring's place after the last step
+    L.part = L.ring + ring_bytes;
+    L.total = L.part + (uint32_t)(tiles * 128 * 4);
     return L;
 }
 
 // FINE: groups that are not whole multiples of 128 (word-major, one scale per
 // 32 k), else one scale per step.
-template <typename T, int MT, int VEC, bool FINE>
-__global__ void __launch_bounds__(kThreads) gemv_w4_kernel(const GemvW4Params p) {
+template <typename T, int VEC, bool FINE>
+__global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__ GemvW4Params p) {
     constexpr Order O = (FINE || VEC != 16) ? kWordMajor : kLaneMajor;
     pdl_wait();
-    extern __shared__ __align__(16) uint8_t smem[];
-    const W4Layout L = w4_layout(p.R, p.steps, MT);
+    extern __shared__ __align__(128) uint8_t smem[];
+    const W4Layout L = w4_layout(p.R, p.tiles, p.kw, p.steps);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tile = warp / p.kw, kw = warp - tile * p.kw;
     const int g = lane >> 2, t = lane & 3;
-    const int n0 = blockIdx.x * 16 * MT;
+    const int n0 = (blockIdx.x * p.tiles + tile) * 16;
     const int nbytes = (p.K + 1) / 2;
     const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
+    const int per_round = p.kw * p.steps, stride = gridDim.y * per_round;
 
-    // this lane's columns: g and g + 8 of each 16 (clamped; the extra ones are not stored)
-    const uint8_t *row[MT][2];
-    int64_t col[MT][2];
+    // this lane's columns, g and g + 8 of the tile (clamped; the extra ones are not stored)
+    const int64_t c0 = min(n0 + g, p.N - 1), c1 = min(n0 + g + 8, p.N - 1);
+    const uint8_t *row0 = p.codes + c0 * p.code_stride, *row1 = p.codes + c1 * p.code_stride;
+    const char *srow0 = p.scales + c0 * p.scale_stride, *srow1 = p.scales + c1 * p.scale_stride;
+    const uint8_t *zrow0 = p.zeros + c0 * p.zero_stride, *zrow1 = p.zeros + c1 * p.zero_stride;
+    auto fetch = [&](int kb, int left) {
+        Scales<FINE> q;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            col[m][h] = min(n0 + 16 * m + 8 * h + g, p.N - 1);
-            row[m][h] = p.codes + col[m][h] * p.code_stride;
-        }
-    const int ses = elem_bytes(p.scale_dtype);
-
-    float acc[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-
-    // Rounds: kWarps * steps blocks of k at a time, a cluster's blocks taking
-    // turns; warp w takes `steps` consecutive ones.
-    const int per_round = kWarps * p.steps;
-    for (int kb_round = blockIdx.y * per_round; kb_round < blocks_k; kb_round += gridDim.y * per_round) {
-        const int kb0 = kb_round + warp * p.steps;
-        const int nst = min(p.steps, blocks_k - kb0);  // may be negative: nothing for this warp
-        uint32_t w[kBatch][MT][2][4];
-        float sc[FINE ? kBatch : 1][MT][2];
-        uint32_t zc[FINE ? kBatch : 1][MT][2];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            if (u < nst)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        load_codes<VEC, O>(w[u][m][h], row[m][h], (kb0 + u) * kBlockK, t, nbytes);
-        // scales and zero points: lane t of a quad fetches step t's (or run t's of each
-        // step, FINE) and the quad shares them by shuffles
-#pragma unroll
-        for (int u = 0; u < (FINE ? kBatch : 1); ++u) {
-            const int k = FINE ? (kb0 + u) * kBlockK + 32 * t : (kb0 + t) * kBlockK;
-            const bool ok = k < p.K && (FINE ? u : t) < nst;
-            const int grp = ok ? k / p.group : 0;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    sc[u][m][h] = ok ? load_elem(p.scales + col[m][h] * p.scale_stride + (int64_t)grp * ses,
-                                                 p.scale_dtype)
-                                     : 0.f;
-                    const uint32_t z = !p.zeros ? 8u : ok ? p.zeros[col[m][h] * p.zero_stride + grp] & 15u : 0u;
-                    zc[u][m][h] = Pair<T>::kNegMagic | (z * 0x00010001u);
-                }
-        }
-        if (kb_round != (int)blockIdx.y * per_round) __syncthreads();  // the previous round's x is read
-        // x of this round, in the order the words meet it
-        for (int e = threadIdx.x; e < p.R * per_round * 16; e += kThreads) {
-            const int r = e / (per_round * 16), i = e - r * (per_round * 16);
-            const int kb = i >> 4, c = (i >> 2) & 3, q = i & 3;
-            *reinterpret_cast<uint4 *>(smem + r * L.pitch + i * 16) =
-                x_pairs(p, r, (kb_round + kb) * kBlockK + order_k(O, c, q), p.x_vec16);
-        }
-        __syncthreads();
-        const uint8_t *xs = smem + g * L.pitch + warp * p.steps * 256 + t * 16;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (u >= nst) break;
-            float d[MT][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[m][i] = 0.f;
-                if (O == kWordMajor && VEC == 16) {
-                    quad_transpose(w[u][m][0], t);
-                    quad_transpose(w[u][m][1], t);
+        for (int u = 0; u < Scales<FINE>::kN; ++u) {
+            const int k = FINE ? (kb + u) * kBlockK + 32 * t : (kb + t) * kBlockK;
+            q.s0[u] = q.s1[u] = 0u;
+            q.z0[u] = q.z1[u] = 8u;
+            if ((FINE ? u : t) < left && k < p.K) {  // a run past the end has the scale 0 and the sum 0
+                const int grp = p.group_shift >= 0 ? k >> p.group_shift : k / p.group;
+                q.s0[u] = scale_bits(srow0, grp, p.scale_dtype);
+                q.s1[u] = scale_bits(srow1, grp, p.scale_dtype);
+                if (p.zeros) {
+                    q.z0[u] = __ldg(zrow0 + grp);
+                    q.z1[u] = __ldg(zrow1 + grp);
                 }
             }
+        }
+        return q;
+    };
+
+    // This warp's batches of steps: in each round of per_round blocks of k (a cluster's blocks
+    // take rounds in turn) p.steps consecutive steps.  The copies walk two batches ahead.
+    const uint32_t ring = smem_u32(smem) + L.ring + (uint32_t)warp * kRingBytes + (uint32_t)lane * 16;
+    int next_kb = blockIdx.y * per_round + kw * p.steps, next_left = p.steps;
+    auto copy_batch = [&](uint32_t half) {
+        const int n = min(min(next_left, kBatch), blocks_k - next_kb);
+        if (n == kBatch && (next_kb + kBatch) * (kBlockK / 2) <= nbytes && VEC == 16) {
+            const uint8_t *a = row0 + next_kb * (kBlockK / 2) + 16 * t, *b = row1 + next_kb * (kBlockK / 2) + 16 * t;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (g < p.R) x = *reinterpret_cast<const uint4 *>(xs + u * 256 + c * 64);
+            for (int u = 0; u < kBatch; ++u) {
+                copy16(half + u * kStageBytes, a + u * (kBlockK / 2));
+                copy16(half + u * kStageBytes + 512, b + u * (kBlockK / 2));
+            }
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < n; ++u) {
+                copy_codes<VEC, O>(half + u * kStageBytes, row0, (next_kb + u) * kBlockK, t, nbytes);
+                copy_codes<VEC, O>(half + u * kStageBytes + 512, row1, (next_kb + u) * kBlockK, t, nbytes);
+            }
+        }
+        copy_commit();
+        next_kb += kBatch;
+        next_left -= kBatch;
+        if (next_left <= 0) {
+            next_kb += next_left + stride - p.steps;
+            next_left = p.steps;
+        }
+    };
+    copy_batch(ring);
+    copy_batch(ring + kBatch * kStageBytes);
+
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t half = 0;
+    if (threadIdx.x < 64) *reinterpret_cast<uint32_t *>(smem + L.zero + threadIdx.x * 4) = 0u;
+    for (int kb_round = blockIdx.y * per_round; kb_round < blocks_k; kb_round += stride) {
+        const int kb0 = kb_round + kw * p.steps;
+        const int nst = min(p.steps, blocks_k - kb0);  // may be negative: nothing for this warp
+        Scales<FINE> ahead = fetch(kb0, nst);
+        if (kb_round != (int)blockIdx.y * per_round) __syncthreads();  // the previous round's x is read
+        // x of this round, in the order the words meet it
+        {
+            const int chunks = min(per_round, blocks_k - kb_round) * 16;
+            for (int r = 0; r < p.R; ++r)
+                for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
+                    const int k = (kb_round + (i >> 4)) * kBlockK + order_k(O, (i >> 2) & 3, i & 3);
+                    uint4 h;
+                    if (p.x_vec16 && k + 8 <= p.K)
+                        h = *reinterpret_cast<const uint4 *>(p.x.ptr + r * p.x_ld + (int64_t)k * 2);
+                    else
+                        h = x_elements(p.x, r, k, p.K);
+                    *reinterpret_cast<uint4 *>(smem + r * L.pitch + i * 16) = x_pairs(h);
+                }
+        }
+        __syncthreads();
+        // rows of the tensor instruction's N side past R read zeros
+        uint32_t xs = smem_u32(smem) + t * 16 + (g < p.R ? g * L.pitch + kw * p.steps * 256 : L.zero);
+        const uint32_t xstep = g < p.R ? 256 : 0;
+        for (int st = 0; st < p.steps; st += kBatch) {
+            const Scales<FINE> q = ahead;
+            if (st + kBatch < nst) ahead = fetch(kb0 + st + kBatch, nst - st - kBatch);
+            float s0[Scales<FINE>::kN], s1[Scales<FINE>::kN];
+            typename Pair<T>::Zero own0[Scales<FINE>::kN], own1[Scales<FINE>::kN];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int su = FINE ? u : 0, src = FINE ? c : u;  // who holds this run's scale
-                    const uint32_t z0 = __shfl_sync(0xffffffffu, zc[su][m][0], (lane & ~3) | src);
-                    const uint32_t z1 = __shfl_sync(0xffffffffu, zc[su][m][1], (lane & ~3) | src);
-                    word_mma<T>(d[m], w[u][m][0][c], w[u][m][1][c], z0, z1, x);
+            for (int u = 0; u < Scales<FINE>::kN; ++u) {
+                s0[u] = scale_value(q.s0[u], p.scale_dtype);
+                s1[u] = scale_value(q.s1[u], p.scale_dtype);
+                own0[u] = Pair<T>::zero(q.z0[u] & 15u);
+                own1[u] = Pair<T>::zero(q.z1[u] & 15u);
+            }
+            copy_wait<1>();
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u, xs += xstep) {
+                if (st + u >= nst) break;
+                const uint4 v0 = ld_shared_v4(ring + half + u * kStageBytes);
+                const uint4 v1 = ld_shared_v4(ring + half + u * kStageBytes + 512);
+                uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                if (O == kWordMajor && VEC == 16) {
+                    quad_transpose(w0, t);
+                    quad_transpose(w1, t);
+                }
+                const float none[4] = {0.f, 0.f, 0.f, 0.f};
+                float d[4];
+                typename Pair<T>::Zero z0, z1;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int at = FINE ? u : 0, src = (lane & ~3) | (FINE ? c : u);  // who holds this run's scale
+                    if (FINE || c == 0) {
+                        z0 = own0[at].from(src);
+                        z1 = own1[at].from(src);
+                    }
+                    const uint4 x = ld_shared_v4(xs + c * 64);
+                    if (FINE || c == 0) word_mma<T>(d, none, w0[c], w1[c], z0, z1, x);
+                    else word_mma<T>(d, d, w0[c], w1[c], z0, z1, x);
                     if (FINE || c == 3) {
-                        const float s0 = __shfl_sync(0xffffffffu, sc[su][m][0], (lane & ~3) | src);
-                        const float s1 = __shfl_sync(0xffffffffu, sc[su][m][1], (lane & ~3) | src);
-                        acc[m][0] = fmaf(s0, d[m][0], acc[m][0]);
-                        acc[m][1] = fmaf(s0, d[m][1], acc[m][1]);
-                        acc[m][2] = fmaf(s1, d[m][2], acc[m][2]);
-                        acc[m][3] = fmaf(s1, d[m][3], acc[m][3]);
-                        if (FINE)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) d[m][i] = 0.f;
+                        const float a0 = __shfl_sync(0xffffffffu, s0[at], src);
+                        const float a1 = __shfl_sync(0xffffffffu, s1[at], src);
+                        acc[0] = fmaf(a0, d[0], acc[0]);
+                        acc[1] = fmaf(a0, d[1], acc[1]);
+                        acc[2] = fmaf(a1, d[2], acc[2]);
+                        acc[3] = fmaf(a1, d[3], acc[3]);
                     }
                 }
             }
+            copy_batch(ring + half);
+            half ^= kBatch * kStageBytes;
         }
     }
+    copy_wait<0>();
     pdl_release();
 
-    // The warps' sums: [warp][m][row r of x][16 columns].
+    // The warps' sums: [tile][warp along k][row r of x][16 columns], in the ring's place.
+    __syncthreads();
     float *red = reinterpret_cast<float *>(smem + L.red), *part = reinterpret_cast<float *>(smem + L.part);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            red[((warp * MT + m) * 8 + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[m][i];
+    for (int i = 0; i < 4; ++i) red[(warp * 8 + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[i];
     __syncthreads();
     const bool single = gridDim.y == 1;
     auto store = [&](int e, float sum) {
-        const int n = n0 + (e >> 7) * 16 + (e & 15), r = (e >> 4) & 7;
+        const int n = (blockIdx.x * p.tiles + (e >> 7)) * 16 + (e & 15), r = (e >> 4) & 7;
         if (r >= p.R || n >= p.N) return;
-        char *yp = const_cast<char *>(p.y.ptr) + axis_offset(p.y.row, r) + axis_offset(p.y.col, n);
-        const float v = epi_value(sum, p.alpha, 1.f, p.beta, yp, p.y.dtype);
-        store_elem(yp, p.y.dtype, epi_fuse(v, p.bias, n, p.act, p.y.dtype != DG_F32));
+        char *yp = const_cast<char *>(p.y.ptr);
+        if (p.y_plain) yp += r * p.y_rs + n * p.y_cs;
+        else yp += axis_offset(p.y.row, r) + axis_offset(p.y.col, n);
+        float v = epi_value(sum, p.alpha, 1.f, p.beta, yp, p.y.dtype);
+        if (p.bias != nullptr || p.act != DG_ACT_NONE) v = epi_fuse(v, p.bias, n, p.act, p.y.dtype != DG_F32);
+        store_elem(yp, p.y.dtype, v);
     };
-    for (int e = threadIdx.x; e < MT * 128; e += kThreads) {
+    for (int e = threadIdx.x; e < p.tiles * 128; e += blockDim.x) {
+        if (((e >> 4) & 7) >= p.R) continue;
         float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) sum += red[i * MT * 128 + e];
+        for (int i = 0; i < p.kw; ++i) sum += red[((e >> 7) * p.kw + i) * 128 + (e & 127)];
         if (single) store(e, sum);
         else part[e] = sum;
     }
@@ -339,7 +438,8 @@ __global__ void __launch_bounds__(kThreads) gemv_w4_kernel(const GemvW4Params p)
     __syncthreads();
     cluster_sync();
     const int ranks = gridDim.y;
-    for (int e = (int)cluster_ctarank() + ranks * threadIdx.x; e < MT * 128; e += ranks * kThreads) {
+    for (int e = (int)cluster_ctarank() + ranks * threadIdx.x; e < p.tiles * 128; e += ranks * blockDim.x) {
+        if (((e >> 4) & 7) >= p.R) continue;
         float sum = 0.f;
         for (int q = 0; q < ranks; ++q) sum += dsmem_ld_f32(dsmem_map(smem_u32(part + e), q));
         store(e, sum);
@@ -347,27 +447,23 @@ __global__ void __launch_bounds__(kThreads) gemv_w4_kernel(const GemvW4Params p)
     cluster_sync();  // keep every block's sums alive until all remote reads are done
 }
 
-template <typename T, int MT, int VEC, bool FINE>
+template <typename T, int VEC, bool FINE>
 cudaError_t run(const GemvW4Params &p, int split, cudaStream_t s) {
     static SmemLimit limit;
-    auto kern = gemv_w4_kernel<T, MT, VEC, FINE>;
-    const size_t smem = w4_layout(p.R, p.steps, MT).total;
-    const cudaError_t e = limit.ensure(kern, smem);
+    auto kern = gemv_w4_kernel<T, VEC, FINE>;
+    const size_t smem = w4_layout(p.R, p.tiles, p.kw, p.steps).total;
+    const cudaError_t e = limit.ensure(kern, smem, true);
     if (e != cudaSuccess) return e;
-    return launch_ex(kern, dim3((p.N + 16 * MT - 1) / (16 * MT), split), dim3(kThreads), smem, s, dim3(1, split, 1),
-                     p.pdl, p);
-}
-
-template <typename T, int MT, int VEC>
-cudaError_t run_fine(const GemvW4Params &p, int split, cudaStream_t s) {
-    return p.group % kBlockK ? run<T, MT, VEC, true>(p, split, s) : run<T, MT, VEC, false>(p, split, s);
+    return launch_ex(kern, dim3((p.N + 16 * p.tiles - 1) / (16 * p.tiles), split), dim3(32 * p.kw * p.tiles), smem, s,
+                     dim3(1, split, 1), p.pdl, p);
 }
 
 template <typename T>
-cudaError_t run_vec(const GemvW4Params &p, int mt, int vec, int split, cudaStream_t s) {
-    if (vec == 16) return mt == 2 ? run_fine<T, 2, 16>(p, split, s) : run_fine<T, 1, 16>(p, split, s);
-    if (vec == 4) return run_fine<T, 1, 4>(p, split, s);
-    return run_fine<T, 1, 1>(p, split, s);
+cudaError_t run_vec(const GemvW4Params &p, int vec, int split, cudaStream_t s) {
+    const bool fine = p.group % kBlockK != 0;
+    if (vec == 16) return fine ? run<T, 16, true>(p, split, s) : run<T, 16, false>(p, split, s);
+    if (vec == 4) return fine ? run<T, 4, true>(p, split, s) : run<T, 4, false>(p, split, s);
+    return fine ? run<T, 1, true>(p, split, s) : run<T, 1, false>(p, split, s);
 }
 
 }  // namespace
@@ -375,18 +471,26 @@ cudaError_t run_vec(const GemvW4Params &p, int mt, int vec, int split, cudaStrea
 cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.codes) | (p.N > 1 ? (uintptr_t)p.code_stride : 0);
     const int vec = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
-    const int mt = (vec == 16 && p.R > 4) ? 2 : 1;
-    const int tiles = (p.N + 16 * mt - 1) / (16 * mt);
     const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
-    // k split over a cluster while there are too few column tiles for three blocks per SM and every
-    // warp keeps at least one block of k
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= num_sms * 3 && blocks_k >= kWarps * split * 2) split *= 2;
-    const int per_warp = (blocks_k + kWarps * split - 1) / (kWarps * split);
-    const int rounds = (per_warp + kBatch - 1) / kBatch;
+    const int64_t col_tiles = (p.N + 15) / 16;
+    // A warp costs some hundred instructions besides its steps, so k is shared by no more warps than
+    // it takes to give every SM about twelve: first within the block, or, with several rows of x,
+    // first across the cluster, whose blocks then stage a smaller slice of x each.
+    int ways = 1;
+    static const int WT = getenv("WT") ? atoi(getenv("WT")) : 12;
+    static const int WB = getenv("WB") ? atoi(getenv("WB")) : 8;
+    while (ways < 64 && col_tiles * ways < (int64_t)num_sms * WT && ways * 2 <= blocks_k) ways *= 2;
+    const int first = std::min(ways, 8), second = ways / first;
+    const int split = p.R > 2 ? first : second;
+    p.kw = p.R > 2 ? second : first;
+    p.tiles = std::max(1, WB / p.kw);
+    const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * p.kw));  // steps whose x fits 48 KB
+    const int per_warp = (blocks_k + p.kw * split - 1) / (p.kw * split);
+    const int rounds = (per_warp + most - 1) / most;
     p.steps = (per_warp + rounds - 1) / rounds;
-    if (p.in_dtype == DG_BF16) return run_vec<__nv_bfloat16>(p, mt, vec, split, s);
-    if (p.in_dtype == DG_F16) return run_vec<__half>(p, mt, vec, split, s);
+    p.group_shift = (p.group & (p.group - 1)) == 0 ? __builtin_ctz((unsigned)p.group) : -1;
+    if (p.in_dtype == DG_BF16) return run_vec<__nv_bfloat16>(p, vec, split, s);
+    if (p.in_dtype == DG_F16) return run_vec<__half>(p, vec, split, s);
     return cudaErrorInvalidValue;
 }
 
