@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
@@ -170,6 +171,13 @@ lib = _load()
 
 # ------------------------------------------------------------------ views
 
+# dg_view and dg_w4 as packed bytes: filling a ctypes structure field by field
+# costs several times as much, and small products are bound by the call.
+_VIEW = struct.Struct("=Qii8qiI")
+_W4 = struct.Struct("=3Q5q2i2i")
+assert _VIEW.size == ctypes.sizeof(dg_view) and _W4.size == ctypes.sizeof(dg_w4)
+
+
 def make_view(ptr: int, shape, stride_bytes, row_dims: int, dtype) -> dg_view:
     """A dg_view from a raw device address, up to 4 dims, BYTE strides."""
     if isinstance(dtype, str):
@@ -204,12 +212,17 @@ def _torch_dtype_code(t) -> int:
 def view(t, row_dims: int = 1) -> dg_view:
     """A dg_view of a torch tensor in place (its strides, in bytes, as they are)."""
     code = _torch_dtype_code(t)
-    es = t.element_size()
-    shape = tuple(t.shape) if t.dim() > 0 else (1,)
-    stride = tuple(s * es for s in t.stride()) if t.dim() > 0 else (es,)
-    if len(shape) > 4:
+    es = ELEM_SIZE[code]
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n == 2:
+        return dg_view.from_buffer_copy(_VIEW.pack(t.data_ptr(), 2, row_dims, shape[0], shape[1], 1, 1,
+                                                   stride[0] * es, stride[1] * es, 0, 0, code, 0))
+    if n > 4:
         raise ValueError("views have at most 4 dims")
-    return make_view(t.data_ptr(), shape, stride, row_dims, code)
+    if n == 0:
+        shape, stride = (1,), (1,)
+    return make_view(t.data_ptr(), shape, [s * es for s in stride], row_dims, code)
 
 
 def _as_view(x, row_dims=1):
@@ -224,11 +237,23 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _stream_ptr(stream):
-    if stream is None:
+_raw_stream = None
+
+
+def _current_stream():
+    """The current stream's handle, without the cost of a torch.cuda.Stream object where torch offers it."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
+def _stream_ptr(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -397,23 +422,20 @@ def w4(codes, scales, zeros=None, group: int = 128, K: int | None = None) -> dg_
     n, nbytes = codes.shape
     K = 2 * nbytes if K is None else int(K)
     groups = -(-K // group) if group > 0 else -1
+    cs, ss = codes.stride(), scales.stride()
+    zs = (0, 1) if zeros is None else zeros.stride()
     if codes.dtype != torch.uint8 or (zeros is not None and zeros.dtype != torch.uint8):
         raise TypeError("codes and zeros must be uint8")
     if nbytes != (K + 1) // 2:
         raise ValueError(f"codes must have ceil(K / 2) = {(K + 1) // 2} bytes a row, not {nbytes}")
-    for t in (scales, zeros):
-        if t is not None and tuple(t.shape) != (n, groups):
-            raise ValueError(f"scales and zeros must be [{n}, {groups}]")
-    for t in (codes, scales, zeros):
-        if t is not None and t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError("codes, scales and zeros must be contiguous along their last dim")
-    w = dg_w4()
-    w.codes, w.scales = codes.data_ptr(), scales.data_ptr()
-    w.K, w.N, w.group, w.scale_dtype = K, n, int(group), _torch_dtype_code(scales)
-    w.code_stride, w.scale_stride = codes.stride(0), scales.stride(0) * scales.element_size()
-    if zeros is not None:
-        w.zeros, w.zero_stride = zeros.data_ptr(), zeros.stride(0)
-    return w
+    if scales.shape != (n, groups) or (zeros is not None and zeros.shape != (n, groups)):
+        raise ValueError(f"scales and zeros must be [{n}, {groups}]")
+    if (cs[1] != 1 and nbytes > 1) or ((ss[1] != 1 or zs[1] != 1) and groups > 1):
+        raise ValueError("codes, scales and zeros must be contiguous along their last dim")
+    code = _torch_dtype_code(scales)
+    return dg_w4.from_buffer_copy(_W4.pack(codes.data_ptr(), scales.data_ptr(),
+                                           0 if zeros is None else zeros.data_ptr(), K, n, cs[0],
+                                           ss[0] * ELEM_SIZE[code], zs[0], int(group), code, 0, 0))
 
 
 def gemv_w4(x, codes, scales, y, zeros=None, group: int = 128, alpha: float = 1.0, beta: float = 0.0,
@@ -424,8 +446,8 @@ def gemv_w4(x, codes, scales, y, zeros=None, group: int = 128, alpha: float = 1.
     xv = view(x, 1 if x.dim() > 1 else 0)
     yv = view(y, 1 if y.dim() > 1 else 0)
     W = w4(codes, scales, zeros, group, x.shape[-1])
-    epi = None if bias is None and act in ("none", DG_ACT_NONE) else epilogue(bias, act)
-    st = dg_gemv_w4(xv, W, yv, alpha, beta, epi, stream)
+    epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
+    st = lib.dg_gemv_w4(ctypes.byref(xv), ctypes.byref(W), ctypes.byref(yv), alpha, beta, epi, _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_gemv_w4")
     return y
