@@ -1089,6 +1089,54 @@ int early_launch_mode() { return g_pdl.load(); }
 
 void count_launch() { g_launches.fetch_add(1); }
 
+dg_status ce_pair(const dg_view *X, const dg_view *W, const dg_view *G, float alpha, const CeTile &ce, bool dry,
+                  cudaStream_t stream) {
+    if (g_pair.load() == 0 || (g_force_kind.load() != 0 && g_force_kind.load() != DG_KIND_UMMA))
+        return DG_ERR_UNSUPPORTED;
+    DeviceState *ds = nullptr;
+    dg_status st = device_state(&ds);
+    if (st != DG_OK) return st;
+    // the statistics store no C: a view of the right shape that nothing writes stands in
+    dg_view c;
+    if (G) {
+        c = *G;
+    } else {
+        std::memset(&c, 0, sizeof(c));
+        ViewInfo xi, wi;
+        if ((st = analyse(X, false, &xi)) != DG_OK || (st = analyse(W, false, &wi)) != DG_OK) return st;
+        c.ptr = ce.part;
+        c.ndim = 2;
+        c.row_dims = 1;
+        c.shape[0] = xi.rows;
+        c.shape[1] = wi.cols;
+        c.stride[0] = (wi.cols * 2 + 15) / 16 * 16;
+        c.stride[1] = 2;
+        c.dtype = DG_BF16;
+    }
+    Override ov;
+    ov.bn = 256;
+    ov.split = 1;
+    ov.pair = 1;
+    ov.sk = 0;
+    ov.epi_tma = G ? 1 : 0;
+    Views v{X, W, &c, {}, {}, {}};
+    Plan pl;
+    if ((st = make_plan(v, alpha, 0.f, ds->num_sms, &pl, false, &ov)) != DG_OK) return st;
+    if (pl.info.kind != DG_KIND_UMMA || !pl.info.cta_pair) return DG_ERR_UNSUPPORTED;
+    if (!G) pl.info.pair_half_tiles = 0;  // whole tiles have whole slots
+    if (dry) return DG_OK;
+    LaunchRec rec;
+    if ((st = prepare(v, pl, alpha, 0.f, nullptr, nullptr, nullptr, DG_ACT_NONE, ds, nullptr, &rec)) != DG_OK)
+        return st;
+    rec.umma.ce = ce;
+    rec.umma.k_chunk = 2048 / pl.info.block_k;  // k per accumulator: see ce_stats_rows_long
+    if (launch_umma_pair_ce(rec.umma, &rec.t0, &rec.t1, &rec.t2, G != nullptr, rec.grid, rec.smem, stream) !=
+        cudaSuccess)
+        return DG_ERR_CUDA;
+    g_launches.fetch_add(1);
+    return DG_OK;
+}
+
 }  // namespace dg
 
 using namespace dg;

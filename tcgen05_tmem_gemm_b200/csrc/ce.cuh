@@ -1,0 +1,191 @@
+// The linear cross entropy's arithmetic on logits, shared by its own kernels
+// and by the tensor-core kernel's epilogues.
+#pragma once
+
+#include "common.cuh"
+#include "umma_common.cuh"
+
+namespace dg {
+
+// What a row's target means, besides a column of the vocabulary.
+constexpr int kIgnored = -1, kInvalid = -2;
+
+__device__ __forceinline__ int read_target(const int64_t *target, int64_t ignore_index, int64_t V, int64_t t) {
+    const int64_t y = target[t];
+    if (y == ignore_index) return kIgnored;
+    return (y < 0 || y >= V) ? kInvalid : (int)y;
+}
+
+// exp(x) = 2^(x log2 e) with the hardware's power of two (relative error
+// about 2^-22, below the FP32 sums it goes into).
+__device__ __forceinline__ float exp_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
+// A row's logits as a pair (m, s): their maximum and sum of exp(z - m); m ==
+// -infinity means none (or all -infinity).  A NaN or +infinity among the
+// logits ends as s = NaN.  join: two pairs as one.
+__device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
+    const float mx = fmaxf(m, m2);
+    const float a = m == -INFINITY ? (s != s ? s : 0.f) : s * exp_fast(m - mx);
+    const float b = m2 == -INFINITY ? (s2 != s2 ? s2 : 0.f) : s2 * exp_fast(m2 - mx);
+    m = mx;
+    s = a + b;
+}
+
+// Another N logits: one pass, the running sum rescaled when the maximum moves.
+template <int N>
+__device__ __forceinline__ void join_logits(float &m, float &s, const float (&z)[N]) {
+    float mx = m;
+#pragma unroll
+    for (int c = 0; c < N; ++c) mx = fmaxf(mx, z[c]);
+    if (mx == -INFINITY) {  // nothing but -infinity, and perhaps NaN
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (z[c] != z[c]) s = z[c];
+        return;
+    }
+    // four sums: their additions do not wait for one another
+    float a[4] = {m == -INFINITY ? (s != s ? s : 0.f) : s * exp_fast(m - mx), 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < N; ++c) a[c & 3] += exp_fast(z[c] - mx);
+    m = mx;
+    s = (a[0] + a[1]) + (a[2] + a[3]);
+}
+
+// The logit of column `hit` (relative to the first of the N) if it is one of them.
+template <int N>
+__device__ __forceinline__ void keep_target(const float (&z)[N], int hit, float *out) {
+    if ((unsigned)hit < (unsigned)N) {
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (c == hit) *out = z[c];
+    }
+}
+
+// 32 accumulator columns as logits alpha * acc, -infinity past the last column.
+__device__ __forceinline__ void logits32(float (&z)[32], float alpha, uint32_t t_addr, int j, int Nj) {
+    uint32_t r[32];
+    tmem_ld16(t_addr, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+    tmem_ld16(t_addr + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) z[c] = alpha * __uint_as_float(r[c]);
+    if (j + 32 > Nj) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (j + c >= Nj) z[c] = -INFINITY;
+    }
+}
+
+// Columns of a tile per slot of CeTile::part; a tile has two slots.
+constexpr int kSlotCols = 128;
+
+// One warp's 32 rows (this thread's row i) x 256 columns from j0 of a tile:
+// the row's pair goes to the tile's first slot, its second is left empty.
+__device__ __forceinline__ void ce_stats_rows(const CeTile &ce, float alpha, uint32_t t_row, int i, int Mi, int j0,
+                                              int Nj) {
+    const bool ok = i < Mi;
+    const int y = ok ? read_target(ce.target, ce.ignore_index, ce.V, i) : kIgnored;
+    float m = -INFINITY, s = 0.f;
+    for (int c0 = 0; c0 < 2 * kSlotCols && j0 + c0 < Nj; c0 += 32) {
+        float z[32];
+        __syncwarp();
+        logits32(z, alpha, t_row + (uint32_t)c0, j0 + c0, Nj);
+        join_logits(m, s, z);
+        if (y >= 0) keep_target(z, y - ce.v0 - j0 - c0, ce.ztarget + i);
+    }
+    if (!ok) return;
+    float2 *slot = ce.part + (int64_t)(j0 / kSlotCols) * ce.T + i;
+    slot[0] = make_float2(m, s);
+    if (j0 + kSlotCols < Nj) slot[ce.T] = make_float2(-INFINITY, 0.f);
+}
+
+// The same for a long k, with a warp for each of the tile's two slots (`half`).
+// The tensor core adds each step's products to the accumulator with
+// truncation, so a logit's error grows with the steps (the loss was off by
+// 1.4e-6 of itself at k = 4096, the truncations all pointing the same way);
+// every chunk of k starts a fresh accumulator, and the chunks are added here,
+// rounded to nearest, in registers.
+__device__ __forceinline__ void ce_stats_rows_long(float (&sums)[kSlotCols], const CeTile &ce, float alpha,
+                                                   uint32_t t_row, int i, int Mi, int j0, int Nj, bool half,
+                                                   bool first, bool last) {
+    const int j = j0 + (half ? kSlotCols : 0);
+    const uint32_t t_addr = t_row + (half ? kSlotCols : 0);
+#pragma unroll
+    for (int c0 = 0; c0 < kSlotCols; c0 += 16) {
+        uint32_t r[16];
+        __syncwarp();
+        tmem_ld16(t_addr + (uint32_t)c0, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const float v = __uint_as_float(r[c]);
+            sums[c0 + c] = first ? v : sums[c0 + c] + v;
+        }
+    }
+    if (!last || j >= Nj) return;
+    const bool ok = i < Mi;
+    const int y = ok ? read_target(ce.target, ce.ignore_index, ce.V, i) : kIgnored;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int c0 = 0; c0 < kSlotCols; c0 += 32) {
+        float z[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) z[c] = j + c0 + c < Nj ? alpha * sums[c0 + c] : -INFINITY;
+        join_logits(m, s, z);
+        if (y >= 0) keep_target(z, y - ce.v0 - j - c0, ce.ztarget + i);
+    }
+    if (ok) ce.part[(int64_t)(j / kSlotCols) * ce.T + i] = make_float2(m, s);
+}
+
+// One warp's 32 rows x w columns of G = scale (exp(z - lse) - 1[v == target]),
+// zero in rows that take no part, through tensor stores in blocks of 32 rows x
+// 64 columns (the layout and its double buffering are epilogue_rows_tma's).
+__device__ __forceinline__ void ce_grad_rows_tma(const CeTile &ce, const EpiParams &e, const CUtensorMap *gmap,
+                                                 uint32_t stage, uint32_t t_row, int i_base, int Mi, int j0, int w,
+                                                 int Nj, int lane, uint32_t &nblk) {
+    if (i_base >= Mi) return;  // the whole warp is below G (warp-uniform)
+    const bool bf16_out = e.c_dtype == DG_BF16;
+    const float alpha = e.alpha;
+    RowGrad row{0.f, 0.f, kIgnored, 0};
+    if (i_base + lane < Mi) row = ce.rows[i_base + lane];
+    for (int c0 = 0; c0 < w && j0 + c0 < Nj; c0 += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld16(t_row + (uint32_t)(c0 + 32 * h), *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+            tmem_ld16(t_row + (uint32_t)(c0 + 32 * h + 16), *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+            tmem_ld_wait();
+            float g[32];
+            const int hit = row.target - ce.v0 - j0 - c0 - 32 * h;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float q = exp_fast(alpha * __uint_as_float(r[c]) - row.lse);
+                g[c] = row.target < 0 ? 0.f : row.scale * (c == hit ? q - 1.f : q);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                p[16 * h + c] = bf16_out ? pack2<true>(g[2 * c], g[2 * c + 1]) : pack2<false>(g[2 * c], g[2 * c + 1]);
+        }
+        const uint32_t buf = stage + (nblk & 1u) * kEpiBlockBytes;
+        if (lane == 0) bulk_wait_read<1>();  // the copy that last read this block is done with it
+        __syncwarp();
+        const uint32_t rowa = buf + (uint32_t)lane * 128u;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            st_shared_v4(rowa + ((uint32_t)(u ^ (lane & 7)) << 4), p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(gmap, buf, j0 + c0, i_base);
+            bulk_commit();
+        }
+        ++nblk;
+    }
+}
+
+}  // namespace dg

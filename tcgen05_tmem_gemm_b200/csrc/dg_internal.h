@@ -99,6 +99,24 @@ __host__ __device__ inline int64_t epi_row_offset(const EpiParams &e, int64_t i)
     return off;
 }
 
+// What the gradient's kernels of the linear cross entropy need of a row.
+struct RowGrad {
+    float lse, scale;  // G = scale * (exp(z - lse) - 1[v == target])
+    int32_t target;    // negative: the row of G is zero
+    int32_t pad_;
+};
+
+// The linear cross entropy's part of a tensor-core launch: the tile's logits
+// are those of vocabulary columns v0 ...
+struct CeTile {
+    const int64_t *target;
+    int64_t ignore_index, T, V;
+    int32_t v0, pad_;
+    float2 *part;            // statistics: [slot of 128 columns][T] pairs (maximum, sum of exponentials)
+    float *ztarget;          // statistics: the target's logit per row
+    const RowGrad *rows;     // gradient
+};
+
 struct UmmaParams {
     int32_t Mi, Nj, K;       // tensor-core problem: D[Mi x Nj] = P[Mi x K] Q[K x Nj]
     int32_t bn;              // tile width along j (64, 128 or 256)
@@ -137,6 +155,9 @@ struct UmmaParams {
     float *sk_part;          // per (pair, CTA): 128 rows x bn FP32, column by column
     uint32_t *sk_flag;       // per (pair, CTA, epilogue warp): sequence tag of the partial rows last written
     uint32_t *sk_hdr;        // [0] sequence number of the last completed launch, [1] CTAs done
+    // linear cross entropy (instances of the CTA-pair kernel)
+    CeTile ce;
+    int32_t k_chunk;         // statistics: k stages per accumulator (0: all)
     // control
     int *err_word;
     uint64_t timeout_ns;
@@ -208,6 +229,9 @@ int umma_max_stages(int bn, bool gather, bool epi_tma, int split);
 uint32_t umma_split_out_bytes(int bn, int split);  // ring bytes a split-K partial is staged in
 cudaError_t launch_umma_pair(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
                              const CUtensorMap *tc, bool fp8, int grid, size_t smem, cudaStream_t s);
+// The linear cross entropy's instances: statistics of the logits, or (grad) their gradient stored to C.
+cudaError_t launch_umma_pair_ce(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
+                                const CUtensorMap *tc, bool grad, int grid, size_t smem, cudaStream_t s);
 size_t umma_pair_smem_bytes(int bn, int stages, bool epi_tma, int ksub);
 int umma_pair_max_stages(int bn, bool epi_tma, int ksub);
 
@@ -225,5 +249,10 @@ bool device_pointer(const void *p);                       // device memory of th
 dg_status device_info(int *num_sms, int **err_word);      // the current device's, set up on first use
 int early_launch_mode();                                  // DG_OPT_EARLY_LAUNCH
 void count_launch();                                      // one kernel enqueued (dg_launch_count)
+// The logits' tiles of the linear cross entropy by the CTA-pair kernel: statistics (G null) or the
+// gradient of the logits into G.  DG_ERR_UNSUPPORTED, with nothing enqueued, when the operands or
+// the options do not allow it.  dry: only say whether they do.
+dg_status ce_pair(const dg_view *X, const dg_view *W, const dg_view *G, float alpha, const CeTile &ce, bool dry,
+                  cudaStream_t stream);
 
 }  // namespace dg

@@ -14,44 +14,17 @@
 #include <cmath>
 #include <cstring>
 
-#include "common.cuh"
+#include "ce.cuh"
 
 namespace dg {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kStatCols = 2048;                    // logits per block of ce_stats_kernel
 constexpr int64_t kForwardPiece = int64_t(256) << 20;  // most bytes of one piece of logits (forward)
 constexpr int64_t kGradPiece = int64_t(512) << 20;     // most bytes of one piece of G
+constexpr int kUsualSms = 148;                     // where no device is asked (workspace sizes)
 constexpr int kPieceCols = 256;                    // pieces are whole multiples of this many columns
-
-// What a row's target means.
-constexpr int kIgnored = -1, kInvalid = -2;
-
-__device__ __forceinline__ int read_target(const int64_t *target, int64_t ignore_index, int64_t V, int64_t t) {
-    const int64_t y = target[t];
-    if (y == ignore_index) return kIgnored;
-    return (y < 0 || y >= V) ? kInvalid : (int)y;
-}
-
-// exp(x) = 2^(x log2 e) with the hardware's power of two (relative error
-// about 2^-22, below the FP32 sums it goes into).
-__device__ __forceinline__ float exp_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
-    return y;
-}
-
-// The pair (m, s) with one more; m == -inf means an empty pair.  A NaN or
-// +infinity among the logits ends as s = NaN.
-__device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
-    const float mx = fmaxf(m, m2);
-    const float a = m == -INFINITY ? (s != s ? s : 0.f) : s * exp_fast(m - mx);
-    const float b = m2 == -INFINITY ? (s2 != s2 ? s2 : 0.f) : s2 * exp_fast(m2 - mx);
-    m = mx;
-    s = a + b;
-}
 
 // One block per row and run of kStatCols columns of a piece of FP32 logits:
 // the run's (m, s), and the target's logit if it lies in the run.
@@ -129,19 +102,15 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// What the gradient's kernels need of a row.
-struct RowGrad {
-    float lse, scale;  // G = scale * (exp(z - lse) - 1[v == target])
-    int32_t target;    // negative: the row of G is zero
-    int32_t pad_;
-};
-
-// F16 only: the power of two that brings the largest |dloss| of a row that
-// counts to [2^9, 2^10), and its inverse in `undo` (n entries, a constant
-// scale array for the products).  One block.
+// 16-bit pieces of G: dloss is divided by the largest |dloss| of a row that
+// counts, so that a gradient that is the same for all rows (a mean) is exactly
+// 1 and G's -1 + p at the target is rounded next to 1, where the rounding of
+// dloss * (p - 1) would shift a row as a whole; F16 pieces are also scaled to
+// the middle of F16's range (2^9).  norm[0] = that factor, norm[1] = its
+// inverse, which the products multiply their FP32 sums by.  One block.
 __global__ void __launch_bounds__(1024)
     ce_norm_kernel(const char *dloss, int64_t dloss_stride, const int64_t *target, int64_t ignore_index, int64_t T,
-                   int64_t V, float *norm, float *undo, int64_t n) {
+                   int64_t V, float top, float *norm) {
     pdl_wait_then_release();
     __shared__ float red[32];
     float big = 0.f;
@@ -155,35 +124,45 @@ __global__ void __launch_bounds__(1024)
     __syncthreads();
     big = red[threadIdx.x & 31];
     for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-    int e = 0;
-    if (big > 0.f) frexpf(big, &e);  // big = f 2^e, f in [1/2, 1)
-    e = 10 - e;
-    e = min(max(e, -126), 126);      // both powers stay normal
-    if (threadIdx.x == 0) *norm = ldexpf(1.f, e);
-    for (int64_t i = threadIdx.x; i < n; i += 1024) undo[i] = ldexpf(1.f, -e);
+    if (threadIdx.x == 0) {
+        // below 2^-100 the division would leave FP32's range; such gradients are scaled as far as 2^100 goes
+        big = big > 0.f ? fmaxf(big, 0x1p-100f) : 1.f;
+        norm[0] = big;
+        norm[1] = big / top;
+    }
 }
 
 // Per row: its RowGrad, and (xc != null) a copy of X's row, zero in rows that
 // take no part, so that whatever those rows hold stays out of dW.
 __global__ void __launch_bounds__(256)
     ce_rows_kernel(const DevView x, int D, int64_t T, int64_t V, const int64_t *target, int64_t ignore_index,
-                   const float *lse, const char *dloss, int64_t dloss_stride, const float *norm, RowGrad *rows,
-                   char *xc, int64_t ldx, int *err_word) {
+                   const float *lse, const char *dloss, int64_t dloss_stride, const float *norm, float top,
+                   RowGrad *rows, float *undo, int64_t undo_n, char *xc, int64_t ldx, int vec, int *err_word) {
     pdl_wait_then_release();
     const int64_t t = blockIdx.x;
     const int y = target ? read_target(target, ignore_index, V, t) : 0;
     if (rows && threadIdx.x == 0) {
         RowGrad r;
         r.lse = lse[t];
-        r.scale = y < 0 ? 0.f : *reinterpret_cast<const float *>(dloss + t * dloss_stride) * (norm ? *norm : 1.f);
+        r.scale = y < 0 ? 0.f : *reinterpret_cast<const float *>(dloss + t * dloss_stride);
+        if (norm) r.scale = r.scale / norm[0] * top;
         r.target = y;
         r.pad_ = 0;
         rows[t] = r;
         if (y == kInvalid && err_word) atomicCAS(err_word, 0, (int)DG_ERR_VALUE);
     }
+    if (undo)  // the inverse for every row of the products
+        for (int64_t i = t * 256 + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * 256) undo[i] = norm[1];
     if (!xc) return;
     const char *src = x.ptr + axis_offset(x.row, t);
     char *dst = xc + t * ldx;
+    if (vec) {  // 16 bytes at a time
+        const int n = D * elem_bytes(x.dtype) / 16;
+        for (int d = threadIdx.x; d < n; d += 256)
+            reinterpret_cast<uint4 *>(dst)[d] =
+                y < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldcs(reinterpret_cast<const uint4 *>(src) + d);
+        return;
+    }
     if (x.dtype == DG_F32) {
         for (int d = threadIdx.x; d < D; d += 256)
             reinterpret_cast<float *>(dst)[d] =
@@ -293,21 +272,47 @@ int64_t take(Layout *l, int64_t bytes) {
 // (a copy costs T D elements, a gathered operand slows every tile).
 bool forward_copies_x(const Problem &p) { return p.tensor && !p.x.tma_ok; }
 
+int64_t undo_count(const Problem &p) { return std::max(p.T, std::max(p.D, p.V)); }
 int64_t stat_slots(int64_t piece) { return (piece + kStatCols - 1) / kStatCols; }
+int64_t tile_slots(int64_t piece) { return (piece + kSlotCols - 1) / kSlotCols; }
 
-Layout forward_layout(const Problem &p, int64_t piece) {
+// Whether the CTA-pair kernel makes the logits: enough 256 x 256 tiles for
+// its pairs of SMs, operands it can read through TMA.
+bool tiles_worth_it(const Problem &p, int num_sms) {
+    return p.tensor && p.w.tma_ok && p.T > 128 && ((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms;
+}
+
+// 16-byte rows of X for its copy.
+int x_vec(const dg_view *X, const Problem &p) {
+    bool ok = p.x.col.n <= 1 && (p.x.col.n == 0 || p.x.col.stride[0] == p.es) && p.D * p.es % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(X->ptr) % 16 == 0;
+    for (int d = 0; d < p.x.row.n; ++d) ok = ok && p.x.row.stride[d] % 16 == 0;
+    return ok;
+}
+
+CeTile tile_of(const Problem &p, const int64_t *target, int64_t ignore_index, int64_t v0) {
+    CeTile c{};
+    c.target = target;
+    c.ignore_index = ignore_index;
+    c.T = p.T;
+    c.V = p.V;
+    c.v0 = (int32_t)v0;
+    return c;
+}
+
+Layout forward_layout(const Problem &p, int64_t piece, bool tiles) {
     Layout l;
     l.ldx = align256(p.D * p.es);
     l.ldz = align256(piece * 4);
     l.xc = take(&l, forward_copies_x(p) ? p.T * l.ldx : 0);
-    l.part = take(&l, stat_slots(piece) * p.T * 8);
+    l.part = take(&l, (tiles ? tile_slots(piece) : stat_slots(piece)) * p.T * 8);
     l.run = take(&l, p.T * 8);
     l.ztarget = take(&l, p.T * 4);
-    l.z = take(&l, p.T * l.ldz);
+    l.z = take(&l, tiles ? 0 : p.T * l.ldz);
     return l;
 }
 
-Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int dx_dtype) {
+Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int dx_dtype, bool tiles) {
     Layout l;
     l.ldx = align256(p.D * p.es);
     l.ldz = align256(piece * 4);
@@ -315,10 +320,10 @@ Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     l.xc = take(&l, need_dw || forward_copies_x(p) ? p.T * l.ldx : 0);
     l.rows = take(&l, p.T * (int64_t)sizeof(RowGrad));
     l.norm = take(&l, 256);
-    l.undo = take(&l, p.es == 2 ? std::max(p.T, std::max(p.D, p.V)) * 4 : 0);
+    l.undo = take(&l, p.es == 2 ? undo_count(p) * 4 : 0);
     l.acc = take(&l, need_dx && piece < p.V && dx_dtype != DG_F32 ? p.T * p.D * 4 : 0);
     l.g = take(&l, p.T * l.ldg);
-    l.z = take(&l, p.T * l.ldz);
+    l.z = take(&l, tiles ? 0 : p.T * l.ldz);
     return l;
 }
 
@@ -334,6 +339,15 @@ int64_t piece_for(const Problem &p, int64_t bytes, int64_t per_col) {
     const int64_t even = ((p.V + n - 1) / n + kPieceCols - 1) / kPieceCols * kPieceCols;
     return std::min(cols, even);
 }
+
+// The largest useful pieces: of logits, of the tiles' pairs (64 bytes of
+// pairs per row and 1024 columns), of G.
+int64_t forward_piece(const Problem &p, bool tiles) {
+    if (!tiles) return piece_for(p, kForwardPiece, p.T * 4);
+    const int64_t cols = kForwardPiece / (p.T * 8) * kSlotCols;
+    return cols >= p.V ? p.V : std::max<int64_t>(cols / kPieceCols * kPieceCols, kPieceCols);
+}
+int64_t grad_piece(const Problem &p) { return piece_for(p, kGradPiece, p.T * p.es); }
 
 dg_status launched(cudaError_t e) {
     if (e != cudaSuccess) return DG_ERR_CUDA;
@@ -380,8 +394,9 @@ dg_status dg_linear_ce_workspace(const dg_view *X, const dg_view *W, int64_t *le
     if (!least || !best) return DG_ERR_NULL;
     Problem p;
     DG_TRY(check_problem(X, W, &p));
-    *least = forward_layout(p, piece_min(p)).total;
-    *best = forward_layout(p, piece_for(p, kForwardPiece, p.T * 4)).total;
+    const bool tiles = tiles_worth_it(p, kUsualSms);
+    *least = forward_layout(p, piece_min(p), false).total;
+    *best = std::max(*least, forward_layout(p, forward_piece(p, tiles), tiles).total);
     return DG_OK;
 }
 
@@ -395,26 +410,33 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     if (reinterpret_cast<uintptr_t>(target) % 8 || reinterpret_cast<uintptr_t>(loss) % 4 ||
         reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256)
         return DG_ERR_ALIGN;
-    auto layout_of = [&](int64_t piece) { return forward_layout(p, piece); };
-    const int64_t piece = fit_piece(p, workspace_bytes, piece_for(p, kForwardPiece, p.T * 4), layout_of);
-    if (piece == 0) return DG_ERR_SHAPE;
+    if (forward_layout(p, piece_min(p), false).total > workspace_bytes) return DG_ERR_SHAPE;
     int num_sms = 0, *err_word = nullptr;
     DG_TRY(device_info(&num_sms, &err_word));
     if ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
         !device_pointer(loss) || !device_pointer(lse) || !device_pointer(workspace))
         return DG_ERR_POINTER;
-    const Layout l = layout_of(piece);
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int pdl = early_launch_mode() != 0;
     const dim3 one(1, 1, 1);
-    dg_view xv = *X;
+    // the copy of X, if there is one, comes first in the workspace
+    const dg_view xv = forward_copies_x(p) ? view2(ws, p.T, p.D, align256(p.D * p.es), p.es, X->dtype) : *X;
+    bool tiles = tiles_worth_it(p, num_sms);
+    if (tiles) {
+        CeTile ce = tile_of(p, target, ignore_index, 0);
+        ce.part = reinterpret_cast<float2 *>(ws);
+        tiles = ce_pair(&xv, W, nullptr, alpha, ce, true, s) == DG_OK;
+    }
+    auto layout_of = [&](int64_t piece) { return forward_layout(p, piece, tiles); };
+    const int64_t piece = fit_piece(p, workspace_bytes, forward_piece(p, tiles), layout_of);
+    if (piece == 0) return DG_ERR_SHAPE;
+    const Layout l = layout_of(piece);
     if (forward_copies_x(p)) {
         DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x),
                                   (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
-                                  (const char *)nullptr, (int64_t)0, (const float *)nullptr, (RowGrad *)nullptr,
-                                  ws + l.xc, l.ldx, (int *)nullptr)));
-        xv = view2(ws + l.xc, p.T, p.D, l.ldx, p.es, X->dtype);
+                                  (const char *)nullptr, (int64_t)0, (const float *)nullptr, 1.f, (RowGrad *)nullptr,
+                                  (float *)nullptr, (int64_t)0, ws + l.xc, l.ldx, x_vec(X, p), (int *)nullptr)));
     }
     float2 *part = reinterpret_cast<float2 *>(ws + l.part), *run = reinterpret_cast<float2 *>(ws + l.run);
     float *ztarget = reinterpret_cast<float *>(ws + l.ztarget), *z = reinterpret_cast<float *>(ws + l.z);
@@ -422,13 +444,22 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
         const int64_t cols = std::min(piece, p.V - v0);
         const dg_view wv = view2(p.wm.ptr + v0 * p.wm.cs, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
         const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
-        DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
-        const int chunks = (int)stat_slots(cols);
-        DG_TRY(launched(launch_ex(ce_stats_kernel, dim3((unsigned)(p.T * chunks)), dim3(256), 0, s, one, pdl,
-                                  (const float *)z, l.ldz / 4, p.T, p.V, (int)v0, (int)cols, chunks, target,
-                                  ignore_index, part, ztarget)));
+        int slots;
+        if (tiles) {
+            CeTile ce = tile_of(p, target, ignore_index, v0);
+            ce.part = part;
+            ce.ztarget = ztarget;
+            DG_TRY(ce_pair(&xv, &wv, nullptr, alpha, ce, false, s));
+            slots = (int)tile_slots(cols);
+        } else {
+            DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
+            slots = (int)stat_slots(cols);
+            DG_TRY(launched(launch_ex(ce_stats_kernel, dim3((unsigned)(p.T * slots)), dim3(256), 0, s, one, pdl,
+                                      (const float *)z, l.ldz / 4, p.T, p.V, (int)v0, (int)cols, slots, target,
+                                      ignore_index, part, ztarget)));
+        }
         DG_TRY(launched(launch_ex(ce_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, s, one, pdl,
-                                  (const float2 *)part, chunks, p.T, p.V, v0 == 0, v0 + cols == p.V, run, target,
+                                  (const float2 *)part, slots, p.T, p.V, v0 == 0, v0 + cols == p.V, run, target,
                                   ignore_index, (const float *)ztarget, loss, lse, err_word)));
     }
     return DG_OK;
@@ -457,8 +488,6 @@ dg_status check_grad(const dg_view *X, const dg_view *W, const dg_view *dX, cons
     return DG_OK;
 }
 
-int64_t grad_piece(const Problem &p) { return piece_for(p, kGradPiece, p.T * p.es); }
-
 }  // namespace
 }  // namespace dg
 
@@ -470,8 +499,9 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W, const 
     Problem p;
     DG_TRY(check_grad(X, W, dX, dW, &p));
     const int dxt = dX ? dX->dtype : DG_F32;
-    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt).total;
-    *best = grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt).total;
+    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false).total;
+    *best = std::max(*least, grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt,
+                                         tiles_worth_it(p, kUsualSms)).total);
     return DG_OK;
 }
 
@@ -494,9 +524,8 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             return DG_ERR_ALIGN;
     }
     const int dxt = dX ? dX->dtype : DG_F32;
-    auto layout_of = [&](int64_t piece) { return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt); };
-    const int64_t piece = p.T > 0 ? fit_piece(p, workspace_bytes, grad_piece(p), layout_of) : p.V;
-    if (p.T > 0 && piece == 0) return DG_ERR_SHAPE;
+    if (p.T > 0 && grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false).total > workspace_bytes)
+        return DG_ERR_SHAPE;
     DG_TRY(device_info(&num_sms, &err_word));
     if (p.T > 0 && ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
                     !device_pointer(lse) || !device_pointer(dloss) || !device_pointer(workspace)))
@@ -508,24 +537,48 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         if (!dW) return DG_OK;
         return launched(launch_scale_c(dev_of(dW, p.dw), p.D, p.V, 0.f, nullptr, DG_ACT_NONE, pdl, s));
     }
-    const Layout l = layout_of(piece);
     char *ws = static_cast<char *>(workspace);
+    // a row that takes no part has no use for its logits, so dW's copy of X serves them too; it
+    // comes first in the workspace
+    const bool copy = dW != nullptr || forward_copies_x(p);
+    const int64_t ldx = align256(p.D * p.es);
+    const dg_view xv = copy ? view2(ws, p.T, p.D, ldx, p.es, X->dtype) : *X;
+    const dg_view xt = view2(ws, p.D, p.T, p.es, ldx, X->dtype);
+    bool tiles = tiles_worth_it(p, num_sms);
+    auto layout_of = [&](int64_t piece) {
+        return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt, tiles);
+    };
+    int64_t piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
+    if (tiles) {
+        // the tensor stores of G take pieces of 64 columns or more, the last one too
+        while (piece > 0 && piece < p.V && p.V % piece != 0 && p.V % piece < 64) piece -= kPieceCols;
+        if (piece > 0) {
+            const Layout t = layout_of(piece);
+            const dg_view gv = view2(ws + t.g, p.T, std::min(piece, p.V), t.ldg, p.es, X->dtype);
+            const dg_view wv = view2(p.wm.ptr, p.D, std::min(piece, p.V), p.wm.rs, p.wm.cs, W->dtype);
+            tiles = ce_pair(&xv, &wv, &gv, alpha, tile_of(p, target, ignore_index, 0), true, s) == DG_OK;
+        }
+        if (piece <= 0 || !tiles) {
+            tiles = false;
+            piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
+        }
+    }
+    if (piece == 0) return DG_ERR_SHAPE;
+    const Layout l = layout_of(piece);
     RowGrad *rows = reinterpret_cast<RowGrad *>(ws + l.rows);
     float *norm = nullptr, *undo = nullptr;
-    if (X->dtype == DG_F16) {
+    const float top = X->dtype == DG_F16 ? 512.f : 1.f;
+    if (p.tensor) {
         norm = reinterpret_cast<float *>(ws + l.norm);
         undo = reinterpret_cast<float *>(ws + l.undo);
         DG_TRY(launched(launch_ex(ce_norm_kernel, one, dim3(1024), 0, s, one, pdl,
                                   reinterpret_cast<const char *>(dloss), dloss_stride, target, ignore_index, p.T, p.V,
-                                  norm, undo, std::max(p.T, std::max(p.D, p.V)))));
+                                  top, norm)));
     }
-    const bool copy = dW != nullptr || forward_copies_x(p);
     DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
                               p.T, p.V, target, ignore_index, lse, reinterpret_cast<const char *>(dloss), dloss_stride,
-                              (const float *)norm, rows, copy ? ws + l.xc : (char *)nullptr, l.ldx, err_word)));
-    // a row that takes no part has no use for its logits, so the copy serves them too
-    const dg_view xv = copy ? view2(ws + l.xc, p.T, p.D, l.ldx, p.es, X->dtype) : *X;
-    const dg_view xt = view2(ws + l.xc, p.D, p.T, p.es, l.ldx, X->dtype);
+                              (const float *)norm, top, rows, undo, undo_count(p), copy ? ws : (char *)nullptr, ldx,
+                              x_vec(X, p), err_word)));
     char *g = ws + l.g;
     float *z = reinterpret_cast<float *>(ws + l.z);
     const bool sum = dX && piece < p.V;                        // dX is summed over several pieces
@@ -536,13 +589,20 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         char *wp = p.wm.ptr + v0 * p.wm.cs;
         const dg_view wv = view2(wp, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
         const dg_view wt = view2(wp, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
-        const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
-        DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
-        const int64_t blocks = p.T * ((cols + 1023) / 1024);
-        DG_TRY(launched(launch_ex(ce_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, s, one, pdl, (const float *)z,
-                                  l.ldz / 4, p.T, (int)v0, (int)cols, (const RowGrad *)rows, g, l.ldg, X->dtype)));
         const dg_view gv = view2(g, p.T, cols, l.ldg, p.es, X->dtype);
         const dg_view gt = view2(g, cols, p.T, p.es, l.ldg, X->dtype);
+        if (tiles) {
+            CeTile ce = tile_of(p, target, ignore_index, v0);
+            ce.rows = rows;
+            DG_TRY(ce_pair(&xv, &wv, &gv, alpha, ce, false, s));
+        } else {
+            const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
+            DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
+            const int64_t blocks = p.T * ((cols + 1023) / 1024);
+            DG_TRY(launched(launch_ex(ce_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, s, one, pdl,
+                                      (const float *)z, l.ldz / 4, p.T, (int)v0, (int)cols, (const RowGrad *)rows, g,
+                                      l.ldg, X->dtype)));
+        }
         if (dX) DG_TRY(dg_gemm(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, undo, nullptr, stream));
         if (dW) {
             // the product in the order that gives dW's unit stride to the columns of the output
