@@ -36,23 +36,26 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
 }
 
 // Another N logits: one pass, the running sum rescaled when the maximum moves.
+// Four chains for the maximum and eight for the sum, so that few instructions
+// wait for one another (a warp has its scheduler almost to itself).
 template <int N>
 __device__ __forceinline__ void join_logits(float &m, float &s, const float (&z)[N]) {
-    float mx = m;
+    float mx[4] = {m, z[1], z[2], z[3]};
+    mx[0] = fmaxf(mx[0], z[0]);
 #pragma unroll
-    for (int c = 0; c < N; ++c) mx = fmaxf(mx, z[c]);
-    if (mx == -INFINITY) {  // nothing but -infinity, and perhaps NaN
+    for (int c = 4; c < N; ++c) mx[c & 3] = fmaxf(mx[c & 3], z[c]);
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    if (top == -INFINITY) {  // nothing but -infinity, and perhaps NaN
 #pragma unroll
         for (int c = 0; c < N; ++c)
             if (z[c] != z[c]) s = z[c];
         return;
     }
-    // four sums: their additions do not wait for one another
-    float a[4] = {m == -INFINITY ? (s != s ? s : 0.f) : s * exp_fast(m - mx), 0.f, 0.f, 0.f};
+    float a[8] = {m == -INFINITY ? (s != s ? s : 0.f) : s * exp_fast(m - top), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < N; ++c) a[c & 3] += exp_fast(z[c] - mx);
-    m = mx;
-    s = (a[0] + a[1]) + (a[2] + a[3]);
+    for (int c = 0; c < N; ++c) a[c & 7] += exp_fast(z[c] - top);
+    m = top;
+    s = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
 }
 
 // The logit of column `hit` (relative to the first of the N) if it is one of them.
@@ -65,12 +68,13 @@ __device__ __forceinline__ void keep_target(const float (&z)[N], int hit, float 
     }
 }
 
-// 32 accumulator columns as logits alpha * acc, -infinity past the last column.
-__device__ __forceinline__ void logits32(float (&z)[32], float alpha, uint32_t t_addr, int j, int Nj) {
-    uint32_t r[32];
-    tmem_ld16(t_addr, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-    tmem_ld16(t_addr + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
-    tmem_ld_wait();
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    tmem_ld16(addr, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+    tmem_ld16(addr + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+}
+
+// 32 accumulators as logits alpha * acc of columns j .., -infinity at and past Nj.
+__device__ __forceinline__ void logits32(float (&z)[32], float alpha, const uint32_t (&r)[32], int j, int Nj) {
 #pragma unroll
     for (int c = 0; c < 32; ++c) z[c] = alpha * __uint_as_float(r[c]);
     if (j + 32 > Nj) {
@@ -80,40 +84,44 @@ __device__ __forceinline__ void logits32(float (&z)[32], float alpha, uint32_t t
     }
 }
 
-// Columns of a tile per slot of CeTile::part; a tile has two slots.
+// Columns of a tile per epilogue warp, and per slot of CeTile::part.
 constexpr int kSlotCols = 128;
 
-// One warp's 32 rows (this thread's row i) x 256 columns from j0 of a tile:
-// the row's pair goes to the tile's first slot, its second is left empty.
-__device__ __forceinline__ void ce_stats_rows(const CeTile &ce, float alpha, uint32_t t_row, int i, int Mi, int j0,
+// One warp's 32 rows (this thread's row i) x 128 columns from j: the row's
+// pair goes to the columns' slot.  A thread holds one row, so nothing crosses
+// lanes; the TMEM load of the next 32 columns is in flight while 32 are
+// reduced.
+__device__ __forceinline__ void ce_stats_rows(const CeTile &ce, float alpha, uint32_t t_addr, int i, int Mi, int j,
                                               int Nj) {
+    if (j >= Nj) return;
     const bool ok = i < Mi;
+    uint32_t r[2][32];
+    __syncwarp();
+    tmem_ld32(t_addr, r[0]);
     const int y = ok ? read_target(ce.target, ce.ignore_index, ce.V, i) : kIgnored;
     float m = -INFINITY, s = 0.f;
-    for (int c0 = 0; c0 < 2 * kSlotCols && j0 + c0 < Nj; c0 += 32) {
+#pragma unroll
+    for (int q = 0; q < kSlotCols / 32; ++q) {
+        tmem_ld_wait();
+        if (q + 1 < kSlotCols / 32) tmem_ld32(t_addr + 32 * (q + 1), r[(q + 1) & 1]);
         float z[32];
-        __syncwarp();
-        logits32(z, alpha, t_row + (uint32_t)c0, j0 + c0, Nj);
+        logits32(z, alpha, r[q & 1], j + 32 * q, Nj);
         join_logits(m, s, z);
-        if (y >= 0) keep_target(z, y - ce.v0 - j0 - c0, ce.ztarget + i);
+        if (y >= 0) keep_target(z, y - ce.v0 - j - 32 * q, ce.ztarget + i);
+        __syncwarp();
     }
-    if (!ok) return;
-    float2 *slot = ce.part + (int64_t)(j0 / kSlotCols) * ce.T + i;
-    slot[0] = make_float2(m, s);
-    if (j0 + kSlotCols < Nj) slot[ce.T] = make_float2(-INFINITY, 0.f);
+    if (ok) ce.part[(int64_t)(j / kSlotCols) * ce.T + i] = make_float2(m, s);
 }
 
-// The same for a long k, with a warp for each of the tile's two slots (`half`).
+// The same for a long k.
 // The tensor core adds each step's products to the accumulator with
 // truncation, so a logit's error grows with the steps (the loss was off by
 // 1.4e-6 of itself at k = 4096, the truncations all pointing the same way);
 // every chunk of k starts a fresh accumulator, and the chunks are added here,
 // rounded to nearest, in registers.
 __device__ __forceinline__ void ce_stats_rows_long(float (&sums)[kSlotCols], const CeTile &ce, float alpha,
-                                                   uint32_t t_row, int i, int Mi, int j0, int Nj, bool half,
-                                                   bool first, bool last) {
-    const int j = j0 + (half ? kSlotCols : 0);
-    const uint32_t t_addr = t_row + (half ? kSlotCols : 0);
+                                                   uint32_t t_addr, int i, int Mi, int j, int Nj, bool first,
+                                                   bool last) {
 #pragma unroll
     for (int c0 = 0; c0 < kSlotCols; c0 += 16) {
         uint32_t r[16];
@@ -143,48 +151,47 @@ __device__ __forceinline__ void ce_stats_rows_long(float (&sums)[kSlotCols], con
 
 // One warp's 32 rows x w columns of G = scale (exp(z - lse) - 1[v == target]),
 // zero in rows that take no part, through tensor stores in blocks of 32 rows x
-// 64 columns (the layout and its double buffering are epilogue_rows_tma's).
+// 64 columns (in epilogue_rows_tma's layout).  The two warps of a quarter take
+// blocks in turn, each through one staging block of its own.
 __device__ __forceinline__ void ce_grad_rows_tma(const CeTile &ce, const EpiParams &e, const CUtensorMap *gmap,
                                                  uint32_t stage, uint32_t t_row, int i_base, int Mi, int j0, int w,
-                                                 int Nj, int lane, uint32_t &nblk) {
+                                                 int Nj, int lane, int first) {
     if (i_base >= Mi) return;  // the whole warp is below G (warp-uniform)
     const bool bf16_out = e.c_dtype == DG_BF16;
     const float alpha = e.alpha;
     RowGrad row{0.f, 0.f, kIgnored, 0};
     if (i_base + lane < Mi) row = ce.rows[i_base + lane];
-    for (int c0 = 0; c0 < w && j0 + c0 < Nj; c0 += 64) {
-        uint32_t p[32];
+    for (int c0 = first; c0 < w && j0 + c0 < Nj; c0 += 128) {
+        uint32_t r[2][32], p[32];
+        tmem_ld32(t_row + (uint32_t)c0, r[0]);
+        tmem_ld_wait();
+        tmem_ld32(t_row + (uint32_t)c0 + 32, r[1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_ld16(t_row + (uint32_t)(c0 + 32 * h), *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-            tmem_ld16(t_row + (uint32_t)(c0 + 32 * h + 16), *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
-            tmem_ld_wait();
+            if (h) tmem_ld_wait();
             float g[32];
             const int hit = row.target - ce.v0 - j0 - c0 - 32 * h;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-                const float q = exp_fast(alpha * __uint_as_float(r[c]) - row.lse);
+                const float q = exp_fast(alpha * __uint_as_float(r[h][c]) - row.lse);
                 g[c] = row.target < 0 ? 0.f : row.scale * (c == hit ? q - 1.f : q);
             }
 #pragma unroll
             for (int c = 0; c < 16; ++c)
                 p[16 * h + c] = bf16_out ? pack2<true>(g[2 * c], g[2 * c + 1]) : pack2<false>(g[2 * c], g[2 * c + 1]);
         }
-        const uint32_t buf = stage + (nblk & 1u) * kEpiBlockBytes;
-        if (lane == 0) bulk_wait_read<1>();  // the copy that last read this block is done with it
+        if (lane == 0) bulk_wait_read<0>();  // the copy that last read the block is done with it
         __syncwarp();
-        const uint32_t rowa = buf + (uint32_t)lane * 128u;
+        const uint32_t rowa = stage + (uint32_t)lane * 128u;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             st_shared_v4(rowa + ((uint32_t)(u ^ (lane & 7)) << 4), p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            tma_store_2d(gmap, buf, j0 + c0, i_base);
+            tma_store_2d(gmap, stage, j0 + c0, i_base);
             bulk_commit();
         }
-        ++nblk;
     }
 }
 

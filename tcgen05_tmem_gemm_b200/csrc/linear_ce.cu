@@ -66,25 +66,32 @@ __global__ void __launch_bounds__(256)
 
 // Joins the `slots` pairs of each row of a piece, in slot order, with the
 // row's pair of the earlier pieces; the last piece writes lse and loss.
-// 32 rows per block, eight warps walk the slots.
-__global__ void __launch_bounds__(256)
+// 32 rows per block; kJoinWarps warps share the slots, four loads in flight each.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps)
     ce_join_kernel(const float2 *part, int slots, int64_t T, int64_t V, bool first, bool last, float2 *run,
                    const int64_t *target, int64_t ignore_index, const float *ztarget, float *loss, float *lse,
                    int *err_word) {
     pdl_wait_then_release();
-    __shared__ float2 red[8][32];
+    __shared__ float2 red[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * 32 + lane;
     float m = -INFINITY, s = 0.f;
     if (t < T)
-        for (int i = warp; i < slots; i += 8) {
-            const float2 q = part[(int64_t)i * T + t];
-            join(m, s, q.x, q.y);
+        for (int i0 = warp; i0 < slots; i0 += 4 * kJoinWarps) {
+            float2 q[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kJoinWarps;
+                q[u] = i < slots ? part[(int64_t)i * T + t] : make_float2(-INFINITY, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) join(m, s, q[u].x, q[u].y);
         }
     red[warp][lane] = make_float2(m, s);
     __syncthreads();
     if (warp != 0 || t >= T) return;
-    for (int w = 1; w < 8; ++w) join(m, s, red[w][lane].x, red[w][lane].y);
+    for (int w = 1; w < kJoinWarps; ++w) join(m, s, red[w][lane].x, red[w][lane].y);
     if (!first) join(m, s, run[t].x, run[t].y);
     if (!last) {
         run[t] = make_float2(m, s);
@@ -458,7 +465,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
                                       (const float *)z, l.ldz / 4, p.T, p.V, (int)v0, (int)cols, slots, target,
                                       ignore_index, part, ztarget)));
         }
-        DG_TRY(launched(launch_ex(ce_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, s, one, pdl,
+        DG_TRY(launched(launch_ex(ce_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(32 * kJoinWarps), 0, s, one, pdl,
                                   (const float2 *)part, slots, p.T, p.V, v0 == 0, v0 + cols == p.V, run, target,
                                   ignore_index, (const float *)ztarget, loss, lse, err_word)));
     }

@@ -196,11 +196,13 @@ __device__ __forceinline__ float *sk_slot(const UmmaParams &p, int q, uint32_t r
 }
 
 // What the epilogue does with a tile.  EPI_CE_STATS_LONG: EPI_CE_STATS over a
-// long k, summed in chunks (see ce_stats_rows_long); it has eight epilogue
-// warps, two per quarter of the TMEM lanes, each with half of the columns.
+// long k, summed in chunks (see ce_stats_rows_long).  The cross entropy's
+// epilogues compute an exponential per element and have eight warps, two per
+// quarter of the TMEM lanes.
 enum : int { EPI_STORE = 0, EPI_CE_STATS = 1, EPI_CE_STATS_LONG = 2, EPI_CE_GRAD = 3 };
 
-constexpr int pair_threads(int epi) { return epi == EPI_CE_STATS_LONG ? 320 : 192; }
+__host__ __device__ constexpr int pair_epi_warps(int epi) { return epi == EPI_STORE ? 4 : 8; }
+__host__ __device__ constexpr int pair_threads(int epi) { return 64 + 32 * pair_epi_warps(epi); }
 
 template <bool FP8, int KSUB, int EPI>
 __global__ void __launch_bounds__(pair_threads(EPI), 1)
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, CHUNKED ? 16 : 8);  // the epilogue warps of both CTAs of the pair
+            mbar_init(bar_tempty + 8 * b, 2 * pair_epi_warps(EPI));  // the epilogue warps of both CTAs of the pair
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -422,14 +424,15 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * p.bn);
             const int j0 = pw.j0;
             if (EPI != EPI_STORE) {
+                const int half = warp >= 6 ? 1 : 0, c0 = half * kSlotCols;  // the two warps of a quarter
                 if (EPI == EPI_CE_STATS)
-                    ce_stats_rows(p.ce, e.alpha, t_row, i, p.Mi, j0, p.Nj);
+                    ce_stats_rows(p.ce, e.alpha, t_row + c0, i, p.Mi, j0 + c0, p.Nj);
                 else if (EPI == EPI_CE_STATS_LONG)
-                    ce_stats_rows_long(sums, p.ce, e.alpha, t_row, i, p.Mi, j0, p.Nj, warp >= 6, pw.kb0 == 0,
+                    ce_stats_rows_long(sums, p.ce, e.alpha, t_row + c0, i, p.Mi, j0 + c0, p.Nj, pw.kb0 == 0,
                                        pw.kb1 == p.kb_total);
                 else
-                    ce_grad_rows_tma(p.ce, e, &tmap_c, sbase + L.epi_off + (uint32_t)quarter * 2u * kEpiBlockBytes,
-                                     t_row, i - lane, p.Mi, j0, pw.w, p.Nj, lane, nblk);
+                    ce_grad_rows_tma(p.ce, e, &tmap_c, sbase + L.epi_off + (uint32_t)(warp - 2) * kEpiBlockBytes,
+                                     t_row, i - lane, p.Mi, j0, pw.w, p.Nj, lane, 64 * half);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(dsmem_map(bar_tempty + 8 * b, 0));
