@@ -284,6 +284,7 @@ struct Override {
     int stages = 0;      // pipeline depth (at most what shared memory holds)
     int gemv_split = 0;  // GEMV_N k splits
     int ksub = 0;        // CTA-pair stage depth in 128-byte k sub-blocks: 1 or 2
+    bool no_swap = false;  // thin products too keep A on the tensor-core M side (not an autotune choice)
     bool any() const {
         return bn || split || pair >= 0 || sk >= 0 || gcl || epi_tma >= 0 || stages || gemv_split || ksub;
     }
@@ -333,7 +334,7 @@ bool umma_plan(const Views &v, int64_t M, int64_t N, int64_t K, float beta, int 
     bool swap;
     if (!a_tma) swap = false;       // A is loaded by threads as the M-side operand
     else if (!b_tma) swap = true;   // B is, after the swap
-    else swap = thin;
+    else swap = thin && !ov->no_swap;
     // C: the epilogue addresses a row (i) through any number of merged dims,
     // computed once per row (a layout transform such as writing an NCHW
     // output from an [N*H*W, C] product), and walks j with one stride
@@ -643,7 +644,7 @@ dg_status make_plan(Views &v, float alpha, float beta, int num_sms, Plan *pl, bo
             if (forced) return DG_ERR_UNSUPPORTED;
             if (ov && umma_plan(v, M, N, K, beta, num_sms, allow_sk, pl)) return DG_OK;
         } else {
-            if (M <= 8) {
+            if (M <= 8 && !(force && force->no_swap)) {
                 if (gemv_applicable(v, M, N, K, DG_KIND_GEMV_N)) {
                     in.kind = DG_KIND_GEMV_N;
                     if (!gemv_n_split(M, N, K, num_sms, &in, ov ? ov->gemv_split : 0)) {
@@ -1089,52 +1090,93 @@ int early_launch_mode() { return g_pdl.load(); }
 
 void count_launch() { g_launches.fetch_add(1); }
 
-dg_status ce_pair(const dg_view *X, const dg_view *W, const dg_view *G, float alpha, const CeTile &ce, bool dry,
-                  cudaStream_t stream) {
+dg_status pair_call(PairCall &c, cudaStream_t stream) {
     if (g_pair.load() == 0 || (g_force_kind.load() != 0 && g_force_kind.load() != DG_KIND_UMMA))
         return DG_ERR_UNSUPPORTED;
     DeviceState *ds = nullptr;
     dg_status st = device_state(&ds);
     if (st != DG_OK) return st;
-    // the statistics store no C: a view of the right shape that nothing writes stands in
-    dg_view c;
-    if (G) {
-        c = *G;
+    ViewInfo ai, bi;
+    if ((st = analyse(c.A, false, &ai)) != DG_OK || (st = analyse(c.B, false, &bi)) != DG_OK) return st;
+    const bool stats = c.use == kPairStats, partial = c.use == kPairPartial;
+    // the plan is made for C [M x N]; the statistics store none, and partial sums several planes of one:
+    // a view of the right shape stands in, which nothing writes
+    dg_view cv;
+    if (stats || partial) {
+        std::memset(&cv, 0, sizeof(cv));
+        cv.ptr = stats ? static_cast<void *>(c.ce.part) : c.C->ptr;
+        cv.ndim = 2;
+        cv.row_dims = 1;
+        cv.shape[0] = ai.rows;
+        cv.shape[1] = bi.cols;
+        cv.stride[0] = partial ? c.C->stride[0] : (bi.cols * 4 + 15) / 16 * 16;
+        cv.stride[1] = 4;
+        cv.dtype = DG_F32;
     } else {
-        std::memset(&c, 0, sizeof(c));
-        ViewInfo xi, wi;
-        if ((st = analyse(X, false, &xi)) != DG_OK || (st = analyse(W, false, &wi)) != DG_OK) return st;
-        c.ptr = ce.part;
-        c.ndim = 2;
-        c.row_dims = 1;
-        c.shape[0] = xi.rows;
-        c.shape[1] = wi.cols;
-        c.stride[0] = (wi.cols * 2 + 15) / 16 * 16;
-        c.stride[1] = 2;
-        c.dtype = DG_BF16;
+        cv = *c.C;
     }
+    Views v{c.A, c.B, &cv, {}, {}, {}};
     Override ov;
     ov.bn = 256;
     ov.split = 1;
     ov.pair = 1;
     ov.sk = 0;
-    ov.epi_tma = G ? 1 : 0;
-    Views v{X, W, &c, {}, {}, {}};
+    ov.no_swap = true;
+    ov.epi_tma = 0;  // decided below: the plan's rule leaves out C of fewer than 32 rows
+    if (c.use == kPairWide) ov.ksub = 1;  // more, smaller stages beside its 64 KB of staging blocks
     Plan pl;
-    if ((st = make_plan(v, alpha, 0.f, ds->num_sms, &pl, false, &ov)) != DG_OK) return st;
-    if (pl.info.kind != DG_KIND_UMMA || !pl.info.cta_pair) return DG_ERR_UNSUPPORTED;
-    if (!G) pl.info.pair_half_tiles = 0;  // whole tiles have whole slots
-    if (dry) return DG_OK;
+    if ((st = make_plan(v, c.alpha, 0.f, ds->num_sms, &pl, false, &ov)) != DG_OK) return st;
+    dg_plan_info &in = pl.info;
+    if (in.kind != DG_KIND_UMMA || !in.cta_pair || in.swap_ab) return DG_ERR_UNSUPPORTED;
+    if (stats || partial) in.pair_half_tiles = 0;  // whole tiles: the slots' and planes' layout
+    const int ksub = in.block_k / (128 / elem_size(c.A->dtype));
+    if (!stats) {
+        // C through tensor stores in blocks of 128 bytes: row-major, 16-byte aligned rows
+        if (!v.c.tma_ok || v.c.unit_dim != 1 || in.N < 128 / elem_size(cv.dtype)) return DG_ERR_UNSUPPORTED;
+        in.epi_tma_store = 1;
+        const int warps = c.use == kPairWide ? 8 : 4;  // pairs of staging blocks
+        in.stages = umma_pair_max_stages(in.block_n, true, ksub, warps);
+        pl.smem = umma_pair_smem_bytes(in.block_n, in.stages, true, ksub, warps);
+    }
+    if (c.dry) return DG_OK;
     LaunchRec rec;
-    if ((st = prepare(v, pl, alpha, 0.f, nullptr, nullptr, nullptr, DG_ACT_NONE, ds, nullptr, &rec)) != DG_OK)
+    if ((st = prepare(v, pl, c.alpha, 0.f, c.scale_a, nullptr, nullptr, DG_ACT_NONE, ds, nullptr, &rec)) != DG_OK)
         return st;
-    rec.umma.ce = ce;
-    rec.umma.k_chunk = 2048 / pl.info.block_k;  // k per accumulator: see ce_stats_rows_long
-    if (launch_umma_pair_ce(rec.umma, &rec.t0, &rec.t1, &rec.t2, G != nullptr, rec.grid, rec.smem, stream) !=
-        cudaSuccess)
+    UmmaParams &p = rec.umma;
+    p.ce = c.ce;
+    p.k_chunk = std::max(1, 2048 / in.block_k);  // statistics: see ce_stats_rows_long
+    if (partial) {
+        if (!encode_2d_box(&rec.t2, DG_F32, c.C->ptr, in.N, c.C->shape[0], c.C->stride[0], 32, 32, true))
+            return DG_ERR_UNSUPPORTED;
+        p.k_chunk = (p.kb_total + c.chunks - 1) / c.chunks;
+        p.plane_rows = (int32_t)(c.C->shape[0] / c.chunks);
+        c.chunks = (p.kb_total + p.k_chunk - 1) / p.k_chunk;
+        p.num_units = p.full_units * c.chunks;
+        rec.grid = 2 * std::min(p.num_units, ds->num_sms / 2);
+    }
+    if (launch_umma_pair_use(p, &rec.t0, &rec.t1, &rec.t2, c.use, rec.grid, rec.smem, stream) != cudaSuccess)
         return DG_ERR_CUDA;
     g_launches.fetch_add(1);
     return DG_OK;
+}
+
+dg_status gemm_tiles(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta,
+                     const float *scale_a, cudaStream_t stream) {
+    ViewInfo ai;
+    dg_status st = analyse(A, false, &ai);
+    if (st != DG_OK) return st;
+    if (ai.rows > 8 || g_force_kind.load() != 0) return dg_gemm(A, B, C, alpha, beta, scale_a, nullptr, stream);
+    Views v{A, B, C, {}, {}, {}};
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds)) != DG_OK) return st;
+    const Override rule;
+    Plan pl;
+    if ((st = make_plan(v, alpha, beta, ds->num_sms, &pl, false, &rule)) != DG_OK) return st;
+    if (pl.info.kind != DG_KIND_GEMV_K || !umma_plan(v, pl.info.M, pl.info.N, pl.info.K, beta, ds->num_sms, false, &pl))
+        return dg_gemm(A, B, C, alpha, beta, scale_a, nullptr, stream);
+    LaunchRec rec;
+    st = build_launch(v, pl, alpha, beta, scale_a, nullptr, nullptr, DG_ACT_NONE, ds, stream, &rule, &rec);
+    return st == DG_OK ? fire(rec, stream) : st;
 }
 
 }  // namespace dg

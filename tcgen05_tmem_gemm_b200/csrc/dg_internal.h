@@ -157,7 +157,8 @@ struct UmmaParams {
     uint32_t *sk_hdr;        // [0] sequence number of the last completed launch, [1] CTAs done
     // linear cross entropy (instances of the CTA-pair kernel)
     CeTile ce;
-    int32_t k_chunk;         // statistics: k stages per accumulator (0: all)
+    int32_t k_chunk;         // statistics, partial sums: k stages per accumulator
+    int32_t plane_rows;      // partial sums: rows of C's map from one chunk of k to the next
     // control
     int *err_word;
     uint64_t timeout_ns;
@@ -229,11 +230,17 @@ int umma_max_stages(int bn, bool gather, bool epi_tma, int split);
 uint32_t umma_split_out_bytes(int bn, int split);  // ring bytes a split-K partial is staged in
 cudaError_t launch_umma_pair(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
                              const CUtensorMap *tc, bool fp8, int grid, size_t smem, cudaStream_t s);
-// The linear cross entropy's instances: statistics of the logits, or (grad) their gradient stored to C.
-cudaError_t launch_umma_pair_ce(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
-                                const CUtensorMap *tc, bool grad, int grid, size_t smem, cudaStream_t s);
-size_t umma_pair_smem_bytes(int bn, int stages, bool epi_tma, int ksub);
-int umma_pair_max_stages(int bn, bool epi_tma, int ksub);
+// What a launch of the CTA-pair kernel's other instances (umma_pair_ce.cu) does.
+enum PairUse : int {
+    kPairStats,    // linear cross entropy: statistics of the logits
+    kPairGrad,     // their gradient, stored to C
+    kPairWide,     // C = the product, eight epilogue warps (a short k)
+    kPairPartial   // FP32 sums of p.k_chunk stages of k each, plane by plane
+};
+cudaError_t launch_umma_pair_use(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
+                                 const CUtensorMap *tc, PairUse use, int grid, size_t smem, cudaStream_t s);
+size_t umma_pair_smem_bytes(int bn, int stages, bool epi_tma, int ksub, int epi_warps = 4);
+int umma_pair_max_stages(int bn, bool epi_tma, int ksub, int epi_warps = 4);
 
 cudaError_t launch_gemv_n(const GemvParams &p, const CUtensorMap *tmap_w, cudaStream_t s, int *grid_out);
 size_t gemv_n_smem_bytes(int r_inst, int kper);
@@ -249,10 +256,23 @@ bool device_pointer(const void *p);                       // device memory of th
 dg_status device_info(int *num_sms, int **err_word);      // the current device's, set up on first use
 int early_launch_mode();                                  // DG_OPT_EARLY_LAUNCH
 void count_launch();                                      // one kernel enqueued (dg_launch_count)
-// The logits' tiles of the linear cross entropy by the CTA-pair kernel: statistics (G null) or the
-// gradient of the logits into G.  DG_ERR_UNSUPPORTED, with nothing enqueued, when the operands or
-// the options do not allow it.  dry: only say whether they do.
-dg_status ce_pair(const dg_view *X, const dg_view *W, const dg_view *G, float alpha, const CeTile &ce, bool dry,
-                  cudaStream_t stream);
+// One launch of the CTA-pair kernel for the linear cross entropy: A B in 256 x 256 tiles, used as
+// `use` says.  C: G or the product (null for the statistics; for partial sums an FP32 [chunks *
+// plane_rows x N] view, plane_rows a multiple of 256).  DG_ERR_UNSUPPORTED, with nothing enqueued, when the
+// operands or the options do not allow it.  dry: only say whether they do.
+struct PairCall {
+    const dg_view *A, *B, *C;
+    float alpha;
+    const float *scale_a;
+    PairUse use;
+    CeTile ce;
+    int chunks;  // partial sums: planes asked for, and on return those written
+    bool dry;
+};
+dg_status pair_call(PairCall &c, cudaStream_t stream);
+// dg_gemm that leaves the GEMVs out: their K-contiguous kernel keeps x in shared memory per pair of
+// columns and is made for few columns.
+dg_status gemm_tiles(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta,
+                     const float *scale_a, cudaStream_t stream);
 
 }  // namespace dg

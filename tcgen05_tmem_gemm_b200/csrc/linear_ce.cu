@@ -206,6 +206,25 @@ __global__ void __launch_bounds__(256) ce_round_kernel(const float *acc, int64_t
     for (int d = threadIdx.x; d < D; d += 256) store_elem(row + axis_offset(out.col, d), out.dtype, acc[t * ld + d]);
 }
 
+// dX from the planes of partial sums (FP32, in plane order) and, with several
+// pieces of the vocabulary, the sum over the earlier ones: the running sum to
+// acc_out, or (acc_out null) alpha * norm[1] times the whole sum to dX.
+__global__ void __launch_bounds__(256)
+    ce_planes_kernel(const float *planes, int64_t ld, int used, int64_t plane_rows, const float *acc_in,
+                     float *acc_out, float alpha, const float *norm, const DevView out, int D) {
+    pdl_wait_then_release();
+    const int64_t t = blockIdx.x;
+    const float f = alpha * norm[1];
+    char *row = const_cast<char *>(out.ptr) + axis_offset(out.row, t);
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float v = acc_in ? acc_in[t * D + d] : 0.f;
+#pragma unroll 4
+        for (int c = 0; c < used; ++c) v += planes[(c * plane_rows + t) * ld + d];
+        if (acc_out) acc_out[t * D + d] = v;
+        else store_elem(row + axis_offset(out.col, d), out.dtype, f * v);
+    }
+}
+
 // ------------------------------------------------------------------- host side
 
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -264,8 +283,8 @@ dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
 
 // The workspace's parts, each 256-byte aligned, for pieces of `piece` columns.
 struct Layout {
-    int64_t xc = 0, part = 0, run = 0, ztarget = 0, z = 0, rows = 0, norm = 0, undo = 0, g = 0, acc = 0;
-    int64_t ldx = 0, ldz = 0, ldg = 0;
+    int64_t xc = 0, part = 0, run = 0, ztarget = 0, z = 0, rows = 0, norm = 0, undo = 0, g = 0, acc = 0, planes = 0;
+    int64_t ldx = 0, ldz = 0, ldg = 0, ldp = 0;
     int64_t total = 0;
 };
 
@@ -286,7 +305,7 @@ int64_t tile_slots(int64_t piece) { return (piece + kSlotCols - 1) / kSlotCols; 
 // Whether the CTA-pair kernel makes the logits: enough 256 x 256 tiles for
 // its pairs of SMs, operands it can read through TMA.
 bool tiles_worth_it(const Problem &p, int num_sms) {
-    return p.tensor && p.w.tma_ok && p.T > 128 && ((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms;
+    return p.tensor && p.w.tma_ok && ((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms;
 }
 
 // 16-byte rows of X for its copy.
@@ -319,7 +338,27 @@ Layout forward_layout(const Problem &p, int64_t piece, bool tiles) {
     return l;
 }
 
-Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int dx_dtype, bool tiles) {
+// dX = G W^T has few tiles and a long k (the vocabulary) when there are few
+// rows: the planes of partial sums that k is then split into, so that the
+// tiles times the planes fill the pairs of SMs in whole rounds (0: one product
+// without planes).  Up to four rows the GEMV over W's rows serves.
+int plane_count(const Problem &p, int num_sms) {
+    if (!p.tensor || p.T <= 4 || p.D < 32) return 0;
+    const int64_t pairs = num_sms / 2, tiles = ((p.T + 255) / 256) * ((p.D + 255) / 256);
+    if (tiles >= 2 * num_sms) return 0;
+    auto busy = [&](int64_t n) { return (double)(tiles * n) / (double)((tiles * n + pairs - 1) / pairs * pairs); };
+    int best = 0;
+    double most = busy(1) + 0.1;  // worth it from a tenth on: a plane costs its write and its read
+    for (int n = 2; n <= 16 && n * 1024 <= p.V; ++n)
+        if (busy(n) - 0.005 * n > most) {
+            most = busy(n) - 0.005 * n;
+            best = n;
+        }
+    return best;
+}
+
+Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int dx_dtype, bool tiles,
+                   int planes) {
     Layout l;
     l.ldx = align256(p.D * p.es);
     l.ldz = align256(piece * 4);
@@ -328,7 +367,9 @@ Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     l.rows = take(&l, p.T * (int64_t)sizeof(RowGrad));
     l.norm = take(&l, 256);
     l.undo = take(&l, p.es == 2 ? undo_count(p) * 4 : 0);
-    l.acc = take(&l, need_dx && piece < p.V && dx_dtype != DG_F32 ? p.T * p.D * 4 : 0);
+    l.acc = take(&l, need_dx && piece < p.V && (dx_dtype != DG_F32 || planes > 0) ? p.T * p.D * 4 : 0);
+    l.ldp = align256(p.D * 4);
+    l.planes = take(&l, planes * ((p.T + 255) / 256 * 256) * l.ldp);
     l.g = take(&l, p.T * l.ldg);
     l.z = take(&l, tiles ? 0 : p.T * l.ldz);
     return l;
@@ -370,6 +411,8 @@ DevView dev_of(const dg_view *v, const ViewInfo &vi) {
     d.dtype = v->dtype;
     return d;
 }
+
+dg_status pair_once(PairCall c, cudaStream_t s) { return pair_call(c, s); }
 
 // The largest piece whose layout fits `bytes` (0: not even the smallest).
 template <typename LayoutOf>
@@ -433,7 +476,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     if (tiles) {
         CeTile ce = tile_of(p, target, ignore_index, 0);
         ce.part = reinterpret_cast<float2 *>(ws);
-        tiles = ce_pair(&xv, W, nullptr, alpha, ce, true, s) == DG_OK;
+        tiles = pair_once(PairCall{&xv, W, nullptr, alpha, nullptr, kPairStats, ce, 0, true}, s) == DG_OK;
     }
     auto layout_of = [&](int64_t piece) { return forward_layout(p, piece, tiles); };
     const int64_t piece = fit_piece(p, workspace_bytes, forward_piece(p, tiles), layout_of);
@@ -456,10 +499,10 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
             CeTile ce = tile_of(p, target, ignore_index, v0);
             ce.part = part;
             ce.ztarget = ztarget;
-            DG_TRY(ce_pair(&xv, &wv, nullptr, alpha, ce, false, s));
+            DG_TRY(pair_once(PairCall{&xv, &wv, nullptr, alpha, nullptr, kPairStats, ce, 0, false}, s));
             slots = (int)tile_slots(cols);
         } else {
-            DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
+            DG_TRY(gemm_tiles(&xv, &wv, &zv, alpha, 0.f, nullptr, s));
             slots = (int)stat_slots(cols);
             DG_TRY(launched(launch_ex(ce_stats_kernel, dim3((unsigned)(p.T * slots)), dim3(256), 0, s, one, pdl,
                                       (const float *)z, l.ldz / 4, p.T, p.V, (int)v0, (int)cols, slots, target,
@@ -495,6 +538,19 @@ dg_status check_grad(const dg_view *X, const dg_view *W, const dg_view *dX, cons
     return DG_OK;
 }
 
+// dW's product, k = T: with few rows the stores of its large output take
+// longer than the products, and get twice the epilogue warps.
+dg_status product(const dg_view *A, const dg_view *B, const dg_view *C, const Problem &p, int num_sms, float alpha,
+                  const float *undo, cudaStream_t s) {
+    const int64_t tiles = ((A->shape[0] + 255) / 256) * ((B->shape[1] + 255) / 256);
+    if (p.tensor && alpha != 0.f && p.T <= 1024 && tiles * 2 >= num_sms) {
+        PairCall call{A, B, C, alpha, undo, kPairWide, {}, 0, false};
+        const dg_status st = pair_call(call, s);
+        if (st != DG_ERR_UNSUPPORTED) return st;
+    }
+    return gemm_tiles(A, B, C, alpha, 0.f, undo, s);
+}
+
 }  // namespace
 }  // namespace dg
 
@@ -506,9 +562,9 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W, const 
     Problem p;
     DG_TRY(check_grad(X, W, dX, dW, &p));
     const int dxt = dX ? dX->dtype : DG_F32;
-    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false).total;
+    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, 0).total;
     *best = std::max(*least, grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt,
-                                         tiles_worth_it(p, kUsualSms)).total);
+                                         tiles_worth_it(p, kUsualSms), dX ? plane_count(p, kUsualSms) : 0).total);
     return DG_OK;
 }
 
@@ -531,7 +587,7 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             return DG_ERR_ALIGN;
     }
     const int dxt = dX ? dX->dtype : DG_F32;
-    if (p.T > 0 && grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false).total > workspace_bytes)
+    if (p.T > 0 && grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, 0).total > workspace_bytes)
         return DG_ERR_SHAPE;
     DG_TRY(device_info(&num_sms, &err_word));
     if (p.T > 0 && ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
@@ -552,9 +608,12 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     const dg_view xv = copy ? view2(ws, p.T, p.D, ldx, p.es, X->dtype) : *X;
     const dg_view xt = view2(ws, p.D, p.T, p.es, ldx, X->dtype);
     bool tiles = tiles_worth_it(p, num_sms);
+    int planes = dX ? plane_count(p, num_sms) : 0;
+    const int64_t plane_rows = (p.T + 255) / 256 * 256;
     auto layout_of = [&](int64_t piece) {
-        return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt, tiles);
+        return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt, tiles, planes);
     };
+    if (layout_of(grad_piece(p)).total > workspace_bytes) planes = 0;  // a small workspace has room for G only
     int64_t piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
     if (tiles) {
         // the tensor stores of G take pieces of 64 columns or more, the last one too
@@ -563,7 +622,7 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             const Layout t = layout_of(piece);
             const dg_view gv = view2(ws + t.g, p.T, std::min(piece, p.V), t.ldg, p.es, X->dtype);
             const dg_view wv = view2(p.wm.ptr, p.D, std::min(piece, p.V), p.wm.rs, p.wm.cs, W->dtype);
-            tiles = ce_pair(&xv, &wv, &gv, alpha, tile_of(p, target, ignore_index, 0), true, s) == DG_OK;
+            tiles = pair_once(PairCall{&xv, &wv, &gv, alpha, nullptr, kPairGrad, {}, 0, true}, s) == DG_OK;
         }
         if (piece <= 0 || !tiles) {
             tiles = false;
@@ -571,6 +630,14 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         }
     }
     if (piece == 0) return DG_ERR_SHAPE;
+    if (planes > 0) {
+        const Layout t = layout_of(piece);
+        const int64_t cols = std::min(piece, p.V);
+        const dg_view gv = view2(ws + t.g, p.T, cols, t.ldg, p.es, X->dtype);
+        const dg_view wt = view2(p.wm.ptr, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
+        const dg_view pv = view2(ws + t.planes, planes * plane_rows, p.D, t.ldp, 4, DG_F32);
+        if (pair_once(PairCall{&gv, &wt, &pv, 1.f, nullptr, kPairPartial, {}, planes, true}, s) != DG_OK) planes = 0;
+    }
     const Layout l = layout_of(piece);
     RowGrad *rows = reinterpret_cast<RowGrad *>(ws + l.rows);
     float *norm = nullptr, *undo = nullptr;
@@ -589,7 +656,8 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     char *g = ws + l.g;
     float *z = reinterpret_cast<float *>(ws + l.z);
     const bool sum = dX && piece < p.V;                        // dX is summed over several pieces
-    const bool own_acc = sum && dxt != DG_F32;                 // in the workspace, rounded at the end
+    const bool own_acc = sum && planes == 0 && dxt != DG_F32;  // in the workspace, rounded at the end
+    float *acc = reinterpret_cast<float *>(ws + l.acc);
     const dg_view accv = own_acc ? view2(ws + l.acc, p.T, p.D, p.D * 4, 4, DG_F32) : (dX ? *dX : xv);
     for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
         const int64_t cols = std::min(piece, p.V - v0);
@@ -601,25 +669,38 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         if (tiles) {
             CeTile ce = tile_of(p, target, ignore_index, v0);
             ce.rows = rows;
-            DG_TRY(ce_pair(&xv, &wv, &gv, alpha, ce, false, s));
+            DG_TRY(pair_once(PairCall{&xv, &wv, &gv, alpha, nullptr, kPairGrad, ce, 0, false}, s));
         } else {
             const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
-            DG_TRY(dg_gemm(&xv, &wv, &zv, alpha, 0.f, nullptr, nullptr, stream));
+            DG_TRY(gemm_tiles(&xv, &wv, &zv, alpha, 0.f, nullptr, s));
             const int64_t blocks = p.T * ((cols + 1023) / 1024);
             DG_TRY(launched(launch_ex(ce_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, s, one, pdl,
                                       (const float *)z, l.ldz / 4, p.T, (int)v0, (int)cols, (const RowGrad *)rows, g,
                                       l.ldg, X->dtype)));
         }
-        if (dX) DG_TRY(dg_gemm(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, undo, nullptr, stream));
+        if (dX && planes > 0) {
+            const dg_view pv = view2(ws + l.planes, planes * plane_rows, p.D, l.ldp, 4, DG_F32);
+            PairCall call{&gv, &wt, &pv, 1.f, nullptr, kPairPartial, {}, planes, false};
+            DG_TRY(pair_call(call, s));
+            const int used = call.chunks;
+            const bool first = v0 == 0, last = v0 + cols == p.V;
+            DG_TRY(launched(launch_ex(ce_planes_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl,
+                                      reinterpret_cast<const float *>(ws + l.planes), l.ldp / 4, used, plane_rows,
+                                      first ? (const float *)nullptr : (const float *)acc,
+                                      last ? (float *)nullptr : acc, alpha, (const float *)norm, dev_of(dX, p.dx),
+                                      (int)p.D)));
+        } else if (dX) {
+            DG_TRY(gemm_tiles(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, undo, s));
+        }
         if (dW) {
             // the product in the order that gives dW's unit stride to the columns of the output
             char *op = p.dwm.ptr + v0 * p.dwm.cs;
             if (p.dw.unit_dim == 2) {
                 const dg_view ov = view2(op, cols, p.D, p.dwm.cs, p.dwm.rs, p.dwm.dtype);
-                DG_TRY(dg_gemm(&gt, &xv, &ov, alpha, 0.f, undo, nullptr, stream));
+                DG_TRY(product(&gt, &xv, &ov, p, num_sms, alpha, undo, s));
             } else {
                 const dg_view ov = view2(op, p.D, cols, p.dwm.rs, p.dwm.cs, p.dwm.dtype);
-                DG_TRY(dg_gemm(&xt, &gv, &ov, alpha, 0.f, undo, nullptr, stream));
+                DG_TRY(product(&xt, &gv, &ov, p, num_sms, alpha, undo, s));
             }
         }
     }

@@ -6,13 +6,13 @@
 
 namespace dg {
 
-size_t umma_pair_smem_bytes(int bn, int stages, bool epi_tma, int ksub) {
-    return pair_layout(bn, stages, epi_tma, ksub).total;
+size_t umma_pair_smem_bytes(int bn, int stages, bool epi_tma, int ksub, int epi_warps) {
+    return pair_layout(bn, stages, epi_tma, ksub, epi_warps).total;
 }
 
-int umma_pair_max_stages(int bn, bool epi_tma, int ksub) {
+int umma_pair_max_stages(int bn, bool epi_tma, int ksub, int epi_warps) {
     int s = 2;
-    while (s < 12 && pair_layout(bn, s + 1, epi_tma, ksub).total <= 227 * 1024) ++s;
+    while (s < 12 && pair_layout(bn, s + 1, epi_tma, ksub, epi_warps).total <= 227 * 1024) ++s;
     return s;
 }
 

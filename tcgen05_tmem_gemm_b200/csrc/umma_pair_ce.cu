@@ -1,5 +1,5 @@
-// Paired-CTA tensor-core kernel: the instances whose epilogue serves the
-// linear cross entropy (the kernel is in umma_pair_kernel.cuh).
+// Paired-CTA tensor-core kernel: the instances that serve the linear cross
+// entropy and its gradient (the kernel is in umma_pair_kernel.cuh).
 #include <atomic>
 
 #include "umma_pair_kernel.cuh"
@@ -19,20 +19,25 @@ cudaError_t run_pair(const UmmaParams &p, const CUtensorMap *tp, const CUtensorM
 }
 
 template <int KSUB>
-cudaError_t run_epi(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq, const CUtensorMap *tc,
-                    bool grad, int grid, size_t smem, cudaStream_t s) {
-    if (grad) return run_pair<KSUB, EPI_CE_GRAD>(p, tp, tq, tc, grid, smem, s);
-    if (p.k_chunk > 0 && p.k_chunk < p.kb_total) return run_pair<KSUB, EPI_CE_STATS_LONG>(p, tp, tq, tc, grid, smem, s);
-    return run_pair<KSUB, EPI_CE_STATS>(p, tp, tq, tc, grid, smem, s);
+cudaError_t run_use(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq, const CUtensorMap *tc,
+                    PairUse use, int grid, size_t smem, cudaStream_t s) {
+    switch (use) {
+    case kPairStats:
+        if (p.k_chunk < p.kb_total) return run_pair<KSUB, EPI_CE_STATS_LONG>(p, tp, tq, tc, grid, smem, s);
+        return run_pair<KSUB, EPI_CE_STATS>(p, tp, tq, tc, grid, smem, s);
+    case kPairGrad: return run_pair<KSUB, EPI_CE_GRAD>(p, tp, tq, tc, grid, smem, s);
+    case kPairWide: return run_pair<KSUB, EPI_STORE_WIDE>(p, tp, tq, tc, grid, smem, s);
+    default: return run_pair<KSUB, EPI_PARTIAL>(p, tp, tq, tc, grid, smem, s);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_umma_pair_ce(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
-                                const CUtensorMap *tc, bool grad, int grid, size_t smem, cudaStream_t s) {
-    if (p.bn != 256 || (grad && !p.epi_tma)) return cudaErrorInvalidValue;
-    if (p.ksub == 1) return run_epi<1>(p, tp, tq, tc, grad, grid, smem, s);
-    if (p.ksub == 2) return run_epi<2>(p, tp, tq, tc, grad, grid, smem, s);
+cudaError_t launch_umma_pair_use(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMap *tq,
+                                 const CUtensorMap *tc, PairUse use, int grid, size_t smem, cudaStream_t s) {
+    if (p.bn != 256 || p.k_chunk < 1 || (use == kPairStats) == (p.epi_tma != 0)) return cudaErrorInvalidValue;
+    if (p.ksub == 1) return run_use<1>(p, tp, tq, tc, use, grid, smem, s);
+    if (p.ksub == 2) return run_use<2>(p, tp, tq, tc, use, grid, smem, s);
     return cudaErrorInvalidValue;
 }
 

@@ -24,6 +24,8 @@
 // gradient of the logits and store that (EPI_CE_GRAD).
 #pragma once
 
+#include <climits>
+
 #include "common.cuh"
 #include "sm100.cuh"
 #include "umma_common.cuh"
@@ -48,7 +50,8 @@ struct PairLayout {
     uint32_t a_bytes, b_bytes, stage_bytes, epi_off, bar_off, aux_off, total;
 };
 
-__host__ __device__ inline PairLayout pair_layout(int bn, int stages, bool epi_tma, int ksub) {
+// epi_warps: those of the tensor-store epilogue, two staging blocks each.
+__host__ __device__ inline PairLayout pair_layout(int bn, int stages, bool epi_tma, int ksub, int epi_warps = 4) {
     PairLayout L;
     L.a_sub = kHalfM * kRowBytes;
     L.b_sub = (uint32_t)(bn / 2) * kRowBytes;
@@ -56,7 +59,7 @@ __host__ __device__ inline PairLayout pair_layout(int bn, int stages, bool epi_t
     L.b_bytes = (uint32_t)ksub * L.b_sub;
     L.stage_bytes = L.a_bytes + L.b_bytes;  // a multiple of 1024: bn is a multiple of 16
     L.epi_off = L.stage_bytes * stages;
-    L.bar_off = L.epi_off + (epi_tma ? kEpiStoreBytes : 0u);
+    L.bar_off = L.epi_off + (epi_tma ? (uint32_t)epi_warps * 2u * kEpiBlockBytes : 0u);
     // full[S], empty[S], tfull[2], tempty[2], drain
     L.aux_off = L.bar_off + 8 * (2 * stages + 5);
     L.total = L.aux_off + 16 + 1024;
@@ -95,7 +98,7 @@ struct PairWork {
     int ti, j0, w;   // tile row, first column, columns
     int kb0, kb1;    // k blocks [kb0, kb1)
     int role;
-    int sk_first;    // kSkOwner: the tile's first k block in the Stream-K run
+    int sk_first;    // kSkOwner: the tile's first k block in the Stream-K run; kWhole: the chunk of k
 };
 
 // Pair c's share [lo, hi) of the Stream-K run of `total` k blocks.
@@ -111,28 +114,35 @@ __device__ __forceinline__ void sk_range(int64_t total, int c, int P, int64_t &l
 // c, c + P, ... below dp_tiles.  A tile's owner holds its last k blocks and
 // so has the highest pair index of the tile: owners wait only on pairs with
 // lower indices, which are launched no later than they are.
-// CHUNKED: every tile is a run of units of p.k_chunk k blocks each (the last
+// K_CHUNKS: every tile is a run of units of p.k_chunk k blocks each (the last
 // one shorter), whose accumulators the epilogue adds up in registers.
-template <bool CHUNKED>
+// K_SPLIT: the chunks are units of their own, spread over the pairs.
+enum : int { K_WHOLE = 0, K_CHUNKS = 1, K_SPLIT = 2 };
+template <int KMODE>
 __device__ __forceinline__ bool pair_work(const UmmaParams &p, int c, int P, int idx, PairWork &w) {
     const int KB = p.kb_total;
-    if (CHUNKED || p.sk_tiles == 0) {
+    if (KMODE != K_WHOLE || p.sk_tiles == 0) {
         int tile = idx, chunk = 0;
-        if (CHUNKED) {
+        if (KMODE == K_CHUNKS) {
             const int chunks = (KB + p.k_chunk - 1) / p.k_chunk;
             tile = idx / chunks;
             chunk = idx - tile * chunks;
         }
-        const int u = c + tile * P;
+        int u = c + tile * P;
         if (u >= p.num_units) return false;
+        if (KMODE == K_SPLIT) {
+            const int tiles = p.tiles_i * p.tiles_j;
+            chunk = u / tiles;
+            u -= chunk * tiles;
+        }
         const PairUnit pu = pair_unit(u, p);
         w.ti = pu.ti;
         w.j0 = pu.j0;
         w.w = pu.w;
-        w.kb0 = CHUNKED ? chunk * p.k_chunk : 0;
-        w.kb1 = CHUNKED ? min(KB, w.kb0 + p.k_chunk) : KB;
+        w.kb0 = KMODE != K_WHOLE ? chunk * p.k_chunk : 0;
+        w.kb1 = KMODE != K_WHOLE ? min(KB, w.kb0 + p.k_chunk) : KB;
         w.role = kWhole;
-        w.sk_first = 0;
+        w.sk_first = chunk;
         return true;
     }
     int64_t lo, hi;
@@ -198,10 +208,22 @@ __device__ __forceinline__ float *sk_slot(const UmmaParams &p, int q, uint32_t r
 // What the epilogue does with a tile.  EPI_CE_STATS_LONG: EPI_CE_STATS over a
 // long k, summed in chunks (see ce_stats_rows_long).  The cross entropy's
 // epilogues compute an exponential per element and have eight warps, two per
-// quarter of the TMEM lanes.
-enum : int { EPI_STORE = 0, EPI_CE_STATS = 1, EPI_CE_STATS_LONG = 2, EPI_CE_GRAD = 3 };
+// quarter of the TMEM lanes.  EPI_STORE_WIDE: EPI_STORE with eight warps, for a
+// k so short that the stores take longer than the products.  EPI_PARTIAL: each
+// chunk of k stores its FP32 sums to a plane of its own (p.plane_rows rows of
+// C's map further), for few tiles and a long k.
+enum : int {
+    EPI_STORE = 0,
+    EPI_CE_STATS = 1,
+    EPI_CE_STATS_LONG = 2,
+    EPI_CE_GRAD = 3,
+    EPI_STORE_WIDE = 4,
+    EPI_PARTIAL = 5
+};
 
-__host__ __device__ constexpr int pair_epi_warps(int epi) { return epi == EPI_STORE ? 4 : 8; }
+__host__ __device__ constexpr int pair_epi_warps(int epi) {
+    return epi == EPI_STORE || epi == EPI_PARTIAL ? 4 : 8;
+}
 __host__ __device__ constexpr int pair_threads(int epi) { return 64 + 32 * pair_epi_warps(epi); }
 
 template <bool FP8, int KSUB, int EPI>
@@ -217,7 +239,8 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
     if (p.pdl == 1) pdl_release();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const PairLayout L = pair_layout(p.bn, p.stages, p.epi_tma != 0, KSUB);
+    const PairLayout L = pair_layout(p.bn, p.stages, p.epi_tma != 0, KSUB,
+                                     EPI == EPI_STORE_WIDE ? 8 : 4);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + L.bar_off;
     const uint32_t bar_empty = bar_full + 8 * p.stages;
@@ -227,7 +250,7 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L.aux_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.aux_off + 4);
 
-    constexpr bool CHUNKED = EPI == EPI_CE_STATS_LONG;
+    constexpr int KMODE = EPI == EPI_CE_STATS_LONG ? K_CHUNKS : EPI == EPI_PARTIAL ? K_SPLIT : K_WHOLE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
             int it = 0, s = 0;
             uint32_t ph = 0;
             PairWork pw;
-            for (int idx = 0; !*abort_flag && pair_work<CHUNKED>(p, cluster_id, nclusters, idx, pw); ++idx) {
+            for (int idx = 0; !*abort_flag && pair_work<KMODE>(p, cluster_id, nclusters, idx, pw); ++idx) {
                 const int i0 = pw.ti * 2 * kHalfM + (int)rank * kHalfM;
                 const int cw = pw.w / 2;  // this CTA's columns of the unit
                 const int j0 = pw.j0 + (int)rank * cw;
@@ -367,7 +390,7 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
             uint32_t ph = 0;
             bool ok = true;
             PairWork pw;
-            for (int idx = 0; ok && pair_work<CHUNKED>(p, cluster_id, nclusters, idx, pw); ++idx, ++local) {
+            for (int idx = 0; ok && pair_work<KMODE>(p, cluster_id, nclusters, idx, pw); ++idx, ++local) {
                 const uint32_t idesc = pw.w == bn ? idesc_full : idesc_half;
                 const int b = local & 1;
                 const uint32_t tph = (uint32_t)(local >> 1) & 1u;
@@ -415,7 +438,7 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
         int local = 0;
         uint32_t nblk = 0;  // tensor-store blocks this warp has issued
         PairWork pw;
-        for (int idx = 0; pair_work<CHUNKED>(p, cluster_id, nclusters, idx, pw); ++idx, ++local) {
+        for (int idx = 0; pair_work<KMODE>(p, cluster_id, nclusters, idx, pw); ++idx, ++local) {
             const int b = local & 1;
             const uint32_t tph = (uint32_t)(local >> 1) & 1u;
             if (!mbar_wait(bar_tfull + 8 * b, tph, wc)) break;
@@ -430,9 +453,25 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
                 else if (EPI == EPI_CE_STATS_LONG)
                     ce_stats_rows_long(sums, p.ce, e.alpha, t_row + c0, i, p.Mi, j0 + c0, p.Nj, pw.kb0 == 0,
                                        pw.kb1 == p.kb_total);
-                else
+                else if (EPI == EPI_CE_GRAD)
                     ce_grad_rows_tma(p.ce, e, &tmap_c, sbase + L.epi_off + (uint32_t)(warp - 2) * kEpiBlockBytes,
                                      t_row, i - lane, p.Mi, j0, pw.w, p.Nj, lane, 64 * half);
+                else {
+                    const uint32_t blocks = sbase + L.epi_off + (uint32_t)(warp - 2) * 2u * kEpiBlockBytes;
+                    __syncwarp();
+                    if (EPI == EPI_PARTIAL) {
+                        const int plane = pw.sk_first * p.plane_rows;
+                        if (i - lane < p.Mi)  // rows of the plane past Mi are written with zeros, and not read
+                            epilogue_rows_tma<4>(e, &tmap_c, blocks, t_row, plane + i - lane, INT_MAX, j0, pw.w, p.Nj,
+                                                 lane, nblk);
+                    } else if (e.c_dtype == DG_F32) {
+                        epilogue_rows_tma<4>(e, &tmap_c, blocks, t_row, i - lane, p.Mi, j0, pw.w, p.Nj, lane, nblk,
+                                             half, 2);
+                    } else {
+                        epilogue_rows_tma<2>(e, &tmap_c, blocks, t_row, i - lane, p.Mi, j0, pw.w, p.Nj, lane, nblk,
+                                             half, 2);
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(dsmem_map(bar_tempty + 8 * b, 0));
