@@ -214,15 +214,15 @@ __global__ void __launch_bounds__(256)
                      float *acc_out, float alpha, const float *norm, const DevView out, int D) {
     pdl_wait_then_release();
     const int64_t t = blockIdx.x;
-    const float f = alpha * norm[1];
-    char *row = const_cast<char *>(out.ptr) + axis_offset(out.row, t);
-    for (int d = threadIdx.x; d < D; d += 256) {
-        float v = acc_in ? acc_in[t * D + d] : 0.f;
-#pragma unroll 4
-        for (int c = 0; c < used; ++c) v += planes[(c * plane_rows + t) * ld + d];
-        if (acc_out) acc_out[t * D + d] = v;
-        else store_elem(row + axis_offset(out.col, d), out.dtype, f * v);
-    }
+    const int d = blockIdx.y * 256 + threadIdx.x;
+    if (d >= D) return;
+    float v = acc_in ? acc_in[t * D + d] : 0.f;
+#pragma unroll 8
+    for (int c = 0; c < used; ++c) v += planes[(c * plane_rows + t) * ld + d];
+    if (acc_out) acc_out[t * D + d] = v;
+    else
+        store_elem(const_cast<char *>(out.ptr) + axis_offset(out.row, t) + axis_offset(out.col, d), out.dtype,
+                   alpha * norm[1] * v);
 }
 
 // ------------------------------------------------------------------- host side
@@ -543,7 +543,7 @@ dg_status check_grad(const dg_view *X, const dg_view *W, const dg_view *dX, cons
 dg_status product(const dg_view *A, const dg_view *B, const dg_view *C, const Problem &p, int num_sms, float alpha,
                   const float *undo, cudaStream_t s) {
     const int64_t tiles = ((A->shape[0] + 255) / 256) * ((B->shape[1] + 255) / 256);
-    if (p.tensor && alpha != 0.f && p.T <= 1024 && tiles * 2 >= num_sms) {
+    if (p.tensor && alpha != 0.f && p.T <= 256 && tiles * 2 >= num_sms) {
         PairCall call{A, B, C, alpha, undo, kPairWide, {}, 0, false};
         const dg_status st = pair_call(call, s);
         if (st != DG_ERR_UNSUPPORTED) return st;
@@ -684,7 +684,7 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             DG_TRY(pair_call(call, s));
             const int used = call.chunks;
             const bool first = v0 == 0, last = v0 + cols == p.V;
-            DG_TRY(launched(launch_ex(ce_planes_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl,
+            DG_TRY(launched(launch_ex(ce_planes_kernel, dim3((unsigned)p.T, (unsigned)((p.D + 255) / 256)), dim3(256), 0, s, one, pdl,
                                       reinterpret_cast<const float *>(ws + l.planes), l.ldp / 4, used, plane_rows,
                                       first ? (const float *)nullptr : (const float *)acc,
                                       last ? (float *)nullptr : acc, alpha, (const float *)norm, dev_of(dX, p.dx),
