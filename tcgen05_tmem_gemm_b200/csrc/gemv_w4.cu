@@ -35,6 +35,7 @@
 // in distributed shared memory, in a fixed order.
 #include <algorithm>
 #include <cstdlib>
+#include <cstdio>
 
 #include "common.cuh"
 #include "sm100.cuh"
@@ -115,54 +116,30 @@ struct Pair<__half> {
     }
 };
 
-// The four words a lane multiplies in one step.  Word c of lane t (t = lane %
-// 4) holds k = 32 t + 8 c (kLaneMajor: a lane's 16 bytes as loaded) or
-// k = 32 c + 8 t (kWordMajor: word c of all four lanes lies in one run of 32
-// k, so groups of 32 can be scaled one by one).
-enum Order { kLaneMajor, kWordMajor };
-
-__device__ __forceinline__ int order_k(Order o, int c, int t) { return o == kLaneMajor ? 32 * t + 8 * c : 32 * c + 8 * t; }
-
-// Lane-major to word-major: a 4 x 4 transpose among the four lanes of a quad.
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
-#pragma unroll
-    for (int step = 1; step <= 2; ++step) {
-        const bool hi = t & step;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int a = step == 1 ? 2 * p : p, b = a + step;  // the pair of words that trade places
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? w[a] : w[b], step);
-            if (hi) w[a] = got;
-            else w[b] = got;
-        }
-    }
-}
-
-// Copies one step's 16 bytes of one column into this lane's slot, zeros past
-// the column's `nbytes`.  VEC: the alignment of every column's codes.
-template <int VEC, Order O>
-__device__ __forceinline__ void copy_codes(uint32_t slot, const uint8_t *row, int k0, int t, int nbytes) {
-    if (VEC == 16) {  // the lane's 16 bytes; a word-major kernel transposes them after the read
-        const int b = k0 / 2 + 16 * t, n = min(max(nbytes - b, 0), 16);
+// Copies the lane's 16 bytes of one column from byte b into its slot, zeros
+// past the column's `nbytes`.  VEC: the alignment of every column's codes.
+template <int VEC>
+__device__ __forceinline__ void copy_codes(uint32_t slot, const uint8_t *row, int b, int nbytes) {
+    if (VEC == 16) {
+        const int n = min(max(nbytes - b, 0), 16);
         asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(slot), "l"(row + (n > 0 ? b : 0)),
                      "r"(n)
                      : "memory");
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int b = (k0 + order_k(O, c, t)) / 2;
-            if (VEC == 4) {
-                const int n = min(max(nbytes - b, 0), 4);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + 4 * c),
-                             "l"(row + (n > 0 ? b : 0)), "r"(n)
-                             : "memory");
-            } else {
-                uint32_t w = 0;
+    for (int c = 0; c < 4; ++c, b += 4) {
+        if (VEC == 4) {
+            const int n = min(max(nbytes - b, 0), 4);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + 4 * c),
+                         "l"(row + (n > 0 ? b : 0)), "r"(n)
+                         : "memory");
+        } else {
+            uint32_t w = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (b + i < nbytes) w |= (uint32_t)__ldg(row + b + i) << (8 * i);
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + 4 * c), "r"(w) : "memory");
-            }
+            for (int i = 0; i < 4; ++i)
+                if (b + i < nbytes) w |= (uint32_t)__ldg(row + b + i) << (8 * i);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + 4 * c), "r"(w) : "memory");
         }
     }
 }
@@ -182,18 +159,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
-}
-
-// One word's eight codes of two columns (g and g + 8 of the M side) times x:
-// d = c + two tensor instructions.
-template <typename T>
-__device__ __forceinline__ void word_mma(float (&d)[4], const float (&c)[4], uint32_t w0, uint32_t w1,
-                                         typename Pair<T>::Zero z0, typename Pair<T>::Zero z1, const uint4 &x) {
-    uint32_t a[4], b[4];
-    Pair<T>::unpack(a, w0, z0);
-    Pair<T>::unpack(b, w1, z1);
-    Pair<T>::mma(d, a[0], b[0], a[1], b[1], x.x, x.y, c);
-    Pair<T>::mma(d, a[2], b[2], a[3], b[3], x.z, x.w, d);
 }
 
 // Eight 16-bit x, h = k .. k+7, as the four pairs (k+j, k+j+4).
@@ -230,12 +195,20 @@ __device__ __forceinline__ float scale_value(uint32_t bits, int dtype) {
     return __half2float(__ushort_as_half((unsigned short)bits));
 }
 
-// The scales and zero points of this lane's two columns for one batch of
-// steps, as loaded.  !FINE: lane t of a quad holds those of the t-th step;
-// FINE: of every step's t-th run of 32 k.  The quad shares them by shuffles.
-template <bool FINE>
+// How the runs of 32 k that the four lanes of a quad hold in one step share
+// scales: SETS = 1, all four (groups that are multiples of 128); 2, lanes 0-1
+// and 2-3 (multiples of 64); 4, each has its own.  A tensor instruction sums
+// over the quad, so with several sets the sums are kept apart through x: a
+// column of the N side whose x is zero in the other sets' lanes sums one set
+// only.  PACKED: the columns hold 8 / SETS rows of x for every set at once;
+// else one pass of instructions per set, over the same unpacked codes.
+//
+// Scales and zero points of this lane's two columns for one batch of steps, as
+// loaded: SETS = 1, lane t holds those of the t-th step and the quad shares
+// them by shuffles; else those of its own set in every step.
+template <int SETS>
 struct Scales {
-    static constexpr int kN = FINE ? kBatch : 1;
+    static constexpr int kN = SETS == 1 ? 1 : kBatch;
     uint32_t s0[kN], s1[kN], z0[kN], z1[kN];
 };
 
@@ -258,11 +231,10 @@ __host__ __device__ inline W4Layout w4_layout(int R, int tiles, int kw, int step
     return L;
 }
 
-// FINE: groups that are not whole multiples of 128 (word-major, one scale per
-// 32 k), else one scale per step.
-template <typename T, int VEC, bool FINE>
+template <typename T, int VEC, int SETS, bool PACKED>
 __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__ GemvW4Params p) {
-    constexpr Order O = (FINE || VEC != 16) ? kWordMajor : kLaneMajor;
+    constexpr int kRows = PACKED ? 8 / SETS : 8;    // rows of x per set of columns
+    constexpr int kPasses = PACKED ? 1 : SETS;
     pdl_wait();
     extern __shared__ __align__(128) uint8_t smem[];
     const W4Layout L = w4_layout(p.R, p.tiles, p.kw, p.steps);
@@ -280,13 +252,14 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     const char *srow0 = p.scales + c0 * p.scale_stride, *srow1 = p.scales + c1 * p.scale_stride;
     const uint8_t *zrow0 = p.zeros + c0 * p.zero_stride, *zrow1 = p.zeros + c1 * p.zero_stride;
     auto fetch = [&](int kb, int left) {
-        Scales<FINE> q;
+        Scales<SETS> q;
 #pragma unroll
-        for (int u = 0; u < Scales<FINE>::kN; ++u) {
-            const int k = FINE ? (kb + u) * kBlockK + 32 * t : (kb + t) * kBlockK;
+        for (int u = 0; u < Scales<SETS>::kN; ++u) {
+            // (with two sets the first of the set's two runs, which may be the only one before K)
+            const int k = SETS == 1 ? (kb + t) * kBlockK : (kb + u) * kBlockK + 128 / SETS * (t * SETS / 4);
             q.s0[u] = q.s1[u] = 0u;
             q.z0[u] = q.z1[u] = 8u;
-            if ((FINE ? u : t) < left && k < p.K) {  // a run past the end has the scale 0 and the sum 0
+            if ((SETS == 1 ? t : u) < left && k < p.K) {  // a run past the end has the scale 0 and the sum 0
                 const int grp = p.group_shift >= 0 ? k >> p.group_shift : k / p.group;
                 q.s0[u] = scale_bits(srow0, grp, p.scale_dtype);
                 q.s1[u] = scale_bits(srow1, grp, p.scale_dtype);
@@ -315,8 +288,8 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
         } else {
 #pragma unroll 1
             for (int u = 0; u < n; ++u) {
-                copy_codes<VEC, O>(half + u * kStageBytes, row0, (next_kb + u) * kBlockK, t, nbytes);
-                copy_codes<VEC, O>(half + u * kStageBytes + 512, row1, (next_kb + u) * kBlockK, t, nbytes);
+                copy_codes<VEC>(half + u * kStageBytes, row0, (next_kb + u) * (kBlockK / 2) + 16 * t, nbytes);
+                copy_codes<VEC>(half + u * kStageBytes + 512, row1, (next_kb + u) * (kBlockK / 2) + 16 * t, nbytes);
             }
         }
         copy_commit();
@@ -336,14 +309,15 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     for (int kb_round = blockIdx.y * per_round; kb_round < blocks_k; kb_round += stride) {
         const int kb0 = kb_round + kw * p.steps;
         const int nst = min(p.steps, blocks_k - kb0);  // may be negative: nothing for this warp
-        Scales<FINE> ahead = fetch(kb0, nst);
+        Scales<SETS> ahead = fetch(kb0, nst);
         if (kb_round != (int)blockIdx.y * per_round) __syncthreads();  // the previous round's x is read
         // x of this round, in the order the words meet it
         {
             const int chunks = min(per_round, blocks_k - kb_round) * 16;
             for (int r = 0; r < p.R; ++r)
                 for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
-                    const int k = (kb_round + (i >> 4)) * kBlockK + order_k(O, (i >> 2) & 3, i & 3);
+                    // position [step][word c][lane t] holds k = 32 t + 8 c ..
+                    const int k = (kb_round + (i >> 4)) * kBlockK + 32 * (i & 3) + 8 * ((i >> 2) & 3);
                     uint4 h;
                     if (p.x_vec16 && k + 8 <= p.K)
                         h = *reinterpret_cast<const uint4 *>(p.x.ptr + r * p.x_ld + (int64_t)k * 2);
@@ -353,53 +327,63 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
                 }
         }
         __syncthreads();
-        // rows of the tensor instruction's N side past R read zeros
-        uint32_t xs = smem_u32(smem) + t * 16 + (g < p.R ? g * L.pitch + kw * p.steps * 256 : L.zero);
-        const uint32_t xstep = g < p.R ? 256 : 0;
-        for (int st = 0; st < p.steps; st += kBatch) {
-            const Scales<FINE> q = ahead;
-            if (st + kBatch < nst) ahead = fetch(kb0 + st + kBatch, nst - st - kBatch);
-            float s0[Scales<FINE>::kN], s1[Scales<FINE>::kN];
-            typename Pair<T>::Zero own0[Scales<FINE>::kN], own1[Scales<FINE>::kN];
+        // this lane's x, column g of the N side; zeros where the column has no row or, with several
+        // sets, not this lane's
+        const uint32_t xrow = smem_u32(smem) + t * 16 + (g % kRows) * L.pitch + kw * p.steps * 256;
+        const uint32_t xzero = smem_u32(smem) + t * 16 + L.zero;
+        uint32_t xs[kPasses], xstep[kPasses];
 #pragma unroll
-            for (int u = 0; u < Scales<FINE>::kN; ++u) {
-                s0[u] = scale_value(q.s0[u], p.scale_dtype);
-                s1[u] = scale_value(q.s1[u], p.scale_dtype);
-                own0[u] = Pair<T>::zero(q.z0[u] & 15u);
-                own1[u] = Pair<T>::zero(q.z1[u] & 15u);
-            }
+        for (int i = 0; i < kPasses; ++i) {
+            const bool mine = g % kRows < p.R && (SETS == 1 || t * SETS / 4 == (PACKED ? g / kRows : i));
+            xs[i] = mine ? xrow : xzero;
+            xstep[i] = mine ? 256 : 0;
+        }
+        for (int st = 0; st < p.steps; st += kBatch) {
+            const Scales<SETS> q = ahead;
+            if (st + kBatch < nst) ahead = fetch(kb0 + st + kBatch, nst - st - kBatch);
             copy_wait<1>();
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u, xs += xstep) {
+            for (int u = 0; u < kBatch; ++u) {
                 if (st + u >= nst) break;
                 const uint4 v0 = ld_shared_v4(ring + half + u * kStageBytes);
                 const uint4 v1 = ld_shared_v4(ring + half + u * kStageBytes + 512);
-                uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-                if (O == kWordMajor && VEC == 16) {
-                    quad_transpose(w0, t);
-                    quad_transpose(w1, t);
+                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                const int at = SETS == 1 ? 0 : u;
+                typename Pair<T>::Zero z0 = Pair<T>::zero(q.z0[at] & 15u), z1 = Pair<T>::zero(q.z1[at] & 15u);
+                float s0 = scale_value(q.s0[at], p.scale_dtype), s1 = scale_value(q.s1[at], p.scale_dtype);
+                if (SETS == 1) {  // lane u of the quad has this step's
+                    z0 = z0.from((lane & ~3) | u);
+                    z1 = z1.from((lane & ~3) | u);
+                    s0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) | u);
+                    s1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) | u);
                 }
                 const float none[4] = {0.f, 0.f, 0.f, 0.f};
-                float d[4];
-                typename Pair<T>::Zero z0, z1;
+                float d[kPasses][4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int at = FINE ? u : 0, src = (lane & ~3) | (FINE ? c : u);  // who holds this run's scale
-                    if (FINE || c == 0) {
-                        z0 = own0[at].from(src);
-                        z1 = own1[at].from(src);
+                    uint32_t a[4], b[4];
+                    Pair<T>::unpack(a, w0[c], z0);
+                    Pair<T>::unpack(b, w1[c], z1);
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i) {
+                        const uint4 x = ld_shared_v4(xs[i] + c * 64);
+                        if (c == 0) Pair<T>::mma(d[i], a[0], b[0], a[1], b[1], x.x, x.y, none);
+                        else Pair<T>::mma(d[i], a[0], b[0], a[1], b[1], x.x, x.y, d[i]);
+                        Pair<T>::mma(d[i], a[2], b[2], a[3], b[3], x.z, x.w, d[i]);
                     }
-                    const uint4 x = ld_shared_v4(xs + c * 64);
-                    if (FINE || c == 0) word_mma<T>(d, none, w0[c], w1[c], z0, z1, x);
-                    else word_mma<T>(d, d, w0[c], w1[c], z0, z1, x);
-                    if (FINE || c == 3) {
-                        const float a0 = __shfl_sync(0xffffffffu, s0[at], src);
-                        const float a1 = __shfl_sync(0xffffffffu, s1[at], src);
-                        acc[0] = fmaf(a0, d[0], acc[0]);
-                        acc[1] = fmaf(a0, d[1], acc[1]);
-                        acc[2] = fmaf(a1, d[2], acc[2]);
-                        acc[3] = fmaf(a1, d[3], acc[3]);
+                }
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    float f0 = s0, f1 = s1;
+                    if (kPasses > 1) {  // the lane of this set
+                        f0 = __shfl_sync(0xffffffffu, s0, (lane & ~3) | (4 / SETS * i));
+                        f1 = __shfl_sync(0xffffffffu, s1, (lane & ~3) | (4 / SETS * i));
                     }
+                    acc[0] = fmaf(f0, d[i][0], acc[0]);
+                    acc[1] = fmaf(f0, d[i][1], acc[1]);
+                    acc[2] = fmaf(f1, d[i][2], acc[2]);
+                    acc[3] = fmaf(f1, d[i][3], acc[3]);
+                    xs[i] += xstep[i];
                 }
             }
             copy_batch(ring + half);
@@ -409,7 +393,7 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     copy_wait<0>();
     pdl_release();
 
-    // The warps' sums: [tile][warp along k][row r of x][16 columns], in the ring's place.
+    // The warps' sums: [tile][warp along k][column of the N side][16 columns of W], in the ring's place.
     __syncthreads();
     float *red = reinterpret_cast<float *>(smem + L.red), *part = reinterpret_cast<float *>(smem + L.part);
 #pragma unroll
@@ -429,7 +413,10 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     for (int e = threadIdx.x; e < p.tiles * 128; e += blockDim.x) {
         if (((e >> 4) & 7) >= p.R) continue;
         float sum = 0.f;
-        for (int i = 0; i < p.kw; ++i) sum += red[((e >> 7) * p.kw + i) * 128 + (e & 127)];
+        for (int i = 0; i < p.kw; ++i)
+#pragma unroll
+            for (int q = 0; q < (PACKED ? SETS : 1); ++q)  // a row's columns of the N side, one per set
+                sum += red[((e >> 7) * p.kw + i) * 128 + (e & 127) + q * kRows * 16];
         if (single) store(e, sum);
         else part[e] = sum;
     }
@@ -447,10 +434,10 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     cluster_sync();  // keep every block's sums alive until all remote reads are done
 }
 
-template <typename T, int VEC, bool FINE>
+template <typename T, int VEC, int SETS, bool PACKED>
 cudaError_t run(const GemvW4Params &p, int split, cudaStream_t s) {
     static SmemLimit limit;
-    auto kern = gemv_w4_kernel<T, VEC, FINE>;
+    auto kern = gemv_w4_kernel<T, VEC, SETS, PACKED>;
     const size_t smem = w4_layout(p.R, p.tiles, p.kw, p.steps).total;
     const cudaError_t e = limit.ensure(kern, smem, true);
     if (e != cudaSuccess) return e;
@@ -458,12 +445,18 @@ cudaError_t run(const GemvW4Params &p, int split, cudaStream_t s) {
                      dim3(1, split, 1), p.pdl, p);
 }
 
+template <typename T, int VEC>
+cudaError_t run_sets(const GemvW4Params &p, int split, cudaStream_t s) {
+    if (p.group % 128 == 0) return run<T, VEC, 1, false>(p, split, s);
+    if (p.group % 64 == 0) return p.R <= 4 ? run<T, VEC, 2, true>(p, split, s) : run<T, VEC, 2, false>(p, split, s);
+    return p.R <= 2 ? run<T, VEC, 4, true>(p, split, s) : run<T, VEC, 4, false>(p, split, s);
+}
+
 template <typename T>
 cudaError_t run_vec(const GemvW4Params &p, int vec, int split, cudaStream_t s) {
-    const bool fine = p.group % kBlockK != 0;
-    if (vec == 16) return fine ? run<T, 16, true>(p, split, s) : run<T, 16, false>(p, split, s);
-    if (vec == 4) return fine ? run<T, 4, true>(p, split, s) : run<T, 4, false>(p, split, s);
-    return fine ? run<T, 1, true>(p, split, s) : run<T, 1, false>(p, split, s);
+    if (vec == 16) return run_sets<T, 16>(p, split, s);
+    if (vec == 4) return run_sets<T, 4>(p, split, s);
+    return run_sets<T, 1>(p, split, s);
 }
 
 }  // namespace
@@ -473,21 +466,47 @@ cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const int vec = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
     const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
     const int64_t col_tiles = (p.N + 15) / 16;
-    // A warp costs some hundred instructions besides its steps, so k is shared by no more warps than
-    // it takes to give every SM about twelve: first within the block, or, with several rows of x,
-    // first across the cluster, whose blocks then stage a smaller slice of x each.
-    int ways = 1;
-    static const int WT = getenv("WT") ? atoi(getenv("WT")) : 12;
-    static const int WB = getenv("WB") ? atoi(getenv("WB")) : 8;
-    while (ways < 64 && col_tiles * ways < (int64_t)num_sms * WT && ways * 2 <= blocks_k) ways *= 2;
-    const int first = std::min(ways, 8), second = ways / first;
-    const int split = p.R > 2 ? first : second;
-    p.kw = p.R > 2 ? second : first;
-    p.tiles = std::max(1, WB / p.kw);
-    const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * p.kw));  // steps whose x fits 48 KB
-    const int per_warp = (blocks_k + p.kw * split - 1) / (p.kw * split);
-    const int rounds = (per_warp + most - 1) / most;
-    p.steps = (per_warp + rounds - 1) / rounds;
+    // How k is shared: kw warps of a block and `split` blocks of a cluster, over blocks of `tiles` column
+    // tiles.  The cheapest by a model of one SM's time: rounds of resident blocks x (a block's warps x
+    // (steps + fixed work of a warp) at the issue rate that this many warps reach + staging x).
+    const int sets = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
+    const int step_cost = 150 + (p.R * sets > 8 ? 16 * sets : 0);
+    double least = 0;
+    int split = 1;
+    for (int kw = 1; kw <= 8; kw *= 2)
+        for (int tiles = 1; tiles * kw <= 8; tiles *= 2)
+            for (int sp = 1; sp <= 8; ++sp) {
+                if ((kw > 1 || sp > 1) && kw * sp > blocks_k) continue;
+                const int per_warp = (blocks_k + kw * sp - 1) / (kw * sp);
+                const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * kw));  // steps whose x fits 48 KB
+                const int rounds = (per_warp + most - 1) / most, steps = (per_warp + rounds - 1) / rounds;
+                const int64_t blocks = (col_tiles + tiles - 1) / tiles * sp;
+                const int64_t smem = w4_layout(p.R, tiles, kw, steps).total + 1024;
+                const int resident = (int)std::min<int64_t>(std::min<int64_t>(24 / (kw * tiles), 228 * 1024 / smem),
+                                                            (blocks + num_sms - 1) / num_sms);
+                const int64_t waves = (blocks + (int64_t)resident * num_sms - 1) / ((int64_t)resident * num_sms);
+                const double warps = resident * kw * tiles / 4.0;  // per scheduler
+                const double rate = std::min(0.8, 0.16 * warps);
+                const double x_cost = 40.0 * rounds * ((double)p.R * kw * steps * 16 / (32 * kw * tiles) + 8);
+                const double t = waves * (warps * (rounds * steps * step_cost + 500 + x_cost) / rate) + (sp > 1 ? 1500 : 0);
+                if (least == 0 || t < least) {
+                    least = t;
+                    p.kw = kw;
+                    p.tiles = tiles;
+                    p.steps = steps;
+                    split = sp;
+                }
+            }
+    if (getenv("W4")) {
+        int kw, tl, sp;
+        sscanf(getenv("W4"), "%d,%d,%d", &kw, &tl, &sp);
+        p.kw = kw; p.tiles = tl; split = sp;
+        const int per_warp = (blocks_k + kw * sp - 1) / (kw * sp);
+        const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * kw));
+        const int rounds = (per_warp + most - 1) / most;
+        p.steps = (per_warp + rounds - 1) / rounds;
+    }
+    if (getenv("W4P")) printf("kw %d tiles %d split %d steps %d blocks_k %d est %.0f\n", p.kw, p.tiles, split, p.steps, blocks_k, least);
     p.group_shift = (p.group & (p.group - 1)) == 0 ? __builtin_ctz((unsigned)p.group) : -1;
     if (p.in_dtype == DG_BF16) return run_vec<__nv_bfloat16>(p, vec, split, s);
     if (p.in_dtype == DG_F16) return run_vec<__half>(p, vec, split, s);
