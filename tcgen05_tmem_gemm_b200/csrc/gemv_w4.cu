@@ -34,8 +34,6 @@
 // are few columns.  Partial sums meet in shared memory and, across a cluster,
 // in distributed shared memory, in a fixed order.
 #include <algorithm>
-#include <cstdlib>
-#include <cstdio>
 
 #include "common.cuh"
 #include "sm100.cuh"
@@ -466,47 +464,24 @@ cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const int vec = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
     const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
     const int64_t col_tiles = (p.N + 15) / 16;
-    // How k is shared: kw warps of a block and `split` blocks of a cluster, over blocks of `tiles` column
-    // tiles.  The cheapest by a model of one SM's time: rounds of resident blocks x (a block's warps x
-    // (steps + fixed work of a warp) at the issue rate that this many warps reach + staging x).
-    const int sets = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-    const int step_cost = 150 + (p.R * sets > 8 ? 16 * sets : 0);
-    double least = 0;
-    int split = 1;
-    for (int kw = 1; kw <= 8; kw *= 2)
-        for (int tiles = 1; tiles * kw <= 8; tiles *= 2)
-            for (int sp = 1; sp <= 8; ++sp) {
-                if ((kw > 1 || sp > 1) && kw * sp > blocks_k) continue;
-                const int per_warp = (blocks_k + kw * sp - 1) / (kw * sp);
-                const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * kw));  // steps whose x fits 48 KB
-                const int rounds = (per_warp + most - 1) / most, steps = (per_warp + rounds - 1) / rounds;
-                const int64_t blocks = (col_tiles + tiles - 1) / tiles * sp;
-                const int64_t smem = w4_layout(p.R, tiles, kw, steps).total + 1024;
-                const int resident = (int)std::min<int64_t>(std::min<int64_t>(24 / (kw * tiles), 228 * 1024 / smem),
-                                                            (blocks + num_sms - 1) / num_sms);
-                const int64_t waves = (blocks + (int64_t)resident * num_sms - 1) / ((int64_t)resident * num_sms);
-                const double warps = resident * kw * tiles / 4.0;  // per scheduler
-                const double rate = std::min(0.8, 0.16 * warps);
-                const double x_cost = 40.0 * rounds * ((double)p.R * kw * steps * 16 / (32 * kw * tiles) + 8);
-                const double t = waves * (warps * (rounds * steps * step_cost + 500 + x_cost) / rate) + (sp > 1 ? 1500 : 0);
-                if (least == 0 || t < least) {
-                    least = t;
-                    p.kw = kw;
-                    p.tiles = tiles;
-                    p.steps = steps;
-                    split = sp;
-                }
-            }
-    if (getenv("W4")) {
-        int kw, tl, sp;
-        sscanf(getenv("W4"), "%d,%d,%d", &kw, &tl, &sp);
-        p.kw = kw; p.tiles = tl; split = sp;
-        const int per_warp = (blocks_k + kw * sp - 1) / (kw * sp);
-        const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * kw));
-        const int rounds = (per_warp + most - 1) / most;
-        p.steps = (per_warp + rounds - 1) / rounds;
-    }
-    if (getenv("W4P")) printf("kw %d tiles %d split %d steps %d blocks_k %d est %.0f\n", p.kw, p.tiles, split, p.steps, blocks_k, least);
+    // k is shared by as many warps as it takes to give every SM about twelve, and no more: a warp costs
+    // some hundred instructions besides its steps (1 x 4096 x 14336 on B200: 14.2 us at 12 warps per SM, 15.4 at
+    // 24, 16.1 at 6).  With one or two rows of x within the block first; with more across the cluster
+    // first, whose blocks then stage a smaller slice of x each.
+    int ways = 1;
+    while (ways < 64 && col_tiles * ways < (int64_t)num_sms * 12 && ways * 2 <= blocks_k) ways *= 2;
+    const int first = std::min(ways, 8), second = ways / first;
+    const int split = p.R > 2 ? first : second;
+    p.kw = p.R > 2 ? second : first;
+    // blocks of eight warps share a slice of x between more column tiles; four where that is cheap (few rows)
+    // and k is not shared, or the slices are small (8 x 14336 x 4096: 31 us with eight, 55 with four;
+    // 3 x 5000 x 5003: 18 and 15.8; 1 x 4096 x 128000: 78 and 73)
+    const int warps = (p.R > 4 || (p.R <= 2 && ways > 1)) ? 8 : 4;
+    p.tiles = std::max(1, warps / p.kw);
+    const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * p.kw));  // steps whose x fits 48 KB
+    const int per_warp = (blocks_k + p.kw * split - 1) / (p.kw * split);
+    const int rounds = (per_warp + most - 1) / most;
+    p.steps = (per_warp + rounds - 1) / rounds;
     p.group_shift = (p.group & (p.group - 1)) == 0 ? __builtin_ctz((unsigned)p.group) : -1;
     if (p.in_dtype == DG_BF16) return run_vec<__nv_bfloat16>(p, vec, split, s);
     if (p.in_dtype == DG_F16) return run_vec<__half>(p, vec, split, s);
