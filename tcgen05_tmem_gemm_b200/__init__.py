@@ -453,6 +453,20 @@ def gemv_w4(x, codes, scales, y, zeros=None, group: int = 128, alpha: float = 1.
     return y
 
 
+class _Torch:
+    """torch, imported on first use: the binding itself does not need it."""
+
+    def __getattr__(self, name):
+        import torch
+
+        value = getattr(torch, name)
+        setattr(self, name, value)
+        return value
+
+
+_torch = _Torch()
+
+
 def _vector(t, name, dtype, n):
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
@@ -461,14 +475,12 @@ def _vector(t, name, dtype, n):
 
 def _workspace(nbytes: int, stream):
     """Device bytes of torch's pool, allocated on the stream that uses them."""
-    import torch
-
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        return _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        stream = _torch.cuda.ExternalStream(stream)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(nbytes, dtype=_torch.uint8, device="cuda")
 
 
 def linear_ce(x, w, target, loss, lse, alpha: float = 1.0, ignore_index: int = -100, stream=None, workspace=None,
@@ -479,16 +491,20 @@ def linear_ce(x, w, target, loss, lse, alpha: float = 1.0, ignore_index: int = -
     weight.t()), target int64, loss and lse float32, one per row.  `workspace`
     is a uint8 tensor (at least dg_linear_ce_workspace's bytes); None takes one
     from torch's pool.  Raises DgError on a bad status; returns (loss, lse)."""
-    import torch
-
     xv, wv = view(x, x.dim() - 1 if x_row_dims is None else x_row_dims), view(w)
     rows = x.numel() // x.shape[-1] if x.shape[-1] else target.numel()
-    _vector(target, "target", torch.int64, rows)
-    _vector(loss, "loss", torch.float32, rows)
-    _vector(lse, "lse", torch.float32, rows)
+    _vector(target, "target", _torch.int64, rows)
+    _vector(loss, "loss", _torch.float32, rows)
+    _vector(lse, "lse", _torch.float32, rows)
+    xr, wr = ctypes.byref(xv), ctypes.byref(wv)
     if workspace is None:
-        workspace = _workspace(dg_linear_ce_workspace(xv, wv)[1], stream)
-    st = dg_linear_ce(xv, wv, target, ignore_index, alpha, loss, lse, workspace, workspace.numel(), stream)
+        least, best = ctypes.c_int64(), ctypes.c_int64()
+        st = lib.dg_linear_ce_workspace(xr, wr, ctypes.byref(least), ctypes.byref(best))
+        if st != DG_OK:
+            raise DgError(st, "dg_linear_ce_workspace")
+        workspace = _workspace(best.value, stream)
+    st = lib.dg_linear_ce(xr, wr, target.data_ptr(), ignore_index, alpha, loss.data_ptr(), lse.data_ptr(),
+                          workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_linear_ce")
     return loss, lse
@@ -501,24 +517,29 @@ def linear_ce_grad(x, w, target, lse, dloss, dx=None, dw=None, alpha: float = 1.
     one per row, or one value for all rows (one element, or expanded from one);
     lse is what linear_ce wrote.  Raises DgError on a bad status; returns
     (dx, dw)."""
-    import torch
-
     rd = x.dim() - 1 if x_row_dims is None else x_row_dims
     xv, wv = view(x, rd), view(w)
     dxv = None if dx is None else view(dx, rd)
     dwv = None if dw is None else view(dw)
     rows = x.numel() // x.shape[-1] if x.shape[-1] else target.numel()
-    _vector(target, "target", torch.int64, rows)
-    _vector(lse, "lse", torch.float32, rows)
-    shared = dloss.numel() == 1 or all(s == 0 for s, n in zip(dloss.stride(), dloss.shape) if n > 1)
+    _vector(target, "target", _torch.int64, rows)
+    _vector(lse, "lse", _torch.float32, rows)
+    shared = dloss.numel() == 1 or not any(dloss.stride())  # one value, or expanded from one
     if not shared:
-        _vector(dloss, "dloss", torch.float32, rows)
-    elif dloss.dtype != torch.float32 or dloss.numel() not in (1, rows):
+        _vector(dloss, "dloss", _torch.float32, rows)
+    elif dloss.dtype != _torch.float32 or dloss.numel() not in (1, rows):
         raise ValueError(f"dloss must be a float32 tensor of 1 or {rows} elements")
+    xr, wr = ctypes.byref(xv), ctypes.byref(wv)
+    dxr, dwr = None if dx is None else ctypes.byref(dxv), None if dw is None else ctypes.byref(dwv)
     if workspace is None:
-        workspace = _workspace(dg_linear_ce_grad_workspace(xv, wv, dxv, dwv)[1], stream)
-    st = dg_linear_ce_grad(xv, wv, target, ignore_index, alpha, lse, dloss, 0 if shared else 4, dxv, dwv, workspace,
-                           workspace.numel(), stream)
+        least, best = ctypes.c_int64(), ctypes.c_int64()
+        st = lib.dg_linear_ce_grad_workspace(xr, wr, dxr, dwr, ctypes.byref(least), ctypes.byref(best))
+        if st != DG_OK:
+            raise DgError(st, "dg_linear_ce_grad_workspace")
+        workspace = _workspace(best.value, stream)
+    st = lib.dg_linear_ce_grad(xr, wr, target.data_ptr(), ignore_index, alpha, lse.data_ptr(), dloss.data_ptr(),
+                               0 if shared else 4, dxr, dwr, workspace.data_ptr(), workspace.numel(),
+                               _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_linear_ce_grad")
     return dx, dw

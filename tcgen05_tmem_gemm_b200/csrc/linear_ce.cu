@@ -23,6 +23,7 @@ namespace {
 constexpr int kStatCols = 2048;                    // logits per block of ce_stats_kernel
 constexpr int64_t kForwardPiece = int64_t(256) << 20;  // most bytes of one piece of logits (forward)
 constexpr int64_t kGradPiece = int64_t(512) << 20;     // most bytes of one piece of G
+constexpr int64_t kShortDim = 1024;
 constexpr int kUsualSms = 148;                     // where no device is asked (workspace sizes)
 constexpr int kPieceCols = 256;                    // pieces are whole multiples of this many columns
 
@@ -114,52 +115,76 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 // 1 and G's -1 + p at the target is rounded next to 1, where the rounding of
 // dloss * (p - 1) would shift a row as a whole; F16 pieces are also scaled to
 // the middle of F16's range (2^9).  norm[0] = that factor, norm[1] = its
-// inverse, which the products multiply their FP32 sums by.  One block.
-__global__ void __launch_bounds__(1024)
-    ce_norm_kernel(const char *dloss, int64_t dloss_stride, const int64_t *target, int64_t ignore_index, int64_t T,
-                   int64_t V, float top, float *norm) {
-    pdl_wait_then_release();
-    __shared__ float red[32];
+// inverse, which the products multiply their FP32 sums by.
+__device__ __forceinline__ float largest_dloss(const char *dloss, int64_t dloss_stride, const int64_t *target,
+                                               int64_t ignore_index, int64_t T, int64_t V, float (&red)[32]) {
     float big = 0.f;
-    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    for (int64_t t = threadIdx.x; t < T; t += blockDim.x) {
         if (read_target(target, ignore_index, V, t) < 0) continue;
         const float g = fabsf(*reinterpret_cast<const float *>(dloss + t * dloss_stride));
         if (g < INFINITY) big = fmaxf(big, g);
     }
     for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
+    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = big;
     __syncthreads();
     big = red[threadIdx.x & 31];
     for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    // below 2^-100 the division would leave FP32's range; such gradients are scaled as far as 2^100 goes
+    return big > 0.f ? fmaxf(big, 0x1p-100f) : 1.f;
+}
+
+__global__ void __launch_bounds__(1024)
+    ce_norm_kernel(const char *dloss, int64_t dloss_stride, const int64_t *target, int64_t ignore_index, int64_t T,
+                   int64_t V, float top, float *norm) {
+    pdl_wait_then_release();
+    __shared__ float red[32];
+    const float big = largest_dloss(dloss, dloss_stride, target, ignore_index, T, V, red);
     if (threadIdx.x == 0) {
-        // below 2^-100 the division would leave FP32's range; such gradients are scaled as far as 2^100 goes
-        big = big > 0.f ? fmaxf(big, 0x1p-100f) : 1.f;
         norm[0] = big;
         norm[1] = big / top;
     }
 }
 
+// Up to this many rows every block of ce_rows_kernel finds the largest dloss
+// itself, which saves the launch of ce_norm_kernel.
+constexpr int64_t kOwnNormRows = 2048;
+
 // Per row: its RowGrad, and (xc != null) a copy of X's row, zero in rows that
 // take no part, so that whatever those rows hold stays out of dW.
 __global__ void __launch_bounds__(256)
     ce_rows_kernel(const DevView x, int D, int64_t T, int64_t V, const int64_t *target, int64_t ignore_index,
-                   const float *lse, const char *dloss, int64_t dloss_stride, const float *norm, float top,
+                   const float *lse, const char *dloss, int64_t dloss_stride, float *norm, int own_norm, float top,
                    RowGrad *rows, float *undo, int64_t undo_n, char *xc, int64_t ldx, int vec, int *err_word) {
     pdl_wait_then_release();
     const int64_t t = blockIdx.x;
     const int y = target ? read_target(target, ignore_index, V, t) : 0;
+    __shared__ float red[32];
+    float big = 1.f;
+    if (norm) {
+        if (own_norm) {
+            big = largest_dloss(dloss, dloss_stride, target, ignore_index, T, V, red);
+            if (t == 0 && threadIdx.x == 0) {
+                norm[0] = big;
+                norm[1] = big / top;
+            }
+        } else {
+            big = norm[0];
+        }
+    }
     if (rows && threadIdx.x == 0) {
         RowGrad r;
         r.lse = lse[t];
         r.scale = y < 0 ? 0.f : *reinterpret_cast<const float *>(dloss + t * dloss_stride);
-        if (norm) r.scale = r.scale / norm[0] * top;
+        if (norm) r.scale = r.scale / big * top;
         r.target = y;
         r.pad_ = 0;
         rows[t] = r;
         if (y == kInvalid && err_word) atomicCAS(err_word, 0, (int)DG_ERR_VALUE);
     }
     if (undo)  // the inverse for every row of the products
-        for (int64_t i = t * 256 + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * 256) undo[i] = norm[1];
+        for (int64_t i = t * 256 + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * 256) undo[i] = big / top;
     if (!xc) return;
     const char *src = x.ptr + axis_offset(x.row, t);
     char *dst = xc + t * ldx;
@@ -284,7 +309,7 @@ dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
 // The workspace's parts, each 256-byte aligned, for pieces of `piece` columns.
 struct Layout {
     int64_t xc = 0, part = 0, run = 0, ztarget = 0, z = 0, rows = 0, norm = 0, undo = 0, g = 0, acc = 0, planes = 0;
-    int64_t ldx = 0, ldz = 0, ldg = 0, ldp = 0;
+    int64_t ldx = 0, ldz = 0, ldg = 0;
     int64_t total = 0;
 };
 
@@ -302,10 +327,13 @@ int64_t undo_count(const Problem &p) { return std::max(p.T, std::max(p.D, p.V));
 int64_t stat_slots(int64_t piece) { return (piece + kStatCols - 1) / kStatCols; }
 int64_t tile_slots(int64_t piece) { return (piece + kSlotCols - 1) / kSlotCols; }
 
-// Whether the CTA-pair kernel makes the logits: enough 256 x 256 tiles for
-// its pairs of SMs, operands it can read through TMA.
+// Whether the CTA-pair kernel makes the logits: operands it can read through
+// TMA, and either enough 256 x 256 tiles for its pairs of SMs, or more rows
+// than the thin products' swapped tiles take, or a k so short that a round of
+// tiles takes no longer than the launch it saves.
 bool tiles_worth_it(const Problem &p, int num_sms) {
-    return p.tensor && p.w.tma_ok && ((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms;
+    return p.tensor && p.w.tma_ok &&
+           (((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms || p.T > 64 || p.D <= kShortDim);
 }
 
 // 16-byte rows of X for its copy.
@@ -338,27 +366,41 @@ Layout forward_layout(const Problem &p, int64_t piece, bool tiles) {
     return l;
 }
 
-// dX = G W^T has few tiles and a long k (the vocabulary) when there are few
-// rows: the planes of partial sums that k is then split into, so that the
-// tiles times the planes fill the pairs of SMs in whole rounds (0: one product
-// without planes).  Up to four rows the GEMV over W's rows serves.
-int plane_count(const Problem &p, int num_sms) {
-    if (!p.tensor || p.T <= 4 || p.D < 32) return 0;
-    const int64_t pairs = num_sms / 2, tiles = ((p.T + 255) / 256) * ((p.D + 255) / 256);
+// A product [M x K] [K x N] of few tiles and a long k (dX, whose k is the
+// vocabulary, with few rows; dW, whose k is the rows, of a small layer): the
+// planes of partial sums that k is split into, so that the tiles times the
+// planes fill the pairs of SMs in whole rounds (0: one product without planes).
+int plane_count(int64_t M, int64_t N, int64_t K, int num_sms) {
+    if (N < 32) return 0;
+    const int64_t pairs = num_sms / 2, tiles = ((M + 255) / 256) * ((N + 255) / 256);
     if (tiles >= 2 * num_sms) return 0;
     auto busy = [&](int64_t n) { return (double)(tiles * n) / (double)((tiles * n + pairs - 1) / pairs * pairs); };
     int best = 0;
     double most = busy(1) + 0.1;  // worth it from a tenth on: a plane costs its write and its read
-    for (int n = 2; n <= 16 && n * 1024 <= p.V; ++n)
+    for (int n = 2; n <= 16 && n * 256 <= K && tiles * n <= 4 * pairs; ++n)
         if (busy(n) - 0.005 * n > most) {
             most = busy(n) - 0.005 * n;
             best = n;
         }
     return best;
 }
+int64_t plane_bytes(int64_t M, int64_t N, int planes) { return planes * ((M + 255) / 256 * 256) * align256(N * 4); }
+
+// Those of dX (up to four rows the GEMV over W's rows serves) and of a piece of dW.
+struct Planes {
+    int dx = 0, dw = 0;
+};
+Planes plan_planes(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int num_sms) {
+    Planes n;
+    if (!p.tensor) return n;
+    const int64_t cols = std::min(piece, p.V);
+    if (need_dx && p.T > 4) n.dx = plane_count(p.T, p.D, cols, num_sms);
+    if (need_dw) n.dw = p.dw.unit_dim == 2 ? plane_count(cols, p.D, p.T, num_sms) : plane_count(p.D, cols, p.T, num_sms);
+    return n;
+}
 
 Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, int dx_dtype, bool tiles,
-                   int planes) {
+                   Planes n) {
     Layout l;
     l.ldx = align256(p.D * p.es);
     l.ldz = align256(piece * 4);
@@ -367,9 +409,10 @@ Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     l.rows = take(&l, p.T * (int64_t)sizeof(RowGrad));
     l.norm = take(&l, 256);
     l.undo = take(&l, p.es == 2 ? undo_count(p) * 4 : 0);
-    l.acc = take(&l, need_dx && piece < p.V && (dx_dtype != DG_F32 || planes > 0) ? p.T * p.D * 4 : 0);
-    l.ldp = align256(p.D * 4);
-    l.planes = take(&l, planes * ((p.T + 255) / 256 * 256) * l.ldp);
+    l.acc = take(&l, need_dx && piece < p.V && (dx_dtype != DG_F32 || n.dx > 0) ? p.T * p.D * 4 : 0);
+    const int64_t cols = std::min(piece, p.V);
+    l.planes = take(&l, std::max(plane_bytes(p.T, p.D, n.dx),
+                                 p.dw.unit_dim == 2 ? plane_bytes(cols, p.D, n.dw) : plane_bytes(p.D, cols, n.dw)));
     l.g = take(&l, p.T * l.ldg);
     l.z = take(&l, tiles ? 0 : p.T * l.ldz);
     return l;
@@ -392,7 +435,7 @@ int64_t piece_for(const Problem &p, int64_t bytes, int64_t per_col) {
 // pairs per row and 1024 columns), of G.
 int64_t forward_piece(const Problem &p, bool tiles) {
     if (!tiles) return piece_for(p, kForwardPiece, p.T * 4);
-    const int64_t cols = kForwardPiece / (p.T * 8) * kSlotCols;
+    const int64_t cols = kForwardPiece / (std::max<int64_t>(p.T, 1) * 8) * kSlotCols;
     return cols >= p.V ? p.V : std::max<int64_t>(cols / kPieceCols * kPieceCols, kPieceCols);
 }
 int64_t grad_piece(const Problem &p) { return piece_for(p, kGradPiece, p.T * p.es); }
@@ -485,7 +528,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     if (forward_copies_x(p)) {
         DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x),
                                   (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
-                                  (const char *)nullptr, (int64_t)0, (const float *)nullptr, 1.f, (RowGrad *)nullptr,
+                                  (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f, (RowGrad *)nullptr,
                                   (float *)nullptr, (int64_t)0, ws + l.xc, l.ldx, x_vec(X, p), (int *)nullptr)));
     }
     float2 *part = reinterpret_cast<float2 *>(ws + l.part), *run = reinterpret_cast<float2 *>(ws + l.run);
@@ -538,14 +581,46 @@ dg_status check_grad(const dg_view *X, const dg_view *W, const dg_view *dX, cons
     return DG_OK;
 }
 
-// dW's product, k = T: with few rows the stores of its large output take
-// longer than the products, and get twice the epilogue warps.
-dg_status product(const dg_view *A, const dg_view *B, const dg_view *C, const Problem &p, int num_sms, float alpha,
-                  const float *undo, cudaStream_t s) {
+// call's product in planes at `planes`; on return call.chunks is the number written.
+dg_status in_planes(PairCall &call, char *planes, cudaStream_t s) {
+    const int64_t M = call.A->shape[0], N = call.B->shape[1], rows = call.chunks * ((M + 255) / 256 * 256);
+    const dg_view pv = view2(planes, rows, N, align256(N * 4), 4, DG_F32);
+    call.C = &pv;
+    const dg_status st = pair_call(call, s);
+    call.C = nullptr;
+    return st;
+}
+
+// alpha * norm[1] times the product through planes, to `out` or (acc_out) to the running sum.
+dg_status planes_product(PairCall call, char *planes, const DevView &out, const float *acc_in, float *acc_out,
+                         float alpha, const float *norm, int pdl, cudaStream_t s) {
+    const int64_t M = call.A->shape[0], N = call.B->shape[1];
+    DG_TRY(in_planes(call, planes, s));
+    return launched(launch_ex(ce_planes_kernel, dim3((unsigned)M, (unsigned)((N + 255) / 256)), dim3(256), 0, s,
+                              dim3(1, 1, 1), pdl, reinterpret_cast<const float *>(planes), align256(N * 4) / 4,
+                              call.chunks, (M + 255) / 256 * 256, acc_in, acc_out, alpha, norm, out, (int)N));
+}
+
+// dW's product, k = T.  Few tiles: planes, or the paired tiles all the same
+// (the single-CTA kernel's split of k takes 48 us for 120 x 1024 x 4000, a
+// round of paired tiles 11).  Many tiles with few rows: the stores of the large
+// output take longer than the products, and get twice the epilogue warps
+// (32000 x 64 x 4096: 93 -> 85 us; slower from k = 777 on).
+dg_status product(const dg_view *A, const dg_view *B, const dg_view *C, const Problem &p, int num_sms, int planes,
+                  char *plane_space, float alpha, const float *norm, const float *undo, int pdl, cudaStream_t s) {
     const int64_t tiles = ((A->shape[0] + 255) / 256) * ((B->shape[1] + 255) / 256);
-    if (p.tensor && alpha != 0.f && p.T <= 256 && tiles * 2 >= num_sms) {
-        PairCall call{A, B, C, alpha, undo, kPairWide, {}, 0, false};
-        const dg_status st = pair_call(call, s);
+    if (p.tensor && alpha != 0.f) {
+        dg_status st = DG_ERR_UNSUPPORTED;
+        if (planes > 0 && B->shape[1] < (int64_t)65535 * 256) {
+            ViewInfo ci;
+            DG_TRY(analyse(C, true, &ci));
+            st = planes_product(PairCall{A, B, nullptr, 1.f, nullptr, kPairPartial, {}, planes, false}, plane_space,
+                                dev_of(C, ci), nullptr, nullptr, alpha, norm, pdl, s);
+        }
+        if (st == DG_ERR_UNSUPPORTED && (tiles * 2 < num_sms || p.T <= 256)) {
+            PairCall call{A, B, C, alpha, undo, kPairWide, {}, 0, false};
+            st = pair_call(call, s);
+        }
         if (st != DG_ERR_UNSUPPORTED) return st;
     }
     return gemm_tiles(A, B, C, alpha, 0.f, undo, s);
@@ -562,9 +637,11 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W, const 
     Problem p;
     DG_TRY(check_grad(X, W, dX, dW, &p));
     const int dxt = dX ? dX->dtype : DG_F32;
-    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, 0).total;
+    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total;
     *best = std::max(*least, grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt,
-                                         tiles_worth_it(p, kUsualSms), dX ? plane_count(p, kUsualSms) : 0).total);
+                                         tiles_worth_it(p, kUsualSms),
+                                         plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, kUsualSms))
+                                 .total);
     return DG_OK;
 }
 
@@ -587,7 +664,8 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             return DG_ERR_ALIGN;
     }
     const int dxt = dX ? dX->dtype : DG_F32;
-    if (p.T > 0 && grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, 0).total > workspace_bytes)
+    if (p.T > 0 && grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total >
+                       workspace_bytes)
         return DG_ERR_SHAPE;
     DG_TRY(device_info(&num_sms, &err_word));
     if (p.T > 0 && ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
@@ -608,12 +686,11 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     const dg_view xv = copy ? view2(ws, p.T, p.D, ldx, p.es, X->dtype) : *X;
     const dg_view xt = view2(ws, p.D, p.T, p.es, ldx, X->dtype);
     bool tiles = tiles_worth_it(p, num_sms);
-    int planes = dX ? plane_count(p, num_sms) : 0;
-    const int64_t plane_rows = (p.T + 255) / 256 * 256;
+    Planes planes = plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, num_sms);
     auto layout_of = [&](int64_t piece) {
         return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt, tiles, planes);
     };
-    if (layout_of(grad_piece(p)).total > workspace_bytes) planes = 0;  // a small workspace has room for G only
+    if (layout_of(grad_piece(p)).total > workspace_bytes) planes = Planes{};  // a small workspace has room for G only
     int64_t piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
     if (tiles) {
         // the tensor stores of G take pieces of 64 columns or more, the last one too
@@ -630,13 +707,13 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         }
     }
     if (piece == 0) return DG_ERR_SHAPE;
-    if (planes > 0) {
+    if (planes.dx > 0) {
         const Layout t = layout_of(piece);
         const int64_t cols = std::min(piece, p.V);
         const dg_view gv = view2(ws + t.g, p.T, cols, t.ldg, p.es, X->dtype);
         const dg_view wt = view2(p.wm.ptr, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
-        const dg_view pv = view2(ws + t.planes, planes * plane_rows, p.D, t.ldp, 4, DG_F32);
-        if (pair_once(PairCall{&gv, &wt, &pv, 1.f, nullptr, kPairPartial, {}, planes, true}, s) != DG_OK) planes = 0;
+        PairCall call{&gv, &wt, nullptr, 1.f, nullptr, kPairPartial, {}, planes.dx, true};
+        if (in_planes(call, ws + t.planes, s) != DG_OK) planes.dx = 0;
     }
     const Layout l = layout_of(piece);
     RowGrad *rows = reinterpret_cast<RowGrad *>(ws + l.rows);
@@ -645,18 +722,19 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     if (p.tensor) {
         norm = reinterpret_cast<float *>(ws + l.norm);
         undo = reinterpret_cast<float *>(ws + l.undo);
-        DG_TRY(launched(launch_ex(ce_norm_kernel, one, dim3(1024), 0, s, one, pdl,
-                                  reinterpret_cast<const char *>(dloss), dloss_stride, target, ignore_index, p.T, p.V,
-                                  top, norm)));
+        if (p.T > kOwnNormRows)
+            DG_TRY(launched(launch_ex(ce_norm_kernel, one, dim3(1024), 0, s, one, pdl,
+                                      reinterpret_cast<const char *>(dloss), dloss_stride, target, ignore_index, p.T,
+                                      p.V, top, norm)));
     }
     DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
                               p.T, p.V, target, ignore_index, lse, reinterpret_cast<const char *>(dloss), dloss_stride,
-                              (const float *)norm, top, rows, undo, undo_count(p), copy ? ws : (char *)nullptr, ldx,
-                              x_vec(X, p), err_word)));
+                              norm, p.T <= kOwnNormRows ? 1 : 0, top, rows, undo, undo_count(p),
+                              copy ? ws : (char *)nullptr, ldx, x_vec(X, p), err_word)));
     char *g = ws + l.g;
     float *z = reinterpret_cast<float *>(ws + l.z);
     const bool sum = dX && piece < p.V;                        // dX is summed over several pieces
-    const bool own_acc = sum && planes == 0 && dxt != DG_F32;  // in the workspace, rounded at the end
+    const bool own_acc = sum && planes.dx == 0 && dxt != DG_F32;  // in the workspace, rounded at the end
     float *acc = reinterpret_cast<float *>(ws + l.acc);
     const dg_view accv = own_acc ? view2(ws + l.acc, p.T, p.D, p.D * 4, 4, DG_F32) : (dX ? *dX : xv);
     for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
@@ -678,17 +756,11 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
                                       (const float *)z, l.ldz / 4, p.T, (int)v0, (int)cols, (const RowGrad *)rows, g,
                                       l.ldg, X->dtype)));
         }
-        if (dX && planes > 0) {
-            const dg_view pv = view2(ws + l.planes, planes * plane_rows, p.D, l.ldp, 4, DG_F32);
-            PairCall call{&gv, &wt, &pv, 1.f, nullptr, kPairPartial, {}, planes, false};
-            DG_TRY(pair_call(call, s));
-            const int used = call.chunks;
+        if (dX && planes.dx > 0) {
             const bool first = v0 == 0, last = v0 + cols == p.V;
-            DG_TRY(launched(launch_ex(ce_planes_kernel, dim3((unsigned)p.T, (unsigned)((p.D + 255) / 256)), dim3(256), 0, s, one, pdl,
-                                      reinterpret_cast<const float *>(ws + l.planes), l.ldp / 4, used, plane_rows,
-                                      first ? (const float *)nullptr : (const float *)acc,
-                                      last ? (float *)nullptr : acc, alpha, (const float *)norm, dev_of(dX, p.dx),
-                                      (int)p.D)));
+            DG_TRY(planes_product(PairCall{&gv, &wt, nullptr, 1.f, nullptr, kPairPartial, {}, planes.dx, false},
+                                  ws + l.planes, dev_of(dX, p.dx), first ? nullptr : acc, last ? nullptr : acc, alpha,
+                                  norm, pdl, s));
         } else if (dX) {
             DG_TRY(gemm_tiles(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, undo, s));
         }
@@ -697,10 +769,10 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             char *op = p.dwm.ptr + v0 * p.dwm.cs;
             if (p.dw.unit_dim == 2) {
                 const dg_view ov = view2(op, cols, p.D, p.dwm.cs, p.dwm.rs, p.dwm.dtype);
-                DG_TRY(product(&gt, &xv, &ov, p, num_sms, alpha, undo, s));
+                DG_TRY(product(&gt, &xv, &ov, p, num_sms, planes.dw, ws + l.planes, alpha, norm, undo, pdl, s));
             } else {
                 const dg_view ov = view2(op, p.D, cols, p.dwm.rs, p.dwm.cs, p.dwm.dtype);
-                DG_TRY(product(&xt, &gv, &ov, p, num_sms, alpha, undo, s));
+                DG_TRY(product(&xt, &gv, &ov, p, num_sms, planes.dw, ws + l.planes, alpha, norm, undo, pdl, s));
             }
         }
     }

@@ -7,7 +7,8 @@ Tolerances, with S[t][v] = |alpha| sum_d |x| |w| and g the upstream gradient:
   lse moves by at most max_v dz, the sum of exponentials by at most
     (512 + V / 1024) 2^-24 of itself (256 logits a thread, then pairs) and 2^-20
     for the exponentials and the logarithm, the result by 2^-23 (|lse| + |z|);
-  G is off by u |G| (its rounding to X's type, u = eps / 2, 0 for F32) plus
+  G is off by u |G| (its rounding to X's type, u = eps / 2, 0 for F32; the
+    division by the largest dloss and back adds 2^-22 |G|) plus
     |g| p (dz + |lse| 2^-22 + 2^-20) + (|g| + 1) 2^-126 (the hardware's power of
     two gives 0 for a result below 2^-126, so p is off by up to 2^-126 there,
     and G may be flushed below 2^-126 itself), and F16 pieces by half a
@@ -89,7 +90,7 @@ def check_grads(x2, w, y, dl, dx, dw, alpha=1.0):
     one = torch.zeros_like(p).scatter_(1, torch.where(kept, y, 0)[:, None], 1.0)
     G = g * (p - one)
     u = 0.0 if x2.dtype == torch.float32 else torch.finfo(x2.dtype).eps / 2
-    dG = u * G.abs() + g.abs() * p * (dz + lse.abs() * 2.0 ** -22 + 2.0 ** -20) + \
+    dG = (u + 2.0 ** -22) * G.abs() + g.abs() * p * (dz + lse.abs() * 2.0 ** -22 + 2.0 ** -20) + \
         (g.abs() + 1) * 2.0 ** -126
     if x2.dtype == torch.float16:
         dG = dG + torch.where(kept, 1.0, 0.0)[:, None].double() * g.abs().max() * 2.0 ** -34
@@ -160,6 +161,26 @@ def test_widths(D, T):
 def test_paired_tiles(dtype, order):
     # enough rows and columns for the paired tensor-core tiles, with both edges inside a tile
     run_both(513, 320, 19300, dtype, alpha=0.75, order=order)
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 31, 32, 100])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_paired_tiles_with_few_rows(T, out):
+    run_both(T, 192, 19000, "bf16", out=out)
+
+
+@pytest.mark.parametrize("T,D,V", [(3000, 64, 300), (2500, 100, 65), (2049, 520, 1000), (5000, 32, 64), (700, 2048, 64)])
+@pytest.mark.parametrize("order", ["vd", "dv"])
+def test_small_layers_with_many_rows(T, D, V, order):
+    # few tiles: k of dX and of dW split into planes of partial sums
+    run_both(T, D, V, "f16", order=order)
+    run_both(T, D, V, "bf16", order=order, out="f32", alpha=-0.25)
+
+
+@pytest.mark.parametrize("V", [19000, 19201, 25600 + 40])
+def test_pieces_that_end_in_few_columns(V):
+    for fraction in (0.15, 0.5, 0.9):
+        run_both(290, 64, V, "bf16", fraction=fraction)
 
 
 def test_paired_and_plain_tiles_agree():
