@@ -27,7 +27,7 @@
 // Work split.  It streams W once and is bound by HBM, so what counts is bytes
 // in flight and few instructions per byte.  A warp owns 16 columns and a share
 // of k, in steps of 128 k; every lane copies the 16 bytes of each of its two
-// columns that it will itself unpack into a ring of kStages steps in shared
+// columns that it will itself unpack into a ring of two batches of steps in shared
 // memory (cp.async: no registers, no synchronisation between lanes, bytes past
 // a column's end arrive as zeros).  A block is column tiles x warps along k
 // over one staged slice of x; blocks of a cluster share k further where there
@@ -43,11 +43,12 @@ namespace dg {
 namespace {
 
 constexpr int kBlockK = 128;   // k per step of a warp: 16 bytes of codes per lane and column
-constexpr int kStages = 8;     // steps of a warp in flight: two batches
-constexpr uint32_t kStageBytes = 32 * 2 * 16;
-constexpr uint32_t kRingBytes = kStages * kStageBytes;  // per warp
-
+// A batch of steps of a warp in the ring: per step, lane and column 16 bytes
+// or, where the columns do not start at multiples of 16 (VEC false), per column
+// the aligned 16-byte chunks that hold the batch's 256 bytes.
+constexpr uint32_t kLooseColumn = (256 + 16) + 16;
 constexpr int kBatch = 4;      // steps between waits
+__host__ __device__ constexpr uint32_t batch_bytes(bool vec) { return vec ? kBatch * 32 * 2 * 16 : 16 * kLooseColumn; }
 
 // (w & mask) | bits in one instruction (two literals would take two).
 __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
@@ -114,32 +115,42 @@ struct Pair<__half> {
     }
 };
 
-// Copies the lane's 16 bytes of one column from byte b into its slot, zeros
-// past the column's `nbytes`.  VEC: the alignment of every column's codes.
-template <int VEC>
-__device__ __forceinline__ void copy_codes(uint32_t slot, const uint8_t *row, int b, int nbytes) {
-    if (VEC == 16) {
-        const int n = min(max(nbytes - b, 0), 16);
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(slot), "l"(row + (n > 0 ? b : 0)),
-                     "r"(n)
-                     : "memory");
-        return;
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c, b += 4) {
-        if (VEC == 4) {
-            const int n = min(max(nbytes - b, 0), 4);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + 4 * c),
-                         "l"(row + (n > 0 ? b : 0)), "r"(n)
-                         : "memory");
+// Copies the lane's 16 bytes of one column from byte b into its place, zeros
+// past the column's `nbytes`.  The column starts at a multiple of 16.
+__device__ __forceinline__ void copy_codes(uint32_t to, const uint8_t *row, int b, int nbytes) {
+    const int n = min(max(nbytes - b, 0), 16);
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(row + (n > 0 ? b : 0)), "r"(n)
+                 : "memory");
+}
+
+// A batch's codes of 16 columns at any alignment: `bytes` bytes of each column
+// from byte b on, as the aligned 16-byte chunks that hold them (17 for a whole
+// batch; half a warp copies a column's first 16).  Bytes before a column or
+// past its end are not read: the copy of a last chunk is cut short, a first
+// chunk that the column starts inside of is put together byte by byte.
+__device__ __forceinline__ void copy_loose(uint32_t to, uint8_t *to_ptr, const uint8_t *codes, int64_t stride, int n0,
+                                           int N, int b, int bytes, int nbytes, int lane) {
+    auto chunk = [&](int col, int c) {
+        const uint8_t *row = codes + (int64_t)min(n0 + col, N - 1) * stride;
+        const int d = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+        if (16 * c >= d + bytes) return;
+        const int at = b - d + 16 * c;  // the chunk's first byte in the column
+        if (at < 0) {
+            for (int q = d; q < 16; ++q)
+                if (q - d < nbytes) to_ptr[col * kLooseColumn + q] = row[q - d];
         } else {
-            uint32_t w = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (b + i < nbytes) w |= (uint32_t)__ldg(row + b + i) << (8 * i);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + 4 * c), "r"(w) : "memory");
+            const int n = min(max(nbytes - at, 0), 16);
+            if (n > 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + col * kLooseColumn + 16 * c),
+                             "l"(row + at), "r"(n)
+                             : "memory");
+            else
+                *reinterpret_cast<uint4 *>(to_ptr + col * kLooseColumn + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
         }
-    }
+    };
+#pragma unroll 4
+    for (int j = 0; j < 8; ++j) chunk(2 * j + (lane >> 4), lane & 15);
+    if (lane < 16) chunk(lane, 16);
 }
 
 __device__ __forceinline__ void copy16(uint32_t slot, const uint8_t *src) {
@@ -150,35 +161,28 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 // Eight 16-bit x, h = k .. k+7, as the four pairs (k+j, k+j+4).
 __device__ __forceinline__ uint4 x_pairs(const uint4 &h) {
     return make_uint4(__byte_perm(h.x, h.z, 0x5410), __byte_perm(h.x, h.z, 0x7632), __byte_perm(h.y, h.w, 0x5410),
                       __byte_perm(h.y, h.w, 0x7632));
 }
 
-// x of k .. k+7 of row r, element by element, zeros at and past K.
-__device__ __forceinline__ uint4 x_elements(const DevView &x, int r, int k, int K) {
+// x of k .. k+7 of row r, element by element (eight loads in flight), zeros at
+// and past K.
+__device__ __noinline__ uint4 x_elements(const DevView &x, int r, int k, int K) {
     const char *row = x.ptr + axis_offset(x.row, r);
-    uint32_t h[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-    for (int i = 7; i >= 0; --i) {  // shifted in from the top, so no index into h varies
-        const uint32_t v =
-            k + i < K ? *reinterpret_cast<const uint16_t *>(row + axis_offset(x.col, k + i)) : (uint16_t)0;
-        h[3] = (h[3] << 16) | (h[2] >> 16);
-        h[2] = (h[2] << 16) | (h[1] >> 16);
-        h[1] = (h[1] << 16) | (h[0] >> 16);
-        h[0] = (h[0] << 16) | v;
+    uint32_t e[8];
+    if (x.col.n <= 1) {
+        const int64_t cs = x.col.stride[0];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            e[i] = k + i < K ? *reinterpret_cast<const uint16_t *>(row + (k + i) * cs) : (uint16_t)0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            e[i] = k + i < K ? *reinterpret_cast<const uint16_t *>(row + axis_offset(x.col, k + i)) : (uint16_t)0;
     }
-    return make_uint4(h[0], h[1], h[2], h[3]);
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
 // The raw bits of a scale, converted where it is used, so that the load can
@@ -217,25 +221,26 @@ struct W4Layout {
 
 // A block of `tiles` column tiles and `kw` warps along k, each taking `steps`
 // steps per round.
-__host__ __device__ inline W4Layout w4_layout(int R, int tiles, int kw, int steps) {
+__host__ __device__ inline W4Layout w4_layout(int R, int tiles, int kw, int steps, bool vec) {
     W4Layout L;
     L.pitch = (uint32_t)(kw * steps * kBlockK * 2 + 64);  // rows 64 bytes apart modulo 128: no bank conflicts
     L.zero = (uint32_t)R * L.pitch;
     L.ring = (L.zero + 256 + 127) / 128 * 128;
-    const uint32_t ring_bytes = (uint32_t)(tiles * kw) * kRingBytes;
+    const uint32_t ring_bytes = (uint32_t)(tiles * kw) * 2 * batch_bytes(vec);
     L.red = L.ring;  // the sums take the ring's place after the last step
     L.part = L.ring + ring_bytes;
     L.total = L.part + (uint32_t)(tiles * 128 * 4);
     return L;
 }
 
-template <typename T, int VEC, int SETS, bool PACKED>
-__global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__ GemvW4Params p) {
+template <typename T, bool VEC, int SETS, bool PACKED>
+__global__ void __launch_bounds__(256, VEC ? 2 : 3) gemv_w4_kernel(const __grid_constant__ GemvW4Params p) {
     constexpr int kRows = PACKED ? 8 / SETS : 8;    // rows of x per set of columns
     constexpr int kPasses = PACKED ? 1 : SETS;
     pdl_wait();
     extern __shared__ __align__(128) uint8_t smem[];
-    const W4Layout L = w4_layout(p.R, p.tiles, p.kw, p.steps);
+    constexpr uint32_t kStageBytes = 32 * 2 * 16, kColumn = kStageBytes / 2, kBatchBytes = batch_bytes(VEC);
+    const W4Layout L = w4_layout(p.R, p.tiles, p.kw, p.steps, VEC);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tile = warp / p.kw, kw = warp - tile * p.kw;
     const int g = lane >> 2, t = lane & 3;
@@ -247,6 +252,12 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     // this lane's columns, g and g + 8 of the tile (clamped; the extra ones are not stored)
     const int64_t c0 = min(n0 + g, p.N - 1), c1 = min(n0 + g + 8, p.N - 1);
     const uint8_t *row0 = p.codes + c0 * p.code_stride, *row1 = p.codes + c1 * p.code_stride;
+    const uint32_t shift0 = 8 * (uint32_t)(reinterpret_cast<uintptr_t>(row0) & 3);
+    const uint32_t shift1 = 8 * (uint32_t)(reinterpret_cast<uintptr_t>(row1) & 3);
+    // where this lane's words of the batch's first step lie (VEC false)
+    const uint32_t loose0 = g * kLooseColumn + (uint32_t)(reinterpret_cast<uintptr_t>(row0) & 12) + 16 * t;
+    const uint32_t loose1 = (g + 8) * kLooseColumn + (uint32_t)(reinterpret_cast<uintptr_t>(row1) & 12) + 16 * t;
+    (void)shift0, (void)shift1, (void)loose0, (void)loose1;
     const char *srow0 = p.scales + c0 * p.scale_stride, *srow1 = p.scales + c1 * p.scale_stride;
     const uint8_t *zrow0 = p.zeros + c0 * p.zero_stride, *zrow1 = p.zeros + c1 * p.zero_stride;
     auto fetch = [&](int kb, int left) {
@@ -272,23 +283,29 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
 
     // This warp's batches of steps: in each round of per_round blocks of k (a cluster's blocks
     // take rounds in turn) p.steps consecutive steps.  The copies walk two batches ahead.
-    const uint32_t ring = smem_u32(smem) + L.ring + (uint32_t)warp * kRingBytes + (uint32_t)lane * 16;
+    uint8_t *const mine = smem + L.ring + (uint32_t)warp * 2 * kBatchBytes + (VEC ? (uint32_t)lane * 16 : 0u);
+    const uint32_t ring = smem_u32(mine);
     int next_kb = blockIdx.y * per_round + kw * p.steps, next_left = p.steps;
     auto copy_batch = [&](uint32_t half) {
         const int n = min(min(next_left, kBatch), blocks_k - next_kb);
-        if (n == kBatch && (next_kb + kBatch) * (kBlockK / 2) <= nbytes && VEC == 16) {
+        if (n == kBatch && (next_kb + kBatch) * (kBlockK / 2) <= nbytes && VEC) {
             const uint8_t *a = row0 + next_kb * (kBlockK / 2) + 16 * t, *b = row1 + next_kb * (kBlockK / 2) + 16 * t;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 copy16(half + u * kStageBytes, a + u * (kBlockK / 2));
-                copy16(half + u * kStageBytes + 512, b + u * (kBlockK / 2));
+                copy16(half + u * kStageBytes + kColumn, b + u * (kBlockK / 2));
             }
-        } else {
+        } else if (VEC) {
 #pragma unroll 1
             for (int u = 0; u < n; ++u) {
-                copy_codes<VEC>(half + u * kStageBytes, row0, (next_kb + u) * (kBlockK / 2) + 16 * t, nbytes);
-                copy_codes<VEC>(half + u * kStageBytes + 512, row1, (next_kb + u) * (kBlockK / 2) + 16 * t, nbytes);
+                const int b = (next_kb + u) * (kBlockK / 2) + 16 * t;
+                copy_codes(half + u * kStageBytes, row0, b, nbytes);
+                copy_codes(half + u * kStageBytes + kColumn, row1, b, nbytes);
             }
+        } else if (n > 0) {
+            __syncwarp();  // every lane has read what lay here
+            copy_loose(half, mine + (half - ring), p.codes, p.code_stride, n0, p.N, next_kb * (kBlockK / 2),
+                       n * (kBlockK / 2), nbytes, lane);
         }
         copy_commit();
         next_kb += kBatch;
@@ -299,7 +316,7 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
         }
     };
     copy_batch(ring);
-    copy_batch(ring + kBatch * kStageBytes);
+    copy_batch(ring + kBatchBytes);
 
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t half = 0;
@@ -327,25 +344,36 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
         __syncthreads();
         // this lane's x, column g of the N side; zeros where the column has no row or, with several
         // sets, not this lane's
-        const uint32_t xrow = smem_u32(smem) + t * 16 + (g % kRows) * L.pitch + kw * p.steps * 256;
-        const uint32_t xzero = smem_u32(smem) + t * 16 + L.zero;
+        const uint32_t xrow = t * 16 + (g % kRows) * L.pitch + kw * p.steps * 256, xzero = t * 16 + L.zero;
         uint32_t xs[kPasses], xstep[kPasses];
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const bool mine = g % kRows < p.R && (SETS == 1 || t * SETS / 4 == (PACKED ? g / kRows : i));
-            xs[i] = mine ? xrow : xzero;
-            xstep[i] = mine ? 256 : 0;
+            const bool real = g % kRows < p.R && (SETS == 1 || t * SETS / 4 == (PACKED ? g / kRows : i));
+            xs[i] = real ? xrow : xzero;
+            xstep[i] = real ? 256 : 0;
         }
         for (int st = 0; st < p.steps; st += kBatch) {
             const Scales<SETS> q = ahead;
             if (st + kBatch < nst) ahead = fetch(kb0 + st + kBatch, nst - st - kBatch);
             copy_wait<1>();
+            if (!VEC) __syncwarp();  // the lanes copied for one another
+            // plain loads: the compiler may move a step's loads over the step before
+            auto step = [&](int u) {
+                uint32_t w0[4], w1[4];
+                if (VEC) {
+                    const uint4 v0 = *reinterpret_cast<const uint4 *>(mine + half + u * kStageBytes);
+                    const uint4 v1 = *reinterpret_cast<const uint4 *>(mine + half + u * kStageBytes + kColumn);
+                    w0[0] = v0.x, w0[1] = v0.y, w0[2] = v0.z, w0[3] = v0.w;
+                    w1[0] = v1.x, w1[1] = v1.y, w1[2] = v1.z, w1[3] = v1.w;
+                } else {
+                    const uint32_t *v0 = reinterpret_cast<const uint32_t *>(mine + half + loose0 + u * 64);
+                    const uint32_t *v1 = reinterpret_cast<const uint32_t *>(mine + half + loose1 + u * 64);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (st + u >= nst) break;
-                const uint4 v0 = ld_shared_v4(ring + half + u * kStageBytes);
-                const uint4 v1 = ld_shared_v4(ring + half + u * kStageBytes + 512);
-                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                    for (int c = 0; c < 4; ++c) {
+                        w0[c] = __funnelshift_r(v0[c], v0[c + 1], shift0);
+                        w1[c] = __funnelshift_r(v1[c], v1[c + 1], shift1);
+                    }
+                }
                 const int at = SETS == 1 ? 0 : u;
                 typename Pair<T>::Zero z0 = Pair<T>::zero(q.z0[at] & 15u), z1 = Pair<T>::zero(q.z1[at] & 15u);
                 float s0 = scale_value(q.s0[at], p.scale_dtype), s1 = scale_value(q.s1[at], p.scale_dtype);
@@ -364,7 +392,7 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
                     Pair<T>::unpack(b, w1[c], z1);
 #pragma unroll
                     for (int i = 0; i < kPasses; ++i) {
-                        const uint4 x = ld_shared_v4(xs[i] + c * 64);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + xs[i] + u * xstep[i] + c * 64);
                         if (c == 0) Pair<T>::mma(d[i], a[0], b[0], a[1], b[1], x.x, x.y, none);
                         else Pair<T>::mma(d[i], a[0], b[0], a[1], b[1], x.x, x.y, d[i]);
                         Pair<T>::mma(d[i], a[2], b[2], a[3], b[3], x.z, x.w, d[i]);
@@ -381,11 +409,20 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
                     acc[1] = fmaf(f0, d[i][1], acc[1]);
                     acc[2] = fmaf(f1, d[i][2], acc[2]);
                     acc[3] = fmaf(f1, d[i][3], acc[3]);
-                    xs[i] += xstep[i];
                 }
+            };
+            if (st + kBatch <= nst) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) step(u);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kBatch - 1; ++u)
+                    if (st + u < nst) step(u);
             }
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) xs[i] += kBatch * xstep[i];
             copy_batch(ring + half);
-            half ^= kBatch * kStageBytes;
+            half = kBatchBytes - half;
         }
     }
     copy_wait<0>();
@@ -432,36 +469,29 @@ __global__ void __launch_bounds__(256, 3) gemv_w4_kernel(const __grid_constant__
     cluster_sync();  // keep every block's sums alive until all remote reads are done
 }
 
-template <typename T, int VEC, int SETS, bool PACKED>
+template <typename T, bool VEC, int SETS, bool PACKED>
 cudaError_t run(const GemvW4Params &p, int split, cudaStream_t s) {
     static SmemLimit limit;
     auto kern = gemv_w4_kernel<T, VEC, SETS, PACKED>;
-    const size_t smem = w4_layout(p.R, p.tiles, p.kw, p.steps).total;
+    const size_t smem = w4_layout(p.R, p.tiles, p.kw, p.steps, VEC).total;
     const cudaError_t e = limit.ensure(kern, smem, true);
     if (e != cudaSuccess) return e;
     return launch_ex(kern, dim3((p.N + 16 * p.tiles - 1) / (16 * p.tiles), split), dim3(32 * p.kw * p.tiles), smem, s,
                      dim3(1, split, 1), p.pdl, p);
 }
 
-template <typename T, int VEC>
+template <typename T, bool VEC>
 cudaError_t run_sets(const GemvW4Params &p, int split, cudaStream_t s) {
     if (p.group % 128 == 0) return run<T, VEC, 1, false>(p, split, s);
     if (p.group % 64 == 0) return p.R <= 4 ? run<T, VEC, 2, true>(p, split, s) : run<T, VEC, 2, false>(p, split, s);
     return p.R <= 2 ? run<T, VEC, 4, true>(p, split, s) : run<T, VEC, 4, false>(p, split, s);
 }
 
-template <typename T>
-cudaError_t run_vec(const GemvW4Params &p, int vec, int split, cudaStream_t s) {
-    if (vec == 16) return run_sets<T, 16>(p, split, s);
-    if (vec == 4) return run_sets<T, 4>(p, split, s);
-    return run_sets<T, 1>(p, split, s);
-}
-
 }  // namespace
 
 cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.codes) | (p.N > 1 ? (uintptr_t)p.code_stride : 0);
-    const int vec = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 1;
+    const bool vec = at % 16 == 0;
     const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
     const int64_t col_tiles = (p.N + 15) / 16;
     // k is shared by as many warps as it takes to give every SM about twelve, and no more: a warp costs
@@ -483,9 +513,9 @@ cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const int rounds = (per_warp + most - 1) / most;
     p.steps = (per_warp + rounds - 1) / rounds;
     p.group_shift = (p.group & (p.group - 1)) == 0 ? __builtin_ctz((unsigned)p.group) : -1;
-    if (p.in_dtype == DG_BF16) return run_vec<__nv_bfloat16>(p, vec, split, s);
-    if (p.in_dtype == DG_F16) return run_vec<__half>(p, vec, split, s);
-    return cudaErrorInvalidValue;
+    if (p.in_dtype == DG_BF16)
+        return vec ? run_sets<__nv_bfloat16, true>(p, split, s) : run_sets<__nv_bfloat16, false>(p, split, s);
+    return vec ? run_sets<__half, true>(p, split, s) : run_sets<__half, false>(p, split, s);
 }
 
 }  // namespace dg
