@@ -34,6 +34,7 @@
 // are few columns.  Partial sums meet in shared memory and, across a cluster,
 // in distributed shared memory, in a fixed order.
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "sm100.cuh"
@@ -48,6 +49,7 @@ constexpr int kBlockK = 128;   // k per step of a warp: 16 bytes of codes per la
 // the aligned 16-byte chunks that hold the batch's 256 bytes.
 constexpr uint32_t kLooseColumn = (256 + 16) + 16;
 constexpr int kBatch = 4;      // steps between waits
+constexpr int kMostX = 48 * 1024;  // most bytes of x staged by a block
 __host__ __device__ constexpr uint32_t batch_bytes(bool vec) { return vec ? kBatch * 32 * 2 * 16 : 16 * kLooseColumn; }
 
 // (w & mask) | bits in one instruction (two literals would take two).
@@ -123,6 +125,9 @@ __device__ __forceinline__ void copy_codes(uint32_t to, const uint8_t *row, int 
                  : "memory");
 }
 
+__device__ __forceinline__ void copy16(uint32_t slot, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
+}
 // A batch's codes of 16 columns at any alignment: `bytes` bytes of each column
 // from byte b on, as the aligned 16-byte chunks that hold them (17 for a whole
 // batch; half a warp copies a column's first 16).  Bytes before a column or
@@ -130,6 +135,23 @@ __device__ __forceinline__ void copy_codes(uint32_t to, const uint8_t *row, int 
 // chunk that the column starts inside of is put together byte by byte.
 __device__ __forceinline__ void copy_loose(uint32_t to, uint8_t *to_ptr, const uint8_t *codes, int64_t stride, int n0,
                                            int N, int b, int bytes, int nbytes, int lane) {
+    if (b >= 16 && bytes == kBatch * (kBlockK / 2) && b + bytes + 16 <= nbytes && n0 + 16 <= N) {  // all chunks whole
+        const uint8_t *row = codes + (int64_t)(n0 + (lane >> 4)) * stride;
+        const int64_t step = 2 * stride, off = b + 16 * (lane & 15);
+        uint32_t at = to + (lane >> 4) * kLooseColumn + 16 * (lane & 15);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            copy16(at, reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15)) + off);
+            row += step;
+            at += 2 * kLooseColumn;
+        }
+        if (lane < 16) {
+            const uint8_t *last = codes + (int64_t)(n0 + lane) * stride;
+            copy16(to + lane * kLooseColumn + 256,
+                   reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(last) & ~uintptr_t(15)) + b + 256);
+        }
+        return;
+    }
     auto chunk = [&](int col, int c) {
         const uint8_t *row = codes + (int64_t)min(n0 + col, N - 1) * stride;
         const int d = (int)(reinterpret_cast<uintptr_t>(row) & 15);
@@ -148,14 +170,11 @@ __device__ __forceinline__ void copy_loose(uint32_t to, uint8_t *to_ptr, const u
                 *reinterpret_cast<uint4 *>(to_ptr + col * kLooseColumn + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
         }
     };
-#pragma unroll 4
+#pragma unroll 1
     for (int j = 0; j < 8; ++j) chunk(2 * j + (lane >> 4), lane & 15);
     if (lane < 16) chunk(lane, 16);
 }
 
-__device__ __forceinline__ void copy16(uint32_t slot, const uint8_t *src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -333,11 +352,9 @@ __global__ void __launch_bounds__(256, VEC ? 2 : 3) gemv_w4_kernel(const __grid_
                 for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
                     // position [step][word c][lane t] holds k = 32 t + 8 c ..
                     const int k = (kb_round + (i >> 4)) * kBlockK + 32 * (i & 3) + 8 * ((i >> 2) & 3);
-                    uint4 h;
-                    if (p.x_vec16 && k + 8 <= p.K)
-                        h = *reinterpret_cast<const uint4 *>(p.x.ptr + r * p.x_ld + (int64_t)k * 2);
-                    else
-                        h = x_elements(p.x, r, k, p.K);
+                    const uint4 h = p.x_vec16 && k + 8 <= p.K
+                                        ? *reinterpret_cast<const uint4 *>(p.x.ptr + r * p.x_ld + (int64_t)k * 2)
+                                        : x_elements(p.x, r, k, p.K);
                     *reinterpret_cast<uint4 *>(smem + r * L.pitch + i * 16) = x_pairs(h);
                 }
         }
@@ -494,24 +511,40 @@ cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const bool vec = at % 16 == 0;
     const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
     const int64_t col_tiles = (p.N + 15) / 16;
-    // k is shared by as many warps as it takes to give every SM about twelve, and no more: a warp costs
-    // some hundred instructions besides its steps (1 x 4096 x 14336 on B200: 14.2 us at 12 warps per SM, 15.4 at
-    // 24, 16.1 at 6).  With one or two rows of x within the block first; with more across the cluster
-    // first, whose blocks then stage a smaller slice of x each.
-    int ways = 1;
-    while (ways < 64 && col_tiles * ways < (int64_t)num_sms * 12 && ways * 2 <= blocks_k) ways *= 2;
-    const int first = std::min(ways, 8), second = ways / first;
-    const int split = p.R > 2 ? first : second;
-    p.kw = p.R > 2 ? second : first;
-    // blocks of eight warps share a slice of x between more column tiles; four where that is cheap (few rows)
-    // and k is not shared, or the slices are small (8 x 14336 x 4096: 31 us with eight, 55 with four;
-    // 3 x 5000 x 5003: 18 and 15.8; 1 x 4096 x 128000: 78 and 73)
-    const int warps = (p.R > 4 || (p.R <= 2 && ways > 1)) ? 8 : 4;
-    p.tiles = std::max(1, warps / p.kw);
-    const int most = std::max(1, 48 * 1024 / (p.R * kBlockK * 2 * p.kw));  // steps whose x fits 48 KB
-    const int per_warp = (blocks_k + p.kw * split - 1) / (p.kw * split);
-    const int rounds = (per_warp + most - 1) / most;
-    p.steps = (per_warp + rounds - 1) / rounds;
+    // How many warps share k (`ways`, within the block first, or across the cluster first, whose blocks
+    // then stage a smaller slice of x each) and how many warps a block has.  The cheapest by a model in units of a warp's step: an SM's warps take turns, a warp
+    // costs about five steps besides its own, staging a chunk of x a third of one, a round of x staged
+    // behind the first eight, a cluster's exchange two; fourteen warps or fewer wait on latencies and take
+    // the same time.  Blocks that do not fit at once cost whole waves while there are few waves
+    // (1 x 10293 x 31689: 121 us in 1.1 waves, 97 in one).
+    double least = 0;
+    int split = 1;
+    for (int ways = 1; ways <= 64 && (ways == 1 || ways <= blocks_k); ways *= 2)
+        for (int option = 0; option < 4; ++option) {
+            const int warps = option & 1 ? 8 : 4;
+            const int first = std::min(ways, 8), second = ways / first;
+            const int sp = option & 2 ? first : second, kw = option & 2 ? second : first;
+            const int tiles = std::max(1, warps / kw);
+            const int most = std::max(1, kMostX / (p.R * kBlockK * 2 * kw));  // steps whose x fits
+            const int per_warp = (blocks_k + kw * sp - 1) / (kw * sp);
+            const int rounds = (per_warp + most - 1) / most, steps = (per_warp + rounds - 1) / rounds;
+            const int64_t blocks = (col_tiles + tiles - 1) / tiles * sp;
+            const int64_t smem = w4_layout(p.R, tiles, kw, steps, vec).total + 1024;
+            const int64_t fit = std::min<int64_t>((vec ? 16 : 24) / (kw * tiles), 228 * 1024 / smem);
+            const int64_t resident = std::min<int64_t>(fit, (blocks + num_sms - 1) / num_sms);
+            double waves = (double)blocks / (double)(resident * num_sms);
+            waves = waves <= 3 ? std::ceil(waves) : waves + 0.3;
+            const double chunks = (double)p.R * kw * steps * 16 / (32 * kw * tiles);
+            const double work = rounds * (steps + chunks / 3) + 5 + 8 * (rounds - 1) + (sp > 1 ? 2 : 0);
+            const double cost = waves * work * std::max<double>(14, (double)(resident * kw * tiles));
+            if (least == 0 || cost < least) {
+                least = cost;
+                p.kw = kw;
+                p.tiles = tiles;
+                p.steps = steps;
+                split = sp;
+            }
+        }
     p.group_shift = (p.group & (p.group - 1)) == 0 ? __builtin_ctz((unsigned)p.group) : -1;
     if (p.in_dtype == DG_BF16)
         return vec ? run_sets<__nv_bfloat16, true>(p, split, s) : run_sets<__nv_bfloat16, false>(p, split, s);
