@@ -49,6 +49,7 @@ constexpr int kBlockK = 128;   // k per step of a warp: 16 bytes of codes per la
 // the aligned 16-byte chunks that hold the batch's 256 bytes.
 constexpr uint32_t kLooseColumn = (256 + 16) + 16;
 constexpr int kBatch = 4;      // steps between waits
+constexpr int kMaxWarps = 16;  // per block; at 128 registers a thread also per SM
 constexpr int kMostX = 48 * 1024;  // most bytes of x staged by a block
 __host__ __device__ constexpr uint32_t batch_bytes(bool vec) { return vec ? kBatch * 32 * 2 * 16 : 16 * kLooseColumn; }
 
@@ -253,7 +254,7 @@ __host__ __device__ inline W4Layout w4_layout(int R, int tiles, int kw, int step
 }
 
 template <typename T, bool VEC, int SETS, bool PACKED>
-__global__ void __launch_bounds__(256, VEC ? 2 : 3) gemv_w4_kernel(const __grid_constant__ GemvW4Params p) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) gemv_w4_kernel(const __grid_constant__ GemvW4Params p) {
     constexpr int kRows = PACKED ? 8 / SETS : 8;    // rows of x per set of columns
     constexpr int kPasses = PACKED ? 1 : SETS;
     pdl_wait();
@@ -504,51 +505,87 @@ cudaError_t run_sets(const GemvW4Params &p, int split, cudaStream_t s) {
     return p.R <= 2 ? run<T, VEC, 4, true>(p, split, s) : run<T, VEC, 4, false>(p, split, s);
 }
 
+// The shape of the launch: kw warps of a block share k, and `split` blocks of a cluster (which then stage
+// a smaller slice of x each); a block has `tiles` tiles of columns.  The cheapest by a model in units
+// of a warp's step: an SM's warps take turns, a warp costs about five steps besides its own, staging a
+// chunk of x a third of one, a round of x behind the first eight, a cluster's exchange two; fourteen
+// warps or fewer wait on latencies and take the same time.  Blocks that do not fit at once cost whole
+// waves while there are few (B200: 1 x 10293 x 31689 121 us in 1.1 waves, 70 in one; 8 x 10240 x 31689
+// 80 us with two blocks of eight warps per SM, 62 with one of sixteen; 1 x 4096 x 128000 73 us with
+// four of four, 85 with one of sixteen).
+struct Shape {
+    int kw = 1, tiles = 1, steps = 1, split = 1;
+};
+Shape best_shape(const GemvW4Params &p, bool vec, int num_sms) {
+    const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
+    const int64_t col_tiles = (p.N + 15) / 16;
+    Shape best;
+    double least = 0;
+    for (int i = 0; i < 16 * kMaxWarps; ++i) {
+        const int kw = 1 << (i & 3), split = 1 << (i >> 2 & 3), tiles = (i >> 4) + 1;
+        if ((kw > 1 || split > 1) && kw * split > blocks_k) continue;
+        if (tiles * kw > kMaxWarps || (tiles > 1 && tiles > col_tiles)) continue;
+        if (tiles * kw < 4 && tiles < col_tiles) continue;  // blocks of four warps and more
+        const int most = std::max(1, kMostX / (p.R * kBlockK * 2 * kw));  // steps whose x fits
+        const int per_warp = (blocks_k + kw * split - 1) / (kw * split);
+        const int rounds = (per_warp + most - 1) / most, steps = (per_warp + rounds - 1) / rounds;
+        const int64_t blocks = (col_tiles + tiles - 1) / tiles * split;
+        const int64_t smem = w4_layout(p.R, tiles, kw, steps, vec).total + 1024;
+        const int64_t fit = std::min<int64_t>(kMaxWarps / (kw * tiles), 228 * 1024 / smem);
+        if (fit == 0) continue;
+        const int64_t resident = std::min<int64_t>(fit, (blocks + num_sms - 1) / num_sms);
+        // a cluster's blocks lie in one group of some 18 SMs, not all of which are filled
+        const double spread = split < 4 ? 1 : resident > 1 ? 0.9 : split == 4 ? 0.85 : 0.75;
+        double waves = (double)blocks / (spread * (double)(resident * num_sms));
+        waves = waves <= 3 ? std::ceil(waves) : waves + 0.3;
+        const double chunks = (double)p.R * kw * steps * 16 / (32 * kw * tiles);
+        const double alone = waves > 1 ? 8.0 / (double)(resident * resident) : 0;  // little runs while a block starts
+        const double work = rounds * (steps + chunks / 3) + 5 + alone + 8 * (rounds - 1) + (split > 1 ? 2 : 0);
+        const double cost = waves * work * std::max<double>(14, (double)(resident * kw * tiles));
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = Shape{kw, tiles, steps, split};
+        }
+    }
+    return best;
+}
+
+// A thread's latest shapes, by the sizes they depend on (finding one takes
+// as long as launching).
+struct ShapeKey {
+    int R, K, N, vec, num_sms;
+};
+Shape shape_of(const GemvW4Params &p, bool vec, int num_sms) {
+    constexpr int kKept = 16;
+    static thread_local ShapeKey keys[kKept] = {};
+    static thread_local Shape shapes[kKept];
+    static thread_local int next = 0;
+    const ShapeKey key{p.R, p.K, p.N, vec ? 1 : 0, num_sms};
+    for (int i = 0; i < kKept; ++i)
+        if (keys[i].R == key.R && keys[i].K == key.K && keys[i].N == key.N && keys[i].vec == key.vec &&
+            keys[i].num_sms == key.num_sms)
+            return shapes[i];
+    const Shape s = best_shape(p, vec, num_sms);
+    keys[next] = key;
+    shapes[next] = s;
+    next = (next + 1) % kKept;
+    return s;
+}
+
 }  // namespace
 
 cudaError_t launch_gemv_w4(GemvW4Params p, int num_sms, cudaStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.codes) | (p.N > 1 ? (uintptr_t)p.code_stride : 0);
     const bool vec = at % 16 == 0;
-    const int blocks_k = (p.K + kBlockK - 1) / kBlockK;
-    const int64_t col_tiles = (p.N + 15) / 16;
-    // How many warps share k (`ways`, within the block first, or across the cluster first, whose blocks
-    // then stage a smaller slice of x each) and how many warps a block has.  The cheapest by a model in units of a warp's step: an SM's warps take turns, a warp
-    // costs about five steps besides its own, staging a chunk of x a third of one, a round of x staged
-    // behind the first eight, a cluster's exchange two; fourteen warps or fewer wait on latencies and take
-    // the same time.  Blocks that do not fit at once cost whole waves while there are few waves
-    // (1 x 10293 x 31689: 121 us in 1.1 waves, 97 in one).
-    double least = 0;
-    int split = 1;
-    for (int ways = 1; ways <= 64 && (ways == 1 || ways <= blocks_k); ways *= 2)
-        for (int option = 0; option < 4; ++option) {
-            const int warps = option & 1 ? 8 : 4;
-            const int first = std::min(ways, 8), second = ways / first;
-            const int sp = option & 2 ? first : second, kw = option & 2 ? second : first;
-            const int tiles = std::max(1, warps / kw);
-            const int most = std::max(1, kMostX / (p.R * kBlockK * 2 * kw));  // steps whose x fits
-            const int per_warp = (blocks_k + kw * sp - 1) / (kw * sp);
-            const int rounds = (per_warp + most - 1) / most, steps = (per_warp + rounds - 1) / rounds;
-            const int64_t blocks = (col_tiles + tiles - 1) / tiles * sp;
-            const int64_t smem = w4_layout(p.R, tiles, kw, steps, vec).total + 1024;
-            const int64_t fit = std::min<int64_t>((vec ? 16 : 24) / (kw * tiles), 228 * 1024 / smem);
-            const int64_t resident = std::min<int64_t>(fit, (blocks + num_sms - 1) / num_sms);
-            double waves = (double)blocks / (double)(resident * num_sms);
-            waves = waves <= 3 ? std::ceil(waves) : waves + 0.3;
-            const double chunks = (double)p.R * kw * steps * 16 / (32 * kw * tiles);
-            const double work = rounds * (steps + chunks / 3) + 5 + 8 * (rounds - 1) + (sp > 1 ? 2 : 0);
-            const double cost = waves * work * std::max<double>(14, (double)(resident * kw * tiles));
-            if (least == 0 || cost < least) {
-                least = cost;
-                p.kw = kw;
-                p.tiles = tiles;
-                p.steps = steps;
-                split = sp;
-            }
-        }
+    const Shape shape = shape_of(p, vec, num_sms);
+    p.kw = shape.kw;
+    p.tiles = shape.tiles;
+    p.steps = shape.steps;
     p.group_shift = (p.group & (p.group - 1)) == 0 ? __builtin_ctz((unsigned)p.group) : -1;
     if (p.in_dtype == DG_BF16)
-        return vec ? run_sets<__nv_bfloat16, true>(p, split, s) : run_sets<__nv_bfloat16, false>(p, split, s);
-    return vec ? run_sets<__half, true>(p, split, s) : run_sets<__half, false>(p, split, s);
+        return vec ? run_sets<__nv_bfloat16, true>(p, shape.split, s)
+                   : run_sets<__nv_bfloat16, false>(p, shape.split, s);
+    return vec ? run_sets<__half, true>(p, shape.split, s) : run_sets<__half, false>(p, shape.split, s);
 }
 
 }  // namespace dg
