@@ -1,7 +1,7 @@
 /*
  * libdg — strided-view GEMM for NVIDIA B200 (sm_100a).
  *
- * C ABI.  Every entry point computes (part of) the deep-learning GEMM
+ * C ABI.  Most entry points compute (part of) the deep-learning GEMM
  *
  *     C[m][n] = alpha * sa[m] * sb[n] * sum_k A[m][k] * B[k][n]  +  beta * C[m][n]
  *
@@ -9,7 +9,9 @@
  * template of §4.1; "DeepGEMM deep dive", §1.1 for the operation and §2.4 for
  * the FP8 rescale), with FP32 accumulation, over operands given as strided
  * "views" that are read in place (recalibration page, §2.1-§2.2: no reshape or
- * contiguous() copy).
+ * contiguous() copy).  Two more serve the same weights in language models:
+ * dg_gemv_w4 (products with 4-bit weights) and dg_linear_ce /
+ * dg_linear_ce_grad (the loss of an output layer, and its gradient).
  *
  * Conventions shared by all entry points
  *  - Memory: the caller owns every buffer.  Data pointers are DEVICE pointers
@@ -59,13 +61,16 @@ typedef enum {
     DG_OK = 0,
     DG_ERR_NULL = 1,        /* a required pointer is NULL                        */
     DG_ERR_NDIM = 2,        /* ndim not in 1..4 or row_dims not in 0..ndim        */
-    DG_ERR_SHAPE = 3,       /* negative size, or A/B/C sizes disagree (K, M, N)   */
+    DG_ERR_SHAPE = 3,       /* negative size, or A/B/C sizes disagree (K, M, N);
+                               a workspace that is too small                     */
     DG_ERR_DTYPE = 4,       /* unsupported type or A/B type mismatch              */
     DG_ERR_STRIDE = 5,      /* negative stride, byte extent overflows int64, or
                                C has two elements at one address                 */
     DG_ERR_ALIGN = 6,       /* pointer or stride not a multiple of the element    */
     DG_ERR_POINTER = 7,     /* pointer is not device-accessible                   */
-    DG_ERR_VALUE = 8,       /* alpha or beta not finite                           */
+    DG_ERR_VALUE = 8,       /* alpha or beta not finite; a bad activation, group or
+                               reserved field; a target out of range (reported by
+                               dg_sync_status)                                   */
     DG_ERR_UNSUPPORTED = 9, /* valid request this build does not implement        */
     DG_ERR_CUDA = 10,       /* a CUDA runtime call failed                          */
     DG_ERR_TIMEOUT = 11     /* a device-side wait gave up (see dg_sync_status)    */
@@ -218,8 +223,9 @@ typedef struct {
  * BF16; read only when beta != 0), any strided views; epilogue as in
  * dg_gemm_ex, or NULL.
  *  Arithmetic: code - zero is an exact small integer, its products with x are
- *  summed in FP32 over each group, and the group's sum is multiplied by its
- *  scale in FP32; nothing is rounded to fewer bits before y is stored.
+ *  summed in FP32 within each group (128 k at a time), and the sums are
+ *  multiplied by their scale in FP32; nothing is rounded to fewer bits before y
+ *  is stored.
  *  Partial sums are added in a fixed order: runs are bit-identical.  A NaN or
  *  infinity in x meets every weight (infinity times a weight of 0 is NaN).
  *  alpha == 0 or K == 0 reads neither x nor W.
@@ -242,8 +248,9 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y,
  *
  * The logits exist one piece of the vocabulary at a time: in the tensor
  * core's accumulators, where the epilogue reduces each row of a tile to its
- * maximum and its sum of exponentials, or, for few rows and for operands that
- * the paired tensor-core tiles do not take, in a piece of the workspace.
+ * maximum and its sum of exponentials, or, for operands that the paired
+ * tensor-core tiles do not take (F32, a W that no tensor map covers), in a
+ * piece of the workspace.
  *
  *  X [T x D], W [D x V]: views of one type, F16 or BF16 (tensor cores) or F32
  *    (CUDA cores).  X may be any view of up to 4 dims (e.g. all tokens but
@@ -282,10 +289,12 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W,
  *    overlap X, W or the other.
  *  workspace as above, from dg_linear_ce_grad_workspace.
  * G is held one piece of the vocabulary at a time, rounded to the type of X
- * (as the gradient of logits of that type would be; F16 pieces are scaled by a
- * power of two found on the device, so that neither small probabilities nor a
- * loss scale leave F16's range), and the products are summed in FP32 over all
- * pieces; dX and dW are rounded once.
+ * (as the gradient of logits of that type would be).  16-bit pieces are first
+ * divided by the largest |dloss| of a row that counts, found on the device, and
+ * multiplied back in FP32: a gradient that all rows share then costs no
+ * rounding, and neither small probabilities nor a loss scale leave F16's range.
+ * The products are summed in FP32 over all pieces; dX and dW are rounded once.
+ * Runs are bit-identical.
  */
 dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W,
                             const int64_t *target, int64_t ignore_index,

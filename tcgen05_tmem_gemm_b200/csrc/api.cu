@@ -1574,12 +1574,12 @@ const char *dg_status_string(dg_status s) {
     case DG_OK: return "ok";
     case DG_ERR_NULL: return "null pointer";
     case DG_ERR_NDIM: return "ndim must be 1..4 and row_dims 0..ndim";
-    case DG_ERR_SHAPE: return "shape mismatch or negative size";
+    case DG_ERR_SHAPE: return "shape mismatch, negative size or workspace too small";
     case DG_ERR_DTYPE: return "unsupported element type combination";
     case DG_ERR_STRIDE: return "negative/overflowing stride or overlapping output";
     case DG_ERR_ALIGN: return "pointer or stride not a multiple of the element size";
     case DG_ERR_POINTER: return "pointer is not device memory of the current device";
-    case DG_ERR_VALUE: return "alpha or beta is not finite";
+    case DG_ERR_VALUE: return "a value is out of range or not finite";
     case DG_ERR_UNSUPPORTED: return "request not supported";
     case DG_ERR_CUDA: return "CUDA runtime error";
     case DG_ERR_TIMEOUT: return "a device-side wait timed out";
