@@ -206,6 +206,114 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Up to kFewRows rows against a W whose columns are contiguous (a [V x D]
+// weight): a dot product per row and column on the CUDA cores, bound by W's
+// bytes (the paired tiles multiply 256 rows whatever there are).  A warp takes
+// a column at a time, eight 16-byte loads a lane in flight; x is held in shared
+// memory as FP32, and after the reduction over the warp lane t owns row t: its
+// running (m, s), or its element of G.  Every block leaves one slot of pairs.
+// 4096 x 32000 on B200: 49 us for one row (5.3 TB/s), 62 for two, 100 for four;
+// the tiles take 75 for any of them.
+constexpr int kFewRows = 2;
+constexpr int kFewBlocks = 512;        // most blocks: slots of pairs
+constexpr int kFewLoads = 8;
+template <typename T, int R, bool GRAD>
+__global__ void __launch_bounds__(256, 3)
+    ce_few_kernel(const DevView x, const char *w, int64_t ldw, int D, int rows, int v0, int cols, float alpha,
+                  const CeTile ce, char *g, int64_t ldg) {
+    pdl_wait_then_release();
+    extern __shared__ float xs[];  // [row][chunk of 256][half][lane][4]
+    __shared__ float2 red[8][kFewRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pitch = (D + 255) / 256 * 256;
+    for (int r = 0; r < R; ++r) {
+        const char *row = x.ptr + axis_offset(x.row, r < rows ? r : 0);
+#pragma unroll 4
+        for (int d = threadIdx.x; d < pitch; d += 256) {
+            const float v = r < rows && d < D ? load_elem(row + axis_offset(x.col, d), x.dtype) : 0.f;
+            xs[r * pitch + (d & ~255) + ((d >> 2) & 1) * 128 + ((d >> 3) & 31) * 4 + (d & 3)] = v;
+        }
+    }
+    __syncthreads();
+    RowGrad mine{0.f, 0.f, kIgnored, 0};
+    int y = kIgnored;
+    if (lane < rows) {
+        if (GRAD) mine = ce.rows[lane];
+        else y = read_target(ce.target, ce.ignore_index, ce.V, lane);
+    }
+    float m = -INFINITY, s = 0.f;
+    const int chunks = pitch / 256;
+    for (int c = blockIdx.x * 8 + warp; c < cols; c += gridDim.x * 8) {
+        const char *col = w + (int64_t)c * ldw + lane * 16;
+        float acc[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = 0.f;
+        for (int q0 = 0; q0 < chunks; q0 += kFewLoads) {
+            uint4 v[kFewLoads];
+#pragma unroll
+            for (int q = 0; q < kFewLoads; ++q) {
+                v[q] = make_uint4(0u, 0u, 0u, 0u);
+                if ((q0 + q) * 256 + lane * 8 < D) v[q] = __ldcs(reinterpret_cast<const uint4 *>(col + (q0 + q) * 512));
+            }
+#pragma unroll
+            for (int q = 0; q < kFewLoads; ++q) {
+                if (q0 + q >= chunks) break;
+                float f[8];
+                const uint32_t h[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
+                        f[2 * i] = __uint_as_float(h[i] << 16);
+                        f[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
+                    } else {
+                        const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                        f[2 * i] = t.x;
+                        f[2 * i + 1] = t.y;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float4 *xr = reinterpret_cast<const float4 *>(xs + r * pitch + (q0 + q) * 256) + lane;
+                    const float4 a = xr[0], b = xr[32];
+                    acc[r] = fmaf(a.x, f[0], acc[r]);
+                    acc[r] = fmaf(a.y, f[1], acc[r]);
+                    acc[r] = fmaf(a.z, f[2], acc[r]);
+                    acc[r] = fmaf(a.w, f[3], acc[r]);
+                    acc[r] = fmaf(b.x, f[4], acc[r]);
+                    acc[r] = fmaf(b.y, f[5], acc[r]);
+                    acc[r] = fmaf(b.z, f[6], acc[r]);
+                    acc[r] = fmaf(b.w, f[7], acc[r]);
+                }
+            }
+        }
+        float z[1] = {0.f};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
+            if (lane == r) z[0] = alpha * acc[r];
+        }
+        if (lane < rows) {
+            if (GRAD) {
+                float v = 0.f;
+                if (mine.target >= 0)
+                    v = mine.scale * (exp_fast(z[0] - mine.lse) - (v0 + c == mine.target ? 1.f : 0.f));
+                store_elem(g + lane * ldg + (int64_t)c * 2, x.dtype, v);
+            } else {
+                join_logits(m, s, z);
+                if (y == v0 + c) ce.ztarget[lane] = z[0];
+            }
+        }
+    }
+    if (GRAD) return;
+    if (lane < kFewRows) red[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        for (int i = 1; i < 8; ++i) join(m, s, red[i][lane].x, red[i][lane].y);
+        ce.part[(int64_t)blockIdx.x * ce.T + lane] = make_float2(m, s);
+    }
+}
+
 // A piece of FP32 logits to the piece of G.
 __global__ void __launch_bounds__(256)
     ce_grad_kernel(const float *z, int64_t ldz, int64_t T, int v0, int cols, const RowGrad *rows, char *g, int64_t ldg,
@@ -336,6 +444,40 @@ bool tiles_worth_it(const Problem &p, int num_sms) {
            (((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms || p.T > 64 || p.D <= kShortDim);
 }
 
+// Whether ce_few_kernel makes the logits.
+bool few_rows(const Problem &p) {
+    return p.tensor && p.T <= kFewRows && p.D > 0 && p.D % 8 == 0 && p.w.unit_dim == 2 && p.w.tma_ok &&
+           p.T * ((p.D + 255) / 256 * 256) * 4 <= 64 * 1024;
+}
+
+template <typename T, int R, bool GRAD>
+cudaError_t run_few(const Problem &p, const DevView &x, const char *w, int v0, int cols, float alpha, const CeTile &ce,
+                    char *g, int64_t ldg, int blocks, int pdl, cudaStream_t s) {
+    static SmemLimit limit;
+    const size_t smem = (size_t)R * ((p.D + 255) / 256 * 256) * 4;
+    const cudaError_t e = limit.ensure(ce_few_kernel<T, R, GRAD>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(ce_few_kernel<T, R, GRAD>, dim3(blocks), dim3(256), smem, s, dim3(1, 1, 1), pdl, x, w, p.wm.cs,
+                     (int)p.D, (int)p.T, v0, cols, alpha, ce, g, ldg);
+}
+
+// The blocks of a launch over `cols` columns: three per SM, which is what their registers allow.
+int few_blocks(int64_t cols, int num_sms) {
+    return (int)std::min<int64_t>((cols + 7) / 8, std::min<int64_t>(3 * num_sms, kFewBlocks));
+}
+
+template <bool GRAD>
+cudaError_t launch_few(const Problem &p, const DevView &x, const char *w, int v0, int cols, float alpha,
+                       const CeTile &ce, char *g, int64_t ldg, int num_sms, int pdl, cudaStream_t s) {
+    const int blocks = few_blocks(cols, num_sms);
+    const bool b = x.dtype == DG_BF16;
+    if (p.T == 1)
+        return b ? run_few<__nv_bfloat16, 1, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s)
+                 : run_few<__half, 1, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s);
+    return b ? run_few<__nv_bfloat16, 2, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s)
+             : run_few<__half, 2, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s);
+}
+
 // 16-byte rows of X for its copy.
 int x_vec(const dg_view *X, const Problem &p) {
     bool ok = p.x.col.n <= 1 && (p.x.col.n == 0 || p.x.col.stride[0] == p.es) && p.D * p.es % 16 == 0 &&
@@ -354,15 +496,19 @@ CeTile tile_of(const Problem &p, const int64_t *target, int64_t ignore_index, in
     return c;
 }
 
-Layout forward_layout(const Problem &p, int64_t piece, bool tiles) {
+// How the logits are made: FP32 pieces in the workspace, tiles of the CTA-pair
+// kernel, or the dot products of a few rows (the whole vocabulary at once).
+enum Way { kPieces, kTiles, kFew };
+
+Layout forward_layout(const Problem &p, int64_t piece, Way way) {
     Layout l;
     l.ldx = align256(p.D * p.es);
     l.ldz = align256(piece * 4);
-    l.xc = take(&l, forward_copies_x(p) ? p.T * l.ldx : 0);
-    l.part = take(&l, (tiles ? tile_slots(piece) : stat_slots(piece)) * p.T * 8);
+    l.xc = take(&l, way != kFew && forward_copies_x(p) ? p.T * l.ldx : 0);
+    l.part = take(&l, (way == kFew ? kFewBlocks : way == kTiles ? tile_slots(piece) : stat_slots(piece)) * p.T * 8);
     l.run = take(&l, p.T * 8);
     l.ztarget = take(&l, p.T * 4);
-    l.z = take(&l, tiles ? 0 : p.T * l.ldz);
+    l.z = take(&l, way == kPieces ? p.T * l.ldz : 0);
     return l;
 }
 
@@ -386,7 +532,7 @@ int plane_count(int64_t M, int64_t N, int64_t K, int num_sms) {
 }
 int64_t plane_bytes(int64_t M, int64_t N, int planes) { return planes * ((M + 255) / 256 * 256) * align256(N * 4); }
 
-// Those of dX (up to four rows the GEMV over W's rows serves) and of a piece of dW.
+// Those of dX (for one row the GEMV over W's rows serves) and of a piece of dW.
 struct Planes {
     int dx = 0, dw = 0;
 };
@@ -394,7 +540,7 @@ Planes plan_planes(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     Planes n;
     if (!p.tensor) return n;
     const int64_t cols = std::min(piece, p.V);
-    if (need_dx && p.T > 4) n.dx = plane_count(p.T, p.D, cols, num_sms);
+    if (need_dx && p.T > 1) n.dx = plane_count(p.T, p.D, cols, num_sms);
     if (need_dw) n.dw = p.dw.unit_dim == 2 ? plane_count(cols, p.D, p.T, num_sms) : plane_count(p.D, cols, p.T, num_sms);
     return n;
 }
@@ -433,8 +579,9 @@ int64_t piece_for(const Problem &p, int64_t bytes, int64_t per_col) {
 
 // The largest useful pieces: of logits, of the tiles' pairs (64 bytes of
 // pairs per row and 1024 columns), of G.
-int64_t forward_piece(const Problem &p, bool tiles) {
-    if (!tiles) return piece_for(p, kForwardPiece, p.T * 4);
+int64_t forward_piece(const Problem &p, Way way) {
+    if (way == kFew) return p.V;
+    if (way == kPieces) return piece_for(p, kForwardPiece, p.T * 4);
     const int64_t cols = kForwardPiece / (std::max<int64_t>(p.T, 1) * 8) * kSlotCols;
     return cols >= p.V ? p.V : std::max<int64_t>(cols / kPieceCols * kPieceCols, kPieceCols);
 }
@@ -487,9 +634,9 @@ dg_status dg_linear_ce_workspace(const dg_view *X, const dg_view *W, int64_t *le
     if (!least || !best) return DG_ERR_NULL;
     Problem p;
     DG_TRY(check_problem(X, W, &p));
-    const bool tiles = tiles_worth_it(p, kUsualSms);
-    *least = forward_layout(p, piece_min(p), false).total;
-    *best = std::max(*least, forward_layout(p, forward_piece(p, tiles), tiles).total);
+    const Way way = few_rows(p) ? kFew : tiles_worth_it(p, kUsualSms) ? kTiles : kPieces;
+    *least = forward_layout(p, piece_min(p), kPieces).total;
+    *best = std::max(*least, forward_layout(p, forward_piece(p, way), way).total);
     return DG_OK;
 }
 
@@ -503,7 +650,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     if (reinterpret_cast<uintptr_t>(target) % 8 || reinterpret_cast<uintptr_t>(loss) % 4 ||
         reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256)
         return DG_ERR_ALIGN;
-    if (forward_layout(p, piece_min(p), false).total > workspace_bytes) return DG_ERR_SHAPE;
+    if (forward_layout(p, piece_min(p), kPieces).total > workspace_bytes) return DG_ERR_SHAPE;
     int num_sms = 0, *err_word = nullptr;
     DG_TRY(device_info(&num_sms, &err_word));
     if ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
@@ -515,17 +662,19 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     const dim3 one(1, 1, 1);
     // the copy of X, if there is one, comes first in the workspace
     const dg_view xv = forward_copies_x(p) ? view2(ws, p.T, p.D, align256(p.D * p.es), p.es, X->dtype) : *X;
-    bool tiles = tiles_worth_it(p, num_sms);
-    if (tiles) {
+    Way way = kPieces;
+    if (few_rows(p) && forward_layout(p, p.V, kFew).total <= workspace_bytes) {
+        way = kFew;
+    } else if (tiles_worth_it(p, num_sms)) {
         CeTile ce = tile_of(p, target, ignore_index, 0);
         ce.part = reinterpret_cast<float2 *>(ws);
-        tiles = pair_once(PairCall{&xv, W, nullptr, alpha, nullptr, kPairStats, ce, 0, true}, s) == DG_OK;
+        if (pair_once(PairCall{&xv, W, nullptr, alpha, nullptr, kPairStats, ce, 0, true}, s) == DG_OK) way = kTiles;
     }
-    auto layout_of = [&](int64_t piece) { return forward_layout(p, piece, tiles); };
-    const int64_t piece = fit_piece(p, workspace_bytes, forward_piece(p, tiles), layout_of);
+    auto layout_of = [&](int64_t piece) { return forward_layout(p, piece, way); };
+    const int64_t piece = fit_piece(p, workspace_bytes, forward_piece(p, way), layout_of);
     if (piece == 0) return DG_ERR_SHAPE;
     const Layout l = layout_of(piece);
-    if (forward_copies_x(p)) {
+    if (way != kFew && forward_copies_x(p)) {
         DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x),
                                   (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
                                   (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f, (RowGrad *)nullptr,
@@ -538,7 +687,14 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
         const dg_view wv = view2(p.wm.ptr + v0 * p.wm.cs, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
         const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
         int slots;
-        if (tiles) {
+        if (way == kFew) {
+            CeTile ce = tile_of(p, target, ignore_index, v0);
+            ce.part = part;
+            ce.ztarget = ztarget;
+            DG_TRY(launched(launch_few<false>(p, dev_of(X, p.x), p.wm.ptr, 0, (int)cols, alpha, ce, nullptr, 0, num_sms,
+                                              pdl, s)));
+            slots = few_blocks(cols, num_sms);
+        } else if (way == kTiles) {
             CeTile ce = tile_of(p, target, ignore_index, v0);
             ce.part = part;
             ce.ztarget = ztarget;
@@ -639,7 +795,7 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W, const 
     const int dxt = dX ? dX->dtype : DG_F32;
     *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total;
     *best = std::max(*least, grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt,
-                                         tiles_worth_it(p, kUsualSms),
+                                         few_rows(p) || tiles_worth_it(p, kUsualSms),
                                          plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, kUsualSms))
                                  .total);
     return DG_OK;
@@ -685,14 +841,15 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     const int64_t ldx = align256(p.D * p.es);
     const dg_view xv = copy ? view2(ws, p.T, p.D, ldx, p.es, X->dtype) : *X;
     const dg_view xt = view2(ws, p.D, p.T, p.es, ldx, X->dtype);
-    bool tiles = tiles_worth_it(p, num_sms);
+    const bool few = few_rows(p);
+    bool tiles = few || tiles_worth_it(p, num_sms);  // no FP32 logits in the workspace
     Planes planes = plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, num_sms);
     auto layout_of = [&](int64_t piece) {
         return grad_layout(p, piece, dX != nullptr, dW != nullptr, dxt, tiles, planes);
     };
     if (layout_of(grad_piece(p)).total > workspace_bytes) planes = Planes{};  // a small workspace has room for G only
     int64_t piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
-    if (tiles) {
+    if (tiles && !few) {
         // the tensor stores of G take pieces of 64 columns or more, the last one too
         while (piece > 0 && piece < p.V && p.V % piece != 0 && p.V % piece < 64) piece -= kPieceCols;
         if (piece > 0) {
@@ -744,7 +901,12 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         const dg_view wt = view2(wp, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
         const dg_view gv = view2(g, p.T, cols, l.ldg, p.es, X->dtype);
         const dg_view gt = view2(g, cols, p.T, p.es, l.ldg, X->dtype);
-        if (tiles) {
+        if (few) {
+            CeTile ce = tile_of(p, target, ignore_index, v0);
+            ce.rows = rows;
+            DG_TRY(launched(launch_few<true>(p, dev_of(X, p.x), wp, (int)v0, (int)cols, alpha, ce, g, l.ldg, num_sms,
+                                             pdl, s)));
+        } else if (tiles) {
             CeTile ce = tile_of(p, target, ignore_index, v0);
             ce.rows = rows;
             DG_TRY(pair_once(PairCall{&xv, &wv, &gv, alpha, nullptr, kPairGrad, ce, 0, false}, s));

@@ -169,6 +169,20 @@ def test_paired_tiles_with_few_rows(T, out):
     run_both(T, 192, 19000, "bf16", out=out)
 
 
+def test_very_wide_rows():
+    run_both(3, 20000, 70, "bf16")
+    run_both(130, 16392, 300, "f16", order="dv")
+
+
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("D,V", [(8, 1), (8, 9), (256, 100), (264, 4001), (4096, 3000), (7680, 50), (9000, 70)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_one_and_two_rows(T, D, V, dtype):
+    # dot products against a [V x D] weight, and what they leave to the tiles (wide rows)
+    run_both(T, D, V, dtype, ignored=0.0)
+    run_both(T, D, V, dtype, out="f32", alpha=0.5, ignored=0.6, order="dv")
+
+
 @pytest.mark.parametrize("T,D,V", [(3000, 64, 300), (2500, 100, 65), (2049, 520, 1000), (5000, 32, 64), (700, 2048, 64)])
 @pytest.mark.parametrize("order", ["vd", "dv"])
 def test_small_layers_with_many_rows(T, D, V, order):
@@ -226,7 +240,7 @@ def test_no_features():
     assert bool(((lse - math.log(40)).abs() < 1e-6).all() and torch.equal(loss, lse))
 
 
-@pytest.mark.parametrize("T,V", [(40, 1200), (400, 19000)])
+@pytest.mark.parametrize("T,V", [(2, 300), (40, 1200), (400, 19000)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_ignored_rows_may_hold_anything(T, V, bad):
     x, w, y, dl = inputs(T, 96, V, "bf16")
