@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "ce.cuh"
 
@@ -25,6 +26,7 @@ constexpr int64_t kForwardPiece = int64_t(256) << 20;  // most bytes of one piec
 constexpr int64_t kGradPiece = int64_t(512) << 20;     // most bytes of one piece of G
 constexpr int64_t kShortDim = 1024;
 constexpr int kUsualSms = 148;                     // where no device is asked (workspace sizes)
+
 constexpr int kPieceCols = 256;                    // pieces are whole multiples of this many columns
 
 // One block per row and run of kStatCols columns of a piece of FP32 logits:
@@ -144,6 +146,68 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) {
         norm[0] = big;
         norm[1] = big / top;
+    }
+}
+
+// Copies a matrix from one pair of strides to another, 256 elements of a row
+// per warp and step: a piece of W into rows that start at multiples of 128
+// bytes, or a piece of dW out of them.  The products' tensor copies take no
+// matrix whose rows start off a multiple of 16 bytes, and their threads' loads
+// or stores of single elements cost more than this pass.
+template <typename E>
+__global__ void __launch_bounds__(256)
+    ce_move_kernel(const char *src, int64_t sm, int64_t sn, char *dst, int64_t dm, int64_t dn, int N, int64_t units) {
+    pdl_wait_then_release();
+    const int64_t per = (N + 255) / 256;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * 8) {
+        const int64_t row = u / per;
+        const int n0 = (int)(u - row * per) * 256 + (threadIdx.x & 31);
+        const char *from = src + row * sm;
+        char *to = dst + row * dm;
+        E v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = n0 + 32 * j < N ? *reinterpret_cast<const E *>(from + (n0 + 32 * j) * sn) : E(0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (n0 + 32 * j < N) *reinterpret_cast<E *>(to + (n0 + 32 * j) * dn) = v[j];
+    }
+}
+
+// The same for rows of contiguous 2-byte elements on both sides, in words that
+// are aligned in dst: a word of src that lies across two is joined from them,
+// each of which holds an element of the row (233 MB in rows of 10862 bytes,
+// read and written: 155 us element by element, 77 us in words, 6.1 TB/s).
+__global__ void __launch_bounds__(256)
+    ce_move_words_kernel(const char *src, int64_t sm, char *dst, int64_t dm, int N, int64_t units) {
+    pdl_wait_then_release();
+    const int64_t per = (N + 511) / 512;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * 8) {
+        const int64_t row = u / per;
+        const int part = (int)(u - row * per), lane = threadIdx.x & 31;
+        const uint16_t *from = reinterpret_cast<const uint16_t *>(src + row * sm);
+        uint16_t *to = reinterpret_cast<uint16_t *>(dst + row * dm);
+        const int head = reinterpret_cast<uintptr_t>(to) % 4 ? 1 : 0, words = (N - head) / 2;
+        if (part == 0 && lane == 0 && head) to[0] = from[0];
+        if (part == 0 && lane == 1 && head + 2 * words < N) to[N - 1] = from[N - 1];
+        const bool across = reinterpret_cast<uintptr_t>(from + head) % 4 != 0;
+        const uint32_t *fw = reinterpret_cast<const uint32_t *>(from + head - (across ? 1 : 0));
+        uint32_t *tw = reinterpret_cast<uint32_t *>(to + head);
+        const int w0 = part * 256 + lane;
+        uint32_t v[8];
+        if (across) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int w = w0 + 32 * j;
+                v[j] = w < words ? __funnelshift_r(fw[w], fw[w + 1], 16) : 0u;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = w0 + 32 * j < words ? fw[w0 + 32 * j] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (w0 + 32 * j < words) tw[w0 + 32 * j] = v[j];
     }
 }
 
@@ -392,6 +456,8 @@ struct Problem {
     ViewInfo x, w, dx, dw;
     Mat wm, dwm;
     bool tensor = false;   // 16-bit operands
+    bool copy_w = false;   // pieces of W are copied to a form that TMA can read
+    bool place_dw = false; // pieces of dW are made in the workspace and copied to their place
 };
 
 dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
@@ -411,12 +477,14 @@ dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
     if (p->T > most || p->V > most || p->D > most) return DG_ERR_UNSUPPORTED;
     if (p->w.row.n > 1 || p->w.col.n > 1) return DG_ERR_UNSUPPORTED;
     p->wm = Mat{static_cast<char *>(W->ptr), stride_of(p->w.row, p->es), stride_of(p->w.col, p->es), W->dtype};
+    p->copy_w = p->tensor && !p->w.tma_ok && p->D > 0 && p->V > 0;
     return DG_OK;
 }
 
 // The workspace's parts, each 256-byte aligned, for pieces of `piece` columns.
 struct Layout {
     int64_t xc = 0, part = 0, run = 0, ztarget = 0, z = 0, rows = 0, norm = 0, undo = 0, g = 0, acc = 0, planes = 0;
+    int64_t wc = 0, oc = 0;
     int64_t ldx = 0, ldz = 0, ldg = 0;
     int64_t total = 0;
 };
@@ -435,12 +503,12 @@ int64_t undo_count(const Problem &p) { return std::max(p.T, std::max(p.D, p.V));
 int64_t stat_slots(int64_t piece) { return (piece + kStatCols - 1) / kStatCols; }
 int64_t tile_slots(int64_t piece) { return (piece + kSlotCols - 1) / kSlotCols; }
 
-// Whether the CTA-pair kernel makes the logits: operands it can read through
-// TMA, and either enough 256 x 256 tiles for its pairs of SMs, or more rows
+// Whether the CTA-pair kernel makes the logits: operands (or copies of them)
+// it can read through TMA, and either enough 256 x 256 tiles for its pairs of SMs, or more rows
 // than the thin products' swapped tiles take, or a k so short that a round of
 // tiles takes no longer than the launch it saves.
 bool tiles_worth_it(const Problem &p, int num_sms) {
-    return p.tensor && p.w.tma_ok &&
+    return p.tensor && (p.w.tma_ok || p.copy_w) &&
            (((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms || p.T > 64 || p.D <= kShortDim);
 }
 
@@ -500,6 +568,57 @@ CeTile tile_of(const Problem &p, const int64_t *target, int64_t ignore_index, in
 // kernel, or the dot products of a few rows (the whole vocabulary at once).
 enum Way { kPieces, kTiles, kFew };
 
+// The copy of a piece of W keeps W's order if the columns are contiguous in it,
+// and has each column contiguous otherwise; a single column always is.
+bool copy_in_rows(const Problem &p, int64_t cols) { return p.w.unit_dim == 1 && cols > 1; }
+int64_t copy_pitch(const Problem &p, int64_t cols) {
+    return ((copy_in_rows(p, cols) ? cols : p.D) * p.es + 127) / 128 * 128;
+}
+
+void take_w(const Problem &p, int64_t piece, Layout *l) {
+    const int64_t cols = std::min(piece, p.V);
+    l->wc = take(l, p.copy_w ? (copy_in_rows(p, cols) ? p.D : cols) * copy_pitch(p, cols) : 0);
+}
+
+// Columns v0 .. v0 + cols of W, or the place of their copy.
+dg_view weight_view(const Problem &p, char *ws, const Layout &l, int64_t v0, int64_t cols) {
+    if (!p.copy_w) return view2(p.wm.ptr + v0 * p.wm.cs, p.D, cols, p.wm.rs, p.wm.cs, p.wm.dtype);
+    const int64_t pitch = copy_pitch(p, cols);
+    return copy_in_rows(p, cols) ? view2(ws + l.wc, p.D, cols, pitch, p.es, p.wm.dtype)
+                                 : view2(ws + l.wc, p.D, cols, p.es, pitch, p.wm.dtype);
+}
+
+// A row of n elements of dW where its piece is made.
+int64_t place_pitch(const Problem &p, int64_t n) { return (n * elem_size(p.dwm.dtype) + 127) / 128 * 128; }
+
+dg_view transposed(dg_view v) {
+    std::swap(v.shape[0], v.shape[1]);
+    std::swap(v.stride[0], v.stride[1]);
+    return v;
+}
+
+// An M x N matrix of 2- or 4-byte elements from one pair of strides to another.
+cudaError_t launch_move(const char *src, int64_t sm, int64_t sn, char *dst, int64_t dm, int64_t dn, int es, int64_t M,
+                        int64_t N, int num_sms, int pdl, cudaStream_t s) {
+    const bool in_words = es == 2 && sn == 2 && dn == 2;
+    const int64_t units = M * (in_words ? (N + 511) / 512 : (N + 255) / 256);
+    const int64_t blocks = std::min<int64_t>((units + 7) / 8, (int64_t)num_sms * 8);
+    if (in_words)
+        return launch_ex(ce_move_words_kernel, dim3((unsigned)blocks), dim3(256), 0, s, dim3(1, 1, 1), pdl, src, sm, dst,
+                         dm, (int)N, units);
+    return launch_ex(es == 2 ? ce_move_kernel<uint16_t> : ce_move_kernel<uint32_t>, dim3((unsigned)blocks), dim3(256),
+                     0, s, dim3(1, 1, 1), pdl, src, sm, sn, dst, dm, dn, (int)N, units);
+}
+
+cudaError_t copy_weight(const Problem &p, char *ws, const Layout &l, int64_t v0, int64_t cols, int num_sms, int pdl,
+                        cudaStream_t s) {
+    const char *src = p.wm.ptr + v0 * p.wm.cs;
+    const int64_t pitch = copy_pitch(p, cols);
+    if (copy_in_rows(p, cols))
+        return launch_move(src, p.wm.rs, p.wm.cs, ws + l.wc, pitch, p.es, p.es, p.D, cols, num_sms, pdl, s);
+    return launch_move(src, p.wm.cs, p.wm.rs, ws + l.wc, pitch, p.es, p.es, cols, p.D, num_sms, pdl, s);
+}
+
 Layout forward_layout(const Problem &p, int64_t piece, Way way) {
     Layout l;
     l.ldx = align256(p.D * p.es);
@@ -509,6 +628,7 @@ Layout forward_layout(const Problem &p, int64_t piece, Way way) {
     l.run = take(&l, p.T * 8);
     l.ztarget = take(&l, p.T * 4);
     l.z = take(&l, way == kPieces ? p.T * l.ldz : 0);
+    take_w(p, piece, &l);
     return l;
 }
 
@@ -541,6 +661,8 @@ Planes plan_planes(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     if (!p.tensor) return n;
     const int64_t cols = std::min(piece, p.V);
     if (need_dx && p.T > 1) n.dx = plane_count(p.T, p.D, cols, num_sms);
+    // one plane for a dX whose rows the tensor stores cannot write, up to 256 MB of it
+    if (need_dx && p.T > 1 && n.dx == 0 && !p.dx.tma_ok && plane_bytes(p.T, p.D, 1) <= (int64_t(256) << 20)) n.dx = 1;
     if (need_dw) n.dw = p.dw.unit_dim == 2 ? plane_count(cols, p.D, p.T, num_sms) : plane_count(p.D, cols, p.T, num_sms);
     return n;
 }
@@ -561,10 +683,23 @@ Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
                                  p.dw.unit_dim == 2 ? plane_bytes(cols, p.D, n.dw) : plane_bytes(p.D, cols, n.dw)));
     l.g = take(&l, p.T * l.ldg);
     l.z = take(&l, tiles ? 0 : p.T * l.ldz);
+    take_w(p, piece, &l);
+    if (need_dw && p.place_dw && n.dw == 0)
+        l.oc = take(&l, p.dw.unit_dim == 2 ? cols * place_pitch(p, p.D) : p.D * place_pitch(p, cols));
     return l;
 }
 
+Problem without_copy(Problem p) {
+    p.copy_w = p.place_dw = false;
+    return p;
+}
+
 int64_t piece_min(const Problem &p) { return std::min<int64_t>(std::max<int64_t>(p.V, 1), kPieceCols); }
+
+// Bytes of workspace that the copy of one column of W or dW takes.
+int64_t copied_bytes(const Problem &p) {
+    return std::max(p.copy_w ? p.D * p.es + 128 : 0, p.place_dw ? p.D * elem_size(p.dwm.dtype) + 128 : 0);
+}
 
 // Pieces of equal size, whole multiples of kPieceCols: as many columns as
 // `bytes` of `per_col` bytes each allow.
@@ -581,11 +716,12 @@ int64_t piece_for(const Problem &p, int64_t bytes, int64_t per_col) {
 // pairs per row and 1024 columns), of G.
 int64_t forward_piece(const Problem &p, Way way) {
     if (way == kFew) return p.V;
-    if (way == kPieces) return piece_for(p, kForwardPiece, p.T * 4);
+    if (way == kPieces) return piece_for(p, kForwardPiece, std::max(p.T * 4, copied_bytes(p)));
+    if (p.copy_w) return piece_for(p, kForwardPiece, std::max(p.T, copied_bytes(p)));
     const int64_t cols = kForwardPiece / (std::max<int64_t>(p.T, 1) * 8) * kSlotCols;
     return cols >= p.V ? p.V : std::max<int64_t>(cols / kPieceCols * kPieceCols, kPieceCols);
 }
-int64_t grad_piece(const Problem &p) { return piece_for(p, kGradPiece, p.T * p.es); }
+int64_t grad_piece(const Problem &p) { return piece_for(p, kGradPiece, std::max(p.T * p.es, copied_bytes(p))); }
 
 dg_status launched(cudaError_t e) {
     if (e != cudaSuccess) return DG_ERR_CUDA;
@@ -603,6 +739,13 @@ DevView dev_of(const dg_view *v, const ViewInfo &vi) {
 }
 
 dg_status pair_once(PairCall c, cudaStream_t s) { return pair_call(c, s); }
+
+// The piece, made smaller until the last one has `least` columns or more; 0 or
+// less if none does.
+int64_t no_sliver(const Problem &p, int64_t piece, int64_t least) {
+    while (piece > 0 && piece < p.V && p.V % piece != 0 && p.V % piece < least) piece -= kPieceCols;
+    return piece;
+}
 
 // The largest piece whose layout fits `bytes` (0: not even the smallest).
 template <typename LayoutOf>
@@ -635,8 +778,8 @@ dg_status dg_linear_ce_workspace(const dg_view *X, const dg_view *W, int64_t *le
     Problem p;
     DG_TRY(check_problem(X, W, &p));
     const Way way = few_rows(p) ? kFew : tiles_worth_it(p, kUsualSms) ? kTiles : kPieces;
-    *least = forward_layout(p, piece_min(p), kPieces).total;
-    *best = std::max(*least, forward_layout(p, forward_piece(p, way), way).total);
+    *least = forward_layout(without_copy(p), piece_min(p), kPieces).total;
+    *best = std::max(forward_layout(p, piece_min(p), kPieces).total, forward_layout(p, forward_piece(p, way), way).total);
     return DG_OK;
 }
 
@@ -650,6 +793,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     if (reinterpret_cast<uintptr_t>(target) % 8 || reinterpret_cast<uintptr_t>(loss) % 4 ||
         reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256)
         return DG_ERR_ALIGN;
+    if (forward_layout(p, piece_min(p), kPieces).total > workspace_bytes) p = without_copy(p);  // no room for it
     if (forward_layout(p, piece_min(p), kPieces).total > workspace_bytes) return DG_ERR_SHAPE;
     int num_sms = 0, *err_word = nullptr;
     DG_TRY(device_info(&num_sms, &err_word));
@@ -663,15 +807,25 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     // the copy of X, if there is one, comes first in the workspace
     const dg_view xv = forward_copies_x(p) ? view2(ws, p.T, p.D, align256(p.D * p.es), p.es, X->dtype) : *X;
     Way way = kPieces;
+    int64_t tile_piece = 0;
     if (few_rows(p) && forward_layout(p, p.V, kFew).total <= workspace_bytes) {
         way = kFew;
     } else if (tiles_worth_it(p, num_sms)) {
         CeTile ce = tile_of(p, target, ignore_index, 0);
         ce.part = reinterpret_cast<float2 *>(ws);
-        if (pair_once(PairCall{&xv, W, nullptr, alpha, nullptr, kPairStats, ce, 0, true}, s) == DG_OK) way = kTiles;
+        // TMA reads no single column of a W whose columns are contiguous
+        const int64_t cols = no_sliver(
+            p, fit_piece(p, workspace_bytes, forward_piece(p, kTiles),
+                         [&](int64_t n) { return forward_layout(p, n, kTiles); }), 2);
+        if (cols > 0) {
+            tile_piece = cols;
+            const dg_view wv = weight_view(p, ws, forward_layout(p, cols, kTiles), 0, std::min(cols, p.V));
+            if (pair_once(PairCall{&xv, &wv, nullptr, alpha, nullptr, kPairStats, ce, 0, true}, s) == DG_OK) way = kTiles;
+        }
     }
     auto layout_of = [&](int64_t piece) { return forward_layout(p, piece, way); };
-    const int64_t piece = fit_piece(p, workspace_bytes, forward_piece(p, way), layout_of);
+    const int64_t piece =
+        way == kTiles ? tile_piece : fit_piece(p, workspace_bytes, forward_piece(p, way), layout_of);
     if (piece == 0) return DG_ERR_SHAPE;
     const Layout l = layout_of(piece);
     if (way != kFew && forward_copies_x(p)) {
@@ -684,7 +838,8 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     float *ztarget = reinterpret_cast<float *>(ws + l.ztarget), *z = reinterpret_cast<float *>(ws + l.z);
     for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
         const int64_t cols = std::min(piece, p.V - v0);
-        const dg_view wv = view2(p.wm.ptr + v0 * p.wm.cs, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
+        const dg_view wv = weight_view(p, ws, l, v0, cols);
+        if (p.copy_w) DG_TRY(launched(copy_weight(p, ws, l, v0, cols, num_sms, pdl, s)));
         const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
         int slots;
         if (way == kFew) {
@@ -733,6 +888,7 @@ dg_status check_grad(const dg_view *X, const dg_view *W, const dg_view *dX, cons
         if (p->dw.row.n > 1 || p->dw.col.n > 1) return DG_ERR_UNSUPPORTED;
         const int es = elem_size(dW->dtype);
         p->dwm = Mat{static_cast<char *>(dW->ptr), stride_of(p->dw.row, es), stride_of(p->dw.col, es), dW->dtype};
+        p->place_dw = p->tensor && !p->dw.tma_ok && p->D > 0 && p->V > 0;
     }
     return DG_OK;
 }
@@ -793,8 +949,9 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W, const 
     Problem p;
     DG_TRY(check_grad(X, W, dX, dW, &p));
     const int dxt = dX ? dX->dtype : DG_F32;
-    *least = grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total;
-    *best = std::max(*least, grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt,
+    *least = grad_layout(without_copy(p), piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total;
+    *best = std::max(grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total,
+                     grad_layout(p, grad_piece(p), dX != nullptr, dW != nullptr, dxt,
                                          few_rows(p) || tiles_worth_it(p, kUsualSms),
                                          plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, kUsualSms))
                                  .total);
@@ -820,9 +977,11 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             return DG_ERR_ALIGN;
     }
     const int dxt = dX ? dX->dtype : DG_F32;
-    if (p.T > 0 && grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total >
-                       workspace_bytes)
-        return DG_ERR_SHAPE;
+    const auto least = [&] {
+        return grad_layout(p, piece_min(p), dX != nullptr, dW != nullptr, dxt, false, Planes{}).total;
+    };
+    if (p.T > 0 && least() > workspace_bytes) p = without_copy(p);  // no room for copies
+    if (p.T > 0 && least() > workspace_bytes) return DG_ERR_SHAPE;
     DG_TRY(device_info(&num_sms, &err_word));
     if (p.T > 0 && ((p.D > 0 && (!device_pointer(X->ptr) || !device_pointer(W->ptr))) || !device_pointer(target) ||
                     !device_pointer(lse) || !device_pointer(dloss) || !device_pointer(workspace)))
@@ -849,26 +1008,31 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     };
     if (layout_of(grad_piece(p)).total > workspace_bytes) planes = Planes{};  // a small workspace has room for G only
     int64_t piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
+    if (tiles || planes.dx > 0) {
+        // the tensor copies of G take pieces of 64 columns or more, the last one too
+        piece = no_sliver(p, piece, 64);
+        if (piece <= 0) planes = Planes{};
+    }
     if (tiles && !few) {
-        // the tensor stores of G take pieces of 64 columns or more, the last one too
-        while (piece > 0 && piece < p.V && p.V % piece != 0 && p.V % piece < 64) piece -= kPieceCols;
         if (piece > 0) {
             const Layout t = layout_of(piece);
             const dg_view gv = view2(ws + t.g, p.T, std::min(piece, p.V), t.ldg, p.es, X->dtype);
-            const dg_view wv = view2(p.wm.ptr, p.D, std::min(piece, p.V), p.wm.rs, p.wm.cs, W->dtype);
+            const dg_view wv = weight_view(p, ws, t, 0, std::min(piece, p.V));
             tiles = pair_once(PairCall{&xv, &wv, &gv, alpha, nullptr, kPairGrad, {}, 0, true}, s) == DG_OK;
         }
         if (piece <= 0 || !tiles) {
             tiles = false;
-            piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
+            piece = planes.dx > 0 ? no_sliver(p, fit_piece(p, workspace_bytes, grad_piece(p), layout_of), 64) : 0;
+            if (piece <= 0) planes = Planes{};
         }
     }
+    if (piece <= 0) piece = fit_piece(p, workspace_bytes, grad_piece(p), layout_of);
     if (piece == 0) return DG_ERR_SHAPE;
     if (planes.dx > 0) {
         const Layout t = layout_of(piece);
         const int64_t cols = std::min(piece, p.V);
         const dg_view gv = view2(ws + t.g, p.T, cols, t.ldg, p.es, X->dtype);
-        const dg_view wt = view2(p.wm.ptr, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
+        const dg_view wt = transposed(weight_view(p, ws, t, 0, cols));
         PairCall call{&gv, &wt, nullptr, 1.f, nullptr, kPairPartial, {}, planes.dx, true};
         if (in_planes(call, ws + t.planes, s) != DG_OK) planes.dx = 0;
     }
@@ -897,8 +1061,9 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     for (int64_t v0 = 0; v0 < p.V; v0 += piece) {
         const int64_t cols = std::min(piece, p.V - v0);
         char *wp = p.wm.ptr + v0 * p.wm.cs;
-        const dg_view wv = view2(wp, p.D, cols, p.wm.rs, p.wm.cs, W->dtype);
-        const dg_view wt = view2(wp, cols, p.D, p.wm.cs, p.wm.rs, W->dtype);
+        const dg_view wv = weight_view(p, ws, l, v0, cols);
+        const dg_view wt = transposed(wv);
+        if (p.copy_w) DG_TRY(launched(copy_weight(p, ws, l, v0, cols, num_sms, pdl, s)));
         const dg_view gv = view2(g, p.T, cols, l.ldg, p.es, X->dtype);
         const dg_view gt = view2(g, cols, p.T, p.es, l.ldg, X->dtype);
         if (few) {
@@ -929,13 +1094,17 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         if (dW) {
             // the product in the order that gives dW's unit stride to the columns of the output
             char *op = p.dwm.ptr + v0 * p.dwm.cs;
-            if (p.dw.unit_dim == 2) {
-                const dg_view ov = view2(op, cols, p.D, p.dwm.cs, p.dwm.rs, p.dwm.dtype);
-                DG_TRY(product(&gt, &xv, &ov, p, num_sms, planes.dw, ws + l.planes, alpha, norm, undo, pdl, s));
-            } else {
-                const dg_view ov = view2(op, p.D, cols, p.dwm.rs, p.dwm.cs, p.dwm.dtype);
-                DG_TRY(product(&xt, &gv, &ov, p, num_sms, planes.dw, ws + l.planes, alpha, norm, undo, pdl, s));
-            }
+            const bool cols_first = p.dw.unit_dim == 2;
+            const int64_t M = cols_first ? cols : p.D, N = cols_first ? p.D : cols;
+            const int64_t sm = cols_first ? p.dwm.cs : p.dwm.rs, sn = cols_first ? p.dwm.rs : p.dwm.cs;
+            const int des = elem_size(p.dwm.dtype);
+            const bool place = p.place_dw && planes.dw == 0;
+            const dg_view ov = place ? view2(ws + l.oc, M, N, place_pitch(p, N), des, p.dwm.dtype)
+                                     : view2(op, M, N, sm, sn, p.dwm.dtype);
+            DG_TRY(product(cols_first ? &gt : &xt, cols_first ? &xv : &gv, &ov, p, num_sms, planes.dw, ws + l.planes,
+                           alpha, norm, undo, pdl, s));
+            if (place)
+                DG_TRY(launched(launch_move(ws + l.oc, place_pitch(p, N), des, op, sm, sn, des, M, N, num_sms, pdl, s)));
         }
     }
     if (own_acc)

@@ -374,6 +374,44 @@ def test_unaligned_operands(T, V):
     check_grads(x, w, y, dl, dxo, dwo.t())
 
 
+# W and dW whose rows do not start at multiples of 16 bytes: the products read and make copies of them.
+def off_rows(kind, D, V, dtype):
+    """An empty D x V matrix of the kind on the device, and its storage."""
+    if kind == "steps":  # neither dimension contiguous
+        store = torch.full((V, 2 * D + 3), 7.0, device="cuda", dtype=dtype)
+        return store[:, 1:2 * D + 1:2].t(), store
+    first, second = (V, D) if kind[:2] == "vd" else (D, V)
+    pad = (kind[2:] == " even") * 2 + (kind[2:] == " odd") * 3
+    store = torch.full((first, second + pad), 7.0, device="cuda", dtype=dtype)
+    m = store[:, pad // 2:pad // 2 + second]
+    return (m.t() if first == V else m), store
+
+
+@pytest.mark.parametrize("T,D,V", [(1, 333, 70), (2, 1031, 900), (8, 100, 257), (70, 513, 1025), (300, 2, 3001),
+                                   (300, 2050, 3001), (64, 4099, 501)])
+@pytest.mark.parametrize("kind", ["vd", "vd even", "vd odd", "dv", "dv even", "dv odd", "steps"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_rows_off_sixteen_bytes(T, D, V, kind, out):
+    x, w0, y, dl = inputs(T, D, V, "bf16")
+    w, _ = off_rows(kind, D, V, torch.bfloat16)
+    w.copy_(w0)
+    dx = torch.empty(T, D, device="cuda", dtype=DT[out])
+    dw, store = off_rows(kind, D, V, DT[out])
+    written = torch.zeros_like(store, dtype=torch.bool)
+    written.as_strided(dw.shape, dw.stride(), dw.storage_offset()).fill_(True)
+    least, best = dg.dg_linear_ce_workspace(dg.view(x), dg.view(w))
+    gleast, gbest = dg.dg_linear_ce_grad_workspace(dg.view(x), dg.view(w), dg.view(dx), dg.view(dw))
+    for size, gsize in ((best, gbest), (least, gleast), ((least + best) // 2, (gleast + gbest) // 2)):
+        loss, lse = run_forward(x, w, y, workspace=torch.empty(size, dtype=torch.uint8, device="cuda"))
+        check_forward(x, w0, y, loss, lse)
+        dx.fill_(math.nan)
+        dw.fill_(math.nan)
+        dg.linear_ce_grad(x, w, y, lse, dl, dx, dw, ignore_index=IGNORE,
+                          workspace=torch.empty(gsize, dtype=torch.uint8, device="cuda"))
+        check_grads(x, w0, y, dl, dx, dw)
+        assert bool((store[~written] == 7).all())
+
+
 def test_gradient_against_differences():
     # central differences of the library's own loss along random directions: with the direction scaled
     # so that no logit moves by more than 1 per unit, the third derivative of a row's loss is at most
