@@ -27,6 +27,7 @@ constexpr int64_t kGradPiece = int64_t(512) << 20;     // most bytes of one piec
 constexpr int64_t kShortDim = 1024;
 constexpr int kUsualSms = 148;                     // where no device is asked (workspace sizes)
 
+constexpr int64_t kManyPlaneBlocks = 4096;         // from here on ce_planes_kernel takes four rows a block
 constexpr int kPieceCols = 256;                    // pieces are whole multiples of this many columns
 
 // One block per row and run of kStatCols columns of a piece of FP32 logits:
@@ -211,6 +212,21 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// One row by one block, or zeros in its place.
+template <typename E>
+__device__ __forceinline__ void copy_row(const char *src, int64_t step, char *dst, int D, bool zero) {
+    int d = threadIdx.x;
+    for (; d + 7 * (int)blockDim.x < D; d += 8 * blockDim.x) {
+        E v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const E *>(src + (d + j * (int)blockDim.x) * step);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) reinterpret_cast<E *>(dst)[d + j * (int)blockDim.x] = zero ? E(0) : v[j];
+    }
+    for (; d < D; d += blockDim.x)
+        reinterpret_cast<E *>(dst)[d] = zero ? E(0) : *reinterpret_cast<const E *>(src + d * step);
+}
+
 // Up to this many rows every block of ce_rows_kernel finds the largest dloss
 // itself, which saves the launch of ce_norm_kernel.
 constexpr int64_t kOwnNormRows = 2048;
@@ -248,23 +264,27 @@ __global__ void __launch_bounds__(256)
         if (y == kInvalid && err_word) atomicCAS(err_word, 0, (int)DG_ERR_VALUE);
     }
     if (undo)  // the inverse for every row of the products
-        for (int64_t i = t * 256 + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * 256) undo[i] = big / top;
+        for (int64_t i = t * blockDim.x + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * blockDim.x) undo[i] = big / top;
     if (!xc) return;
     const char *src = x.ptr + axis_offset(x.row, t);
     char *dst = xc + t * ldx;
     if (vec) {  // 16 bytes at a time
         const int n = D * elem_bytes(x.dtype) / 16;
-        for (int d = threadIdx.x; d < n; d += 256)
+#pragma unroll 4
+        for (int d = threadIdx.x; d < n; d += blockDim.x)
             reinterpret_cast<uint4 *>(dst)[d] =
                 y < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldcs(reinterpret_cast<const uint4 *>(src) + d);
         return;
     }
-    if (x.dtype == DG_F32) {
-        for (int d = threadIdx.x; d < D; d += 256)
+    if (x.col.n == 1) {
+        if (x.dtype == DG_F32) copy_row<float>(src, x.col.stride[0], dst, D, y < 0);
+        else copy_row<uint16_t>(src, x.col.stride[0], dst, D, y < 0);
+    } else if (x.dtype == DG_F32) {
+        for (int d = threadIdx.x; d < D; d += blockDim.x)
             reinterpret_cast<float *>(dst)[d] =
                 y < 0 ? 0.f : *reinterpret_cast<const float *>(src + axis_offset(x.col, d));
     } else {
-        for (int d = threadIdx.x; d < D; d += 256)
+        for (int d = threadIdx.x; d < D; d += blockDim.x)
             reinterpret_cast<uint16_t *>(dst)[d] =
                 y < 0 ? 0 : *reinterpret_cast<const uint16_t *>(src + axis_offset(x.col, d));
     }
@@ -406,20 +426,45 @@ __global__ void __launch_bounds__(256) ce_round_kernel(const float *acc, int64_t
 // dX from the planes of partial sums (FP32, in plane order) and, with several
 // pieces of the vocabulary, the sum over the earlier ones: the running sum to
 // acc_out, or (acc_out null) alpha * norm[1] times the whole sum to dX.
+// ROWS rows per block: with many rows a block's start takes longer than its loads
+// (20000 x 1001, one plane: 99 -> 53 us).
+template <int ROWS>
 __global__ void __launch_bounds__(256)
     ce_planes_kernel(const float *planes, int64_t ld, int used, int64_t plane_rows, const float *acc_in,
-                     float *acc_out, float alpha, const float *norm, const DevView out, int D) {
+                     float *acc_out, float alpha, const float *norm, const DevView out, int64_t M, int D) {
     pdl_wait_then_release();
-    const int64_t t = blockIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * ROWS;
     const int d = blockIdx.y * 256 + threadIdx.x;
     if (d >= D) return;
-    float v = acc_in ? acc_in[t * D + d] : 0.f;
-#pragma unroll 8
-    for (int c = 0; c < used; ++c) v += planes[(c * plane_rows + t) * ld + d];
-    if (acc_out) acc_out[t * D + d] = v;
-    else
-        store_elem(const_cast<char *>(out.ptr) + axis_offset(out.row, t) + axis_offset(out.col, d), out.dtype,
-                   alpha * norm[1] * v);
+    const float *from = planes + t0 * ld + d;
+    const int64_t step = plane_rows * ld;
+    float v[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) v[r] = acc_in && t0 + r < M ? acc_in[(t0 + r) * D + d] : 0.f;
+#pragma unroll 4
+    for (int c = 0; c < used; ++c, from += step) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) v[r] += from[r * ld];  // a plane has whole tiles of rows
+    }
+    const int rows = (int)(M - t0 < ROWS ? M - t0 : ROWS);
+    if (acc_out) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            if (r < rows) acc_out[(t0 + r) * D + d] = v[r];
+        return;
+    }
+    char *to = const_cast<char *>(out.ptr) + axis_offset(out.col, d);
+    const float scale = alpha * norm[1];
+    if (out.row.n == 1) {
+        to += t0 * out.row.stride[0];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            if (r < rows) store_elem(to + r * out.row.stride[0], out.dtype, scale * v[r]);
+    } else {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            if (r < rows) store_elem(to + axis_offset(out.row, t0 + r), out.dtype, scale * v[r]);
+    }
 }
 
 // ------------------------------------------------------------------- host side
@@ -545,6 +590,10 @@ cudaError_t launch_few(const Problem &p, const DevView &x, const char *w, int v0
     return b ? run_few<__nv_bfloat16, 2, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s)
              : run_few<__half, 2, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s);
 }
+
+// Threads per row of ce_rows_kernel: with many rows, more of them at once hide
+// the chain of loads at a row's start (20000 rows of 1001 elements: 54 -> 28 us with copy_row).
+int row_threads(int64_t T) { return T > kOwnNormRows ? 64 : 256; }
 
 // 16-byte rows of X for its copy.
 int x_vec(const dg_view *X, const Problem &p) {
@@ -829,7 +878,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     if (piece == 0) return DG_ERR_SHAPE;
     const Layout l = layout_of(piece);
     if (way != kFew && forward_copies_x(p)) {
-        DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x),
+        DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl, dev_of(X, p.x),
                                   (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
                                   (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f, (RowGrad *)nullptr,
                                   (float *)nullptr, (int64_t)0, ws + l.xc, l.ldx, x_vec(X, p), (int *)nullptr)));
@@ -908,9 +957,11 @@ dg_status planes_product(PairCall call, char *planes, const DevView &out, const 
                          float alpha, const float *norm, int pdl, cudaStream_t s) {
     const int64_t M = call.A->shape[0], N = call.B->shape[1];
     DG_TRY(in_planes(call, planes, s));
-    return launched(launch_ex(ce_planes_kernel, dim3((unsigned)M, (unsigned)((N + 255) / 256)), dim3(256), 0, s,
+    const int rows = M * ((N + 255) / 256) >= kManyPlaneBlocks ? 4 : 1;
+    return launched(launch_ex(rows == 4 ? ce_planes_kernel<4> : ce_planes_kernel<1>,
+                              dim3((unsigned)((M + rows - 1) / rows), (unsigned)((N + 255) / 256)), dim3(256), 0, s,
                               dim3(1, 1, 1), pdl, reinterpret_cast<const float *>(planes), align256(N * 4) / 4,
-                              call.chunks, (M + 255) / 256 * 256, acc_in, acc_out, alpha, norm, out, (int)N));
+                              call.chunks, (M + 255) / 256 * 256, acc_in, acc_out, alpha, norm, out, M, (int)N));
 }
 
 // dW's product, k = T.  Few tiles: planes, or the paired tiles all the same
@@ -1048,7 +1099,7 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
                                       reinterpret_cast<const char *>(dloss), dloss_stride, target, ignore_index, p.T,
                                       p.V, top, norm)));
     }
-    DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(256), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
+    DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
                               p.T, p.V, target, ignore_index, lse, reinterpret_cast<const char *>(dloss), dloss_stride,
                               norm, p.T <= kOwnNormRows ? 1 : 0, top, rows, undo, undo_count(p),
                               copy ? ws : (char *)nullptr, ldx, x_vec(X, p), err_word)));
