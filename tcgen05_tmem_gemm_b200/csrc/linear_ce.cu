@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(256)
     float v[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) v[r] = acc_in && t0 + r < M ? acc_in[(t0 + r) * D + d] : 0.f;
-#pragma unroll 4
+#pragma unroll (ROWS == 1 ? 8 : 2)
     for (int c = 0; c < used; ++c, from += step) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) v[r] += from[r * ld];  // a plane has whole tiles of rows
@@ -692,7 +692,10 @@ int plane_count(int64_t M, int64_t N, int64_t K, int num_sms) {
     auto busy = [&](int64_t n) { return (double)(tiles * n) / (double)((tiles * n + pairs - 1) / pairs * pairs); };
     int best = 0;
     double most = busy(1) + 0.1;  // worth it from a tenth on: a plane costs its write and its read
-    for (int n = 2; n <= 16 && n * 256 <= K && tiles * n <= 4 * pairs; ++n)
+    // the sum walks the planes one after another: more than 16 pay from a k of 65536 on
+    // (dX of 3 x 72 from k = 118567: 49 + 5 us with 16 planes, 29 + 11 with 32, 19 + 18 with 64)
+    const int limit = K >= 65536 ? 32 : 16;
+    for (int n = 2; n <= limit && n * 256 <= K && tiles * n <= 4 * pairs; ++n)
         if (busy(n) - 0.005 * n > most) {
             most = busy(n) - 0.005 * n;
             best = n;
