@@ -262,7 +262,8 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y,
  *  loss, lse  device float32[T], all written (lse for ignored rows too).
  *  workspace  device memory, 256-byte aligned, for this call alone until it
  *    has run; at least dg_linear_ce_workspace's `least` bytes.  More bytes
- *    mean fewer and larger pieces.
+ *    mean fewer and larger pieces, and (up to `best`) copies of a 16-bit W
+ *    whose rows do not start at multiples of 16 bytes, which is much faster.
  *  A row whose logits hold a NaN or +infinity has loss and lse NaN; the rows
  *  that are ignored never reach the loss or a gradient, whatever they hold.
  *  Sums are FP32 and in a fixed order.
