@@ -412,6 +412,25 @@ def test_rows_off_sixteen_bytes(T, D, V, kind, out):
         assert bool((store[~written] == 7).all())
 
 
+@pytest.mark.parametrize("V", [513, 769, 65537, 66049, 98305, 99073, 131073])
+@pytest.mark.parametrize("share", [0.0, 0.1, 0.4])
+def test_last_piece_of_one_column(V, share):
+    # W's columns contiguous and its rows aligned, so that no piece is copied
+    T, D = 40, 16
+    x, w0, y, dl = inputs(T, D, V, "bf16")
+    w = torch.zeros(D, V + 7, device="cuda").bfloat16()[:, :V]
+    w.copy_(w0)
+    dx, dw = torch.empty_like(x), torch.empty(D, V + 7, device="cuda")[:, :V]
+    least, best = dg.dg_linear_ce_workspace(dg.view(x), dg.view(w))
+    space = torch.empty(least + int(share * (best - least)), dtype=torch.uint8, device="cuda")
+    loss, lse = run_forward(x, w, y, workspace=space)
+    check_forward(x, w0, y, loss, lse)
+    least, best = dg.dg_linear_ce_grad_workspace(dg.view(x), dg.view(w), dg.view(dx), dg.view(dw))
+    space = torch.empty(least + int(share * (best - least)), dtype=torch.uint8, device="cuda")
+    dg.linear_ce_grad(x, w, y, lse, dl, dx, dw, ignore_index=IGNORE, workspace=space)
+    check_grads(x, w0, y, dl, dx, dw)
+
+
 def test_gradient_against_differences():
     # central differences of the library's own loss along random directions: with the direction scaled
     # so that no logit moves by more than 1 per unit, the third derivative of a row's loss is at most
