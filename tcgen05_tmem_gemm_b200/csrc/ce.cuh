@@ -37,9 +37,11 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
 
 // Another N logits: one pass, the running sum rescaled when the maximum moves.
 // Four chains for the maximum and eight for the sum, so that few instructions
-// wait for one another (a warp has its scheduler almost to itself).
+// wait for one another (a warp has its scheduler almost to itself).  A single
+// logit z is the pair (z, 1): join(m, s, z, 1.f).
 template <int N>
 __device__ __forceinline__ void join_logits(float &m, float &s, const float (&z)[N]) {
+    static_assert(N >= 4, "join_logits starts its four chains with a logit each");
     float mx[4] = {m, z[1], z[2], z[3]};
     mx[0] = fmaxf(mx[0], z[0]);
 #pragma unroll

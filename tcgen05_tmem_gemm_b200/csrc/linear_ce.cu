@@ -370,22 +370,22 @@ __global__ void __launch_bounds__(256, 3)
                 }
             }
         }
-        float z[1] = {0.f};
+        float z = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
-            if (lane == r) z[0] = alpha * acc[r];
+            if (lane == r) z = alpha * acc[r];
         }
         if (lane < rows) {
             if (GRAD) {
                 float v = 0.f;
                 if (mine.target >= 0)
-                    v = mine.scale * (exp_fast(z[0] - mine.lse) - (v0 + c == mine.target ? 1.f : 0.f));
+                    v = mine.scale * (exp_fast(z - mine.lse) - (v0 + c == mine.target ? 1.f : 0.f));
                 store_elem(g + lane * ldg + (int64_t)c * 2, x.dtype, v);
             } else {
-                join_logits(m, s, z);
-                if (y == v0 + c) ce.ztarget[lane] = z[0];
+                join(m, s, z, 1.f);
+                if (y == v0 + c) ce.ztarget[lane] = z;
             }
         }
     }
