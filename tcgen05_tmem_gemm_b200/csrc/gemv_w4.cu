@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) gemv_w4_kernel(const __grid
 
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t half = 0;
-    if (threadIdx.x < 64) *reinterpret_cast<uint32_t *>(smem + L.zero + threadIdx.x * 4) = 0u;
+    // (a block of one column tile and one warp along k has 32 threads)
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) *reinterpret_cast<uint32_t *>(smem + L.zero + i * 4) = 0u;
     for (int kb_round = blockIdx.y * per_round; kb_round < blocks_k; kb_round += stride) {
         const int kb0 = kb_round + kw * p.steps;
         const int nst = min(p.steps, blocks_k - kb0);  // may be negative: nothing for this warp
