@@ -1,5 +1,6 @@
 """dg_gemv_w4 where a block is a single warp: at most 16 columns and 128 k.
 Tolerances are those of test_gpu_gemv_w4."""
+import functools
 import math
 
 import pytest
@@ -11,9 +12,12 @@ from test_gpu_gemv_w4 import run_case, weights
 pytestmark = pytest.mark.gpu
 
 
+big = functools.lru_cache(lambda: weights(4096, 16384, 128)[:2])
+
+
 def leave_nan_in_shared_memory():
     """A call whose activations, all NaN, fill the shared memory of every SM."""
-    codes, scales, _ = weights(4096, 16384, 128)
+    codes, scales = big()
     x = torch.full((8, 4096), math.nan, device="cuda", dtype=torch.bfloat16)
     y = torch.empty(8, 16384, device="cuda")
     for _ in range(3):
