@@ -228,6 +228,7 @@ struct Views {
     const dg_view *A, *B, *C;
     ViewInfo a, b, c;
     int act = DG_ACT_NONE;  // the call's activation: split-K partials add into C only without one
+    bool ordered = false;   // sums in a fixed order whatever DG_OPT_DETERMINISTIC says
 };
 
 uint32_t make_idesc(int in_dtype, bool p_mn, bool q_mn, int bn, int m = 128) {
@@ -512,7 +513,7 @@ bool umma_plan(const Views &v, int64_t M, int64_t N, int64_t K, float beta, int 
     if (gcl > 1) in.grid = (int32_t)std::min<int64_t>(units2, (num_sms / gcl) * gcl);
     // split-K with beta == 1 and FP32 C: the splits can add their partials
     // straight into C through one 2-D tensor map of C (its i group one dim)
-    if (split > 1 && beta == 1.f && v.C->dtype == DG_F32 && v.c.tma_ok && g_deterministic.load() == 0 &&
+    if (split > 1 && beta == 1.f && v.C->dtype == DG_F32 && v.c.tma_ok && g_deterministic.load() == 0 && !v.ordered &&
         v.act == DG_ACT_NONE) {
         in.split_reduce_add = 1;
     }
@@ -986,6 +987,7 @@ struct CallKey {
     const float *sa, *sb;
     const float *bias;
     int act;
+    int ordered;
     int dev;
     uint32_t epoch;
     void *stream;  // a Stream-K launch uses its stream's workspace
@@ -1029,6 +1031,61 @@ dg_status build_launch(Views &v, Plan &pl, float alpha, float beta, const float 
     }
     return prepare(v, pl, alpha, beta, use_ab ? scale_a : nullptr, use_ab ? scale_b : nullptr, bias, act, ds, sk_ws,
                    rec);
+}
+
+// The call of dg_gemm_ex, its arguments taken apart.
+dg_status gemm_call(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta, const float *scale_a,
+                    const float *scale_b, const float *bias, int act, bool ordered, void *stream) {
+    // a call identical to a recent one on this thread and device reuses its
+    // validated plan, parameters and tensor maps
+    CallKey key;
+    std::memset(&key, 0, sizeof(key));
+    key.A = *A;
+    key.B = *B;
+    key.C = *C;
+    key.alpha = alpha;
+    key.beta = beta;
+    key.sa = scale_a;
+    key.sb = scale_b;
+    key.bias = bias;
+    key.act = act;
+    key.ordered = ordered;
+    key.epoch = g_epoch.load();
+    key.stream = stream;
+    if (cudaGetDevice(&key.dev) != cudaSuccess) {
+        cudaGetLastError();
+        key.dev = -1;
+    }
+    if (key.dev >= 0)
+        for (int i = 0; i < 8; ++i)
+            if (t_calls.used[i] && key_equal(t_calls.key[i], key))
+                return fire(t_calls.rec[i], static_cast<cudaStream_t>(stream));
+
+    Views v{A, B, C, {}, {}, {}};
+    v.act = act;
+    v.ordered = ordered;
+    Plan pl;
+    // argument errors are reported before any CUDA call
+    dg_status st = make_plan(v, alpha, beta, 148, &pl);
+    if (st != DG_OK) return st;
+    if (pl.info.kind == DG_KIND_NONE) return DG_OK;
+    DeviceState *ds = nullptr;
+    st = device_state(&ds);
+    if (st != DG_OK) return st;
+    if (ds->num_sms != 148) {
+        st = make_plan(v, alpha, beta, ds->num_sms, &pl);
+        if (st != DG_OK) return st;
+    }
+    const int slot = t_calls.next;
+    t_calls.used[slot] = false;
+    st = build_launch(v, pl, alpha, beta, scale_a, scale_b, bias, act, ds, static_cast<cudaStream_t>(stream), nullptr,
+                      &t_calls.rec[slot]);
+    if (st != DG_OK) return st;
+    key.epoch = g_epoch.load();  // a replaced Stream-K workspace invalidated the cache
+    t_calls.key[slot] = key;
+    t_calls.used[slot] = true;
+    t_calls.next = (slot + 1) % 8;
+    return fire(t_calls.rec[slot], static_cast<cudaStream_t>(stream));
 }
 
 // The variants dg_autotune times for a call whose rule-based plan is `base`.
@@ -1165,15 +1222,19 @@ dg_status gemm_tiles(const dg_view *A, const dg_view *B, const dg_view *C, float
     ViewInfo ai;
     dg_status st = analyse(A, false, &ai);
     if (st != DG_OK) return st;
-    if (ai.rows > 8 || g_force_kind.load() != 0) return dg_gemm(A, B, C, alpha, beta, scale_a, nullptr, stream);
+    const auto by_rule = [&] {
+        return gemm_call(A, B, C, alpha, beta, scale_a, nullptr, nullptr, DG_ACT_NONE, true, stream);
+    };
+    if (ai.rows > 8 || g_force_kind.load() != 0) return by_rule();
     Views v{A, B, C, {}, {}, {}};
+    v.ordered = true;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != DG_OK) return st;
     const Override rule;
     Plan pl;
     if ((st = make_plan(v, alpha, beta, ds->num_sms, &pl, false, &rule)) != DG_OK) return st;
     if (pl.info.kind != DG_KIND_GEMV_K || !umma_plan(v, pl.info.M, pl.info.N, pl.info.K, beta, ds->num_sms, false, &pl))
-        return dg_gemm(A, B, C, alpha, beta, scale_a, nullptr, stream);
+        return by_rule();
     LaunchRec rec;
     st = build_launch(v, pl, alpha, beta, scale_a, nullptr, nullptr, DG_ACT_NONE, ds, stream, &rule, &rec);
     return st == DG_OK ? fire(rec, stream) : st;
@@ -1196,54 +1257,7 @@ dg_status dg_gemm_ex(const dg_view *A, const dg_view *B, const dg_view *C, float
         bias = epilogue->bias;
         act = epilogue->activation;
     }
-    // a call identical to a recent one on this thread and device reuses its
-    // validated plan, parameters and tensor maps
-    CallKey key;
-    std::memset(&key, 0, sizeof(key));
-    key.A = *A;
-    key.B = *B;
-    key.C = *C;
-    key.alpha = alpha;
-    key.beta = beta;
-    key.sa = scale_a;
-    key.sb = scale_b;
-    key.bias = bias;
-    key.act = act;
-    key.epoch = g_epoch.load();
-    key.stream = stream;
-    if (cudaGetDevice(&key.dev) != cudaSuccess) {
-        cudaGetLastError();
-        key.dev = -1;
-    }
-    if (key.dev >= 0)
-        for (int i = 0; i < 8; ++i)
-            if (t_calls.used[i] && key_equal(t_calls.key[i], key))
-                return fire(t_calls.rec[i], static_cast<cudaStream_t>(stream));
-
-    Views v{A, B, C, {}, {}, {}};
-    v.act = act;
-    Plan pl;
-    // argument errors are reported before any CUDA call
-    dg_status st = make_plan(v, alpha, beta, 148, &pl);
-    if (st != DG_OK) return st;
-    if (pl.info.kind == DG_KIND_NONE) return DG_OK;
-    DeviceState *ds = nullptr;
-    st = device_state(&ds);
-    if (st != DG_OK) return st;
-    if (ds->num_sms != 148) {
-        st = make_plan(v, alpha, beta, ds->num_sms, &pl);
-        if (st != DG_OK) return st;
-    }
-    const int slot = t_calls.next;
-    t_calls.used[slot] = false;
-    st = build_launch(v, pl, alpha, beta, scale_a, scale_b, bias, act, ds, static_cast<cudaStream_t>(stream), nullptr,
-                      &t_calls.rec[slot]);
-    if (st != DG_OK) return st;
-    key.epoch = g_epoch.load();  // a replaced Stream-K workspace invalidated the cache
-    t_calls.key[slot] = key;
-    t_calls.used[slot] = true;
-    t_calls.next = (slot + 1) % 8;
-    return fire(t_calls.rec[slot], static_cast<cudaStream_t>(stream));
+    return gemm_call(A, B, C, alpha, beta, scale_a, scale_b, bias, act, false, stream);
 }
 
 dg_status dg_gemm(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta,
