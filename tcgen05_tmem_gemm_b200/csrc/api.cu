@@ -228,7 +228,9 @@ struct Views {
     const dg_view *A, *B, *C;
     ViewInfo a, b, c;
     int act = DG_ACT_NONE;  // the call's activation: split-K partials add into C only without one
-    bool ordered = false;   // sums in a fixed order whatever DG_OPT_DETERMINISTIC says
+    // a product inside another entry point: sums in a fixed order whatever DG_OPT_DETERMINISTIC says, and
+    // no Stream-K, whose workspace belongs to the stream (two graphs captured on one stream would share it)
+    bool inner = false;
 };
 
 uint32_t make_idesc(int in_dtype, bool p_mn, bool q_mn, int bn, int m = 128) {
@@ -513,7 +515,7 @@ bool umma_plan(const Views &v, int64_t M, int64_t N, int64_t K, float beta, int 
     if (gcl > 1) in.grid = (int32_t)std::min<int64_t>(units2, (num_sms / gcl) * gcl);
     // split-K with beta == 1 and FP32 C: the splits can add their partials
     // straight into C through one 2-D tensor map of C (its i group one dim)
-    if (split > 1 && beta == 1.f && v.C->dtype == DG_F32 && v.c.tma_ok && g_deterministic.load() == 0 && !v.ordered &&
+    if (split > 1 && beta == 1.f && v.C->dtype == DG_F32 && v.c.tma_ok && g_deterministic.load() == 0 && !v.inner &&
         v.act == DG_ACT_NONE) {
         in.split_reduce_add = 1;
     }
@@ -987,7 +989,7 @@ struct CallKey {
     const float *sa, *sb;
     const float *bias;
     int act;
-    int ordered;
+    int inner;
     int dev;
     uint32_t epoch;
     void *stream;  // a Stream-K launch uses its stream's workspace
@@ -1035,7 +1037,7 @@ dg_status build_launch(Views &v, Plan &pl, float alpha, float beta, const float 
 
 // The call of dg_gemm_ex, its arguments taken apart.
 dg_status gemm_call(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta, const float *scale_a,
-                    const float *scale_b, const float *bias, int act, bool ordered, void *stream) {
+                    const float *scale_b, const float *bias, int act, bool inner, void *stream) {
     // a call identical to a recent one on this thread and device reuses its
     // validated plan, parameters and tensor maps
     CallKey key;
@@ -1049,7 +1051,7 @@ dg_status gemm_call(const dg_view *A, const dg_view *B, const dg_view *C, float 
     key.sb = scale_b;
     key.bias = bias;
     key.act = act;
-    key.ordered = ordered;
+    key.inner = inner;
     key.epoch = g_epoch.load();
     key.stream = stream;
     if (cudaGetDevice(&key.dev) != cudaSuccess) {
@@ -1063,17 +1065,17 @@ dg_status gemm_call(const dg_view *A, const dg_view *B, const dg_view *C, float 
 
     Views v{A, B, C, {}, {}, {}};
     v.act = act;
-    v.ordered = ordered;
+    v.inner = inner;
     Plan pl;
     // argument errors are reported before any CUDA call
-    dg_status st = make_plan(v, alpha, beta, 148, &pl);
+    dg_status st = make_plan(v, alpha, beta, 148, &pl, !inner);
     if (st != DG_OK) return st;
     if (pl.info.kind == DG_KIND_NONE) return DG_OK;
     DeviceState *ds = nullptr;
     st = device_state(&ds);
     if (st != DG_OK) return st;
     if (ds->num_sms != 148) {
-        st = make_plan(v, alpha, beta, ds->num_sms, &pl);
+        st = make_plan(v, alpha, beta, ds->num_sms, &pl, !inner);
         if (st != DG_OK) return st;
     }
     const int slot = t_calls.next;
@@ -1227,7 +1229,7 @@ dg_status gemm_tiles(const dg_view *A, const dg_view *B, const dg_view *C, float
     };
     if (ai.rows > 8 || g_force_kind.load() != 0) return by_rule();
     Views v{A, B, C, {}, {}, {}};
-    v.ordered = true;
+    v.inner = true;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != DG_OK) return st;
     const Override rule;

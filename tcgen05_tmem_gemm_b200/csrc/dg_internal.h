@@ -272,7 +272,7 @@ struct PairCall {
 dg_status pair_call(PairCall &c, cudaStream_t stream);
 // dg_gemm that leaves the GEMVs out: their K-contiguous kernel keeps x in shared memory per pair of
 // columns and is made for few columns.  Its sums are in a fixed order: with beta 1 and FP32 C the splits
-// of k are not added into C as they arrive.
+// of k are not added into C as they arrive; and it uses no memory but its operands (no Stream-K).
 dg_status gemm_tiles(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta,
                      const float *scale_a, cudaStream_t stream);
 
