@@ -1203,7 +1203,7 @@ dg_status pair_call(PairCall &c, cudaStream_t stream) {
         return st;
     UmmaParams &p = rec.umma;
     p.ce = c.ce;
-    p.k_chunk = std::max(1, 1024 / in.block_k);  // statistics: see ce_stats_rows_long
+    p.k_chunk = std::max(1, 1024 / in.block_k);  // statistics, gradient: see ce_stats_rows_long
     if (partial) {
         if (!encode_2d_box(&rec.t2, DG_F32, c.C->ptr, in.N, c.C->shape[0], c.C->stride[0], 32, 32, true))
             return DG_ERR_UNSUPPORTED;

@@ -197,4 +197,66 @@ __device__ __forceinline__ void ce_grad_rows_tma(const CeTile &ce, const EpiPara
     }
 }
 
+// The same for a long k, whose chunks are added in `sums` as in
+// ce_stats_rows_long: the logits have to be those that lse was made of, or
+// p - 1 at the target of a confident row is nothing but the difference of two
+// errors (at k = 4096 and a logit of 30, one accumulator for all of k put it
+// off by 3e-4).  The sums hold the warp's two blocks of 64 columns.
+__device__ __forceinline__ void ce_grad_rows_long(float (&sums)[kSlotCols], const CeTile &ce, const EpiParams &e,
+                                                  const CUtensorMap *gmap, uint32_t stage, uint32_t t_row, int i_base,
+                                                  int Mi, int j0, int w, int Nj, int lane, int half, bool first,
+                                                  bool last) {
+    const int c0 = 64 * half;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        if (c0 + 128 * b >= w) continue;  // a half-width tile (warp-uniform)
+#pragma unroll
+        for (int q = 0; q < 64; q += 16) {
+            uint32_t r[16];
+            __syncwarp();
+            tmem_ld16(t_row + (uint32_t)(c0 + 128 * b + q), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float v = __uint_as_float(r[c]);
+                sums[64 * b + q + c] = first ? v : sums[64 * b + q + c] + v;
+            }
+        }
+    }
+    if (!last || i_base >= Mi) return;
+    const bool bf16_out = e.c_dtype == DG_BF16;
+    const float alpha = e.alpha;
+    RowGrad row{0.f, 0.f, kIgnored, 0};
+    if (i_base + lane < Mi) row = ce.rows[i_base + lane];
+    const uint32_t rowa = stage + (uint32_t)lane * 128u;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int j = j0 + c0 + 128 * b;
+        if (c0 + 128 * b >= w || j >= Nj) continue;
+        const int hit = row.target - ce.v0 - j;
+        if (lane == 0) bulk_wait_read<0>();  // the copy that last read the block is done with it
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            float g[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float q = exp_fast(alpha * sums[64 * b + 8 * u + c] - row.lse);
+                g[c] = row.target < 0 ? 0.f : row.scale * (8 * u + c == hit ? q - 1.f : q);
+            }
+            uint32_t p[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                p[c] = bf16_out ? pack2<true>(g[2 * c], g[2 * c + 1]) : pack2<false>(g[2 * c], g[2 * c + 1]);
+            st_shared_v4(rowa + ((uint32_t)(u ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(gmap, stage, j, i_base);
+            bulk_commit();
+        }
+    }
+}
+
 }  // namespace dg

@@ -157,7 +157,7 @@ struct UmmaParams {
     uint32_t *sk_hdr;        // [0] sequence number of the last completed launch, [1] CTAs done
     // linear cross entropy (instances of the CTA-pair kernel)
     CeTile ce;
-    int32_t k_chunk;         // statistics, partial sums: k stages per accumulator
+    int32_t k_chunk;         // k stages per accumulator (not kPairWide)
     int32_t plane_rows;      // partial sums: rows of C's map from one chunk of k to the next
     // control
     int *err_word;

@@ -551,9 +551,11 @@ int64_t tile_slots(int64_t piece) { return (piece + kSlotCols - 1) / kSlotCols; 
 // Whether the CTA-pair kernel makes the logits: operands (or copies of them)
 // it can read through TMA, and either enough 256 x 256 tiles for its pairs of SMs, or more rows
 // than the thin products' swapped tiles take, or a k so short that a round of
-// tiles takes no longer than the launch it saves.
+// tiles takes no longer than the launch it saves.  (64 columns: what the
+// gradient's tensor stores take; lse and the gradient then come from the same
+// logits.)
 bool tiles_worth_it(const Problem &p, int num_sms) {
-    return p.tensor && (p.w.tma_ok || p.copy_w) &&
+    return p.tensor && (p.w.tma_ok || p.copy_w) && p.V >= 64 &&
            (((p.T + 255) / 256) * ((p.V + 255) / 256) * 2 >= num_sms || p.T > 64 || p.D <= kShortDim);
 }
 

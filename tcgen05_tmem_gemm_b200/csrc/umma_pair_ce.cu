@@ -25,7 +25,9 @@ cudaError_t run_use(const UmmaParams &p, const CUtensorMap *tp, const CUtensorMa
     case kPairStats:
         if (p.k_chunk < p.kb_total) return run_pair<KSUB, EPI_CE_STATS_LONG>(p, tp, tq, tc, grid, smem, s);
         return run_pair<KSUB, EPI_CE_STATS>(p, tp, tq, tc, grid, smem, s);
-    case kPairGrad: return run_pair<KSUB, EPI_CE_GRAD>(p, tp, tq, tc, grid, smem, s);
+    case kPairGrad:
+        if (p.k_chunk < p.kb_total) return run_pair<KSUB, EPI_CE_GRAD_LONG>(p, tp, tq, tc, grid, smem, s);
+        return run_pair<KSUB, EPI_CE_GRAD>(p, tp, tq, tc, grid, smem, s);
     case kPairWide: return run_pair<KSUB, EPI_STORE_WIDE>(p, tp, tq, tc, grid, smem, s);
     default: return run_pair<KSUB, EPI_PARTIAL>(p, tp, tq, tc, grid, smem, s);
     }

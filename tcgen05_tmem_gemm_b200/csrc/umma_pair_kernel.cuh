@@ -205,8 +205,9 @@ __device__ __forceinline__ float *sk_slot(const UmmaParams &p, int q, uint32_t r
     return p.sk_part + (size_t)(q * 2 + (int)rank) * (size_t)(kHalfM * p.bn);
 }
 
-// What the epilogue does with a tile.  EPI_CE_STATS_LONG: EPI_CE_STATS over a
-// long k, summed in chunks (see ce_stats_rows_long).  The cross entropy's
+// What the epilogue does with a tile.  EPI_CE_STATS_LONG, EPI_CE_GRAD_LONG:
+// EPI_CE_STATS and EPI_CE_GRAD over a long k, summed in chunks (see
+// ce_stats_rows_long, ce_grad_rows_long).  The cross entropy's
 // epilogues compute an exponential per element and have eight warps, two per
 // quarter of the TMEM lanes.  EPI_STORE_WIDE: EPI_STORE with eight warps, for a
 // k so short that the stores take longer than the products.  EPI_PARTIAL: each
@@ -218,7 +219,8 @@ enum : int {
     EPI_CE_STATS_LONG = 2,
     EPI_CE_GRAD = 3,
     EPI_STORE_WIDE = 4,
-    EPI_PARTIAL = 5
+    EPI_PARTIAL = 5,
+    EPI_CE_GRAD_LONG = 6
 };
 
 __host__ __device__ constexpr int pair_epi_warps(int epi) {
@@ -250,7 +252,9 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L.aux_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.aux_off + 4);
 
-    constexpr int KMODE = EPI == EPI_CE_STATS_LONG ? K_CHUNKS : EPI == EPI_PARTIAL ? K_SPLIT : K_WHOLE;
+    constexpr int KMODE = EPI == EPI_CE_STATS_LONG || EPI == EPI_CE_GRAD_LONG ? K_CHUNKS
+                          : EPI == EPI_PARTIAL                                    ? K_SPLIT
+                                                                                  : K_WHOLE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const EpiParams e = p.epi;  // a local copy: its fields stay in registers
-        float sums[128];  // EPI_CE_STATS_LONG: this thread's row and columns, over the chunks so far
+        float sums[128];  // EPI_CE_*_LONG: this thread's row and columns, over the chunks so far
         (void)sums;
         int local = 0;
         uint32_t nblk = 0;  // tensor-store blocks this warp has issued
@@ -456,6 +460,10 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
                 else if (EPI == EPI_CE_GRAD)
                     ce_grad_rows_tma(p.ce, e, &tmap_c, sbase + L.epi_off + (uint32_t)(warp - 2) * kEpiBlockBytes,
                                      t_row, i - lane, p.Mi, j0, pw.w, p.Nj, lane, 64 * half);
+                else if (EPI == EPI_CE_GRAD_LONG)
+                    ce_grad_rows_long(sums, p.ce, e, &tmap_c,
+                                      sbase + L.epi_off + (uint32_t)(warp - 2) * kEpiBlockBytes, t_row, i - lane, p.Mi,
+                                      j0, pw.w, p.Nj, lane, half, pw.kb0 == 0, pw.kb1 == p.kb_total);
                 else {
                     const uint32_t blocks = sbase + L.epi_off + (uint32_t)(warp - 2) * 2u * kEpiBlockBytes;
                     __syncwarp();
