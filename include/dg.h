@@ -290,10 +290,14 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W,
  *    overlap X, W or the other.
  *  workspace as above, from dg_linear_ce_grad_workspace.
  * G is held one piece of the vocabulary at a time, rounded to the type of X
- * (as the gradient of logits of that type would be).  16-bit pieces are first
- * divided by the largest |dloss| of a row that counts, found on the device, and
- * multiplied back in FP32: a gradient that all rows share then costs no
- * rounding, and neither small probabilities nor a loss scale leave F16's range.
+ * (as the gradient of logits of that type would be), whatever the types of dX
+ * and dW.  16-bit pieces are first divided by the largest |dloss| of a row that
+ * counts, found on the device, and multiplied back in FP32: a gradient that all
+ * rows share then costs no rounding, and neither small probabilities nor a loss
+ * scale leave F16's range.  With F16 and a dloss per row, each row of a smaller
+ * |dloss| is also scaled by a power of two, which is taken back in dX's row in
+ * FP32 and in dW through the call's copy of X's row: a row at 2^-24 of the
+ * largest still has its dX to F16's rounding.
  * The products are summed in FP32 over all pieces; dX and dW are rounded once.
  * Runs are bit-identical.
  */

@@ -116,9 +116,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 // 16-bit pieces of G: dloss is divided by the largest |dloss| of a row that
 // counts, so that a gradient that is the same for all rows (a mean) is exactly
 // 1 and G's -1 + p at the target is rounded next to 1, where the rounding of
-// dloss * (p - 1) would shift a row as a whole; F16 pieces are also scaled to
-// the middle of F16's range (2^9).  norm[0] = that factor, norm[1] = its
-// inverse, which the products multiply their FP32 sums by.
+// dloss * (p - 1) would shift a row as a whole.  F16 pieces are also scaled
+// towards the top of F16's range (kTop), and rows of a smaller dloss each by a
+// power of two more (see ce_rows_kernel): their probabilities would be
+// subnormal otherwise.  norm[0] = the largest |dloss|, norm[1] = norm[0] / top,
+// which the products multiply their FP32 sums by.
+constexpr float kTop = 16384.f;  // |G| <= 1 times this: a factor of four below the largest F16
 __device__ __forceinline__ float largest_dloss(const char *dloss, int64_t dloss_stride, const int64_t *target,
                                                int64_t ignore_index, int64_t T, int64_t V, float (&red)[32]) {
     float big = 0.f;
@@ -231,16 +234,76 @@ __device__ __forceinline__ void copy_row(const char *src, int64_t step, char *ds
 // itself, which saves the launch of ce_norm_kernel.
 constexpr int64_t kOwnNormRows = 2048;
 
+// An F16 row's finite elements are below 2^(the result) in magnitude; -100 if they are all 0.
+__device__ __forceinline__ int row_exponent(const DevView &x, const char *src, int D, int vec, uint32_t (&red)[8]) {
+    uint32_t most = 0;
+    auto meet = [&](uint32_t h) {
+        h &= 0x7fffu;
+        if (h < 0x7c00u) most = max(most, h);
+    };
+    if (vec) {
+        for (int d = threadIdx.x; d < D / 8; d += blockDim.x) {
+            const uint4 q = reinterpret_cast<const uint4 *>(src)[d];
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) meet(w[i]), meet(w[i] >> 16);
+        }
+    } else {
+        for (int d = threadIdx.x; d < D; d += blockDim.x)
+            meet(*reinterpret_cast<const uint16_t *>(src + axis_offset(x.col, d)));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
+    __syncthreads();
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) most = max(most, red[i]);
+    int k = -100;
+    if (most) frexpf(__half2float(__ushort_as_half((unsigned short)most)), &k);
+    return k;
+}
+
+// An F16 row times `scale`, a power of two, by one block.
+__device__ __forceinline__ void copy_row_scaled(const DevView &x, const char *src, char *dst, int D, int vec,
+                                                float scale) {
+    auto times = [&](uint32_t h) {
+        return (uint32_t)__half_as_ushort(__float2half_rn(__half2float(__ushort_as_half((unsigned short)h)) * scale));
+    };
+    if (vec) {
+        for (int d = threadIdx.x; d < D / 8; d += blockDim.x) {
+            uint4 q = reinterpret_cast<const uint4 *>(src)[d];
+            uint32_t *w = &q.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = times(w[i] & 0xffffu) | times(w[i] >> 16) << 16;
+            reinterpret_cast<uint4 *>(dst)[d] = q;
+        }
+    } else {
+        for (int d = threadIdx.x; d < D; d += blockDim.x)
+            reinterpret_cast<uint16_t *>(dst)[d] =
+                (uint16_t)times(*reinterpret_cast<const uint16_t *>(src + axis_offset(x.col, d)));
+    }
+}
+
 // Per row: its RowGrad, and (xc != null) a copy of X's row, zero in rows that
 // take no part, so that whatever those rows hold stays out of dW.
+//
+// row_undo != null (F16 pieces, a dloss per row): a row whose |dloss| is 2^e
+// times the largest would have its probabilities in F16's subnormals, so G's
+// row is multiplied by 2^-h, e <= h <= 0, and the factor 2^h goes to dX's row
+// (row_undo[t], FP32) and, for dW's sum over the rows, to the copy of X's row
+// (scale_copy).  h = e where dW is not asked for.  Else h = e + 10: G's 16 384
+// times 2^-10 leaves probabilities above 2^-18 normal, and the rounding of the
+// copy's small elements to multiples of 2^-24 moves dW by no more than 2^-35 of
+// the largest dloss; and the copy's largest element stays at 2^-10 or above.
 __global__ void __launch_bounds__(256)
     ce_rows_kernel(const DevView x, int D, int64_t T, int64_t V, const int64_t *target, int64_t ignore_index,
                    const float *lse, const char *dloss, int64_t dloss_stride, float *norm, int own_norm, float top,
-                   RowGrad *rows, float *undo, int64_t undo_n, char *xc, int64_t ldx, int vec, int *err_word) {
+                   RowGrad *rows, float *undo, int64_t undo_n, float *row_undo, int scale_copy, char *xc, int64_t ldx, int vec,
+                   int *err_word) {
     pdl_wait_then_release();
     const int64_t t = blockIdx.x;
     const int y = target ? read_target(target, ignore_index, V, t) : 0;
     __shared__ float red[32];
+    __shared__ uint32_t red_bits[8];
+    const char *src = xc ? x.ptr + axis_offset(x.row, t) : nullptr;
     float big = 1.f;
     if (norm) {
         if (own_norm) {
@@ -253,21 +316,39 @@ __global__ void __launch_bounds__(256)
             big = norm[0];
         }
     }
+    int h = 0;  // the same for the whole block
+    float scale = 0.f;
+    if (rows && y >= 0) {
+        scale = *reinterpret_cast<const float *>(dloss + t * dloss_stride);
+        if (row_undo) {
+            const float q = fabsf(scale) / big;
+            int e = 0;
+            if (q > 0.f && q < 1.f) frexpf(q, &e);
+            h = max(min(e, 0), -100);
+            if (scale_copy) {
+                h = min(0, h + 10);
+                if (h < 0) h = max(h, min(0, -9 - row_exponent(x, src, D, vec, red_bits)));
+            }
+        }
+    }
     if (rows && threadIdx.x == 0) {
         RowGrad r;
         r.lse = lse[t];
-        r.scale = y < 0 ? 0.f : *reinterpret_cast<const float *>(dloss + t * dloss_stride);
-        if (norm) r.scale = r.scale / big * top;
+        r.scale = norm ? ldexpf(scale, -h) / big * top : scale;
         r.target = y;
         r.pad_ = 0;
         rows[t] = r;
+        if (row_undo) row_undo[t] = ldexpf(big / top, h);
         if (y == kInvalid && err_word) atomicCAS(err_word, 0, (int)DG_ERR_VALUE);
     }
     if (undo)  // the inverse for every row of the products
         for (int64_t i = t * blockDim.x + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * blockDim.x) undo[i] = big / top;
     if (!xc) return;
-    const char *src = x.ptr + axis_offset(x.row, t);
     char *dst = xc + t * ldx;
+    if (scale_copy && h < 0) {
+        copy_row_scaled(x, src, dst, D, vec, ldexpf(1.f, h));
+        return;
+    }
     if (vec) {  // 16 bytes at a time
         const int n = D * elem_bytes(x.dtype) / 16;
 #pragma unroll 4
@@ -425,13 +506,14 @@ __global__ void __launch_bounds__(256) ce_round_kernel(const float *acc, int64_t
 
 // dX from the planes of partial sums (FP32, in plane order) and, with several
 // pieces of the vocabulary, the sum over the earlier ones: the running sum to
-// acc_out, or (acc_out null) alpha * norm[1] times the whole sum to dX.
+// acc_out, or (acc_out null) alpha * norm[1] (or row_undo) times the whole sum to dX.
 // ROWS rows per block: with many rows a block's start takes longer than its loads
 // (20000 x 1001, one plane: 99 -> 53 us).
 template <int ROWS>
 __global__ void __launch_bounds__(256)
     ce_planes_kernel(const float *planes, int64_t ld, int used, int64_t plane_rows, const float *acc_in,
-                     float *acc_out, float alpha, const float *norm, const DevView out, int64_t M, int D) {
+                     float *acc_out, float alpha, const float *norm, const float *row_undo, const DevView out, int64_t M,
+                     int D) {
     pdl_wait_then_release();
     const int64_t t0 = (int64_t)blockIdx.x * ROWS;
     const int d = blockIdx.y * 256 + threadIdx.x;
@@ -454,16 +536,18 @@ __global__ void __launch_bounds__(256)
         return;
     }
     char *to = const_cast<char *>(out.ptr) + axis_offset(out.col, d);
-    const float scale = alpha * norm[1];
+    float scale[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) scale[r] = alpha * (row_undo ? row_undo[t0 + (r < rows ? r : 0)] : norm[1]);
     if (out.row.n == 1) {
         to += t0 * out.row.stride[0];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
-            if (r < rows) store_elem(to + r * out.row.stride[0], out.dtype, scale * v[r]);
+            if (r < rows) store_elem(to + r * out.row.stride[0], out.dtype, scale[r] * v[r]);
     } else {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
-            if (r < rows) store_elem(to + axis_offset(out.row, t0 + r), out.dtype, scale * v[r]);
+            if (r < rows) store_elem(to + axis_offset(out.row, t0 + r), out.dtype, scale[r] * v[r]);
     }
 }
 
@@ -501,6 +585,7 @@ struct Problem {
     ViewInfo x, w, dx, dw;
     Mat wm, dwm;
     bool tensor = false;   // 16-bit operands
+    bool half = false;     // F16
     bool copy_w = false;   // pieces of W are copied to a form that TMA can read
     bool place_dw = false; // pieces of dW are made in the workspace and copied to their place
 };
@@ -517,6 +602,7 @@ dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
     if (X->dtype != W->dtype || X->dtype == DG_E4M3) return DG_ERR_DTYPE;
     p->es = elem_size(X->dtype);
     p->tensor = X->dtype != DG_F32;
+    p->half = X->dtype == DG_F16;
     // the products put T and V on a grid dimension of the CUDA-core kernel
     const int64_t most = int64_t(65535) * 64;
     if (p->T > most || p->V > most || p->D > most) return DG_ERR_UNSUPPORTED;
@@ -529,6 +615,7 @@ dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
 // The workspace's parts, each 256-byte aligned, for pieces of `piece` columns.
 struct Layout {
     int64_t xc = 0, part = 0, run = 0, ztarget = 0, z = 0, rows = 0, norm = 0, undo = 0, g = 0, acc = 0, planes = 0;
+    int64_t xl = 0, row_undo = 0;
     int64_t wc = 0, oc = 0;
     int64_t ldx = 0, ldz = 0, ldg = 0;
     int64_t total = 0;
@@ -543,6 +630,10 @@ int64_t take(Layout *l, int64_t bytes) {
 // X is copied when the tensor cores could not read it in place through TMA
 // (a copy costs T D elements, a gathered operand slows every tile).
 bool forward_copies_x(const Problem &p) { return p.tensor && !p.x.tma_ok; }
+
+// F16: the gradient's copy of X may be scaled row by row, so the logits are
+// made of X itself or of a copy of their own.
+bool own_logits_copy(const Problem &p, bool need_dw) { return p.half && need_dw && forward_copies_x(p); }
 
 int64_t undo_count(const Problem &p) { return std::max(p.T, std::max(p.D, p.V)); }
 int64_t stat_slots(int64_t piece) { return (piece + kStatCols - 1) / kStatCols; }
@@ -731,6 +822,8 @@ Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     l.rows = take(&l, p.T * (int64_t)sizeof(RowGrad));
     l.norm = take(&l, 256);
     l.undo = take(&l, p.es == 2 ? undo_count(p) * 4 : 0);
+    l.row_undo = take(&l, p.half ? p.T * 4 : 0);
+    l.xl = take(&l, own_logits_copy(p, need_dw) ? p.T * l.ldx : 0);
     l.acc = take(&l, need_dx && piece < p.V && (dx_dtype != DG_F32 || n.dx > 0) ? p.T * p.D * 4 : 0);
     const int64_t cols = std::min(piece, p.V);
     l.planes = take(&l, std::max(plane_bytes(p.T, p.D, n.dx),
@@ -886,7 +979,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
         DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl, dev_of(X, p.x),
                                   (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
                                   (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f, (RowGrad *)nullptr,
-                                  (float *)nullptr, (int64_t)0, ws + l.xc, l.ldx, x_vec(X, p), (int *)nullptr)));
+                                  (float *)nullptr, (int64_t)0, (float *)nullptr, 0, ws + l.xc, l.ldx, x_vec(X, p), (int *)nullptr)));
     }
     float2 *part = reinterpret_cast<float2 *>(ws + l.part), *run = reinterpret_cast<float2 *>(ws + l.run);
     float *ztarget = reinterpret_cast<float *>(ws + l.ztarget), *z = reinterpret_cast<float *>(ws + l.z);
@@ -957,16 +1050,16 @@ dg_status in_planes(PairCall &call, char *planes, cudaStream_t s) {
     return st;
 }
 
-// alpha * norm[1] times the product through planes, to `out` or (acc_out) to the running sum.
+// alpha * norm[1] (or row_undo) times the product through planes, to `out` or (acc_out) to the running sum.
 dg_status planes_product(PairCall call, char *planes, const DevView &out, const float *acc_in, float *acc_out,
-                         float alpha, const float *norm, int pdl, cudaStream_t s) {
+                         float alpha, const float *norm, const float *row_undo, int pdl, cudaStream_t s) {
     const int64_t M = call.A->shape[0], N = call.B->shape[1];
     DG_TRY(in_planes(call, planes, s));
     const int rows = M * ((N + 255) / 256) >= kManyPlaneBlocks ? 4 : 1;
     return launched(launch_ex(rows == 4 ? ce_planes_kernel<4> : ce_planes_kernel<1>,
                               dim3((unsigned)((M + rows - 1) / rows), (unsigned)((N + 255) / 256)), dim3(256), 0, s,
                               dim3(1, 1, 1), pdl, reinterpret_cast<const float *>(planes), align256(N * 4) / 4,
-                              call.chunks, (M + 255) / 256 * 256, acc_in, acc_out, alpha, norm, out, M, (int)N));
+                              call.chunks, (M + 255) / 256 * 256, acc_in, acc_out, alpha, norm, row_undo, out, M, (int)N));
 }
 
 // dW's product, k = T.  Few tiles: planes, or the paired tiles all the same
@@ -983,7 +1076,7 @@ dg_status product(const dg_view *A, const dg_view *B, const dg_view *C, const Pr
             ViewInfo ci;
             DG_TRY(analyse(C, true, &ci));
             st = planes_product(PairCall{A, B, nullptr, 1.f, nullptr, kPairPartial, {}, planes, false}, plane_space,
-                                dev_of(C, ci), nullptr, nullptr, alpha, norm, pdl, s);
+                                dev_of(C, ci), nullptr, nullptr, alpha, norm, nullptr, pdl, s);
         }
         if (st == DG_ERR_UNSUPPORTED && (tiles * 2 < num_sms || p.T <= 256)) {
             PairCall call{A, B, C, alpha, undo, kPairWide, {}, 0, false};
@@ -1050,12 +1143,14 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         return launched(launch_scale_c(dev_of(dW, p.dw), p.D, p.V, 0.f, nullptr, DG_ACT_NONE, pdl, s));
     }
     char *ws = static_cast<char *>(workspace);
-    // a row that takes no part has no use for its logits, so dW's copy of X serves them too; it
-    // comes first in the workspace
+    // a row that takes no part has no use for its logits, so dW's copy of X serves them too (but F16's);
+    // it comes first in the workspace
     const bool copy = dW != nullptr || forward_copies_x(p);
     const int64_t ldx = align256(p.D * p.es);
     const dg_view xv = copy ? view2(ws, p.T, p.D, ldx, p.es, X->dtype) : *X;
     const dg_view xt = view2(ws, p.D, p.T, p.es, ldx, X->dtype);
+    // (its place is known with the workspace's layout; until then the other copy's, of the same alignment)
+    dg_view zx = p.half && !forward_copies_x(p) ? *X : xv;
     const bool few = few_rows(p);
     bool tiles = few || tiles_worth_it(p, num_sms);  // no FP32 logits in the workspace
     Planes planes = plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, num_sms);
@@ -1074,7 +1169,7 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             const Layout t = layout_of(piece);
             const dg_view gv = view2(ws + t.g, p.T, std::min(piece, p.V), t.ldg, p.es, X->dtype);
             const dg_view wv = weight_view(p, ws, t, 0, std::min(piece, p.V));
-            tiles = pair_once(PairCall{&xv, &wv, &gv, alpha, nullptr, kPairGrad, {}, 0, true}, s) == DG_OK;
+            tiles = pair_once(PairCall{&zx, &wv, &gv, alpha, nullptr, kPairGrad, {}, 0, true}, s) == DG_OK;
         }
         if (piece <= 0 || !tiles) {
             tiles = false;
@@ -1094,8 +1189,17 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     }
     const Layout l = layout_of(piece);
     RowGrad *rows = reinterpret_cast<RowGrad *>(ws + l.rows);
-    float *norm = nullptr, *undo = nullptr;
-    const float top = X->dtype == DG_F16 ? 512.f : 1.f;
+    float *norm = nullptr, *undo = nullptr, *row_undo = nullptr;
+    const float top = p.half ? kTop : 1.f;
+    if (p.half && dloss_stride != 0) row_undo = reinterpret_cast<float *>(ws + l.row_undo);
+    if (own_logits_copy(p, dW != nullptr) && !few) {
+        zx.ptr = ws + l.xl;
+        DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl,
+                                  dev_of(X, p.x), (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index,
+                                  (const float *)nullptr, (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f,
+                                  (RowGrad *)nullptr, (float *)nullptr, (int64_t)0, (float *)nullptr, 0, ws + l.xl, ldx,
+                                  x_vec(X, p), (int *)nullptr)));
+    }
     if (p.tensor) {
         norm = reinterpret_cast<float *>(ws + l.norm);
         undo = reinterpret_cast<float *>(ws + l.undo);
@@ -1106,8 +1210,8 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     }
     DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
                               p.T, p.V, target, ignore_index, lse, reinterpret_cast<const char *>(dloss), dloss_stride,
-                              norm, p.T <= kOwnNormRows ? 1 : 0, top, rows, undo, undo_count(p),
-                              copy ? ws : (char *)nullptr, ldx, x_vec(X, p), err_word)));
+                              norm, p.T <= kOwnNormRows ? 1 : 0, top, rows, undo, undo_count(p), row_undo,
+                              dW != nullptr ? 1 : 0, copy ? ws : (char *)nullptr, ldx, x_vec(X, p), err_word)));
     char *g = ws + l.g;
     float *z = reinterpret_cast<float *>(ws + l.z);
     const bool sum = dX && piece < p.V;                        // dX is summed over several pieces
@@ -1130,10 +1234,10 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         } else if (tiles) {
             CeTile ce = tile_of(p, target, ignore_index, v0);
             ce.rows = rows;
-            DG_TRY(pair_once(PairCall{&xv, &wv, &gv, alpha, nullptr, kPairGrad, ce, 0, false}, s));
+            DG_TRY(pair_once(PairCall{&zx, &wv, &gv, alpha, nullptr, kPairGrad, ce, 0, false}, s));
         } else {
             const dg_view zv = view2(z, p.T, cols, l.ldz, 4, DG_F32);
-            DG_TRY(gemm_tiles(&xv, &wv, &zv, alpha, 0.f, nullptr, s));
+            DG_TRY(gemm_tiles(&zx, &wv, &zv, alpha, 0.f, nullptr, s));
             const int64_t blocks = p.T * ((cols + 1023) / 1024);
             DG_TRY(launched(launch_ex(ce_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, s, one, pdl,
                                       (const float *)z, l.ldz / 4, p.T, (int)v0, (int)cols, (const RowGrad *)rows, g,
@@ -1143,9 +1247,9 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
             const bool first = v0 == 0, last = v0 + cols == p.V;
             DG_TRY(planes_product(PairCall{&gv, &wt, nullptr, 1.f, nullptr, kPairPartial, {}, planes.dx, false},
                                   ws + l.planes, dev_of(dX, p.dx), first ? nullptr : acc, last ? nullptr : acc, alpha,
-                                  norm, pdl, s));
+                                  norm, row_undo, pdl, s));
         } else if (dX) {
-            DG_TRY(gemm_tiles(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, undo, s));
+            DG_TRY(gemm_tiles(&gv, &wt, &accv, alpha, v0 == 0 ? 0.f : 1.f, row_undo ? row_undo : undo, s));
         }
         if (dW) {
             // the product in the order that gives dW's unit stride to the columns of the output
