@@ -486,13 +486,15 @@ def _workspace(nbytes: int, stream):
 def linear_ce(x, w, target, loss, lse, alpha: float = 1.0, ignore_index: int = -100, stream=None, workspace=None,
               x_row_dims: int | None = None):
     """dg_linear_ce on torch tensors: the cross entropy of the logits alpha * x w
-    against `target`, without keeping the logits.  x is [..., D] (x_row_dims
-    defaults to all dims but the last), w [D, V] (a [V, D] weight is passed as
-    weight.t()), target int64, loss and lse float32, one per row.  `workspace`
-    is a uint8 tensor (at least dg_linear_ce_workspace's bytes); None takes one
-    from torch's pool.  Raises DgError on a bad status; returns (loss, lse)."""
-    xv, wv = view(x, x.dim() - 1 if x_row_dims is None else x_row_dims), view(w)
-    rows = x.numel() // x.shape[-1] if x.shape[-1] else target.numel()
+    against `target`, without keeping the logits.  x is [..., D] (its first
+    x_row_dims dims, by default all but the last, are the rows and the others
+    the features), w [D, V] (a [V, D] weight is passed as weight.t()), target
+    int64, loss and lse float32, one per row.  `workspace` is a uint8 tensor (at
+    least dg_linear_ce_workspace's bytes); None takes one from torch's pool.
+    Raises DgError on a bad status; returns (loss, lse)."""
+    rd = x.dim() - 1 if x_row_dims is None else x_row_dims
+    xv, wv = view(x, rd), view(w)
+    rows = x.shape[:rd].numel()
     _vector(target, "target", _torch.int64, rows)
     _vector(loss, "loss", _torch.float32, rows)
     _vector(lse, "lse", _torch.float32, rows)
@@ -521,7 +523,7 @@ def linear_ce_grad(x, w, target, lse, dloss, dx=None, dw=None, alpha: float = 1.
     xv, wv = view(x, rd), view(w)
     dxv = None if dx is None else view(dx, rd)
     dwv = None if dw is None else view(dw)
-    rows = x.numel() // x.shape[-1] if x.shape[-1] else target.numel()
+    rows = x.shape[:rd].numel()
     _vector(target, "target", _torch.int64, rows)
     _vector(lse, "lse", _torch.float32, rows)
     shared = dloss.numel() == 1 or not any(dloss.stride())  # one value, or expanded from one
