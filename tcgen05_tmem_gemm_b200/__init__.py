@@ -441,10 +441,10 @@ def w4(codes, scales, zeros=None, group: int = 128, K: int | None = None) -> dg_
 def gemv_w4(x, codes, scales, y, zeros=None, group: int = 128, alpha: float = 1.0, beta: float = 0.0,
             stream=None, bias=None, act="none"):
     """dg_gemv_w4 on torch tensors: y = act(alpha * x W + beta * y + bias), W [K x N]
-    given by its codes, scales and zeros (see w4); x is [R, K] or [K], R <= 8.
-    Raises DgError on a bad status."""
-    xv = view(x, 1 if x.dim() > 1 else 0)
-    yv = view(y, 1 if y.dim() > 1 else 0)
+    given by its codes, scales and zeros (see w4); x is [..., K] and y [..., N] with
+    at most 8 rows, or [K] and [N].  Raises DgError on a bad status."""
+    xv = view(x, x.dim() - 1)
+    yv = view(y, y.dim() - 1)
     W = w4(codes, scales, zeros, group, x.shape[-1])
     epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
     st = lib.dg_gemv_w4(ctypes.byref(xv), ctypes.byref(W), ctypes.byref(yv), alpha, beta, epi, _stream_ptr(stream))
