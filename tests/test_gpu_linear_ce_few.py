@@ -1,12 +1,12 @@
 """dg_linear_ce and dg_linear_ce_grad with one and two rows against a [V x D] weight (dot products on the CUDA
-cores), for logits that are not finite.  Tolerances are those of test_gpu_linear_ce."""
+cores), for logits that are not finite, and in several pieces.  Tolerances are those of test_gpu_linear_ce."""
 import math
 
 import pytest
 import torch
 
 import tcgen05_tmem_gemm_b200 as dg
-from test_gpu_linear_ce import check_forward, inputs, run_forward
+from test_gpu_linear_ce import IGNORE, check_forward, check_grads, inputs, run_both, run_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,34 @@ def test_a_nan_among_logits_of_minus_infinity(T):
     masked[177] = math.nan
     _, lse = run_forward(x, masked.t(), y)
     assert bool(lse.isnan().all())
+
+
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("D,V", [(8, 1), (256, 100), (264, 4001), (1032, 9000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_alpha_ignored_rows_and_types(T, D, V, dtype):
+    run_both(T, D, V, dtype, out="f32", alpha=0.5, ignored=0.6)
+    run_both(T, D, V, dtype, out="f32", alpha=-1.75, ignored=0.0)
+
+
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("fraction", [0.0, 0.1, 0.3, 0.8])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_several_pieces(T, fraction, out):
+    # the gradient walks the vocabulary in pieces, the target in any of them
+    for seed_width in (64, 72, 136):
+        run_both(T, seed_width, 5003, "bf16", out=out, fraction=fraction, ignored=0.0)
+    run_both(T, 64, 5003, "f16", out=out, alpha=0.75, fraction=fraction, ignored=0.0)
+
+
+@pytest.mark.parametrize("v", [0, 255, 256, 300, 4999])
+def test_targets_in_every_piece(v):
+    x, w, _, dl = inputs(1, 64, 5000, "bf16", ignored=0.0)
+    y = torch.full((1,), v, device="cuda")
+    loss, lse = run_forward(x, w, y)
+    check_forward(x, w, y, loss, lse)
+    dx, dw = torch.empty(1, 64, device="cuda"), torch.empty(5000, 64, device="cuda").t()
+    least, _ = dg.dg_linear_ce_grad_workspace(dg.view(x), dg.view(w), dg.view(dx), dg.view(dw))
+    ws = torch.empty(least, dtype=torch.uint8, device="cuda")
+    dg.linear_ce_grad(x, w, y, lse, dl, dx, dw, ignore_index=IGNORE, workspace=ws)
+    check_grads(x, w, y, dl, dx, dw)
