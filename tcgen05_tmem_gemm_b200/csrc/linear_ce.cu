@@ -283,7 +283,8 @@ __device__ __forceinline__ void copy_row_scaled(const DevView &x, const char *sr
 }
 
 // Per row: its RowGrad, and (xc != null) a copy of X's row, zero in rows that
-// take no part, so that whatever those rows hold stays out of dW.
+// take no part, so that whatever those rows hold stays out of dW (xl != null:
+// another one).
 //
 // row_undo != null (F16 pieces, a dloss per row): a row whose |dloss| is 2^e
 // times the largest would have its probabilities in F16's subnormals, so G's
@@ -296,7 +297,7 @@ __device__ __forceinline__ void copy_row_scaled(const DevView &x, const char *sr
 __global__ void __launch_bounds__(256)
     ce_rows_kernel(const DevView x, int D, int64_t T, int64_t V, const int64_t *target, int64_t ignore_index,
                    const float *lse, const char *dloss, int64_t dloss_stride, float *norm, int own_norm, float top,
-                   RowGrad *rows, float *undo, int64_t undo_n, float *row_undo, int scale_copy, char *xc, int64_t ldx, int vec,
+                   RowGrad *rows, float *undo, int64_t undo_n, float *row_undo, int scale_copy, char *xc, char *xl, int64_t ldx, int vec,
                    int *err_word) {
     pdl_wait_then_release();
     const int64_t t = blockIdx.x;
@@ -344,31 +345,29 @@ __global__ void __launch_bounds__(256)
     if (undo)  // the inverse for every row of the products
         for (int64_t i = t * blockDim.x + threadIdx.x; i < undo_n; i += (int64_t)gridDim.x * blockDim.x) undo[i] = big / top;
     if (!xc) return;
-    char *dst = xc + t * ldx;
-    if (scale_copy && h < 0) {
-        copy_row_scaled(x, src, dst, D, vec, ldexpf(1.f, h));
-        return;
-    }
-    if (vec) {  // 16 bytes at a time
-        const int n = D * elem_bytes(x.dtype) / 16;
+    auto copy = [&](char *dst) {
+        if (vec) {  // 16 bytes at a time
+            const int n = D * elem_bytes(x.dtype) / 16;
 #pragma unroll 4
-        for (int d = threadIdx.x; d < n; d += blockDim.x)
-            reinterpret_cast<uint4 *>(dst)[d] =
-                y < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldcs(reinterpret_cast<const uint4 *>(src) + d);
-        return;
-    }
-    if (x.col.n == 1) {
-        if (x.dtype == DG_F32) copy_row<float>(src, x.col.stride[0], dst, D, y < 0);
-        else copy_row<uint16_t>(src, x.col.stride[0], dst, D, y < 0);
-    } else if (x.dtype == DG_F32) {
-        for (int d = threadIdx.x; d < D; d += blockDim.x)
-            reinterpret_cast<float *>(dst)[d] =
-                y < 0 ? 0.f : *reinterpret_cast<const float *>(src + axis_offset(x.col, d));
-    } else {
-        for (int d = threadIdx.x; d < D; d += blockDim.x)
-            reinterpret_cast<uint16_t *>(dst)[d] =
-                y < 0 ? 0 : *reinterpret_cast<const uint16_t *>(src + axis_offset(x.col, d));
-    }
+            for (int d = threadIdx.x; d < n; d += blockDim.x)
+                reinterpret_cast<uint4 *>(dst)[d] =
+                    y < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldcs(reinterpret_cast<const uint4 *>(src) + d);
+        } else if (x.col.n == 1) {
+            if (x.dtype == DG_F32) copy_row<float>(src, x.col.stride[0], dst, D, y < 0);
+            else copy_row<uint16_t>(src, x.col.stride[0], dst, D, y < 0);
+        } else if (x.dtype == DG_F32) {
+            for (int d = threadIdx.x; d < D; d += blockDim.x)
+                reinterpret_cast<float *>(dst)[d] =
+                    y < 0 ? 0.f : *reinterpret_cast<const float *>(src + axis_offset(x.col, d));
+        } else {
+            for (int d = threadIdx.x; d < D; d += blockDim.x)
+                reinterpret_cast<uint16_t *>(dst)[d] =
+                    y < 0 ? 0 : *reinterpret_cast<const uint16_t *>(src + axis_offset(x.col, d));
+        }
+    };
+    if (xl) copy(xl + t * ldx);
+    if (scale_copy && h < 0) copy_row_scaled(x, src, xc + t * ldx, D, vec, ldexpf(1.f, h));
+    else copy(xc + t * ldx);
 }
 
 // Up to kFewRows rows against a W whose columns are contiguous (a [V x D]
@@ -631,10 +630,6 @@ int64_t take(Layout *l, int64_t bytes) {
 // (a copy costs T D elements, a gathered operand slows every tile).
 bool forward_copies_x(const Problem &p) { return p.tensor && !p.x.tma_ok; }
 
-// F16: the gradient's copy of X may be scaled row by row, so the logits are
-// made of X itself or of a copy of their own.
-bool own_logits_copy(const Problem &p, bool need_dw) { return p.half && need_dw && forward_copies_x(p); }
-
 int64_t undo_count(const Problem &p) { return std::max(p.T, std::max(p.D, p.V)); }
 int64_t stat_slots(int64_t piece) { return (piece + kStatCols - 1) / kStatCols; }
 int64_t tile_slots(int64_t piece) { return (piece + kSlotCols - 1) / kSlotCols; }
@@ -823,7 +818,7 @@ Layout grad_layout(const Problem &p, int64_t piece, bool need_dx, bool need_dw, 
     l.norm = take(&l, 256);
     l.undo = take(&l, p.es == 2 ? undo_count(p) * 4 : 0);
     l.row_undo = take(&l, p.half ? p.T * 4 : 0);
-    l.xl = take(&l, own_logits_copy(p, need_dw) ? p.T * l.ldx : 0);
+    l.xl = take(&l, p.half && need_dw ? p.T * l.ldx : 0);
     l.acc = take(&l, need_dx && piece < p.V && (dx_dtype != DG_F32 || n.dx > 0) ? p.T * p.D * 4 : 0);
     const int64_t cols = std::min(piece, p.V);
     l.planes = take(&l, std::max(plane_bytes(p.T, p.D, n.dx),
@@ -979,7 +974,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
         DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl, dev_of(X, p.x),
                                   (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index, (const float *)nullptr,
                                   (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f, (RowGrad *)nullptr,
-                                  (float *)nullptr, (int64_t)0, (float *)nullptr, 0, ws + l.xc, l.ldx, x_vec(X, p), (int *)nullptr)));
+                                  (float *)nullptr, (int64_t)0, (float *)nullptr, 0, ws + l.xc, (char *)nullptr, l.ldx, x_vec(X, p), (int *)nullptr)));
     }
     float2 *part = reinterpret_cast<float2 *>(ws + l.part), *run = reinterpret_cast<float2 *>(ws + l.run);
     float *ztarget = reinterpret_cast<float *>(ws + l.ztarget), *z = reinterpret_cast<float *>(ws + l.z);
@@ -1143,14 +1138,13 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
         return launched(launch_scale_c(dev_of(dW, p.dw), p.D, p.V, 0.f, nullptr, DG_ACT_NONE, pdl, s));
     }
     char *ws = static_cast<char *>(workspace);
-    // a row that takes no part has no use for its logits, so dW's copy of X serves them too (but F16's);
-    // it comes first in the workspace
-    const bool copy = dW != nullptr || forward_copies_x(p);
+    // a row that takes no part has no use for its logits, so dW's copy of X serves them too; it
+    // comes first in the workspace.  An F16 copy whose rows may be scaled does not: the logits get their own
+    const bool copy = dW != nullptr || forward_copies_x(p), own_logits = p.half && dW && dloss_stride != 0;
     const int64_t ldx = align256(p.D * p.es);
     const dg_view xv = copy ? view2(ws, p.T, p.D, ldx, p.es, X->dtype) : *X;
     const dg_view xt = view2(ws, p.D, p.T, p.es, ldx, X->dtype);
-    // (its place is known with the workspace's layout; until then the other copy's, of the same alignment)
-    dg_view zx = p.half && !forward_copies_x(p) ? *X : xv;
+    dg_view zx = xv;  // what the logits are made of (its place is known with the layout)
     const bool few = few_rows(p);
     bool tiles = few || tiles_worth_it(p, num_sms);  // no FP32 logits in the workspace
     Planes planes = plan_planes(p, grad_piece(p), dX != nullptr, dW != nullptr, num_sms);
@@ -1192,14 +1186,7 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     float *norm = nullptr, *undo = nullptr, *row_undo = nullptr;
     const float top = p.half ? kTop : 1.f;
     if (p.half && dloss_stride != 0) row_undo = reinterpret_cast<float *>(ws + l.row_undo);
-    if (own_logits_copy(p, dW != nullptr) && !few) {
-        zx.ptr = ws + l.xl;
-        DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl,
-                                  dev_of(X, p.x), (int)p.D, p.T, p.V, (const int64_t *)nullptr, ignore_index,
-                                  (const float *)nullptr, (const char *)nullptr, (int64_t)0, (float *)nullptr, 0, 1.f,
-                                  (RowGrad *)nullptr, (float *)nullptr, (int64_t)0, (float *)nullptr, 0, ws + l.xl, ldx,
-                                  x_vec(X, p), (int *)nullptr)));
-    }
+    if (own_logits) zx.ptr = ws + l.xl;
     if (p.tensor) {
         norm = reinterpret_cast<float *>(ws + l.norm);
         undo = reinterpret_cast<float *>(ws + l.undo);
@@ -1211,7 +1198,9 @@ dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W, const int64_t *t
     DG_TRY(launched(launch_ex(ce_rows_kernel, dim3((unsigned)p.T), dim3(row_threads(p.T)), 0, s, one, pdl, dev_of(X, p.x), (int)p.D,
                               p.T, p.V, target, ignore_index, lse, reinterpret_cast<const char *>(dloss), dloss_stride,
                               norm, p.T <= kOwnNormRows ? 1 : 0, top, rows, undo, undo_count(p), row_undo,
-                              dW != nullptr ? 1 : 0, copy ? ws : (char *)nullptr, ldx, x_vec(X, p), err_word)));
+                              own_logits ? 1 : 0,
+                              copy ? ws : (char *)nullptr, own_logits && !few ? ws + l.xl : (char *)nullptr, ldx,
+                              x_vec(X, p), err_word)));
     char *g = ws + l.g;
     float *z = reinterpret_cast<float *>(ws + l.z);
     const bool sum = dX && piece < p.V;                        // dX is summed over several pieces
