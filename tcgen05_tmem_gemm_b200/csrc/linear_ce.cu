@@ -587,6 +587,7 @@ struct Problem {
     bool half = false;     // F16
     bool copy_w = false;   // pieces of W are copied to a form that TMA can read
     bool place_dw = false; // pieces of dW are made in the workspace and copied to their place
+    int few_slots = kFewBlocks;  // most blocks of ce_few_kernel's statistics: the pairs that the workspace holds
 };
 
 dg_status check_problem(const dg_view *X, const dg_view *W, Problem *p) {
@@ -663,14 +664,14 @@ cudaError_t run_few(const Problem &p, const DevView &x, const char *w, int v0, i
 }
 
 // The blocks of a launch over `cols` columns: three per SM, which is what their registers allow.
-int few_blocks(int64_t cols, int num_sms) {
-    return (int)std::min<int64_t>((cols + 7) / 8, std::min<int64_t>(3 * num_sms, kFewBlocks));
+int few_blocks(const Problem &p, int64_t cols, int num_sms) {
+    return (int)std::min<int64_t>((cols + 7) / 8, std::min<int64_t>(3 * num_sms, p.few_slots));
 }
 
 template <bool GRAD>
 cudaError_t launch_few(const Problem &p, const DevView &x, const char *w, int v0, int cols, float alpha,
                        const CeTile &ce, char *g, int64_t ldg, int num_sms, int pdl, cudaStream_t s) {
-    const int blocks = few_blocks(cols, num_sms);
+    const int blocks = few_blocks(p, cols, num_sms);
     const bool b = x.dtype == DG_BF16;
     if (p.T == 1)
         return b ? run_few<__nv_bfloat16, 1, GRAD>(p, x, w, v0, cols, alpha, ce, g, ldg, blocks, pdl, s)
@@ -761,12 +762,21 @@ Layout forward_layout(const Problem &p, int64_t piece, Way way) {
     l.ldx = align256(p.D * p.es);
     l.ldz = align256(piece * 4);
     l.xc = take(&l, way != kFew && forward_copies_x(p) ? p.T * l.ldx : 0);
-    l.part = take(&l, (way == kFew ? kFewBlocks : way == kTiles ? tile_slots(piece) : stat_slots(piece)) * p.T * 8);
+    l.part = take(&l, (way == kFew ? p.few_slots : way == kTiles ? tile_slots(piece) : stat_slots(piece)) * p.T * 8);
     l.run = take(&l, p.T * 8);
     l.ztarget = take(&l, p.T * 4);
     l.z = take(&l, way == kPieces ? p.T * l.ldz : 0);
     take_w(p, piece, &l);
     return l;
+}
+
+// The pairs of ce_few_kernel that `bytes` hold beside the rest of its layout.  The least workspace of any
+// call holds some, so that its rows always take this way, as their gradient does: lse and the gradient
+// come from the same logits.
+int few_slots(Problem p, int64_t bytes) {
+    p.few_slots = 0;
+    const int64_t room = (bytes - forward_layout(p, p.V, kFew).total) / 256 * 256;
+    return (int)std::max<int64_t>(0, std::min<int64_t>(kFewBlocks, room / (p.T * 8)));
 }
 
 // A product [M x K] [K x N] of few tiles and a long k (dX, whose k is the
@@ -950,7 +960,8 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
     const dg_view xv = forward_copies_x(p) ? view2(ws, p.T, p.D, align256(p.D * p.es), p.es, X->dtype) : *X;
     Way way = kPieces;
     int64_t tile_piece = 0;
-    if (few_rows(p) && forward_layout(p, p.V, kFew).total <= workspace_bytes) {
+    if (few_rows(p)) p.few_slots = few_slots(p, workspace_bytes);
+    if (few_rows(p) && p.few_slots > 0) {
         way = kFew;
     } else if (tiles_worth_it(p, num_sms)) {
         CeTile ce = tile_of(p, target, ignore_index, 0);
@@ -990,7 +1001,7 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W, const int64_t *target
             ce.ztarget = ztarget;
             DG_TRY(launched(launch_few<false>(p, dev_of(X, p.x), p.wm.ptr, 0, (int)cols, alpha, ce, nullptr, 0, num_sms,
                                               pdl, s)));
-            slots = few_blocks(cols, num_sms);
+            slots = few_blocks(p, cols, num_sms);
         } else if (way == kTiles) {
             CeTile ce = tile_of(p, target, ignore_index, v0);
             ce.part = part;

@@ -76,3 +76,28 @@ def test_confident_rows_of_a_long_k(T, D, V, order, dtype):
     tol = e.gather(1, y[:, None])[:, 0] + u * 2 * rest[:, 0] * (1 + grow[:, 0]) + u * e.amax(1) + V * 2.0 ** -33 + \
         (64 + V / 16) * 2.0 ** -23 * 2 * (rest[:, 0] * (1 + grow[:, 0]) + e.amax(1))
     assert bool((sums.abs() <= tol).all()), (float((sums.abs() / tol).max()), float(sums.abs().max()))
+
+
+@pytest.mark.parametrize("T,V", [(1, 500), (2, 500), (2, 9000)])
+@pytest.mark.parametrize("share", [0.0, 0.3])
+def test_few_rows_in_a_small_workspace(T, V, share):
+    # lse made with the least workspace, the gradient with the best: the same dot products
+    D = 4000
+    x, w, y = problem(T, D, V, "bf16", 30.0, "vd")
+    least, best = dg.dg_linear_ce_workspace(dg.view(x), dg.view(w))
+    loss, lse = run_forward(x, w, y, workspace=torch.empty(least + int(share * (best - least)), dtype=torch.uint8,
+                                                           device="cuda"))
+    z = x.double() @ w.double()
+    lse64 = torch.logsumexp(z, 1)
+    # FP32 dot products: D / 256 terms a lane and five steps over the warp, 2^-24 each
+    S = x.double().abs() @ w.double().abs()
+    dz = (D / 256 * 8 + 5) * 2.0 ** -24 * S.amax(1)
+    assert bool(((lse.double() - lse64).abs() <= dz + 2.0 ** -19 + (512 + V / 8) * 2.0 ** -24 + 2.0 ** -23 * lse64).all())
+    dw = torch.empty(w.shape, device="cuda")
+    dg.linear_ce_grad(x, w, y, lse, torch.ones(1, device="cuda"), None, dw, ignore_index=IGNORE)
+    G = dw[D:D + T].double()
+    hit = G.gather(1, y[:, None])[:, 0]
+    # 1 - p is below 1e-8, and so are all terms but one of the sum of exponentials, which is 1: what is left is the
+    # rounding of lse and of z - lse, and the exponential's of a number next to 0
+    e = 2.0 ** -23 * (z.amax(1) + lse64) + 2.0 ** -21
+    assert bool((hit.abs() <= e + 1e-8).all()), float(hit.abs().max())
