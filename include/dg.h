@@ -267,8 +267,13 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y,
  *  A row whose logits hold a NaN or +infinity has loss and lse NaN; the rows
  *  that are ignored never reach the loss or a gradient, whatever they hold.
  *  Sums are FP32 and in a fixed order.
+ *  Logits of 16-bit operands are FP32 sums on the tensor cores, which truncate:
+ *  a logit whose products all have one sign is low by up to 3e-6 of itself per
+ *  1024 k of an accumulator.  The paired tiles start a fresh one every 1024 k;
+ *  one and two rows are rounded to nearest (dot products of a [V x D] weight).
  * Errors: as dg_gemm; DG_ERR_SHAPE also when V == 0 with T > 0, or for a
- * workspace that is too small; DG_ERR_ALIGN for a misaligned array.
+ * workspace that is too small; DG_ERR_ALIGN for a misaligned array;
+ * DG_ERR_UNSUPPORTED for T, D or V above 65535 * 64.
  */
 dg_status dg_linear_ce(const dg_view *X, const dg_view *W,
                        const int64_t *target, int64_t ignore_index,
@@ -300,6 +305,11 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W,
  * largest still has its dX to F16's rounding.
  * The products are summed in FP32 over all pieces; dX and dW are rounded once.
  * Runs are bit-identical.
+ * The logits are made again, as dg_linear_ce makes them where each call has its
+ * best workspace: their errors then cancel in exp(z - lse), and p - 1 at the
+ * target of a confident row is as good as FP32 logits allow.  Where a smaller
+ * workspace makes one of the two calls sum k in other parts, p is off by up to
+ * the error of a logit given above.
  */
 dg_status dg_linear_ce_grad(const dg_view *X, const dg_view *W,
                             const int64_t *target, int64_t ignore_index,

@@ -16,8 +16,10 @@ __device__ __forceinline__ int read_target(const int64_t *target, int64_t ignore
     return (y < 0 || y >= V) ? kInvalid : (int)y;
 }
 
-// exp(x) = 2^(x log2 e) with the hardware's power of two (relative error
-// about 2^-22, below the FP32 sums it goes into).
+// exp(x) = 2^(x log2 e) with the hardware's power of two: relative error about
+// 2^-22 + |x| 2^-23 (the product with log2 e is rounded), and 0 for results
+// below 2^-126.  In lse's sums the terms next to the maximum count, where x is
+// a few units; G's small probabilities are rounded to 16 bits after it.
 __device__ __forceinline__ float exp_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));

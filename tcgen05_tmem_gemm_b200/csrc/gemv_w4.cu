@@ -17,19 +17,27 @@
 // 0x000F000F are the codes of k+j and k+j+4 in the low bits of two 16-bit
 // halves.  OR-ed into the significand of 128 (BF16) or 1024 (F16) they read
 // as 128 + code or 1024 + code, and one packed add of -(128 + zero) leaves
-// code - zero exactly.  F16's longer significand also takes the codes of odd
-// j four bits higher (1024 + 16 code), where a packed multiply-add by 1/16
-// leaves the same and saves the shift: the shifts and masks run on the
-// half-rate integer pipe, which bounds the kernel next to HBM.  The pairs
+// code - zero exactly (the usual conversion of small integers through a
+// floating-point number's significand).  F16's longer significand also takes
+// the codes of odd j four bits higher (1024 + 16 code), where a packed
+// multiply-add by 1/16 leaves the same and saves the shift.  The pairs
 // (k+j, k+j+4) fix the order in which a thread meets k; x is staged in shared
 // memory in the same order.
 //
-// Work split.  It streams W once and is bound by HBM, so what counts is bytes
-// in flight and few instructions per byte.  A warp owns 16 columns and a share
-// of k, in steps of 128 k; every lane copies the 16 bytes of each of its two
-// columns that it will itself unpack into a ring of two batches of steps in shared
-// memory (cp.async: no registers, no synchronisation between lanes, bytes past
-// a column's end arrive as zeros).  A block is column tiles x warps along k
+// What bounds it.  1 x 4096 x 128000 (BF16, groups of 128, zero points): 73 us,
+// 3.7 TB/s.  No unit is full: HBM 44 %, issue slots 56 %, the pipe of the
+// shifts and masks 51 %.  Fourteen warps per SM (registers) run chains of
+// dependent instructions: a warp waits 1.6 cycles per instruction for the one
+// before it, 0.7 for the integer pipe, 0.6 for memory and 0.5 at barriers.
+// Small products are bound by their start: about 6 us until the first codes
+// have come and x is staged.
+//
+// Work split.  It streams W once, so what counts is bytes in flight and few
+// instructions per byte.  A warp owns 16 columns and a share of k, in steps of
+// 128 k; every lane copies the 16 bytes of each of its two columns that it will
+// itself unpack into a ring of two batches of steps in shared memory (cp.async:
+// no registers, no synchronisation between lanes, bytes past a column's end
+// arrive as zeros).  A block is column tiles x warps along k
 // over one staged slice of x; blocks of a cluster share k further where there
 // are few columns.  Partial sums meet in shared memory and, across a cluster,
 // in distributed shared memory, in a fixed order.

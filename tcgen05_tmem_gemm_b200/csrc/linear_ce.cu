@@ -10,6 +10,12 @@
 // to a pair (m, s): their maximum and sum_v exp(z - m); two pairs join as
 //   m = max(m1, m2),  s = s1 exp(m1 - m) + s2 exp(m2 - m),
 // so one pass over the logits is enough and none of them has to be kept.
+//
+// In fewer than 32 bits there is G alone: the two products of the gradients
+// take it as a tensor-core operand, which is rounded to the type of X (two
+// 16-bit parts would double both products).  Its rows are scaled first so that
+// the rounding is relative to each entry (ce_norm_kernel, ce_rows_kernel).
+// Logits, statistics and all sums are FP32.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
