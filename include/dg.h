@@ -301,8 +301,10 @@ dg_status dg_linear_ce(const dg_view *X, const dg_view *W,
  * rows share then costs no rounding, and neither small probabilities nor a loss
  * scale leave F16's range.  With F16 and a dloss per row, each row of a smaller
  * |dloss| is also scaled by a power of two, which is taken back in dX's row in
- * FP32 and in dW through the call's copy of X's row: a row at 2^-24 of the
- * largest still has its dX to F16's rounding.
+ * FP32 and in dW through the call's copy of X's row.  Without dW every row then
+ * has its dX to F16's rounding; with dW rows down to 2^-20 of the largest have
+ * it, if an element of their X is 1 or more in magnitude, and further ones lose
+ * their probabilities below 2^-17 first.
  * The products are summed in FP32 over all pieces; dX and dW are rounded once.
  * Runs are bit-identical.
  * The logits are made again, as dg_linear_ce makes them where each call has its
