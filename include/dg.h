@@ -9,9 +9,11 @@
  * template of §4.1; "DeepGEMM deep dive", §1.1 for the operation and §2.4 for
  * the FP8 rescale), with FP32 accumulation, over operands given as strided
  * "views" that are read in place (recalibration page, §2.1-§2.2: no reshape or
- * contiguous() copy).  Two more serve the same weights in language models:
- * dg_gemv_w4 (products with 4-bit weights) and dg_linear_ce /
- * dg_linear_ce_grad (the loss of an output layer, and its gradient).
+ * contiguous() copy).  Others serve the same weights in language models:
+ * dg_gemv_w4 (products with 4-bit weights), dg_linear_ce / dg_linear_ce_grad
+ * (the loss of an output layer, and its gradient) and dg_gemm_grouped /
+ * dg_gemm_grouped_dw (the products of a layer of experts, and their weights'
+ * gradients).
  *
  * Conventions shared by all entry points
  *  - Memory: the caller owns every buffer.  Data pointers are DEVICE pointers
@@ -328,6 +330,62 @@ dg_status dg_linear_ce_workspace(const dg_view *X, const dg_view *W,
 dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W,
                                       const dg_view *dX, const dg_view *dW,
                                       int64_t *least, int64_t *best);
+
+/*
+ * Grouped products — the layers of experts of a language model: R rows sorted
+ * by group (expert), one weight per group, sizes that only the device knows.
+ *
+ *  offsets  device int64[groups + 1]: the rows of group g are offsets[g] ..
+ *    offsets[g + 1] - 1.  Groups may be empty; rows in front of offsets[0] and
+ *    from offsets[groups] on belong to none.  A group whose offsets decrease or
+ *    leave [0, R] counts as empty and is reported by dg_sync_status as
+ *    DG_ERR_VALUE.
+ *  groups   at most 1024.
+ * One launch each, whatever the sizes; no workspace.  Sums are FP32 and in a
+ * fixed order: runs are bit-identical.
+ * F16, BF16 and E4M3 (both operands alike) run on the tensor cores where every
+ * row, or column, of an operand that is contiguous starts at a multiple of 16
+ * bytes; F32, and any other view, on the CUDA cores (correct, and much slower).
+ */
+
+/*
+ * dg_gemm_grouped — for the rows r of each group g
+ *
+ *     C[r][n] = act( alpha * sa[r] * sb[g][n] * sum_k A[r][k] B[g][k][n]
+ *                    + beta * C[r][n] + bias[g][n] )
+ *
+ * A [R x K] and C [R x N] are views as in dg_gemm; B is a view of three dims
+ * [groups, K, N] with row_dims 2 (a [groups, N, K] weight is passed with its
+ * last two dims exchanged; stride 0 along the groups shares one weight).  The
+ * gradient of A is the same call with dC for A and B's last two dims exchanged.
+ * Rows of C that belong to no group are left as they were.
+ * scale_a device float32[R], scale_b and the epilogue's bias device
+ * float32[groups * N], each or NULL.
+ * alpha == 0 or K == 0 reads neither A nor B; beta == 0 does not read C.
+ * Errors: as dg_gemm_ex; DG_ERR_NDIM for a B that is not [groups, K, N] with
+ * row_dims 2; DG_ERR_UNSUPPORTED for more than 1024 groups or a size of 2^31 -
+ * 2^13 and more.
+ */
+dg_status dg_gemm_grouped(const dg_view *A, const dg_view *B, const dg_view *C,
+                          const int64_t *offsets, int32_t groups,
+                          float alpha, float beta,
+                          const float *scale_a, const float *scale_b,
+                          const dg_epilogue *epilogue, void *stream);
+
+/*
+ * dg_gemm_grouped_dw — the gradients of the groups' weights:
+ *
+ *     dW[g] = alpha * sum_r X[r]^T dY[r] + beta * dW[g]     over the rows r of g
+ *
+ * X [R x K], dY [R x N] (F16, BF16, or E4M3 and F32 on the CUDA cores), dW a
+ * view of three dims [groups, K, N] with row_dims 2, of F32, F16 or BF16.  Every
+ * group's dW is written: that of an empty group becomes beta * dW[g].  Rows
+ * that belong to no group are not read into any sum, whatever they hold.
+ * Errors as above.
+ */
+dg_status dg_gemm_grouped_dw(const dg_view *X, const dg_view *dY, const dg_view *dW,
+                             const int64_t *offsets, int32_t groups,
+                             float alpha, float beta, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *dg_status_string(dg_status s);

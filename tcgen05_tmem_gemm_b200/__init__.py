@@ -140,6 +140,12 @@ def _load():
     L.dg_linear_ce_workspace.restype = ctypes.c_int
     L.dg_linear_ce_grad_workspace.argtypes = [V, V, V, V, P(I64), P(I64)]
     L.dg_linear_ce_grad_workspace.restype = ctypes.c_int
+    I32, F = ctypes.c_int32, ctypes.c_float
+    L.dg_gemm_grouped.argtypes = [V, V, V, ctypes.c_void_p, I32, F, F, ctypes.c_void_p, ctypes.c_void_p,
+                                  P(dg_epilogue), ctypes.c_void_p]
+    L.dg_gemm_grouped.restype = ctypes.c_int
+    L.dg_gemm_grouped_dw.argtypes = [V, V, V, ctypes.c_void_p, I32, F, F, ctypes.c_void_p]
+    L.dg_gemm_grouped_dw.restype = ctypes.c_int
     L.dg_status_string.argtypes = [ctypes.c_int]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_sync_status.argtypes = [ctypes.c_void_p]
@@ -215,6 +221,9 @@ def view(t, row_dims: int = 1) -> dg_view:
     es = ELEM_SIZE[code]
     shape, stride = t.shape, t.stride()
     n = len(shape)
+    if n == 3:
+        return dg_view.from_buffer_copy(_VIEW.pack(t.data_ptr(), 3, row_dims, *shape, 1, stride[0] * es,
+                                                   stride[1] * es, stride[2] * es, 0, code, 0))
     if n == 2:
         return dg_view.from_buffer_copy(_VIEW.pack(t.data_ptr(), 2, row_dims, shape[0], shape[1], 1, 1,
                                                    stride[0] * es, stride[1] * es, 0, 0, code, 0))
@@ -334,6 +343,22 @@ def dg_linear_ce_grad_workspace(X: dg_view, W: dg_view, dX=None, dW=None):
     if st != DG_OK:
         raise DgError(st, "dg_linear_ce_grad_workspace")
     return least.value, best.value
+
+
+def dg_gemm_grouped(A: dg_view, B: dg_view, C: dg_view, offsets, groups: int, alpha: float, beta: float,
+                    scale_a=None, scale_b=None, epi=None, stream=None) -> int:
+    """C[r] = act(alpha * sa[r] * sb[g] * A[r] B[g] + beta * C[r] + bias[g]) for the rows r of each group g; returns
+    the status."""
+    return lib.dg_gemm_grouped(ctypes.byref(A), ctypes.byref(B), ctypes.byref(C), _ptr(offsets), int(groups),
+                               float(alpha), float(beta), _ptr(scale_a), _ptr(scale_b),
+                               None if epi is None else ctypes.byref(epi), _stream_ptr(stream))
+
+
+def dg_gemm_grouped_dw(X: dg_view, dY: dg_view, dW: dg_view, offsets, groups: int, alpha: float, beta: float,
+                       stream=None) -> int:
+    """dW[g] = alpha * X^T dY over the rows of group g + beta * dW[g]; returns the status."""
+    return lib.dg_gemm_grouped_dw(ctypes.byref(X), ctypes.byref(dY), ctypes.byref(dW), _ptr(offsets), int(groups),
+                                  float(alpha), float(beta), _stream_ptr(stream))
 
 
 def dg_sync_status(stream=None) -> int:
@@ -545,3 +570,46 @@ def linear_ce_grad(x, w, target, lse, dloss, dx=None, dw=None, alpha: float = 1.
     if st != DG_OK:
         raise DgError(st, "dg_linear_ce_grad")
     return dx, dw
+
+
+def _groups(offsets, stack) -> int:
+    """The number of groups, from int64 offsets [groups + 1] and a [groups, K, N] tensor."""
+    if offsets.dtype != _torch.int64 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 tensor of groups + 1 elements")
+    if stack.dim() != 3 or stack.shape[0] != offsets.shape[0] - 1:
+        raise ValueError(f"expected [{offsets.shape[0] - 1}, K, N], got {tuple(stack.shape)}")
+    return stack.shape[0]
+
+
+def gemm_grouped(a, b, c, offsets, scale_a=None, scale_b=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
+                 act="none", stream=None):
+    """dg_gemm_grouped on torch tensors: c[r] = act(alpha * scale_a[r] * scale_b[g] * (a[r] b[g]) + beta * c[r] +
+    bias[g]) for the rows r of each group g, offsets[g] <= r < offsets[g + 1].  a is [R, K], b [groups, K, N] (a
+    [groups, N, K] weight is passed as weight.transpose(1, 2)), c [R, N], offsets int64 [groups + 1] on the device;
+    scale_a float32 [R], scale_b and bias float32 [groups, N].  Raises DgError on a bad status; returns c."""
+    groups = _groups(offsets, b)
+    if scale_a is not None:
+        _vector(scale_a, "scale_a", _torch.float32, a.shape[0])
+    for name, t in (("scale_b", scale_b), ("bias", bias)):
+        if t is not None:
+            _vector(t, name, _torch.float32, groups * b.shape[2])
+    av, bv, cv = view(a), view(b, 2), view(c)
+    epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
+    st = lib.dg_gemm_grouped(ctypes.byref(av), ctypes.byref(bv), ctypes.byref(cv), offsets.data_ptr(), groups, alpha,
+                             beta, _ptr(scale_a), _ptr(scale_b), epi, _stream_ptr(stream))
+    if st != DG_OK:
+        raise DgError(st, "dg_gemm_grouped")
+    return c
+
+
+def gemm_grouped_dw(x, dy, dw, offsets, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """dg_gemm_grouped_dw on torch tensors: dw[g] = alpha * x^T dy over the rows of group g + beta * dw[g].  x is
+    [R, K], dy [R, N], dw [groups, K, N] (that of a [groups, N, K] weight is passed as dweight.transpose(1, 2)).
+    Raises DgError on a bad status; returns dw."""
+    groups = _groups(offsets, dw)
+    xv, dyv, dwv = view(x), view(dy), view(dw, 2)
+    st = lib.dg_gemm_grouped_dw(ctypes.byref(xv), ctypes.byref(dyv), ctypes.byref(dwv), offsets.data_ptr(), groups,
+                                alpha, beta, _stream_ptr(stream))
+    if st != DG_OK:
+        raise DgError(st, "dg_gemm_grouped_dw")
+    return dw

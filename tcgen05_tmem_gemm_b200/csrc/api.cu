@@ -1149,6 +1149,28 @@ int early_launch_mode() { return g_pdl.load(); }
 
 void count_launch() { g_launches.fetch_add(1); }
 
+uint64_t wait_timeout_ns() { return (uint64_t)g_timeout_ms.load() * 1000000ull; }
+
+int test_stall() { return g_stall.load(); }
+
+bool tensor_cores_allowed() { return g_force_kind.load() == 0 || g_force_kind.load() == DG_KIND_UMMA; }
+
+bool encode_map(CUtensorMap *m, int dtype, int rank, const void *ptr, const int64_t *dim, const int64_t *stride,
+                const int *box, bool swizzle128) {
+    cuuint64_t gdim[4], gstride[4];
+    cuuint32_t gbox[4], estr[4];
+    for (int d = 0; d < rank; ++d) {
+        gdim[d] = (cuuint64_t)dim[d];
+        gbox[d] = (cuuint32_t)box[d];
+        estr[d] = 1;
+        if (d + 1 < rank) gstride[d] = (cuuint64_t)stride[d];
+    }
+    return g_encode(m, tma_dtype(dtype), (cuuint32_t)rank, const_cast<void *>(ptr), gdim, gstride, gbox, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 dg_status pair_call(PairCall &c, cudaStream_t stream) {
     if (g_pair.load() == 0 || (g_force_kind.load() != 0 && g_force_kind.load() != DG_KIND_UMMA))
         return DG_ERR_UNSUPPORTED;

@@ -256,6 +256,12 @@ bool device_pointer(const void *p);                       // device memory of th
 dg_status device_info(int *num_sms, int **err_word);      // the current device's, set up on first use
 int early_launch_mode();                                  // DG_OPT_EARLY_LAUNCH
 void count_launch();                                      // one kernel enqueued (dg_launch_count)
+uint64_t wait_timeout_ns();                               // DG_OPT_WAIT_TIMEOUT_MS
+int test_stall();                                         // DG_OPT_TEST_STALL
+bool tensor_cores_allowed();                              // DG_OPT_FORCE_KIND asks for no other kind
+// A tensor map of `rank` dims, innermost first, unit stride along the first; stride[d] is dim d + 1's.
+bool encode_map(CUtensorMap *m, int dtype, int rank, const void *ptr, const int64_t *dim, const int64_t *stride,
+                const int *box, bool swizzle128);
 // One launch of the CTA-pair kernel for the linear cross entropy: A B in 256 x 256 tiles, used as
 // `use` says.  C: G or the product (null for the statistics; for partial sums an FP32 [chunks *
 // plane_rows x N] view, plane_rows a multiple of 256).  DG_ERR_UNSUPPORTED, with nothing enqueued, when the
