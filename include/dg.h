@@ -13,7 +13,8 @@
  * dg_gemv_w4 (products with 4-bit weights), dg_linear_ce / dg_linear_ce_grad
  * (the loss of an output layer, and its gradient) and dg_gemm_grouped /
  * dg_gemm_grouped_dw (the products of a layer of experts, and their weights'
- * gradients).
+ * gradients); dg_quantize_mx4, dg_dequantize_mx4 and dg_gemm_mx4 are for 4-bit
+ * floats with block scales.
  *
  * Conventions shared by all entry points
  *  - Memory: the caller owns every buffer.  Data pointers are DEVICE pointers
@@ -386,6 +387,80 @@ dg_status dg_gemm_grouped(const dg_view *A, const dg_view *B, const dg_view *C,
 dg_status dg_gemm_grouped_dw(const dg_view *X, const dg_view *dY, const dg_view *dW,
                              const int64_t *offsets, int32_t groups,
                              float alpha, float beta, void *stream);
+
+/*
+ * A matrix of 4-bit floats with block scales, rows x K (the microscaling
+ * formats MXFP4 and NVFP4):
+ *
+ *     Q[r][k] = scale * s[r][k / block] * e2m1(code[r][k])
+ *
+ * E2M1's codes 0 .. 7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign.
+ *  codes        device uint8, two codes per byte, the even k in the low four
+ *               bits; row r starts at codes + r * code_stride and has
+ *               ceil(K / 2) bytes (K odd: the last byte's high four bits are 0)
+ *  scales       device uint8, one byte per block, 16-byte aligned,
+ *               dg_mx4_scale_bytes bytes.  Of block 32 an E8M0 (2^(byte - 127),
+ *               255 is NaN), of block 16 an E4M3 (127 is NaN; the sign is not
+ *               used).  They lie in tiles of 128 rows by 4 blocks, 512 bytes
+ *               each, as the tensor cores read them: that of row r and block b
+ *               is byte r % 32 * 16 + r % 128 / 32 * 4 + b % 4 of tile
+ *               r / 128 * ceil(ceil(K / block) / 4) + b / 4.  Bytes of a tile
+ *               past the last block of a row must not be NaN
+ *               (dg_quantize_mx4 writes 0); those past the last row are not used
+ *  scale        device float32: a factor of the whole matrix, or NULL (1)
+ *  rows, K      at most 2^31 - 2^13
+ *  code_stride  BYTES between rows of codes
+ *  block        32 or 16
+ */
+typedef struct {
+    const void *codes;
+    const void *scales;
+    const float *scale;
+    int64_t rows, K;
+    int64_t code_stride;
+    int32_t block;
+    int32_t reserved; /* set to 0 */
+} dg_mx4;
+
+/* Bytes of the scales of a rows x K matrix; -1 for sizes or a block that a
+ * dg_mx4 does not have. */
+int64_t dg_mx4_scale_bytes(int64_t rows, int64_t K, int32_t block);
+
+/*
+ * dg_quantize_mx4 — writes codes and scales of x, a view of rows x K (F32, F16
+ * or BF16; any strides, so a transposed view quantises a weight along its other
+ * dim).  q->codes and q->scales are written, q->scale is read.
+ *  The value that is quantised is u = x / scale, in FP32.  With `top` the largest
+ *  |u| of a block,
+ *    block 32:  s = 2^(floor(log2(top)) - 2), at least 2^-127 (and 2^-127 for a
+ *               block of zeros);
+ *    block 16:  s = top / 6, in FP32, then rounded to E4M3 (448 at most);
+ *  and a code is u / s rounded to the nearest E2M1, ties to the even code,
+ *  magnitudes above 6 become 6; a scale that rounds to 0 has codes of 0.
+ *  A block with a NaN or an infinity gets the scale NaN.
+ * Errors: as dg_gemm; DG_ERR_VALUE for a block other than 16 and 32 or a
+ * reserved field that is not 0; DG_ERR_STRIDE for rows of codes that overlap.
+ */
+dg_status dg_quantize_mx4(const dg_view *x, const dg_mx4 *q, void *stream);
+
+/* dg_dequantize_mx4 — y = Q, for a view y of rows x K (F32, F16 or BF16, any
+ * strides): scale * s rounded to FP32, times the code's value, rounded to FP32
+ * and to y's type. */
+dg_status dg_dequantize_mx4(const dg_mx4 *q, const dg_view *y, void *stream);
+
+/*
+ * dg_gemm_mx4 — C = act(alpha * A B^T + beta * C + bias) for two such matrices
+ * of one block size, A [M x K] and B [N x K] (a weight as it is stored), on the
+ * tensor cores; epilogue as in dg_gemm_ex, or NULL.  Products are exact and
+ * summed in FP32, in a fixed order.  A block whose scale is NaN makes its row
+ * (or column) of C NaN.  C's rows and columns are one dim each, of any stride.
+ * alpha == 0 or K == 0 reads neither A nor B.
+ * Errors: as dg_gemm_ex; DG_ERR_VALUE for different blocks; DG_ERR_ALIGN for
+ * codes whose rows do not start at multiples of 16 bytes.
+ */
+dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C,
+                      float alpha, float beta, const dg_epilogue *epilogue,
+                      void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *dg_status_string(dg_status s);

@@ -107,6 +107,14 @@ class dg_w4(ctypes.Structure):
     ]
 
 
+class dg_mx4(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("code_stride", ctypes.c_int64),
+        ("block", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
 class DgError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -146,6 +154,14 @@ def _load():
     L.dg_gemm_grouped.restype = ctypes.c_int
     L.dg_gemm_grouped_dw.argtypes = [V, V, V, ctypes.c_void_p, I32, F, F, ctypes.c_void_p]
     L.dg_gemm_grouped_dw.restype = ctypes.c_int
+    L.dg_mx4_scale_bytes.argtypes = [I64, I64, I32]
+    L.dg_mx4_scale_bytes.restype = I64
+    L.dg_quantize_mx4.argtypes = [V, P(dg_mx4), ctypes.c_void_p]
+    L.dg_quantize_mx4.restype = ctypes.c_int
+    L.dg_dequantize_mx4.argtypes = [P(dg_mx4), V, ctypes.c_void_p]
+    L.dg_dequantize_mx4.restype = ctypes.c_int
+    L.dg_gemm_mx4.argtypes = [P(dg_mx4), P(dg_mx4), V, F, F, P(dg_epilogue), ctypes.c_void_p]
+    L.dg_gemm_mx4.restype = ctypes.c_int
     L.dg_status_string.argtypes = [ctypes.c_int]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_sync_status.argtypes = [ctypes.c_void_p]
@@ -177,11 +193,12 @@ lib = _load()
 
 # ------------------------------------------------------------------ views
 
-# dg_view and dg_w4 as packed bytes: filling a ctypes structure field by field
+# dg_view, dg_w4 and dg_mx4 as packed bytes: filling a ctypes structure field by field
 # costs several times as much, and small products are bound by the call.
 _VIEW = struct.Struct("=Qii8qiI")
 _W4 = struct.Struct("=3Q5q2i2i")
-assert _VIEW.size == ctypes.sizeof(dg_view) and _W4.size == ctypes.sizeof(dg_w4)
+_MX4 = struct.Struct("=3Q3q2i")
+assert _VIEW.size == ctypes.sizeof(dg_view) and _W4.size == ctypes.sizeof(dg_w4) and _MX4.size == ctypes.sizeof(dg_mx4)
 
 
 def make_view(ptr: int, shape, stride_bytes, row_dims: int, dtype) -> dg_view:
@@ -359,6 +376,27 @@ def dg_gemm_grouped_dw(X: dg_view, dY: dg_view, dW: dg_view, offsets, groups: in
     """dW[g] = alpha * X^T dY over the rows of group g + beta * dW[g]; returns the status."""
     return lib.dg_gemm_grouped_dw(ctypes.byref(X), ctypes.byref(dY), ctypes.byref(dW), _ptr(offsets), int(groups),
                                   float(alpha), float(beta), _stream_ptr(stream))
+
+
+def dg_mx4_scale_bytes(rows: int, K: int, block: int) -> int:
+    """Bytes of the scales of a rows x K matrix of 4-bit floats (-1 for sizes that have none)."""
+    return lib.dg_mx4_scale_bytes(int(rows), int(K), int(block))
+
+
+def dg_quantize_mx4(x: dg_view, q: dg_mx4, stream=None) -> int:
+    """Codes and scales of x; returns the status."""
+    return lib.dg_quantize_mx4(ctypes.byref(x), ctypes.byref(q), _stream_ptr(stream))
+
+
+def dg_dequantize_mx4(q: dg_mx4, y: dg_view, stream=None) -> int:
+    """y = the values of q; returns the status."""
+    return lib.dg_dequantize_mx4(ctypes.byref(q), ctypes.byref(y), _stream_ptr(stream))
+
+
+def dg_gemm_mx4(A: dg_mx4, B: dg_mx4, C: dg_view, alpha: float, beta: float, epi=None, stream=None) -> int:
+    """C = act(alpha * A B^T + beta * C + bias) of 4-bit floats; returns the status."""
+    return lib.dg_gemm_mx4(ctypes.byref(A), ctypes.byref(B), ctypes.byref(C), float(alpha), float(beta),
+                           None if epi is None else ctypes.byref(epi), _stream_ptr(stream))
 
 
 def dg_sync_status(stream=None) -> int:
@@ -613,3 +651,60 @@ def gemm_grouped_dw(x, dy, dw, offsets, alpha: float = 1.0, beta: float = 0.0, s
     if st != DG_OK:
         raise DgError(st, "dg_gemm_grouped_dw")
     return dw
+
+
+def empty_mx4(rows: int, K: int, block: int = 32, device="cuda"):
+    """(codes, scales): uninitialised tensors for a rows x K matrix of 4-bit floats, its rows of codes at multiples of
+    16 bytes, as gemm_mx4 wants them.  (K odd: quantize_mx4 zeroes the last byte's unused half.)"""
+    codes = _torch.empty(rows, (K + 31) // 32 * 16, dtype=_torch.uint8, device=device)[:, :(K + 1) // 2]
+    return codes, _torch.empty(max(0, dg_mx4_scale_bytes(rows, K, block)), dtype=_torch.uint8, device=device)
+
+
+def mx4(codes, scales, K: int | None = None, block: int = 32, scale=None) -> dg_mx4:
+    """A dg_mx4 of torch tensors in place: codes uint8 [rows, ceil(K / 2)], two E2M1 codes per byte along k (even k in
+    the low four bits), scales uint8 in tiles (dg_mx4_scale_bytes of them), scale a float32 of one element on the
+    device or None.  K defaults to two per byte."""
+    rows, nbytes = codes.shape
+    K = 2 * nbytes if K is None else int(K)
+    stride = codes.stride()
+    if codes.dtype != _torch.uint8 or scales.dtype != _torch.uint8:
+        raise TypeError("codes and scales must be uint8")
+    if nbytes != (K + 1) // 2 or (nbytes > 1 and stride[1] != 1):
+        raise ValueError(f"codes must have ceil(K / 2) = {(K + 1) // 2} contiguous bytes a row")
+    if scales.numel() != lib.dg_mx4_scale_bytes(rows, K, block) or not scales.is_contiguous():
+        raise ValueError(f"scales must be {lib.dg_mx4_scale_bytes(rows, K, block)} contiguous bytes (block {block})")
+    if scale is not None:
+        _vector(scale, "scale", _torch.float32, 1)
+    return dg_mx4.from_buffer_copy(_MX4.pack(codes.data_ptr(), scales.data_ptr(),
+                                             0 if scale is None else scale.data_ptr(), rows, K, stride[0], block, 0))
+
+
+def quantize_mx4(x, codes, scales, block: int = 32, scale=None, stream=None):
+    """dg_quantize_mx4 on torch tensors: the codes and block scales (see mx4) of x [rows, K] / scale, written in
+    place.  Raises DgError on a bad status; returns (codes, scales)."""
+    xv, q = view(x), mx4(codes, scales, x.shape[-1], block, scale)
+    st = lib.dg_quantize_mx4(ctypes.byref(xv), ctypes.byref(q), _stream_ptr(stream))
+    if st != DG_OK:
+        raise DgError(st, "dg_quantize_mx4")
+    return codes, scales
+
+
+def dequantize_mx4(codes, scales, y, block: int = 32, scale=None, stream=None):
+    """dg_dequantize_mx4 on torch tensors: y [rows, K] = the values of codes and scales (see mx4).  Raises DgError on
+    a bad status; returns y."""
+    yv, q = view(y), mx4(codes, scales, y.shape[-1], block, scale)
+    st = lib.dg_dequantize_mx4(ctypes.byref(q), ctypes.byref(yv), _stream_ptr(stream))
+    if st != DG_OK:
+        raise DgError(st, "dg_dequantize_mx4")
+    return y
+
+
+def gemm_mx4(a: dg_mx4, b: dg_mx4, c, alpha: float = 1.0, beta: float = 0.0, bias=None, act="none", stream=None):
+    """dg_gemm_mx4: c [M, N] = act(alpha * a b^T + beta * c + bias) of a [M, K] and b [N, K] in 4-bit floats (see
+    mx4), c a torch tensor or dg_view.  Raises DgError on a bad status; returns c."""
+    cv = _as_view(c)
+    epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
+    st = lib.dg_gemm_mx4(ctypes.byref(a), ctypes.byref(b), ctypes.byref(cv), alpha, beta, epi, _stream_ptr(stream))
+    if st != DG_OK:
+        raise DgError(st, "dg_gemm_mx4")
+    return c

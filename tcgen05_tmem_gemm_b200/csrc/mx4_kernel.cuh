@@ -1,0 +1,267 @@
+// C = A B^T of 4-bit floats with block scales: tcgen05.mma .block_scale,
+// scales in TMEM.
+//
+// A tile is 128 columns of C by up to 256 of its rows, computed as C^T: the
+// tensor core's M side (P) holds rows of B, its N side (Q) rows of A, so that
+// a single token costs an N of 16.  A stage of the ring is 256 k: 128 bytes of
+// codes per row (tensor copies, 128-byte swizzle) and the scales' tiles as
+// they lie in memory (128 rows by 4 blocks, 512 bytes), which one tcgen05.cp
+// each spreads over the lanes of TMEM.  Every stage has scale columns of its
+// own in TMEM, so a stage's release (its MMAs done) also frees its scales.
+#pragma once
+
+#include "common.cuh"
+#include "sm100.cuh"
+#include "turned_out.cuh"
+
+namespace dg {
+
+struct Mx4Params {
+    int32_t M, N, K;
+    int32_t tile_w;          // rows of C per tile: 128 or 256 (fewer in the last)
+    int32_t tiles_m, tiles_n;
+    int32_t stages;
+    int32_t k_tiles;         // tiles of scales along k
+    const uint8_t *sa, *sb;  // scales of A and of B
+    const float *fa, *fb;    // their tensors' factors, or null
+    uint32_t idesc;          // instruction descriptor without N and scale ids
+    TurnedOut out;
+    int *err_word;
+    uint64_t timeout_ns;
+    int32_t stall_loader;
+    int32_t pdl;
+};
+
+namespace {
+
+constexpr int kMx4Threads = 192;
+constexpr int kMx4K = 256;  // k per stage
+constexpr uint32_t kScaleTile = 512;
+
+struct Mx4Layout {
+    uint32_t p_bytes, q_bytes, sp_bytes, sq_bytes, stage_bytes, turn_off, bar_off, aux_off, total;
+};
+
+// q_rows: rows of Q the ring has room for; scale tiles along k: 256 / (4 block)
+__host__ __device__ inline Mx4Layout mx4_layout(int stages, int block, int tile_w, int q_rows) {
+    Mx4Layout L;
+    const uint32_t t = kMx4K / (4 * block);
+    L.p_bytes = 128 * 128;
+    L.q_bytes = (uint32_t)q_rows * 128;
+    L.sp_bytes = t * kScaleTile;
+    L.sq_bytes = (uint32_t)((tile_w + 127) / 128) * t * kScaleTile;
+    L.stage_bytes = (L.p_bytes + L.q_bytes + L.sp_bytes + L.sq_bytes + 1023) / 1024 * 1024;
+    L.turn_off = L.stage_bytes * stages;
+    L.bar_off = L.turn_off + 4 * kTurnBytes;
+    L.aux_off = L.bar_off + 8 * (2 * stages + 5);
+    L.total = L.aux_off + 16 + 1024;
+    return L;
+}
+
+// TMEM: the accumulators (two of 128 columns, or one of 256), then each stage's scales.
+__host__ __device__ inline int mx4_scale_cols(int block, int tile_w) {
+    return kMx4K / (4 * block) * (4 + 4 * ((tile_w + 127) / 128));
+}
+
+template <int BLOCK>
+__global__ void __launch_bounds__(kMx4Threads, 1)
+    mx4_kernel(const __grid_constant__ CUtensorMap tmap_p, const __grid_constant__ CUtensorMap tmap_q,
+               const __grid_constant__ CUtensorMap tmap_q16, const Mx4Params p, const int q_rows) {
+    constexpr int T = kMx4K / (4 * BLOCK);  // scale tiles per stage
+    if (threadIdx.x == 64 && p.K > 0) {
+        tma_prefetch_desc(&tmap_p);
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_q16);
+    }
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Mx4Layout L = mx4_layout(p.stages, BLOCK, p.tile_w, q_rows);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = sbase + L.bar_off;
+    const uint32_t bar_empty = bar_full + 8 * p.stages;
+    const uint32_t bar_tfull = bar_empty + 8 * p.stages;
+    const uint32_t bar_tempty = bar_tfull + 16;
+    const uint32_t bar_drain = bar_tempty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L.aux_off);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.aux_off + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WaitCtl wc{abort_flag, p.err_word, p.timeout_ns};
+    const int units = p.tiles_m * p.tiles_n;
+    const int buffers = p.tile_w <= 128 ? 2 : 1;  // accumulators
+    const int q_tiles = (p.tile_w + 127) / 128;   // scale tiles along a tile's rows of C
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 4);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512u);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();  // what comes before touches this CTA's own memory only
+
+    // the tile of unit u: m inner, so that CTAs that run at the same time share B's rows
+    auto tile_rows = [&](int u, int &m0, int &n0) {
+        const int tn = u / p.tiles_m;
+        m0 = (u - tn * p.tiles_m) * p.tile_w;
+        n0 = tn * 128;
+        return min(p.tile_w, p.M - m0);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer
+        if (lane == 0) {
+            const int stages = p.stages;
+            const bool stall = p.stall_loader == 1;
+            int it = 0, s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && !*abort_flag && u < units; u += gridDim.x) {
+                int m0, n0;
+                const int rows = tile_rows(u, m0, n0), w = (rows + 15) & ~15, qt = (rows + 127) / 128;
+                for (int k = 0; k < p.K; k += kMx4K, ++it) {
+                    if (!mbar_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!stall) {
+                        const uint32_t full = bar_full + 8 * s, ps = sbase + s * L.stage_bytes, qs = ps + L.p_bytes;
+                        const uint32_t sp = qs + L.q_bytes, sq = sp + L.sp_bytes;
+                        const int t0 = k / (4 * BLOCK);
+                        const uint32_t some = (uint32_t)min(T, p.k_tiles - t0) * kScaleTile;
+                        mbar_arrive_expect_tx(full, L.p_bytes + (uint32_t)w * 128u + (uint32_t)(1 + qt) * some);
+                        tma_load_2d(ps, &tmap_p, full, k / 2, n0);
+                        int c = 0;
+                        for (; c + 64 <= w; c += 64) tma_load_2d(qs + c * 128, &tmap_q, full, k / 2, m0 + c);
+                        for (; c < w; c += 16) tma_load_2d(qs + c * 128, &tmap_q16, full, k / 2, m0 + c);
+                        bulk_load(sp, p.sb + ((int64_t)(n0 / 128) * p.k_tiles + t0) * kScaleTile, some, full);
+                        for (int i = 0; i < qt; ++i)
+                            bulk_load(sq + (uint32_t)(i * T) * kScaleTile,
+                                      p.sa + ((int64_t)(m0 / 128 + i) * p.k_tiles + t0) * kScaleTile, some, full);
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!stall)
+                for (int d = 1; d <= stages && it - d >= 0; ++d) {
+                    const int j = it - d;
+                    mbar_wait_drain(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u, p.timeout_ns);
+                }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            const int stages = p.stages;
+            const uint32_t scale_cols = (uint32_t)mx4_scale_cols(BLOCK, p.tile_w);
+            const uint64_t da0 = make_sw128_desc(sbase, 16u, 1024);
+            const uint64_t db0 = make_sw128_desc(sbase + L.p_bytes, 16u, 1024);
+            const uint64_t ds0 = make_scales_desc(sbase + L.p_bytes + L.q_bytes);
+            int local = 0, s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && p.K > 0 && u < units; u += gridDim.x, ++local) {
+                int m0, n0;
+                const int rows = tile_rows(u, m0, n0), w = (rows + 15) & ~15, qt = (rows + 127) / 128;
+                const uint32_t idesc = p.idesc | (uint32_t)(w >> 3) << 17;
+                const int b = buffers == 2 ? local & 1 : 0, turn = buffers == 2 ? local >> 1 : local;
+                if (!mbar_wait(bar_tempty + 8 * b, ((uint32_t)turn & 1u) ^ 1u, wc)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
+                for (int k = 0; k < p.K; k += kMx4K) {
+                    if (!mbar_wait(bar_full + 8 * s, ph, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t soff = (uint64_t)((s * L.stage_bytes) >> 4);
+                    const uint32_t sfa = tmem_base + 256u + (uint32_t)s * scale_cols, sfb = sfa + 4u * T;
+                    const int left = p.K - k;
+#pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        if (t * 4 * BLOCK >= left) continue;
+                        const uint64_t ds = ds0 + soff + (uint64_t)((t * kScaleTile) >> 4);
+                        tmem_cp_scales(sfa + 4u * t, ds);
+                        for (int i = 0; i < qt; ++i)
+                            tmem_cp_scales(sfb + (uint32_t)(4 * (t * q_tiles + i)),
+                                           ds + (uint64_t)(((1 + i) * T * kScaleTile) >> 4));
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {  // 64 k each
+                        if (kk * 64 >= left) continue;
+                        // blocks of 16: a tile of scales per instruction; of 32: its lower or upper half
+                        const int t = BLOCK == 16 ? kk : kk >> 1;
+                        const uint32_t id = BLOCK == 16 ? 0u : 2u * (uint32_t)(kk & 1);
+                        const uint64_t off = soff + (uint64_t)((kk * 32) >> 4);
+                        umma_mx4<BLOCK>(d_tmem, da0 + off, db0 + off, idesc | id << 4 | id << 29, sfa + 4u * t,
+                                        sfb + (uint32_t)(4 * t * q_tiles), k > 0 || kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(bar_empty + 8 * s);
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                tc_commit(bar_tfull + 8 * b);
+            }
+            pdl_release();
+            tc_commit(bar_drain);
+            mbar_wait_drain(bar_drain, 0, p.timeout_ns);
+        }
+    } else {
+        // ------------------------------------------------------ epilogue
+        const int quarter = warp & 3;
+        const uint32_t turn_at = sbase + L.turn_off + (uint32_t)quarter * kTurnBytes;
+        TurnedOut o = p.out;
+        if (p.fa != nullptr) o.alpha *= *p.fa;
+        if (p.fb != nullptr) o.alpha *= *p.fb;
+        int local = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++local) {
+            int m0, n0;
+            const int rows = tile_rows(u, m0, n0);
+            const int b = buffers == 2 ? local & 1 : 0, turn = buffers == 2 ? local >> 1 : local;
+            if (p.K > 0) {
+                if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)turn & 1u, wc)) break;
+                tc_fence_after();
+            }
+            turned_rows(o, turn_at, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 128), p.K == 0, m0,
+                        rows, n0 + quarter * 32, lane);
+            if (p.K > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_tempty + 8 * b);
+            }
+        }
+    }
+
+    // ---------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512u);
+    }
+}
+
+}  // namespace
+
+}  // namespace dg

@@ -1,0 +1,451 @@
+"""dg_quantize_mx4, dg_dequantize_mx4 and dg_gemm_mx4 against their definitions in FP64.
+
+Quantised codes and scales are compared bit by bit: the definition has no
+tolerance.  Values read back differ by the two FP32 roundings of scale * s * v
+(2^-23 of the value) and half a step of the output's type.
+
+Products are exact in FP32; an instruction adds 64 of them and the running sum,
+each aligned to the largest and cut at FP32's last bit, so it loses at most 65
+times 2^-23 of the largest, and a sum of k products (k / 64 + 1) 65 2^-23 S with
+S the sum of magnitudes: (65 + 1.02 k) 2^-23 S.  The factors, alpha, beta and
+the bias round six times, at most 2^-21 (|z| + |beta c| + |bias|); GeLU's slope
+is below 1.13, its own error 2^-20 |z| (FP32 outputs) or 2^-11 |z|.
+"""
+import math
+
+import pytest
+import torch
+
+import tcgen05_tmem_gemm_b200 as dg
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+ACT = {"none": lambda z: z, "relu": lambda z: z.clamp(min=0),
+       "gelu_tanh": lambda z: 0.5 * z * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))}
+MAGNITUDES = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+
+
+def quantised(x, block, scale=None):
+    """Codes [R, K] and scale bytes [R, blocks] by the definition, on the CPU in FP64."""
+    x = x.cpu()
+    R, K = x.shape
+    n = -(-K // block)
+    u = x.double() if scale is None else (x.double() / scale.cpu().double()).float().double()
+    u = torch.nn.functional.pad(u, (0, n * block - K)).view(R, n, block)
+    bad = ~u.isfinite().all(2)
+    u = torch.where(bad[:, :, None], torch.zeros_like(u), u)
+    top = u.abs().amax(2)
+    if block == 32:
+        e = torch.frexp(top)[1] - 3  # floor(log2(top)) - 2
+        e = torch.where(top > 0, e, torch.full_like(e, -127)).clamp(min=-127)
+        s, unit = (e + 127).to(torch.uint8), torch.ldexp(torch.ones_like(top), e)
+        s = torch.where(bad, torch.full_like(s, 255), s)
+    else:
+        s8 = (top / 6).float().clamp(max=448).to(torch.float8_e4m3fn)
+        s, unit = s8.view(torch.uint8), s8.double()
+        s = torch.where(bad, torch.full_like(s, 127), s)
+    unit = unit[:, :, None]
+    m = torch.where(unit > 0, u.abs() / torch.where(unit > 0, unit, torch.ones_like(unit)), torch.zeros_like(u))
+    d = (m.clamp(max=8)[..., None] - MAGNITUDES).abs()  # far above 6, FP64 no longer tells the distances apart
+    least = d.amin(3, keepdim=True)
+    near = d == least                           # one or two magnitudes
+    even = near & (torch.arange(8) % 2 == 0)
+    code = torch.where(even.any(3), even.int().argmax(3), near.int().argmax(3))
+    sign = torch.signbit(u) & (unit > 0) if block == 16 else torch.signbit(u)
+    return (code + 8 * sign).view(R, n * block)[:, :K].to(torch.uint8), s
+
+
+def tile_index(R, n):
+    r, b = torch.arange(R)[:, None], torch.arange(n)
+    return (r // 128 * ((n + 3) // 4) + b // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4
+
+
+def read_codes(codes, K):
+    c = codes.cpu()
+    return torch.stack((c & 15, c >> 4), 2).view(c.shape[0], -1)[:, :K]
+
+
+def values_of(codes, scales, K, block, scale=None):
+    """The matrix that codes and tiled scales stand for, in FP64."""
+    n = -(-K // block)
+    s = scales.cpu()[tile_index(codes.shape[0], n)]
+    if block == 32:
+        unit = torch.where(s == 255, torch.full(s.shape, math.nan, dtype=torch.float64), torch.ldexp(torch.ones(s.shape, dtype=torch.float64), s.int() - 127))
+    else:
+        unit = (s & 127).view(torch.float8_e4m3fn).double()
+    e = read_codes(codes, K).long()
+    v = MAGNITUDES[e & 7] * torch.where(e > 7, -1.0, 1.0).double() * unit.repeat_interleave(block, 1)[:, :K]
+    return (v if scale is None else v * scale.cpu().double()).cuda()
+
+
+def make(x, block, scale=None, aligned=True, pad=5):
+    """Quantises x; codes stand between guard bytes, scales are all 0xEE before."""
+    R, K = x.shape
+    nb = (K + 1) // 2
+    stride = (nb + 15) // 16 * 16 if aligned else nb + pad
+    off = 64 if aligned else 67
+    flat = torch.full((off + R * stride + 64,), 0xEE, dtype=torch.uint8, device="cuda")
+    codes = torch.as_strided(flat, (R, nb), (stride, 1), off)
+    scales = torch.full((dg.dg_mx4_scale_bytes(R, K, block),), 0xEE, dtype=torch.uint8, device="cuda")
+    before = dg.dg_launch_count()
+    dg.quantize_mx4(x, codes, scales, block=block, scale=scale)
+    assert dg.dg_launch_count() == before + 1 and dg.dg_sync_status() == dg.DG_OK
+    flat = flat.cpu()
+    assert (flat[:off] == 0xEE).all() and (flat[off + R * stride:] == 0xEE).all()
+    if stride > nb and R > 1:
+        assert (torch.as_strided(flat, (R - 1, stride - nb), (stride, 1), off + nb) == 0xEE).all()
+    return codes, scales
+
+
+def check_quantised(x, block, scale=None, aligned=True):
+    R, K = x.shape
+    n = -(-K // block)
+    codes, scales = make(x, block, scale, aligned)
+    want, s = quantised(x, block, scale)
+    got = scales.cpu()
+    at = tile_index(R, n)
+    assert torch.equal(got[at], s), (got[at] != s).nonzero()[:4]
+    e = read_codes(codes, K)
+    assert torch.equal(e, want), (e != want).nonzero()[:4]
+    if K % 2:
+        assert (codes.cpu()[:, -1] >> 4 == 0).all()
+    # the rest of each row's last tile is zeros; rows past the last are not written
+    full = tile_index((R + 127) // 128 * 128, (n + 3) // 4 * 4)
+    assert (got[full[:R, n:]] == 0).all()
+    assert (got[full[R:]] == 0xEE).all()
+    return codes, scales
+
+
+def normal(shape, dtype, seed, spread=3.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(shape, generator=g, device="cuda") * torch.exp(spread * torch.randn(shape, generator=g, device="cuda"))
+    return (x.clamp(-6e4, 6e4) if dtype == "f16" else x).to(DT[dtype])
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("R,K", [(1, 1), (1, 16), (2, 31), (3, 32), (31, 33), (33, 64), (127, 65), (128, 100), (129, 255),
+                                 (5, 256), (7, 257), (2, 1000), (300, 1024), (1, 4096), (9, 5003), (130, 48)])
+def test_quantise_sizes(R, K, dtype, block):
+    check_quantised(normal((R, K), dtype, R * 1000 + K), block)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_quantise_layouts(dtype, block):
+    wide = normal((150, 700), dtype, 1)
+    check_quantised(wide[:, 8:328], block)
+    check_quantised(wide[:, 3:323], block)                 # rows at odd addresses
+    check_quantised(wide[::3, ::2], block)                 # columns two apart
+    check_quantised(wide.t(), block)                       # rows are neighbours
+    check_quantised(wide.t()[5:260, 1:98], block)
+    check_quantised(wide[:, 3:323], block, aligned=False)
+    check_quantised(wide.t()[5:260, 1:98], block, aligned=False)
+    check_quantised(wide[:1].expand(40, 700), block)       # one row for all
+    check_quantised(wide[:, :1].expand(150, 64), block)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_quantise_borders(block):
+    """Values on, just above and just below every rounding border, under several scales."""
+    rows = []
+    borders = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.5])
+    for unit in (1.0, 1.125, 1.25, 1.375, 1.5, 1.625, 1.75, 1.875, 2.0 ** -7 * 1.875, 2.0 ** -9, 2.0 ** 8 * 1.75):
+        row = torch.zeros(32)
+        at = borders * unit
+        row[0] = row[16] = 6 * unit  # the largest: decides the scale
+        row[1:10] = at
+        row[10:16] = at[:6].nextafter(torch.tensor(math.inf))
+        row[17:26] = -at
+        row[26:32] = at[:6].nextafter(torch.tensor(-math.inf))
+        if block == 16:
+            row[8:10] = 0
+            row[24:26] = 0
+        rows.append(row)
+    x = torch.stack(rows).cuda()
+    check_quantised(x, block)
+    check_quantised(x.t().contiguous().t(), block)
+    check_quantised(x.bfloat16(), block)
+    # every significand of the quotient near the borders, F32 values of random last bits
+    g = torch.Generator(device="cuda").manual_seed(3)
+    v = borders[torch.randint(0, 9, (4000, 32), generator=g, device="cuda").cpu()].cuda()
+    unit = (1 + torch.randint(0, 8, (4000, 1), generator=g, device="cuda") / 8)
+    v = (v * unit).view(torch.int32) + torch.randint(-2, 3, (4000, 32), generator=g, device="cuda", dtype=torch.int32)
+    v = v.view(torch.float32)
+    v[:, 0] = v[:, 16] = 6 * unit[:, 0]
+    check_quantised(v.clamp(max=6 * unit.max().item()), block)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_quantise_extremes(block):
+    tiny, big = torch.finfo(torch.float32).smallest_normal, torch.finfo(torch.float32).max
+    x = torch.zeros(12, 64, device="cuda")
+    x[1, 3] = tiny / 4
+    x[2, 5] = -tiny
+    x[3, 7] = big
+    x[4, 9] = -big
+    x[5, 11] = math.inf
+    x[6, 13] = -math.inf
+    x[7, 15] = math.nan
+    x[8, 40] = -math.nan
+    x[9] = -0.0
+    x[10] = torch.linspace(-1e-3, 1e-3, 64)
+    x[11] = torch.logspace(-38, 38, 64)
+    codes, scales = check_quantised(x, block)
+    check_quantised(x.t().contiguous().t(), block)
+    y = torch.empty_like(x)
+    dg.dequantize_mx4(codes, scales, y, block=block)
+    assert y[5].isnan().any() and y[5, 32:].eq(0).all() and not y[11].isnan().any()
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("factor", [1.0, 0.0123, 37.5, 2.0 ** -20])
+def test_quantise_with_a_factor(block, factor):
+    scale = torch.full((1,), factor, device="cuda")
+    for x in (normal((70, 500), "bf16", 5), normal((500, 70), "f32", 6).t()):
+        codes, scales = check_quantised(x, block, scale)
+        y = torch.empty(x.shape, device="cuda")
+        dg.dequantize_mx4(codes, scales, y, block=block, scale=scale)
+        want = values_of(codes, scales, x.shape[1], block, scale)
+        assert bool(((y.double() - want).abs() <= 2.0 ** -23 * want.abs()).all())
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("R,K", [(1, 1), (3, 33), (128, 64), (200, 1000), (5, 4097)])
+def test_read_back(R, K, dtype, block):
+    codes, scales = make(normal((R, K), "f32", R + K, 1.0), block)
+    want = values_of(codes, scales, K, block)
+    eps = torch.finfo(DT[dtype]).eps / 2
+    for y in (torch.full((R, K), math.nan, device="cuda", dtype=DT[dtype]),
+              torch.full((K, R), math.nan, device="cuda", dtype=DT[dtype]).t(),
+              torch.full((R, K + 3), math.nan, device="cuda", dtype=DT[dtype])[:, 1:K + 1],
+              torch.full((R, 2 * K), math.nan, device="cuda", dtype=DT[dtype])[:, ::2]):
+        dg.dequantize_mx4(codes, scales, y, block=block)
+        assert dg.dg_sync_status() == dg.DG_OK
+        err = (y.double() - want).abs()
+        assert bool((err <= eps * want.abs() + 2.0 ** -23 * want.abs() + (2.0 ** -25 if dtype == "f16" else 0)).all())
+
+
+def test_many_rows_and_far_addresses():
+    # more rows than a grid has, codes past 2^32 bytes
+    R, K = 600000, 16
+    x = normal((R, K), "bf16", 9)
+    codes, scales = dg.empty_mx4(R, K, 16)
+    dg.quantize_mx4(x, codes, scales, block=16)
+    y = torch.empty_like(x)
+    dg.dequantize_mx4(codes, scales, y, block=16)
+    assert dg.dg_sync_status() == dg.DG_OK
+    for rows in (slice(0, 50), slice(524270, 524300), slice(R - 50, R)):
+        c, s = quantised(x[rows], 16)
+        assert torch.equal(read_codes(codes[rows], K), c)
+    del x, y, codes, scales
+    R, K = 70000, 32
+    flat = torch.empty(R * 65536, dtype=torch.uint8, device="cuda")
+    codes = torch.as_strided(flat, (R, 16), (65536, 1))
+    x = normal((R, K), "bf16", 10)
+    scales = torch.empty(dg.dg_mx4_scale_bytes(R, K, 32), dtype=torch.uint8, device="cuda")
+    dg.quantize_mx4(x, codes, scales)
+    assert dg.dg_sync_status() == dg.DG_OK
+    assert torch.equal(read_codes(codes[-40:], K), quantised(x[-40:], 32)[0])
+    b, bs = make(normal((24, K), "f32", 11), 32)
+    c = torch.empty(R, 24, device="cuda")
+    dg.gemm_mx4(dg.mx4(codes, scales, K), dg.mx4(b, bs, K), c)
+    A, B = values_of(codes, scales, K, 32), values_of(b, bs, K, 32)
+    assert bool(((c.double() - A @ B.t()).abs() <= (65 + 33) * 2.0 ** -23 * (A.abs() @ B.abs().t())).all())
+
+
+# ---------------------------------------------------------------- the product
+
+def random_operand(R, K, block, seed, spread=1.0):
+    """Random codes under random scales (all finite)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes, _ = dg.empty_mx4(R, K, block)
+    codes.copy_(torch.randint(0, 256, codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+    if K % 2:
+        codes[:, -1] &= 15
+    n = dg.dg_mx4_scale_bytes(R, K, block)
+    lo, hi = (127 - int(8 * spread), 127 + int(8 * spread)) if block == 32 else (56 - int(24 * spread), 56 + int(24 * spread))
+    scales = torch.randint(lo, hi + 1, (n,), generator=g, device="cuda", dtype=torch.uint8)
+    return codes, scales
+
+
+def check_product(M, N, K, block, out="f32", alpha=1.0, beta=0.0, bias=False, act="none", factors=False, c=None, a=None,
+                  b=None):
+    a = random_operand(M, K, block, M + K) if a is None else a
+    b = random_operand(N, K, block, N + K + 1) if b is None else b
+    fa = torch.full((1,), 0.37, device="cuda") if factors else None
+    fb = torch.full((1,), -2.5, device="cuda") if factors else None
+    if c is None:
+        c = normal((M, N), out, 3, 0.0) if beta else torch.full((M, N), math.nan, device="cuda", dtype=DT[out])
+    c0 = c.clone()
+    bs = torch.randn(N, device="cuda") if bias else None
+    before = dg.dg_launch_count()
+    dg.gemm_mx4(dg.mx4(*a, K=K, block=block, scale=fa), dg.mx4(*b, K=K, block=block, scale=fb), c, alpha=alpha, beta=beta,
+                bias=bs, act=act)
+    assert dg.dg_launch_count() == before + 1 and dg.dg_sync_status() == dg.DG_OK
+    A, B = values_of(*a, K, block, fa), values_of(*b, K, block, fb)
+    z = alpha * (A @ B.t()) if alpha and K else torch.zeros(M, N, device="cuda", dtype=torch.float64)
+    S = abs(alpha) * (A.abs() @ B.abs().t()) if alpha and K else torch.zeros_like(z)
+    bc = beta * c0.double() if beta else torch.zeros_like(z)
+    bb = bs.double().expand_as(z) if bias else torch.zeros_like(z)
+    z = z + bc + bb
+    tol = (65 + 1.02 * K) * 2.0 ** -23 * S + 2.0 ** -21 * (z.abs() + bc.abs() + bb.abs())
+    if act == "gelu_tanh":
+        tol = 1.13 * tol + (2.0 ** -20 if out == "f32" else 2.0 ** -11) * z.abs()
+    want = ACT[act](z)
+    assert torch.equal(c.isnan(), want.isnan())
+    tol = tol + torch.finfo(c.dtype).eps / 2 * (want.abs() + tol) + (2.0 ** -25 if out == "f16" else 0)
+    ok = ~want.isnan()
+    if out == "f16":
+        ok &= want.abs() < 6e4
+    err = (c.double() - want).abs()
+    assert bool((err[ok] <= tol[ok]).all()), float((err[ok] / tol[ok]).max())
+    return c
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("K", [2, 16, 30, 32, 33, 62, 64, 66, 96, 127, 128, 130, 160, 192, 224, 256, 258, 300, 512, 1000, 2049])
+def test_product_k(K, block):
+    check_product(40, 136, K, block)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M", [1, 2, 8, 15, 16, 17, 31, 32, 33, 64, 127, 128, 129, 200, 256, 257, 384, 500])
+def test_product_rows(M, block):
+    check_product(M, 128, 320, block)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("N", [1, 2, 31, 32, 33, 100, 127, 128, 129, 255, 1000])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+def test_product_columns(N, out, block):
+    check_product(20, N, 192, block, out)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,N,K", [(700, 20000, 256), (1000, 9000, 160), (257, 19000, 96), (384, 40000, 64)])
+def test_product_wide_tiles(M, N, K, block):
+    """Enough tiles for every SM: those of 256 rows, several per SM."""
+    check_product(M, N, K, block, "bf16")
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("beta", [0.0, -0.5])
+def test_product_epilogue(act, out, beta, block):
+    check_product(70, 200, 128, block, out, alpha=0.01, beta=beta, bias=True, act=act, factors=True)
+
+
+def test_product_of_nothing():
+    for block in (16, 32):
+        check_product(9, 50, 64, block, alpha=0.0, beta=2.0, bias=True)
+        check_product(9, 50, 0, block, beta=0.5)
+        check_product(9, 50, 0, block)
+
+
+def test_product_strides():
+    for block in (16, 32):
+        wide = normal((50, 400), "bf16", 1, 0.0)
+        keep = wide.clone()
+        check_product(50, 120, 128, block, "bf16", c=wide[:, 8:128], beta=1.0)
+        assert torch.equal(wide[:, 128:], keep[:, 128:]) and torch.equal(wide[:, :8], keep[:, :8])
+        check_product(50, 120, 128, block, "bf16", c=wide[:, 3:123])
+        check_product(50, 120, 128, block, "bf16", c=wide[:, ::2][:, :120])
+        check_product(50, 120, 128, block, "f32", c=normal((120, 50), "f32", 2).t())
+        a, s = random_operand(60, 256, block, 4)
+        big = torch.zeros(60, 192, dtype=torch.uint8, device="cuda")
+        big[:, 32:160] = a
+        check_product(60, 64, 256, block, a=(big[:, 32:160], s))
+
+
+def test_product_nan_blocks():
+    for block, code in ((32, 255), (16, 127)):
+        K = 256
+        a, b = random_operand(140, K, block, 1), random_operand(70, K, block, 2)
+        n = K // block
+        a[1][tile_index(140, n)[133, 3]] = code
+        b[1][tile_index(70, n)[9, n - 1]] = code
+        c = check_product(140, 70, K, block, a=a, b=b)
+        assert c[133].isnan().all() and c[:, 9].isnan().all() and int(c.isnan().sum()) == 140 + 70 - 1
+
+
+def test_product_padding_is_not_read():
+    # scales of rows past the last, and codes past K, are anything but 0
+    for block, code in ((32, 255), (16, 127)):
+        M, N, K = 37, 70, 96
+        a, b = random_operand(M, K, block, 1), random_operand(N, K, block, 2)
+        for (codes, scales), R in ((a, M), (b, N)):
+            n = K // block
+            scales[tile_index(128, (n + 3) // 4 * 4)[R:].reshape(-1)] = code
+        full = torch.full((M, 64), 0xFF, dtype=torch.uint8, device="cuda")
+        full[:, :48] = a[0]
+        check_product(M, N, K, block, a=(full[:, :48], a[1]), b=b)
+
+
+def test_quantised_layer():
+    """A linear layer in 4 bits: activations quantised, multiplied by a quantised weight, and its input's gradient
+    through the weight quantised along its other dim; captured, replayed on new inputs."""
+    M, D, H = 100, 512, 384
+    x, w, dy = normal((M, D), "bf16", 1, 0.5), normal((H, D), "bf16", 2, 0.5), normal((M, H), "bf16", 3, 0.5)
+    block = 32
+    qw, qwt = dg.empty_mx4(H, D, block), dg.empty_mx4(D, H, block)
+    dg.quantize_mx4(w, *qw, block=block)
+    dg.quantize_mx4(w.t(), *qwt, block=block)
+    qx, qd = dg.empty_mx4(M, D, block), dg.empty_mx4(M, H, block)
+    y, dx = torch.empty(M, H, device="cuda"), torch.empty(M, D, device="cuda")
+
+    def layer():
+        dg.quantize_mx4(x, *qx, block=block)
+        dg.gemm_mx4(dg.mx4(*qx, K=D, block=block), dg.mx4(*qw, K=D, block=block), y)
+        dg.quantize_mx4(dy, *qd, block=block)
+        dg.gemm_mx4(dg.mx4(*qd, K=H, block=block), dg.mx4(*qwt, K=H, block=block), dx)
+
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    x.copy_(normal((M, D), "bf16", 4, 0.5))
+    dy.copy_(normal((M, H), "bf16", 5, 0.5))
+    graph.replay()
+    assert dg.dg_sync_status() == dg.DG_OK
+    for got, a, b, K in ((y, x, w, D), (dx, dy, w.t(), H)):
+        ca, sa = quantised(a, block)
+        cb, sb = quantised(b, block)
+        A, B = ((MAGNITUDES[(c & 7).long()] * torch.where(c > 7, -1.0, 1.0).double()
+                 * torch.ldexp(torch.ones(s.shape, dtype=torch.float64), s.int() - 127).repeat_interleave(block, 1)).cuda()
+                for c, s in ((ca, sa), (cb, sb)))
+        assert bool(((got.double() - A @ B.t()).abs() <= (65 + 1.02 * K) * 2.0 ** -23 * (A.abs() @ B.abs().t())).all())
+
+
+def test_streams():
+    block = 16
+    ops = [(random_operand(300, 512, block, i), random_operand(400, 512, block, 10 + i)) for i in range(4)]
+    want = [check_product(300, 400, 512, block, "bf16", a=a, b=b) for a, b in ops]
+    streams = [torch.cuda.Stream() for _ in ops]
+    got = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (a, b), c in zip(streams, ops, got):
+            dg.gemm_mx4(dg.mx4(*a, K=512, block=block), dg.mx4(*b, K=512, block=block), c, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and dg.dg_sync_status() == dg.DG_OK
+
+
+def test_bounded_waits():
+    a, b = random_operand(50, 512, 32, 1), random_operand(60, 512, 32, 2)
+    want = check_product(50, 60, 512, 32, a=a, b=b)
+    c = torch.empty_like(want)
+    dg.dg_set_option(dg.DG_OPT_WAIT_TIMEOUT_MS, 20)
+    dg.dg_set_option(dg.DG_OPT_TEST_STALL, 1)
+    try:
+        dg.gemm_mx4(dg.mx4(*a), dg.mx4(*b), c)
+        assert dg.dg_sync_status() == dg.DG_ERR_TIMEOUT
+    finally:
+        dg.dg_set_option(dg.DG_OPT_TEST_STALL, 0)
+        dg.dg_set_option(dg.DG_OPT_WAIT_TIMEOUT_MS, 2000)
+    dg.gemm_mx4(dg.mx4(*a), dg.mx4(*b), c)
+    assert dg.dg_sync_status() == dg.DG_OK and torch.equal(c, want)
