@@ -20,10 +20,10 @@ OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdg.so")
 SOURCES = ["api.cu", "view.cpp", "simt.cu", "gemv.cu", "umma.cu", "umma_gather.cu", "umma_gather_split.cu", "umma_pair.cu",
            "umma_pair_ce.cu", "gemv_w4.cu", "linear_ce.cu", "grouped.cu",
-           "mx4.cu"]
+           "mx4.cu", "mx4_quant.cu"]
 HEADERS = ["dg_internal.h", "sm100.cuh", "common.cuh", "umma_common.cuh", "umma_kernel.cuh", "umma_pair_kernel.cuh",
            "ce.cuh", "turned_out.cuh", "grouped_kernel.cuh",
-           "mx4_kernel.cuh"]
+           "mx4_kernel.cuh", "mx4_quant.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,0 +1,514 @@
+// Kernels of dg_quantize_mx4 and dg_dequantize_mx4.
+//
+// E2M1 has the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4 and 6.  A block of 32 values
+// along k has an E8M0 scale, 2^floor(log2(largest) - 2), which brings the
+// largest to [4, 8) (above 6 it is cut); a block of 16 an E4M3 scale, a sixth
+// of the largest.  Everything is rounded to nearest, ties to even, and every
+// division by a block's scale decides as the exact quotient would.
+#include <algorithm>
+
+#include "mx4_quant.h"
+#include "umma_common.cuh"
+
+namespace dg {
+namespace {
+
+// ------------------------------------------------------------ scales and codes
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The byte of a block's scale from the largest magnitude's bits (NaN and
+// infinities compare above every finite one), and the factor pair (s, r) with
+// which mx4_unit makes x / s: for E8M0 the exact 1 / s, for E4M3 s and its
+// rounded reciprocal.  A block with a NaN or an infinity has the scale NaN and
+// codes of zero.
+template <int BLOCK>
+__device__ __forceinline__ uint32_t mx4_scale(uint32_t top, float &s, float &r) {
+    if (BLOCK == 32) {
+        const int e = max((int)(top >> 23) - 2, 0);  // a subnormal has exponent 0
+        s = 0.f;
+        r = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e): normal for every e up to 252
+        if (top >= kInfBits) {
+            r = 0.f;
+            return 0xff;
+        }
+        return (uint32_t)e;
+    }
+    if (top >= kInfBits) {
+        s = r = 0.f;
+        return 0x7f;
+    }
+    const float want = __fdiv_rn(__uint_as_float(top), 6.f);
+    const uint32_t code = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
+    s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+    r = s > 0.f ? __frcp_rn(s) : 0.f;
+    return code;
+}
+
+// x / s.  For E4M3, x times the rounded reciprocal and one correction by the
+// remainder, which the fused multiply-add gives exactly: the result differs
+// from the exact quotient by little more than half an ulp, is exact where the
+// quotient is an FP32 number, and so lies on E2M1's rounding borders exactly
+// where the quotient does (s has four significant bits: no other quotient comes
+// within half an ulp of a border).
+template <int BLOCK>
+__device__ __forceinline__ float mx4_unit(float x, float s, float r) {
+    if (BLOCK == 32) return r == 0.f ? 0.f : x * r;
+    if (r == 0.f) return 0.f;
+    const float y = x * r;
+    // a zero keeps its sign
+    return __uint_as_float(__float_as_uint(fmaf(fmaf(-y, s, x), r, y)) | (__float_as_uint(x) & 0x80000000u));
+}
+
+// Eight values to eight codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t d;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(d)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return d;
+}
+
+// And back.
+__device__ __forceinline__ void e2m1x8_values(uint32_t e, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(e));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = t.x;
+        v[2 * i + 1] = t.y;
+    }
+}
+
+// The value of a scale's byte.
+template <int BLOCK>
+__device__ __forceinline__ float mx4_scale_value(uint32_t code) {
+    if (BLOCK == 32)
+        return code == 0xff ? __uint_as_float(0x7fffffffu) : __uint_as_float(code ? code << 23 : 1u << 22);
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(code & 0x7f), __NV_E4M3)));
+}
+
+// The division by the matrix's factor: u = x / t, rounded once.
+struct Factor {
+    float t, r;
+    bool divide, plain;  // plain: t is of a size for which quotient() holds
+    __device__ explicit Factor(const float *scale) {
+        divide = scale != nullptr;
+        t = divide ? *scale : 1.f;
+        const float a = fabsf(t);
+        plain = a >= 0x1p-60f && a <= 0x1p60f;
+        r = plain ? __frcp_rn(t) : 0.f;
+    }
+    // x / t from the rounded reciprocal and the exact remainder of a first
+    // quotient: correctly rounded (Markstein 1990, theorem 6.2 of "Computation
+    // of elementary functions on the IBM RISC System/6000 processor") while
+    // the remainder does not underflow.
+    __device__ __forceinline__ float quotient(float x) const {
+        const float y = x * r;
+        return fmaf(fmaf(-y, t, x), r, y);
+    }
+};
+
+// Below this magnitude of a block's largest value its quotients are divided
+// one by one; above it a value whose remainder underflows is so small a part
+// of the largest that its code is 0 in any case.
+constexpr float kLeastPlain = 0x1p-90f;
+
+// 32 neighbouring k of a row as they lie in memory (zeros past K).
+template <int DT>
+struct Lot {
+    static constexpr int ES = DT == DG_F32 ? 4 : 2;
+    static constexpr int W = 8 * ES;  // words
+    uint32_t w[W];
+    __device__ __forceinline__ float operator[](int i) const {
+        if (DT == DG_F32) return __uint_as_float(w[i]);
+        if (DT == DG_BF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu)));
+    }
+    // the largest magnitude of block b, as FP32; NaN if there is one (16-bit magnitudes order as integers)
+    template <int BLOCK>
+    __device__ __forceinline__ uint32_t top(int b) const {
+        constexpr int N = W * BLOCK / 32;
+        uint32_t m = 0;
+        if constexpr (DT == DG_F32) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) m = max(m, w[b * N + i] & 0x7fffffffu);
+            return m;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) m = __vmaxu2(m, w[b * N + i] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+            if (DT == DG_BF16) return m << 16;
+            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) & 0x7fffffffu;
+        }
+    }
+};
+
+// The codes of a lot's 32 values (the first n of them, n >= 32 for all) and, in
+// the low bytes of the result, its 32 / BLOCK scales.
+template <int DT, int BLOCK>
+__device__ __forceinline__ uint32_t encode(const Lot<DT> &x, int n, const Factor &f, uint32_t (&e)[4]) {
+    uint32_t scales = 0;
+#pragma unroll
+    for (int b = 0; b < 32 / BLOCK; ++b) {
+        const uint32_t top = x.template top<BLOCK>(b);
+        float s, r;
+        // the largest |x / t| is that of the largest |x|: rounding keeps the order
+        const uint32_t code = mx4_scale<BLOCK>(f.divide ? abs_bits(__fdiv_rn(__uint_as_float(top), f.t)) : top, s, r);
+        if (b * BLOCK < n) scales |= code << (8 * b);
+        const bool plain = f.plain && __uint_as_float(top) >= kLeastPlain;
+#pragma unroll
+        for (int j = 0; j < BLOCK / 8; ++j) {
+            float u[8];
+            const int at = b * BLOCK + 8 * j;
+            if (!f.divide) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = mx4_unit<BLOCK>(x[at + i], s, r);
+            } else if (plain) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    // a zero has the quotient's sign (a block with a NaN has r = 0 and codes of 0)
+                    const float q = f.quotient(x[at + i]);
+                    u[i] = mx4_unit<BLOCK>(x[at + i] == 0.f ? x[at + i] * f.r : q, s, r);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = mx4_unit<BLOCK>(__fdiv_rn(x[at + i], f.t), s, r);
+            }
+            e[at / 8] = e2m1x8(u);
+        }
+    }
+    if (n < 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i + 8 > n) e[i] &= 8 * i >= n ? 0u : (1u << (4 * (n - 8 * i))) - 1u;
+    }
+    return scales;
+}
+
+// The 16 bytes of 32 codes, of which the first n exist.
+__device__ __forceinline__ void store_codes(uint8_t *out, int align, const uint32_t (&e)[4], int n) {
+    if (align == 16 && n >= 32) {
+        *reinterpret_cast<uint4 *>(out) = make_uint4(e[0], e[1], e[2], e[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (align >= 4 && 8 * i + 8 <= n) {
+            *reinterpret_cast<uint32_t *>(out + 4 * i) = e[i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (8 * i + 2 * j < n) out[4 * i + j] = (uint8_t)(e[i] >> (8 * j));
+        }
+    }
+}
+
+// Four bytes of codes, of which the first n codes exist.
+__device__ __forceinline__ uint32_t load_codes8(const uint8_t *in, int align, int n) {
+    if (align >= 4 && n >= 8) return *reinterpret_cast<const uint32_t *>(in);
+    uint32_t e = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (2 * i < n) e |= (uint32_t)in[i] << (8 * i);
+    return e;
+}
+
+// ------------------------------------------------------------- k contiguous
+
+constexpr int kQuantWarps = 8;
+constexpr int kSpan = 1024;  // k per warp
+
+// Words a warp has in shared memory for `kSpan` elements that start anywhere,
+// one word of padding per lane's 32 elements.
+template <int DT>
+constexpr int kStageWords = (DT == DG_F32 ? kSpan : kSpan / 2) + 33 + 4;
+
+// A warp takes 1024 k of a row, a lane 32 of them: one block of 32 or two of
+// 16, so that no maximum crosses lanes.  VEC: a lane loads its own 64 (or 128)
+// bytes, 16 at a time; the warp's four loads share their lines in L1.
+// Otherwise (rows at any address) the warp copies the row's words, whole
+// 128-byte lines per load, through shared memory.
+template <int DT, int BLOCK, bool VEC>
+__global__ void __launch_bounds__(32 * kQuantWarps) quantize_rows_kernel(const QuantParams p) {
+    pdl_wait_then_release();
+    constexpr int ES = Lot<DT>::ES, W = Lot<DT>::W;
+    __shared__ uint32_t stage[VEC ? 1 : kQuantWarps * kStageWords<DT>];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Factor f(p.q.scale);
+    const int K = (int)p.q.K, k0 = (int)blockIdx.x * kSpan, k = k0 + lane * 32, n = K - k;
+    const uint32_t tile = blockIdx.x * (uint32_t)(kSpan / BLOCK / 4) + (uint32_t)lane / (BLOCK / 8);  // of scales, along k
+    for (int64_t row = (int64_t)blockIdx.y * kQuantWarps + warp; row < p.q.rows; row += (int64_t)gridDim.y * kQuantWarps) {
+        const char *x = p.x.ptr + axis_offset(p.x.row, row) + (int64_t)k0 * ES;
+        Lot<DT> v;
+        if (VEC) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(x + lane * 32 * ES);
+            if (n >= 32) {
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) *reinterpret_cast<uint4 *>(v.w + 4 * i) = from[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const char *at = reinterpret_cast<const char *>(from) + 4 * i;
+                    if (DT == DG_F32) {
+                        v.w[i] = i < n ? *reinterpret_cast<const uint32_t *>(at) : 0u;
+                    } else {
+                        const uint32_t lo = 2 * i < n ? *reinterpret_cast<const uint16_t *>(at) : 0u;
+                        const uint32_t hi = 2 * i + 1 < n ? *reinterpret_cast<const uint16_t *>(at + 2) : 0u;
+                        v.w[i] = lo | hi << 16;
+                    }
+                }
+            }
+        } else {
+            uint32_t *const mine = stage + warp * kStageWords<DT>;
+            const uint32_t odd = DT == DG_F32 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(x) >> 1) & 1u;
+            const char *const words = x - 2 * odd;
+            const int elems = min(kSpan, K - k0), per = 4 / ES;  // elements per word
+            const int count = (elems + (int)odd + per - 1) / per;
+            __syncwarp();
+#pragma unroll 4
+            for (int j = lane; j < count; j += 32) {
+                uint32_t b;
+                const char *at = words + (int64_t)j * 4;
+                if (DT == DG_F32 || (!(odd && j == 0) && per * j + 1 - (int)odd < elems)) {
+                    b = *reinterpret_cast<const uint32_t *>(at);
+                } else {  // a word that is half the row's
+                    const bool low = !(odd && j == 0);
+                    b = (uint32_t)*reinterpret_cast<const uint16_t *>(at + (low ? 0 : 2)) << (low ? 0 : 16);
+                }
+                mine[j + j / W] = b;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const uint32_t b = mine[lane * (W + 1) + i];
+                v.w[i] = DT == DG_F32 ? b
+                                      : __funnelshift_r(b, mine[i + 1 < W ? lane * (W + 1) + i + 1 : (lane + 1) * (W + 1)],
+                                                        16u * odd);
+            }
+            if (n < 32) {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    v.w[i] &= per * i >= n ? 0u : (per == 2 && 2 * i + 1 >= n) ? 0xffffu : 0xffffffffu;
+            }
+        }
+        uint32_t e[4];
+        uint32_t scales = encode<DT, BLOCK>(v, max(n, 0), f, e);
+        // four blocks' scales are one word
+        if (BLOCK == 32) {
+            scales <<= 8 * (lane & 3);
+            scales |= __shfl_xor_sync(0xffffffffu, scales, 1);
+            scales |= __shfl_xor_sync(0xffffffffu, scales, 2);
+        } else {
+            scales <<= 16 * (lane & 1);
+            scales |= __shfl_xor_sync(0xffffffffu, scales, 1);
+        }
+        if (n <= 0) continue;
+        if ((lane & (BLOCK / 8 - 1)) == 0)
+            *reinterpret_cast<uint32_t *>(p.q.scales + (row / 128 * p.q.k_tiles + tile) * 512 + row % 32 * 16 +
+                                          row % 128 / 32 * 4) = scales;
+        store_codes(p.q.codes + row * p.q.code_stride + k / 2, p.q.align, e, n);
+    }
+}
+
+// A warp reads 1024 k of a row back, a lane eight at a time: its stores are
+// whole 512-byte runs.  Rows at any address go through shared memory, as above.
+template <int DT, int BLOCK, bool VEC>
+__global__ void __launch_bounds__(32 * kQuantWarps) dequantize_rows_kernel(const QuantParams p) {
+    pdl_wait_then_release();
+    constexpr int ES = Lot<DT>::ES, W = 2 * ES;  // words of eight values
+    __shared__ uint32_t stage[VEC ? 1 : kQuantWarps * kStageWords<DT>];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float factor = p.q.scale != nullptr ? *p.q.scale : 1.f;
+    const int K = (int)p.q.K, k0 = (int)blockIdx.x * kSpan, n0 = K - k0 - lane * 8;
+    const int block = lane * 8 / BLOCK;  // of the first chunk
+    for (int64_t row = (int64_t)blockIdx.y * kQuantWarps + warp; row < p.q.rows; row += (int64_t)gridDim.y * kQuantWarps) {
+        char *const y = const_cast<char *>(p.x.ptr) + axis_offset(p.x.row, row) + (int64_t)k0 * ES;
+        const uint8_t *codes = p.q.codes + row * p.q.code_stride + k0 / 2 + lane * 4;
+        const uint8_t *scales = p.q.scales + (row / 128 * p.q.k_tiles + blockIdx.x * (uint32_t)(kSpan / BLOCK / 4)) * 512 +
+                                row % 32 * 16 + row % 128 / 32 * 4 + block / 4 * 512 + block % 4;
+        uint32_t *const mine = stage + warp * kStageWords<DT>;
+        uint32_t e[4], s[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int n = n0 - c * 256;
+            e[c] = n > 0 ? load_codes8(codes + c * 128, p.q.align, n) : 0u;
+            s[c] = n > 0 ? scales[c * (64 / BLOCK) * 512] : 0u;
+        }
+        if (!VEC) __syncwarp();  // the last row's words have been stored
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int n = n0 - c * 256;
+            if (n <= 0) continue;
+            const float unit = mx4_scale_value<BLOCK>(s[c]) * factor;
+            float v[8];
+            e2m1x8_values(e[c], v);
+            uint32_t w[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                w[i] = DT == DG_F32 ? __float_as_uint(v[i] * unit)
+                                    : pack2<DT == DG_BF16>(v[2 * i & 7] * unit, v[(2 * i + 1) & 7] * unit);
+            char *const at = y + (c * 256 + lane * 8) * ES;
+            if (VEC && n >= 8) {
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i)
+                    *reinterpret_cast<uint4 *>(at + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            } else if (VEC) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n) {
+                        if (DT == DG_F32) *reinterpret_cast<uint32_t *>(at + 4 * i) = w[i & (W - 1)];
+                        else *reinterpret_cast<uint16_t *>(at + 2 * i) = (uint16_t)(w[i / 2 & (W - 1)] >> (i & 1 ? 16 : 0));
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) mine[(c * 32 + lane) * W + i] = w[i];
+            }
+        }
+        if (VEC) continue;
+        __syncwarp();
+        const uint32_t odd = DT == DG_F32 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(y) >> 1) & 1u;
+        char *const words = y - 2 * odd;
+        const int elems = min(kSpan, K - k0), per = 4 / ES, count = (elems + (int)odd + per - 1) / per;
+#pragma unroll 4
+        for (int j = lane; j < count; j += 32) {
+            char *at = words + (int64_t)j * 4;
+            const uint32_t here = mine[j], b = odd ? __funnelshift_r(j > 0 ? mine[j - 1] : 0u, here, 16) : here;
+            if (DT == DG_F32 || (!(odd && j == 0) && per * j + 1 - (int)odd < elems)) {
+                *reinterpret_cast<uint32_t *>(at) = b;
+            } else {
+                const bool low = !(odd && j == 0);
+                *reinterpret_cast<uint16_t *>(at + (low ? 0 : 2)) = (uint16_t)(b >> (low ? 0 : 16));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ any view
+
+constexpr int kTurnK = 64;  // a thread takes 64 k of a row
+
+// Any view, a thread per row and 64 k: made for rows that are neighbours in
+// memory (a weight along its other dim), whose loads are then whole sectors.
+// ONE: k is one dim.
+template <int DT, int BLOCK, bool ONE>
+__global__ void __launch_bounds__(128) quantize_any_kernel(const QuantParams p) {
+    pdl_wait_then_release();
+    const int64_t row = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (row >= p.q.rows) return;
+    const int K = (int)p.q.K;
+    const Factor f(p.q.scale);
+    const char *x = p.x.ptr + axis_offset(p.x.row, row);
+    uint8_t *scales_row = p.q.scales + row / 128 * p.q.k_tiles * 512 + row % 32 * 16 + row % 128 / 32 * 4;
+    for (int k0 = (int)blockIdx.y * kTurnK; k0 < K; k0 += (int)gridDim.y * kTurnK) {
+        uint32_t scales = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = k0 + 32 * h, n = K - k;
+            if (n <= 0) break;
+            Lot<DT> v;
+            auto put = [&](int i, const char *at) {
+                uint32_t b = 0;
+                if (i < n) {
+                    if (DT == DG_F32) b = *reinterpret_cast<const uint32_t *>(at);
+                    else b = *reinterpret_cast<const uint16_t *>(at);
+                }
+                if (DT == DG_F32) v.w[i & (Lot<DT>::W - 1)] = b;
+                else if (i & 1) v.w[i / 2] |= b << 16;
+                else v.w[i / 2] = b;
+            };
+            if (ONE) {
+                const char *at = x + k * p.col;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) put(i, at + i * p.col);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 32; ++i) put(i, x + axis_offset(p.x.col, min(k + i, K - 1)));
+            }
+            uint32_t e[4];
+            scales |= encode<DT, BLOCK>(v, n, f, e) << (h * (256 / BLOCK));
+            store_codes(p.q.codes + row * p.q.code_stride + k / 2, p.q.align, e, n);
+        }
+        // blocks past the last one of their tile get a zero
+        const int block = k0 / BLOCK;
+        uint8_t *out = scales_row + (int64_t)(block / 4) * 512 + block % 4;
+        if (BLOCK == 16) {
+            *reinterpret_cast<uint32_t *>(out) = scales;
+        } else {
+            *reinterpret_cast<uint16_t *>(out) = (uint16_t)scales;
+            if (k0 + kTurnK >= K && block % 4 == 0) *reinterpret_cast<uint16_t *>(out + 2) = 0;
+        }
+    }
+}
+
+template <int DT, int BLOCK, bool ONE>
+__global__ void __launch_bounds__(128) dequantize_any_kernel(const QuantParams p) {
+    pdl_wait_then_release();
+    const int64_t row = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (row >= p.q.rows) return;
+    const int K = (int)p.q.K;
+    const float factor = p.q.scale != nullptr ? *p.q.scale : 1.f;
+    char *y = const_cast<char *>(p.x.ptr) + axis_offset(p.x.row, row);
+    const uint8_t *codes = p.q.codes + row * p.q.code_stride;
+    const uint8_t *scales_row = p.q.scales + row / 128 * p.q.k_tiles * 512 + row % 32 * 16 + row % 128 / 32 * 4;
+    for (int k0 = (int)blockIdx.y * kTurnK; k0 < K; k0 += (int)gridDim.y * kTurnK) {
+        uint32_t e[kTurnK / 8];
+#pragma unroll
+        for (int j = 0; j < kTurnK / 8; ++j)
+            e[j] = k0 + 8 * j < K ? load_codes8(codes + (k0 + 8 * j) / 2, p.q.align, K - k0 - 8 * j) : 0u;
+#pragma unroll
+        for (int j = 0; j < kTurnK / 8; ++j) {
+            const int k = k0 + 8 * j, block = k / BLOCK;
+            if (k >= K) break;
+            const float unit = mx4_scale_value<BLOCK>(scales_row[(int64_t)(block / 4) * 512 + block % 4]) * factor;
+            float v[8];
+            e2m1x8_values(e[j], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (k + i < K) st_out<DT>(y + (ONE ? (k + i) * p.col : axis_offset(p.x.col, k + i)), v[i] * unit);
+        }
+    }
+}
+
+template <int DT, int BLOCK>
+cudaError_t run(const QuantParams &p, bool back, cudaStream_t s) {
+    // neighbours in a row go to neighbouring lanes; otherwise neighbouring rows do
+    if (p.x.col.n == 0 || (p.x.col.n == 1 && p.col == Lot<DT>::ES)) {
+        const dim3 grid((unsigned)((p.q.K + kSpan - 1) / kSpan),
+                        (unsigned)std::min<int64_t>((p.q.rows + kQuantWarps - 1) / kQuantWarps, 65535));
+        auto kern = back ? (p.vec ? dequantize_rows_kernel<DT, BLOCK, true> : dequantize_rows_kernel<DT, BLOCK, false>)
+                         : (p.vec ? quantize_rows_kernel<DT, BLOCK, true> : quantize_rows_kernel<DT, BLOCK, false>);
+        return launch_ex(kern, grid, dim3(32 * kQuantWarps), 0, s, dim3(1, 1, 1), p.pdl, p);
+    }
+    const dim3 grid((unsigned)((p.q.rows + 127) / 128),
+                    (unsigned)std::min<int64_t>((p.q.K + kTurnK - 1) / kTurnK, 65535));
+    const bool one = p.x.col.n == 1;
+    auto kern = back ? (one ? dequantize_any_kernel<DT, BLOCK, true> : dequantize_any_kernel<DT, BLOCK, false>)
+                     : (one ? quantize_any_kernel<DT, BLOCK, true> : quantize_any_kernel<DT, BLOCK, false>);
+    return launch_ex(kern, grid, dim3(128), 0, s, dim3(1, 1, 1), p.pdl, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quant(const QuantParams &p, int block, bool back, cudaStream_t s) {
+    if (p.x.dtype == DG_F32) return block == 32 ? run<DG_F32, 32>(p, back, s) : run<DG_F32, 16>(p, back, s);
+    if (p.x.dtype == DG_F16) return block == 32 ? run<DG_F16, 32>(p, back, s) : run<DG_F16, 16>(p, back, s);
+    return block == 32 ? run<DG_BF16, 32>(p, back, s) : run<DG_BF16, 16>(p, back, s);
+}
+
+}  // namespace dg
