@@ -23,7 +23,7 @@ SOURCES = ["api.cu", "view.cpp", "simt.cu", "gemv.cu", "umma.cu", "umma_gather.c
            "mx4.cu", "mx4_quant.cu"]
 HEADERS = ["dg_internal.h", "sm100.cuh", "common.cuh", "umma_common.cuh", "umma_kernel.cuh", "umma_pair_kernel.cuh",
            "ce.cuh", "turned_out.cuh", "grouped_kernel.cuh",
-           "mx4_kernel.cuh", "mx4_quant.h"]
+           "mx4_kernel.cuh", "mx4_quant.h", "uniform.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

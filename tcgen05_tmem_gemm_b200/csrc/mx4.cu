@@ -70,8 +70,7 @@ dg_status quant_call(const dg_view *x, const dg_mx4 *q, bool back, cudaStream_t 
 }
 
 template <int BLOCK>
-cudaError_t launch_mx4(Mx4Params p, const CUtensorMap &mp, const CUtensorMap &mq, const CUtensorMap &mq16, int num_sms,
-                       cudaStream_t s) {
+cudaError_t launch_mx4(Mx4Params p, const CUtensorMap (&m)[4], int num_sms, cudaStream_t s) {
     static SmemLimit limit;
     const int q_rows = std::min(p.tile_w, (p.M + 15) / 16 * 16);
     const int most = 256 / mx4_scale_cols(BLOCK, p.tile_w);  // stages that TMEM has scale columns for
@@ -82,8 +81,8 @@ cudaError_t launch_mx4(Mx4Params p, const CUtensorMap &mp, const CUtensorMap &mq
     const cudaError_t e = limit.ensure(mx4_kernel<BLOCK>, smem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>(num_sms, (int64_t)p.tiles_m * p.tiles_n);
-    return launch_ex(mx4_kernel<BLOCK>, dim3(grid), dim3(kMx4Threads), smem, s, dim3(1, 1, 1), p.pdl, mp, mq, mq16, p,
-                     q_rows);
+    return launch_ex(mx4_kernel<BLOCK>, dim3(grid), dim3(kMx4Threads), smem, s, dim3(1, 1, 1), p.pdl, m[0], m[1], m[2], m[3],
+                     p, q_rows);
 }
 
 bool codes_map(CUtensorMap *m, const dg_mx4 *q, int box_rows) {
@@ -91,6 +90,14 @@ bool codes_map(CUtensorMap *m, const dg_mx4 *q, int box_rows) {
     const int64_t dim[2] = {bytes, q->rows}, stride[1] = {q->rows > 1 ? q->code_stride : (bytes + 15) / 16 * 16};
     const int box[2] = {128, box_rows};
     return encode_map(m, DG_E4M3, 2, q->codes, dim, stride, box, true);
+}
+
+// Tiles of scales as words: 128 of a tile, tiles along k, tiles along the rows.
+bool scales_map(CUtensorMap *m, const dg_mx4 *q, int box_rows) {
+    const int64_t tiles = scale_tiles(q->K, q->block);
+    const int64_t dim[3] = {128, tiles, (q->rows + 127) / 128}, stride[2] = {512, tiles * 512};
+    const int box[3] = {128, 64 / q->block, box_rows};
+    return encode_map(m, DG_F32, 3, q->scales, dim, stride, box, false);
 }
 
 }  // namespace
@@ -170,12 +177,12 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     p.timeout_ns = wait_timeout_ns();
     p.stall_loader = test_stall();
     p.pdl = early_launch_mode() != 0;
-    CUtensorMap mp{}, mq{}, mq16{};
-    if (product && (!codes_map(&mp, B, 128) || !codes_map(&mq, A, 64) || !codes_map(&mq16, A, 16)))
+    CUtensorMap m[4] = {};
+    if (product && (!codes_map(&m[0], B, 128) || !codes_map(&m[1], A, std::min(p.tile_w, (p.M + 15) / 16 * 16)) ||
+                    !scales_map(&m[2], B, 1) || !scales_map(&m[3], A, p.tile_w / 128)))
         return DG_ERR_UNSUPPORTED;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = A->block == 32 ? launch_mx4<32>(p, mp, mq, mq16, num_sms, s)
-                                         : launch_mx4<16>(p, mp, mq, mq16, num_sms, s);
+    const cudaError_t e = A->block == 32 ? launch_mx4<32>(p, m, num_sms, s) : launch_mx4<16>(p, m, num_sms, s);
     if (e != cudaSuccess) return DG_ERR_CUDA;
     count_launch();
     return DG_OK;

@@ -11,7 +11,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "sm100.cuh"
+#include "uniform.cuh"
 #include "turned_out.cuh"
 
 namespace dg {
@@ -33,6 +33,16 @@ struct Mx4Params {
 };
 
 namespace {
+
+// 3-D tiled load (see tma_load_2d).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 
 constexpr int kMx4Threads = 192;
 constexpr int kMx4K = 256;  // k per stage
@@ -66,12 +76,14 @@ __host__ __device__ inline int mx4_scale_cols(int block, int tile_w) {
 template <int BLOCK>
 __global__ void __launch_bounds__(kMx4Threads, 1)
     mx4_kernel(const __grid_constant__ CUtensorMap tmap_p, const __grid_constant__ CUtensorMap tmap_q,
-               const __grid_constant__ CUtensorMap tmap_q16, const Mx4Params p, const int q_rows) {
+               const __grid_constant__ CUtensorMap tmap_sp, const __grid_constant__ CUtensorMap tmap_sq,
+               const Mx4Params p, const int q_rows) {
     constexpr int T = kMx4K / (4 * BLOCK);  // scale tiles per stage
     if (threadIdx.x == 64 && p.K > 0) {
         tma_prefetch_desc(&tmap_p);
         tma_prefetch_desc(&tmap_q);
-        tma_prefetch_desc(&tmap_q16);
+        tma_prefetch_desc(&tmap_sp);
+        tma_prefetch_desc(&tmap_sq);
     }
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -85,7 +97,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L.aux_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.aux_off + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const WaitCtl wc{abort_flag, p.err_word, p.timeout_ns};
     const int units = p.tiles_m * p.tiles_n;
     const int buffers = p.tile_w <= 128 ? 2 : 1;  // accumulators
@@ -112,7 +124,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = uniform(*tmem_slot);
     pdl_wait();  // what comes before touches this CTA's own memory only
 
     // the tile of unit u: m inner, so that CTAs that run at the same time share B's rows
@@ -125,83 +137,77 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------- producer
-        if (lane == 0) {
-            const int stages = p.stages;
-            const bool stall = p.stall_loader == 1;
-            int it = 0, s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && !*abort_flag && u < units; u += gridDim.x) {
-                int m0, n0;
-                const int rows = tile_rows(u, m0, n0), w = (rows + 15) & ~15, qt = (rows + 127) / 128;
-                for (int k = 0; k < p.K; k += kMx4K, ++it) {
-                    if (!mbar_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!stall) {
-                        const uint32_t full = bar_full + 8 * s, ps = sbase + s * L.stage_bytes, qs = ps + L.p_bytes;
-                        const uint32_t sp = qs + L.q_bytes, sq = sp + L.sp_bytes;
-                        const int t0 = k / (4 * BLOCK);
-                        const uint32_t some = (uint32_t)min(T, p.k_tiles - t0) * kScaleTile;
-                        mbar_arrive_expect_tx(full, L.p_bytes + (uint32_t)w * 128u + (uint32_t)(1 + qt) * some);
-                        tma_load_2d(ps, &tmap_p, full, k / 2, n0);
-                        int c = 0;
-                        for (; c + 64 <= w; c += 64) tma_load_2d(qs + c * 128, &tmap_q, full, k / 2, m0 + c);
-                        for (; c < w; c += 16) tma_load_2d(qs + c * 128, &tmap_q16, full, k / 2, m0 + c);
-                        bulk_load(sp, p.sb + ((int64_t)(n0 / 128) * p.k_tiles + t0) * kScaleTile, some, full);
-                        for (int i = 0; i < qt; ++i)
-                            bulk_load(sq + (uint32_t)(i * T) * kScaleTile,
-                                      p.sa + ((int64_t)(m0 / 128 + i) * p.k_tiles + t0) * kScaleTile, some, full);
-                    }
-                    if (++s == stages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+        const int stages = p.stages;
+        const bool stall = p.stall_loader == 1;
+        int it = 0, s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            int m0, n0;
+            tile_rows(u, m0, n0);
+            for (int k = 0; k < p.K; k += kMx4K, ++it) {
+                if (!warp_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
+                    ok = false;
+                    break;
+                }
+                if (!stall && elect_one()) {
+                    const uint32_t full = bar_full + 8 * s, ps = sbase + s * L.stage_bytes, qs = ps + L.p_bytes;
+                    const uint32_t sp = qs + L.q_bytes, sq = sp + L.sp_bytes;
+                    const int t0 = k / (4 * BLOCK);
+                    mbar_arrive_expect_tx(full, L.p_bytes + L.q_bytes + L.sp_bytes + L.sq_bytes);
+                    tma_load_2d(ps, &tmap_p, full, k / 2, n0);
+                    tma_load_2d(qs, &tmap_q, full, k / 2, m0);
+                    tma_load_3d(sp, &tmap_sp, full, 0, t0, n0 / 128);
+                    tma_load_3d(sq, &tmap_sq, full, 0, t0, m0 / 128);
+                }
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            if (!stall)
-                for (int d = 1; d <= stages && it - d >= 0; ++d) {
-                    const int j = it - d;
-                    mbar_wait_drain(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u, p.timeout_ns);
-                }
         }
+        if (!stall)
+            for (int d = 1; d <= stages && it - d >= 0; ++d) {
+                const int j = it - d;
+                mbar_wait_drain(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u, p.timeout_ns);
+            }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const int stages = p.stages;
-            const uint32_t scale_cols = (uint32_t)mx4_scale_cols(BLOCK, p.tile_w);
-            const uint64_t da0 = make_sw128_desc(sbase, 16u, 1024);
-            const uint64_t db0 = make_sw128_desc(sbase + L.p_bytes, 16u, 1024);
-            const uint64_t ds0 = make_scales_desc(sbase + L.p_bytes + L.q_bytes);
-            int local = 0, s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && p.K > 0 && u < units; u += gridDim.x, ++local) {
-                int m0, n0;
-                const int rows = tile_rows(u, m0, n0), w = (rows + 15) & ~15, qt = (rows + 127) / 128;
-                const uint32_t idesc = p.idesc | (uint32_t)(w >> 3) << 17;
-                const int b = buffers == 2 ? local & 1 : 0, turn = buffers == 2 ? local >> 1 : local;
-                if (!mbar_wait(bar_tempty + 8 * b, ((uint32_t)turn & 1u) ^ 1u, wc)) break;
+        const int stages = p.stages;
+        const uint32_t scale_cols = (uint32_t)mx4_scale_cols(BLOCK, p.tile_w);
+        const uint64_t da0 = make_sw128_desc(sbase, 16u, 1024);
+        const uint64_t db0 = make_sw128_desc(sbase + L.p_bytes, 16u, 1024);
+        const uint64_t ds0 = make_scales_desc(sbase + L.p_bytes + L.q_bytes);
+        int local = 0, s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && p.K > 0 && u < units; u += gridDim.x, ++local) {
+            int m0, n0;
+            const int rows = tile_rows(u, m0, n0), w = (rows + 15) & ~15;
+            const bool two = rows > 128;  // tiles of Q's scales
+            const uint32_t idesc = p.idesc | (uint32_t)(w >> 3) << 17;
+            const int b = buffers == 2 ? local & 1 : 0, turn = buffers == 2 ? local >> 1 : local;
+            if (!warp_wait(bar_tempty + 8 * b, ((uint32_t)turn & 1u) ^ 1u, wc)) break;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
+            for (int k = 0; k < p.K; k += kMx4K) {
+                if (!warp_wait(bar_full + 8 * s, ph, wc)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
-                for (int k = 0; k < p.K; k += kMx4K) {
-                    if (!mbar_wait(bar_full + 8 * s, ph, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t soff = (uint64_t)((s * L.stage_bytes) >> 4);
-                    const uint32_t sfa = tmem_base + 256u + (uint32_t)s * scale_cols, sfb = sfa + 4u * T;
-                    const int left = p.K - k;
+                const uint64_t soff = (uint64_t)((s * L.stage_bytes) >> 4);
+                const uint32_t sfa = tmem_base + 256u + (uint32_t)s * scale_cols, sfb = sfa + 4u * T;
+                const int left = p.K - k;
+                if (elect_one()) {
 #pragma unroll
                     for (int t = 0; t < T; ++t) {
                         if (t * 4 * BLOCK >= left) continue;
                         const uint64_t ds = ds0 + soff + (uint64_t)((t * kScaleTile) >> 4);
+                        const uint32_t to = sfb + (uint32_t)(4 * t * q_tiles);
                         tmem_cp_scales(sfa + 4u * t, ds);
-                        for (int i = 0; i < qt; ++i)
-                            tmem_cp_scales(sfb + (uint32_t)(4 * (t * q_tiles + i)),
-                                           ds + (uint64_t)(((1 + i) * T * kScaleTile) >> 4));
+                        tmem_cp_scales(to, ds + (uint64_t)((T * kScaleTile) >> 4));
+                        if (two) tmem_cp_scales(to + 4u, ds + (uint64_t)((2 * T * kScaleTile) >> 4));
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {  // 64 k each
@@ -214,18 +220,18 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                                         sfb + (uint32_t)(4 * t * q_tiles), k > 0 || kk > 0 ? 1u : 0u);
                     }
                     tc_commit(bar_empty + 8 * s);
-                    if (++s == stages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
                 }
-                if (!ok) break;
-                tc_commit(bar_tfull + 8 * b);
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
-            pdl_release();
-            tc_commit(bar_drain);
-            mbar_wait_drain(bar_drain, 0, p.timeout_ns);
+            if (!ok) break;
+            if (elect_one()) tc_commit(bar_tfull + 8 * b);
         }
+        pdl_release();
+        if (elect_one()) tc_commit(bar_drain);
+        mbar_wait_drain(bar_drain, 0, p.timeout_ns);
     } else {
         // ------------------------------------------------------ epilogue
         const int quarter = warp & 3;
