@@ -228,10 +228,11 @@ bool tensor_call(const GroupedCall &c, GroupedParams p, int num_sms, cudaStream_
         p.out_gs = csh[0] > 1 ? cst[0] : 0;
         p.tile_w = Mo > 128 ? 256 : 128;
         p.q_rows = p.tile_w / 2;
-        if (!none && (!cut_map(pv, pi, c.R, kd, &m.p) || !cut_map(qv, qi, c.R, kd, &m.q) ||
-                      !cut_map(pv, pi, c.R, 16, &m.p16) || !cut_map(qv, qi, c.R, 16, &m.q16) ||
-                      !cut_map(pv, pi, c.R, 1, &m.p1) || !cut_map(qv, qi, c.R, 1, &m.q1)))
-            return false;
+        if (!none)
+            for (int i = 0; i < 3; ++i) {
+                const int h = i == 0 ? kd : i == 1 ? 16 : 1;
+                if (!cut_map(pv, pi, c.R, h, &m.m[i]) || !cut_map(qv, qi, c.R, h, &m.m[3 + i])) return false;
+            }
         p.idesc |= 3u << 15;  // both operands MN-major
     } else {
         if (c.ci.row.n > 1 || c.ci.col.n > 1) return false;
@@ -239,20 +240,20 @@ bool tensor_call(const GroupedCall &c, GroupedParams p, int num_sms, cudaStream_
         p.out.rs = one_stride(c.ci.row);
         p.out.cs = c.ci.col.n ? c.ci.col.stride[0] : c.ci.es;
         p.tile_w = (int32_t)std::min<int64_t>(256, (c.R + 31) / 32 * 32);
-        p.q_rows = p.tile_w / 2;
+        p.q_rows = p.tile_w <= 32 ? 16 : p.tile_w <= 64 ? 32 : p.tile_w <= 128 ? 64 : 128;
         bool mn = false;
         if (!none) {
             if (!rows_map_ok(c.a, c.ai)) return false;
-            if (!b_map(c, false, 1, &p, &m.p)) {
+            if (!b_map(c, false, 1, &p, &m.m[0])) {
                 mn = true;
-                if (!b_map(c, true, 2, &p, &m.p)) return false;
+                if (!b_map(c, true, 2, &p, &m.m[0])) return false;
             }
             const int es = c.ai.es;
             const int64_t dim[2] = {c.K, c.R}, stride[1] = {map_stride(one_stride(c.ai.row), c.K * es)};
-            const int box[2] = {128 / es, 64}, box16[2] = {128 / es, 16};
-            if (!encode_map(&m.q, dt, 2, c.a->ptr, dim, stride, box, true) ||
-                !encode_map(&m.q16, dt, 2, c.a->ptr, dim, stride, box16, true))
-                return false;
+            for (int i = 0; 16 << i <= p.q_rows; ++i) {
+                const int box[2] = {128 / es, 16 << i};
+                if (!encode_map(&m.m[1 + i], dt, 2, c.a->ptr, dim, stride, box, true)) return false;
+            }
         }
         if (mn) p.idesc |= 1u << 15;
     }

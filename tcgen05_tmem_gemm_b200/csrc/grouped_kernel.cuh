@@ -31,8 +31,8 @@
 #include <climits>
 
 #include "common.cuh"
-#include "sm100.cuh"
 #include "turned_out.cuh"
+#include "uniform.cuh"
 
 namespace dg {
 
@@ -47,7 +47,7 @@ struct GroupedParams {
     int32_t tile_w;          // by k: tile's rows of C; by rows: the most
     int32_t tiles_n;         // 256-column tiles of C
     int32_t stages;
-    int32_t q_rows;          // ring space of Q: rows per CTA and sub-block, at most 128
+    int32_t q_rows;          // ring space of Q: rows per CTA and sub-block, 16 to 128, a power of two
     int32_t p_swap_g;        // by rows: P's map has the group before its second dim
     int32_t p_one_g;         // by rows: all groups share one B
     uint32_t idesc;          // instruction descriptor without N
@@ -60,10 +60,11 @@ struct GroupedParams {
     int32_t pdl;
 };
 
+// By rows: B as {K or N, N or K, group}, then A in boxes of 16, 32, 64 and 128
+// rows.  By k: Y (P), cut, in boxes of a stage's rows, 16 rows and one, then X
+// (Q) likewise.
 struct GroupedMaps {
-    CUtensorMap p, q;      // by rows: B as {K or N, N or K, group}, A in boxes of 64 rows; by k: Y and X, cut
-    CUtensorMap p16, q16;  // by rows: q16 is A in boxes of 16 rows; by k: both, cut, in boxes of 16 rows
-    CUtensorMap p1, q1;    // by k: both in boxes of one row
+    CUtensorMap m[6];
 };
 
 namespace {
@@ -137,6 +138,20 @@ __device__ __forceinline__ bool group_unit(const GroupedParams &p, const GroupTa
     return true;
 }
 
+// group_unit by a whole warp, in uniform registers.
+template <bool BYK>
+__device__ __forceinline__ bool warp_unit(const GroupedParams &p, const GroupTables &t, int u, GroupUnit &x) {
+    const bool any = group_unit<BYK>(p, t, u, x);
+    if (!__any_sync(0xffffffffu, any)) return false;
+    x.g = uniform(x.g);
+    x.r0 = uniform(x.r0);
+    x.w = uniform(x.w);
+    x.n0 = uniform(x.n0);
+    x.k0 = uniform(x.k0);
+    x.k = uniform(x.k);
+    return true;
+}
+
 // The groups' rows from the offsets, checked: a group whose offsets decrease
 // or leave [0, R] has no rows and is reported.
 __device__ __forceinline__ void group_tables(const int64_t *offsets, int groups, int R, int *err_word, int *start,
@@ -191,8 +206,8 @@ __device__ __forceinline__ void group_tiles(const GroupedParams &p, const int *s
 // By k: rows [row, row + v) of one operand, columns c0 .. c0 + cols - 1, to
 // MN-major boxes of KD rows; the rest of v's last 16 rows becomes zeros.
 template <int KD, int BK>
-__device__ __forceinline__ void load_cut(uint32_t dst, const CUtensorMap *m, const CUtensorMap *m16,
-                                         const CUtensorMap *m1, uint32_t full, int c0, int cols, int row, int v, int R) {
+__device__ __forceinline__ void load_cut(uint32_t dst, const CUtensorMap *m, uint32_t full, int c0, int cols, int row,
+                                         int v, int R) {
     const int end = row + v;
     for (int c = 0; c < cols; c += BK, dst += KD * 128) {
         if (end >= KD) {
@@ -202,10 +217,10 @@ __device__ __forceinline__ void load_cut(uint32_t dst, const CUtensorMap *m, con
         for (int i = 0; i < v; i += 16) {
             const int some = min(16, v - i), last = row + i + some;
             if (last >= 16) {
-                tma_load_3d_pair(dst + i * 128, m16, full, c0 + c, 16 - some, last - 16);
+                tma_load_3d_pair(dst + i * 128, m + 1, full, c0 + c, 16 - some, last - 16);
             } else {
                 for (int j = 0; j < 16; ++j)
-                    tma_load_2d_pair(dst + (i + j) * 128, m1, full, c0 + c, j < some ? row + i + j : R);
+                    tma_load_2d_pair(dst + (i + j) * 128, m + 2, full, c0 + c, j < some ? row + i + j : R);
             }
         }
     }
@@ -221,9 +236,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     constexpr uint32_t kMnBox = (uint32_t)KD * 128;  // an MN-major box: KD rows of k, 128 bytes each
 
     if (threadIdx.x == 64 && p.K > 0 && (!BYK || p.R >= KD)) {
-        tma_prefetch_desc(&maps.p);
-        tma_prefetch_desc(&maps.q);
-        if (!BYK) tma_prefetch_desc(&maps.q16);
+        tma_prefetch_desc(&maps.m[0]);
+        if (BYK) tma_prefetch_desc(&maps.m[3]);
     }
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -238,7 +252,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.aux_off + 4);
     int *start = reinterpret_cast<int *>(smem + L.table_off), *size = start + p.groups, *before = size + p.groups;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -275,80 +289,74 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     __syncwarp();
     cluster_sync();  // both CTAs' barriers exist before either signals the other's
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = uniform(*tmem_slot);
     const GroupTables tables{start, size, before};
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
-        if (lane == 0) {
-            const int stages = p.stages;
-            const bool stall = p.stall_loader == 1;
-            int it = 0, s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            GroupUnit x;
-            for (int u = pair; ok && !*abort_flag && group_unit<BYK>(p, tables, u, x); u += pairs) {
-                const int h = x.w / 2;  // this CTA's rows of the tile
-                const int n0 = x.n0 + (int)rank * kPRows, r0 = x.r0 + (int)rank * h;
-                const uint32_t tx_full = 2u * (L.a_bytes + (uint32_t)(KSUB * h) * 128u);
-                const int g = p.p_one_g ? 0 : x.g;
-                for (int k = 0; k < x.k; k += KD, ++it) {
-                    if (!mbar_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!stall) {
-                        const uint32_t full = dsmem_map(bar_full + 8 * s, 0);
-                        uint32_t tx = tx_full;
-                        if (BYK && x.k0 + min(k + KD, x.k) < KD)  // in boxes of 16 rows, as many as there are
-                            tx = 2u * (uint32_t)((kPRows + h) / BK * ((min(KD, x.k - k) + 15) / 16)) * 2048u;
-                        if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, tx);
-                        const uint32_t as = sbase + s * L.stage_bytes, bs = as + L.a_bytes;
-                        if (BYK) {
-                            const int v = min(KD, x.k - k), row = x.k0 + k;
-                            load_cut<KD, BK>(as, &maps.p, &maps.p16, &maps.p1, full, n0, kPRows, row, v, p.R);
-                            load_cut<KD, BK>(bs, &maps.q, &maps.q16, &maps.q1, full, r0, h, row, v, p.R);
+        const int stages = p.stages;
+        const bool stall = p.stall_loader == 1;
+        int it = 0, s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        GroupUnit x;
+        for (int u = pair; ok && warp_unit<BYK>(p, tables, u, x); u += pairs) {
+            const int h = x.w / 2;  // this CTA's rows of the tile
+            const int n0 = x.n0 + (int)rank * kPRows, r0 = x.r0 + (int)rank * h;
+            // by rows, one copy per sub-block: its fixed cost is that of some 55 rows
+            const int size_at = h <= 16 ? 0 : h <= 32 ? 1 : h <= 64 ? 2 : 3, box = BYK ? h : 16 << size_at;
+            const CUtensorMap *const mq = &maps.m[BYK ? 3 : 1 + size_at];
+            const uint32_t tx_full = 2u * (L.a_bytes + (uint32_t)(KSUB * box) * 128u);
+            const int g = p.p_one_g ? 0 : x.g;
+            for (int k = 0; k < x.k; k += KD, ++it) {
+                if (!warp_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
+                    ok = false;
+                    break;
+                }
+                if (!stall && elect_one()) {
+                    const uint32_t full = dsmem_map(bar_full + 8 * s, 0);
+                    uint32_t tx = tx_full;
+                    if (BYK && x.k0 + min(k + KD, x.k) < KD)  // in boxes of 16 rows, as many as there are
+                        tx = 2u * (uint32_t)((kPRows + h) / BK * ((min(KD, x.k - k) + 15) / 16)) * 2048u;
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, tx);
+                    const uint32_t as = sbase + s * L.stage_bytes, bs = as + L.a_bytes;
+                    if (BYK) {
+                        const int v = min(KD, x.k - k), row = x.k0 + k;
+                        load_cut<KD, BK>(as, &maps.m[0], full, n0, kPRows, row, v, p.R);
+                        load_cut<KD, BK>(bs, mq, full, r0, h, row, v, p.R);
+                    } else {
+                        if (P_MN) {
+#pragma unroll
+                            for (int c = 0; c < kPRows / BK; ++c)
+                                tma_load_3d_pair(as + c * kMnBox, &maps.m[0], full, n0 + c * BK, p.p_swap_g ? g : k,
+                                                 p.p_swap_g ? k : g);
                         } else {
-                            if (P_MN) {
 #pragma unroll
-                                for (int c = 0; c < kPRows / BK; ++c)
-                                    tma_load_3d_pair(as + c * kMnBox, &maps.p, full, n0 + c * BK,
-                                                     p.p_swap_g ? g : k, p.p_swap_g ? k : g);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < KSUB; ++j)
-                                    tma_load_3d_pair(as + j * L.a_sub, &maps.p, full, k + j * BK,
-                                                     p.p_swap_g ? g : n0, p.p_swap_g ? n0 : g);
-                            }
-#pragma unroll
-                            for (int j = 0; j < KSUB; ++j) {
-                                const uint32_t q = bs + j * L.b_sub;
-                                int c = 0;
-                                for (; c + 64 <= h; c += 64)
-                                    tma_load_2d_pair(q + c * 128, &maps.q, full, k + j * BK, r0 + c);
-                                for (; c < h; c += 16)
-                                    tma_load_2d_pair(q + c * 128, &maps.q16, full, k + j * BK, r0 + c);
-                            }
+                            for (int j = 0; j < KSUB; ++j)
+                                tma_load_3d_pair(as + j * L.a_sub, &maps.m[0], full, k + j * BK, p.p_swap_g ? g : n0,
+                                                 p.p_swap_g ? n0 : g);
                         }
+#pragma unroll
+                        for (int j = 0; j < KSUB; ++j) tma_load_2d_pair(bs + j * L.b_sub, mq, full, k + j * BK, r0);
                     }
-                    if (++s == stages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                }
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            if (!leader) pdl_release();
-            // full[] of the even CTA counts both CTAs' bytes: once its last
-            // phases complete, every copy of the pair has landed
-            if (leader && !stall)
-                for (int d = 1; d <= stages && it - d >= 0; ++d) {
-                    const int j = it - d;
-                    mbar_wait_drain(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u, p.timeout_ns);
-                }
         }
+        if (!leader) pdl_release();
+        // full[] of the even CTA counts both CTAs' bytes: once its last
+        // phases complete, every copy of the pair has landed
+        if (leader && !stall)
+            for (int d = 1; d <= stages && it - d >= 0; ++d) {
+                const int j = it - d;
+                mbar_wait_drain(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u, p.timeout_ns);
+            }
     } else if (warp == 1) {
         // ----------------------------------------- MMA issuer (even CTA only)
-        if (lane == 0 && leader) {
+        if (leader) {
             const int stages = p.stages;
             const uint32_t stage_bytes = L.stage_bytes;
             constexpr bool Q_MN = BYK;
@@ -361,45 +369,47 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
             uint32_t ph = 0;
             bool ok = true;
             GroupUnit x;
-            for (int u = pair; ok && group_unit<BYK>(p, tables, u, x); u += pairs) {
+            for (int u = pair; ok && warp_unit<BYK>(p, tables, u, x); u += pairs) {
                 if (x.k == 0) continue;
                 const uint32_t idesc = p.idesc | (uint32_t)(x.w >> 3) << 17;
                 const int b = local & 1;
-                if (!mbar_wait(bar_tempty + 8 * b, ((uint32_t)(local >> 1) & 1u) ^ 1u, wc)) break;
+                if (!warp_wait(bar_tempty + 8 * b, ((uint32_t)(local >> 1) & 1u) ^ 1u, wc)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(b * 256);
                 for (int k = 0; k < x.k; k += KD) {
-                    if (!mbar_wait(bar_full + 8 * s, ph, wc)) {
+                    if (!warp_wait(bar_full + 8 * s, ph, wc)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t soff = (uint64_t)((s * stage_bytes) >> 4);
                     const int some = x.k - k;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int sub = 0; sub < KSUB; ++sub) {
+                        for (int sub = 0; sub < KSUB; ++sub) {
 #pragma unroll
-                        for (int kk = 0; kk < kSteps; ++kk) {
-                            if (sub * BK + kk * UK >= some) continue;  // zeros past the end of k
-                            const uint64_t da = da0 + soff + (uint64_t)((sub * p_sstep + kk * p_kstep) >> 4);
-                            const uint64_t db = db0 + soff + (uint64_t)((sub * q_sstep + kk * q_kstep) >> 4);
-                            const uint32_t acc = (k > 0 || sub > 0 || kk > 0) ? 1u : 0u;
-                            if (FP8) umma_f8_pair(d_tmem, da, db, idesc, acc);
-                            else umma_f16_pair(d_tmem, da, db, idesc, acc);
+                            for (int kk = 0; kk < kSteps; ++kk) {
+                                if (sub * BK + kk * UK >= some) continue;  // zeros past the end of k
+                                const uint64_t da = da0 + soff + (uint64_t)((sub * p_sstep + kk * p_kstep) >> 4);
+                                const uint64_t db = db0 + soff + (uint64_t)((sub * q_sstep + kk * q_kstep) >> 4);
+                                const uint32_t acc = (k > 0 || sub > 0 || kk > 0) ? 1u : 0u;
+                                if (FP8) umma_f8_pair(d_tmem, da, db, idesc, acc);
+                                else umma_f16_pair(d_tmem, da, db, idesc, acc);
+                            }
                         }
+                        tc_commit_pair_mc(bar_empty + 8 * s, 0x3);  // the stage is free in both CTAs
                     }
-                    tc_commit_pair_mc(bar_empty + 8 * s, 0x3);  // the stage is free in both CTAs
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
                 if (!ok) break;
-                tc_commit_pair_mc(bar_tfull + 8 * b, 0x3);
+                if (elect_one()) tc_commit_pair_mc(bar_tfull + 8 * b, 0x3);
                 ++local;
             }
             pdl_release();
-            tc_commit_pair_mc(bar_drain, 0x1);
+            if (elect_one()) tc_commit_pair_mc(bar_drain, 0x1);
             mbar_wait_drain(bar_drain, 0, p.timeout_ns);
         }
     } else {
