@@ -69,7 +69,7 @@ struct GroupedMaps {
 
 namespace {
 
-constexpr int kGroupThreads = 192;
+constexpr int kGroupThreads = 64 + 32 * kTurnWarps;
 constexpr int kPRows = 128;  // P's rows (columns of C) per CTA
 
 struct GroupLayout {
@@ -84,7 +84,7 @@ __host__ __device__ inline GroupLayout group_layout(int stages, int ksub, int q_
     L.b_bytes = (uint32_t)ksub * L.b_sub;
     L.stage_bytes = L.a_bytes + L.b_bytes;
     L.turn_off = L.stage_bytes * stages;
-    L.bar_off = L.turn_off + 4 * kTurnBytes;
+    L.bar_off = L.turn_off + kTurnWarps * kTurnBytes;
     L.aux_off = L.bar_off + 8 * (2 * stages + 5);
     L.table_off = L.aux_off + 16;  // start, size, tiles before
     L.total = L.table_off + 4 * (3 * (uint32_t)groups + 1) + 1024;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, 8);  // the epilogue warps of both CTAs
+            mbar_init(bar_tempty + 8 * b, 2 * kTurnWarps);  // the epilogue warps of both CTAs
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -414,8 +414,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
         }
     } else {
         // ------------------------------------------- epilogue (both CTAs)
-        const int quarter = warp & 3;
-        const uint32_t turn = sbase + L.turn_off + (uint32_t)quarter * kTurnBytes;
+        const int quarter = warp & 3, half = warp >= 6 ? 1 : 0;  // the two warps of a quarter take turns
+        const uint32_t turn = sbase + L.turn_off + (uint32_t)(warp - 2) * kTurnBytes;
         int local = 0;
         GroupUnit x;
         for (int u = pair; group_unit<BYK>(p, tables, u, x); u += pairs) {
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                 tc_fence_after();
             }
             turned_rows(o, turn, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256), x.k == 0, x.r0,
-                        x.rows, n0, lane);
+                        x.rows, n0, lane, half, 2);
             if (x.k > 0) {
                 tc_fence_before();
                 __syncwarp();

@@ -44,7 +44,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
         : "memory");
 }
 
-constexpr int kMx4Threads = 192;
+constexpr int kMx4Threads = 64 + 32 * kTurnWarps;
 constexpr int kMx4K = 256;  // k per stage
 constexpr uint32_t kScaleTile = 512;
 
@@ -62,7 +62,7 @@ __host__ __device__ inline Mx4Layout mx4_layout(int stages, int block, int tile_
     L.sq_bytes = (uint32_t)((tile_w + 127) / 128) * t * kScaleTile;
     L.stage_bytes = (L.p_bytes + L.q_bytes + L.sp_bytes + L.sq_bytes + 1023) / 1024 * 1024;
     L.turn_off = L.stage_bytes * stages;
-    L.bar_off = L.turn_off + 4 * kTurnBytes;
+    L.bar_off = L.turn_off + kTurnWarps * kTurnBytes;
     L.aux_off = L.bar_off + 8 * (2 * stages + 5);
     L.total = L.aux_off + 16 + 1024;
     return L;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, 4);
+            mbar_init(bar_tempty + 8 * b, kTurnWarps);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         mbar_wait_drain(bar_drain, 0, p.timeout_ns);
     } else {
         // ------------------------------------------------------ epilogue
-        const int quarter = warp & 3;
-        const uint32_t turn_at = sbase + L.turn_off + (uint32_t)quarter * kTurnBytes;
+        const int quarter = warp & 3, half = warp >= 6 ? 1 : 0;  // the two warps of a quarter take turns
+        const uint32_t turn_at = sbase + L.turn_off + (uint32_t)(warp - 2) * kTurnBytes;
         TurnedOut o = p.out;
         if (p.fa != nullptr) o.alpha *= *p.fa;
         if (p.fb != nullptr) o.alpha *= *p.fb;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 tc_fence_after();
             }
             turned_rows(o, turn_at, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 128), p.K == 0, m0,
-                        rows, n0 + quarter * 32, lane);
+                        rows, n0 + quarter * 32, lane, half, 2);
             if (p.K > 0) {
                 tc_fence_before();
                 __syncwarp();

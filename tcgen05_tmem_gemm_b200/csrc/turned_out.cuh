@@ -3,11 +3,16 @@
 // rows are tiled this way, so that the weight fills the tensor core's fixed
 // side and the rows its adjustable one.
 //
-// After tcgen05.ld a thread holds one n and 32 rows.  A warp turns its 32 x 32
-// block through shared memory and stores whole 64- or 128-byte runs of C's
-// rows; blocks that a vector store does not fit (an odd N, strided or
-// unaligned C) are stored element by element, a warp then writing 32
-// neighbouring columns per row.
+// Three ways to C, per 32 x 32 block of a warp:
+//  - 16-bit C of contiguous columns and aligned rows, beta = 0: TMEM is read in
+//    the fragment layout of 8 x 8 matrices (16x256b), whose packed pairs
+//    stmatrix turns on their way to shared memory; the warp then stores whole
+//    64-byte runs of C's rows, 16 bytes a lane.  About 80 issue slots a block
+//    against 130 with the 32 two-byte stores to shared memory of a thread that
+//    holds one n, and a third of the latencies.
+//  - F32 C: a thread holds one n and 32 rows, and a store of the warp is 128
+//    contiguous bytes of a row: no detour.
+//  - any other C, and beta != 0: the same, element by element.
 #pragma once
 
 #include "umma_common.cuh"
@@ -27,21 +32,97 @@ struct TurnedOut {
     int32_t N;
 };
 
-constexpr uint32_t kTurnBytes = 32 * 32 * 4;  // a warp's staging block
+constexpr uint32_t kTurnBytes = 32 * 32 * 2;  // a warp's staging block
+constexpr int kTurnWarps = 8;                 // epilogue warps: two per quarter of the TMEM lanes
 
-// Rows [r0, r0 + rows) of C, whose accumulators are the TMEM columns from
-// `taddr` (lane quarter included) on, and columns n0 .. n0 + 31.  `empty`: the
-// sums are zero and TMEM is not read.  r0 indexes scale_r and C's rows.
+// 16 lanes x 32 columns in the fragment layout: r[4 j], r[4 j + 1] are lane
+// t / 4, columns 8 j + 2 (t % 4) and the next; r[4 j + 2], r[4 j + 3] lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit elements, turned: the eight rows of matrix q
+// go to the addresses of lanes 8 q .. 8 q + 7.
+__device__ __forceinline__ void stmatrix_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+// Blocks c0 = 32 first, 32 (first + step), ... of a tile: 16-bit C, beta = 0,
+// columns n0 .. n0 + 31 all inside C.
 template <int CD, bool FUSED, int ACT>
-__device__ __forceinline__ void turned_rows_t(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty,
-                                              int64_t r0, int rows, int n0, int lane) {
-    constexpr int ES = CD == DG_F32 ? 4 : 2;
+__device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty, int64_t r0,
+                                              int rows, int n0, int lane, int first, int step) {
+    const int col = 2 * (lane & 3), sub = lane >> 2;
+    float an[4], bn[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        an[q] = o.alpha * (o.scale_n != nullptr ? o.scale_n[n0 + 8 * q + sub] : 1.f);
+        bn[q] = FUSED && o.bias_n != nullptr ? o.bias_n[n0 + 8 * q + sub] : 0.f;
+    }
+    // unit u of row r lies at unit u ^ (r / 2 % 4): neither side has bank conflicts
+    const uint32_t put = stage + (uint32_t)lane * 64u, swz = (uint32_t)(lane >> 1) & 3u;
+    for (int c0 = 32 * first; c0 < rows; c0 += 32 * step) {
+        uint32_t r[2][16];
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
+        } else {
+            __syncwarp();
+            tmem_ld_frag(taddr + (uint32_t)c0, r[0]);
+            tmem_ld_frag(taddr + (16u << 16) + (uint32_t)c0, r[1]);
+            tmem_ld_wait();
+        }
+        float sr[8];
+        if (o.scale_r != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // rows past the last are not stored: any row's scale will do
+                sr[j] = o.scale_r[r0 + min(c0 + 8 * (j >> 1) + col + (j & 1), rows - 1)];
+        }
+        __syncwarp();  // the last block has left the staging block
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // n 8 q .. 8 q + 7
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float a = o.scale_r != nullptr ? an[q] * sr[2 * j + i] : an[q];
+                    v[i] = a * __uint_as_float(r[q >> 1][4 * j + 2 * (q & 1) + i]);
+                    if (FUSED) v[i] = act_fn<ACT, true>(v[i] + bn[q]);
+                }
+                w[j] = pack2<CD == DG_BF16>(v[0], v[1]);
+            }
+            stmatrix_turned(put + ((uint32_t)q ^ swz) * 16u, w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        char *const block = o.c + (r0 + c0) * o.rs + (int64_t)n0 * 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + sub;
+            const float4 w = ld_shared_v4(stage + (uint32_t)row * 64u + (((uint32_t)lane ^ (uint32_t)(row >> 1)) & 3u) * 16u);
+            if (c0 + row < rows) *reinterpret_cast<float4 *>(block + row * o.rs + (lane & 3) * 16) = w;
+        }
+    }
+}
+
+// The same for any C: a thread holds column n0 + lane and 32 rows.
+template <int CD, bool FUSED, int ACT>
+__device__ __forceinline__ void turned_any(const TurnedOut &o, uint32_t taddr, bool empty, int64_t r0, int rows, int n0,
+                                           int lane, int first, int step) {
     const int n = n0 + lane;
     const bool n_ok = n < o.N;
     const float an = o.alpha * (o.scale_n != nullptr && n_ok ? o.scale_n[n] : 1.f);
     const float bn = FUSED && o.bias_n != nullptr && n_ok ? o.bias_n[n] : 0.f;
-    const bool vec = o.vec && n0 + 32 <= o.N;
-    for (int c0 = 0; c0 < rows; c0 += 32) {
+    for (int c0 = 32 * first; c0 < rows; c0 += 32 * step) {
         const int some = min(32, rows - c0);
         uint32_t r[32];
         if (empty) {
@@ -54,7 +135,7 @@ __device__ __forceinline__ void turned_rows_t(const TurnedOut &o, uint32_t stage
             tmem_ld_wait();
         }
         float v[32];
-        char *const block = o.c + (r0 + c0) * o.rs + (int64_t)n0 * o.cs;
+        char *const at = o.c + (r0 + c0) * o.rs + (int64_t)n * o.cs;
         if (o.scale_r != nullptr) {
             const float sr = o.scale_r[r0 + c0 + min(lane, some - 1)];  // one row's per lane
 #pragma unroll
@@ -68,8 +149,7 @@ __device__ __forceinline__ void turned_rows_t(const TurnedOut &o, uint32_t stage
             for (int h = 0; h < 32; h += 8) {
                 float old[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    old[c] = n_ok && h + c < some ? ld_out<CD>(block + (h + c) * o.rs + lane * o.cs) : 0.f;
+                for (int c = 0; c < 8; ++c) old[c] = n_ok && h + c < some ? ld_out<CD>(at + (h + c) * o.rs) : 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[h + c] = fmaf(o.beta, old[c], v[h + c]);
             }
@@ -78,55 +158,45 @@ __device__ __forceinline__ void turned_rows_t(const TurnedOut &o, uint32_t stage
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = act_fn<ACT, CD != DG_F32>(v[c] + bn);
         }
-        if (!vec) {
-            if (n_ok) {
+        if (n_ok) {
+            char *to = at;
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < some) st_out<CD>(block + c * o.rs + lane * o.cs, v[c]);
-            }
-            continue;
-        }
-        // [row][n] in shared memory, without padding: a warp writes one row's 32
-        // values at a time, and reads 512 contiguous bytes per instruction
-        __syncwarp();
-        const uint32_t at = stage + (uint32_t)lane * ES;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            if (CD == DG_F32) {
-                st_shared_f32(at + c * 128u, v[c]);
-            } else {
-                const uint32_t h = CD == DG_BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[c]))
-                                                 : (uint32_t)__half_as_ushort(__float2half_rn(v[c]));
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + c * 64u), "h"((uint16_t)h) : "memory");
-            }
-        }
-        __syncwarp();
-        constexpr int UNITS = 32 * ES / 16;  // 16-byte units per row
-#pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            const int e = i * 32 + lane, row = e / UNITS;
-            const float4 w = ld_shared_v4(stage + (uint32_t)e * 16u);
-            if (row < some) *reinterpret_cast<float4 *>(block + row * o.rs + (e % UNITS) * 16) = w;
+            for (int c = 0; c < 32; ++c, to += o.rs)
+                if (c < some) st_out<CD>(to, v[c]);
         }
     }
 }
 
 template <bool FUSED, int ACT>
-__device__ __forceinline__ void turned_rows_d(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty,
-                                              int64_t r0, int rows, int n0, int lane) {
-    if (o.dtype == DG_F32) turned_rows_t<DG_F32, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane);
-    else if (o.dtype == DG_BF16) turned_rows_t<DG_BF16, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane);
-    else turned_rows_t<DG_F16, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane);
+__device__ __forceinline__ void turned_rows_d(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty, int64_t r0,
+                                              int rows, int n0, int lane, int first, int step) {
+    if (o.dtype == DG_F32) {
+        turned_any<DG_F32, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
+    } else if (o.vec && o.beta == 0.f && n0 + 32 <= o.N) {
+        if (o.dtype == DG_BF16)
+            turned_fast16<DG_BF16, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+        else turned_fast16<DG_F16, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+    } else if (o.dtype == DG_BF16) {
+        turned_any<DG_BF16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
+    } else {
+        turned_any<DG_F16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
+    }
 }
 
+// Rows [r0, r0 + rows) of C, whose accumulators are the TMEM columns from
+// `taddr` (lane quarter included) on, and columns n0 .. n0 + 31: the blocks of
+// 32 rows first, first + step, ...  `empty`: the sums are zero and TMEM is not
+// read.  r0 indexes scale_r and C's rows.  stage: kTurnBytes of the warp's own.
 __device__ __forceinline__ void turned_rows(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty, int64_t r0,
-                                            int rows, int n0, int lane) {
+                                            int rows, int n0, int lane, int first, int step) {
     if (n0 >= o.N) return;
     if (o.act == DG_ACT_GELU_TANH)
-        turned_rows_d<true, DG_ACT_GELU_TANH>(o, stage, taddr, empty, r0, rows, n0, lane);
-    else if (o.act == DG_ACT_RELU) turned_rows_d<true, DG_ACT_RELU>(o, stage, taddr, empty, r0, rows, n0, lane);
-    else if (o.bias_n != nullptr) turned_rows_d<true, DG_ACT_NONE>(o, stage, taddr, empty, r0, rows, n0, lane);
-    else turned_rows_d<false, DG_ACT_NONE>(o, stage, taddr, empty, r0, rows, n0, lane);
+        turned_rows_d<true, DG_ACT_GELU_TANH>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+    else if (o.act == DG_ACT_RELU)
+        turned_rows_d<true, DG_ACT_RELU>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+    else if (o.bias_n != nullptr)
+        turned_rows_d<true, DG_ACT_NONE>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+    else turned_rows_d<false, DG_ACT_NONE>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
 }
 
 }  // namespace dg
