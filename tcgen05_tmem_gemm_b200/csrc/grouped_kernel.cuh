@@ -299,8 +299,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
         int it = 0, s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        GroupUnit x;
-        for (int u = pair; ok && warp_unit<BYK>(p, tables, u, x); u += pairs) {
+        GroupUnit x, next;
+        int u = pair;
+        bool more = warp_unit<BYK>(p, tables, u, x);
+        for (; ok && more; x = next) {
             const int h = x.w / 2;  // this CTA's rows of the tile
             const int n0 = x.n0 + (int)rank * kPRows, r0 = x.r0 + (int)rank * h;
             // by rows, one copy per sub-block: its fixed cost is that of some 55 rows
@@ -344,7 +346,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                     s = 0;
                     ph ^= 1u;
                 }
+                // finding a unit takes some 1000 cycles: while the first copies of this one are on their way
+                if (k == 0) more = warp_unit<BYK>(p, tables, u += pairs, next);
             }
+            if (x.k == 0) more = warp_unit<BYK>(p, tables, u += pairs, next);
         }
         if (!leader) pdl_release();
         // full[] of the even CTA counts both CTAs' bytes: once its last
@@ -368,9 +373,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
             int local = 0, s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            GroupUnit x;
-            for (int u = pair; ok && warp_unit<BYK>(p, tables, u, x); u += pairs) {
-                if (x.k == 0) continue;
+            GroupUnit x, next;
+            int u = pair;
+            bool more = warp_unit<BYK>(p, tables, u, x);
+            for (; ok && more; x = next) {
+                if (x.k == 0) {
+                    more = warp_unit<BYK>(p, tables, u += pairs, next);
+                    continue;
+                }
                 const uint32_t idesc = p.idesc | (uint32_t)(x.w >> 3) << 17;
                 const int b = local & 1;
                 if (!warp_wait(bar_tempty + 8 * b, ((uint32_t)(local >> 1) & 1u) ^ 1u, wc)) break;
@@ -403,6 +413,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                         s = 0;
                         ph ^= 1u;
                     }
+                    if (k == 0) more = warp_unit<BYK>(p, tables, u += pairs, next);  // beside the first MMAs
                 }
                 if (!ok) break;
                 if (elect_one()) tc_commit_pair_mc(bar_tfull + 8 * b, 0x3);
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
             if (x.k > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(dsmem_map(bar_tempty + 8 * b, 0));
+                if (lane == 0) mbar_arrive_tmem(dsmem_map(bar_tempty + 8 * b, 0));
                 ++local;
             }
         }

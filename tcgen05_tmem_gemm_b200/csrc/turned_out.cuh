@@ -58,8 +58,8 @@ __device__ __forceinline__ void stmatrix_turned(uint32_t addr, uint32_t a, uint3
 // Blocks c0 = 32 first, 32 (first + step), ... of a tile: 16-bit C, beta = 0,
 // columns n0 .. n0 + 31 all inside C.
 template <int CD, bool FUSED, int ACT>
-__device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty, int64_t r0,
-                                              int rows, int n0, int lane, int first, int step) {
+__device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage, uint32_t taddr, int64_t r0, int rows,
+                                              int n0, int lane, int first, int step) {
     const int col = 2 * (lane & 3), sub = lane >> 2;
     float an[4], bn[4];
 #pragma unroll
@@ -69,27 +69,25 @@ __device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage
     }
     // unit u of row r lies at unit u ^ (r / 2 % 4): neither side has bank conflicts
     const uint32_t put = stage + (uint32_t)lane * 64u, swz = (uint32_t)(lane >> 1) & 3u;
+    if (32 * first >= rows) return;
+    uint32_t r[2][16];
+    __syncwarp();
+    tmem_ld_frag(taddr + 32u * first, r[0]);
+    tmem_ld_frag(taddr + (16u << 16) + 32u * first, r[1]);
+    char *at = o.c + (r0 + 32 * first + sub) * o.rs + (int64_t)n0 * 2 + (lane & 3) * 16;
+    const int64_t eight = 8 * o.rs, ahead = (int64_t)(32 * step - 32) * o.rs;
+#pragma unroll 1
     for (int c0 = 32 * first; c0 < rows; c0 += 32 * step) {
-        uint32_t r[2][16];
-        if (empty) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0;
-        } else {
-            __syncwarp();
-            tmem_ld_frag(taddr + (uint32_t)c0, r[0]);
-            tmem_ld_frag(taddr + (16u << 16) + (uint32_t)c0, r[1]);
-            tmem_ld_wait();
-        }
+        tmem_ld_wait();
         float sr[8];
         if (o.scale_r != nullptr) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)  // rows past the last are not stored: any row's scale will do
                 sr[j] = o.scale_r[r0 + min(c0 + 8 * (j >> 1) + col + (j & 1), rows - 1)];
         }
-        __syncwarp();  // the last block has left the staging block
+        uint32_t w[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {  // n 8 q .. 8 q + 7
-            uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float v[2];
@@ -99,18 +97,26 @@ __device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage
                     v[i] = a * __uint_as_float(r[q >> 1][4 * j + 2 * (q & 1) + i]);
                     if (FUSED) v[i] = act_fn<ACT, true>(v[i] + bn[q]);
                 }
-                w[j] = pack2<CD == DG_BF16>(v[0], v[1]);
+                w[q][j] = pack2<CD == DG_BF16>(v[0], v[1]);
             }
-            stmatrix_turned(put + ((uint32_t)q ^ swz) * 16u, w[0], w[1], w[2], w[3]);
         }
-        __syncwarp();
-        char *const block = o.c + (r0 + c0) * o.rs + (int64_t)n0 * 2;
+        if (c0 + 32 * step < rows) {  // the next block's, beside the rest of this one
+            __syncwarp();
+            tmem_ld_frag(taddr + (uint32_t)(c0 + 32 * step), r[0]);
+            tmem_ld_frag(taddr + (16u << 16) + (uint32_t)(c0 + 32 * step), r[1]);
+        }
+        __syncwarp();  // the last block has left the staging block
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int q = 0; q < 4; ++q)
+            stmatrix_turned(put + ((uint32_t)q ^ swz) * 16u, w[q][0], w[q][1], w[q][2], w[q][3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i, at += eight) {
             const int row = i * 8 + sub;
-            const float4 w = ld_shared_v4(stage + (uint32_t)row * 64u + (((uint32_t)lane ^ (uint32_t)(row >> 1)) & 3u) * 16u);
-            if (c0 + row < rows) *reinterpret_cast<float4 *>(block + row * o.rs + (lane & 3) * 16) = w;
+            const float4 t = ld_shared_v4(stage + (uint32_t)row * 64u + (((uint32_t)lane ^ (uint32_t)(row >> 1)) & 3u) * 16u);
+            if (c0 + row < rows) *reinterpret_cast<float4 *>(at) = t;
         }
+        at += ahead;
     }
 }
 
@@ -122,6 +128,7 @@ __device__ __forceinline__ void turned_any(const TurnedOut &o, uint32_t taddr, b
     const bool n_ok = n < o.N;
     const float an = o.alpha * (o.scale_n != nullptr && n_ok ? o.scale_n[n] : 1.f);
     const float bn = FUSED && o.bias_n != nullptr && n_ok ? o.bias_n[n] : 0.f;
+#pragma unroll 1
     for (int c0 = 32 * first; c0 < rows; c0 += 32 * step) {
         const int some = min(32, rows - c0);
         uint32_t r[32];
@@ -135,7 +142,7 @@ __device__ __forceinline__ void turned_any(const TurnedOut &o, uint32_t taddr, b
             tmem_ld_wait();
         }
         float v[32];
-        char *const at = o.c + (r0 + c0) * o.rs + (int64_t)n * o.cs;
+        char *const at = o.c + (r0 + c0) * o.rs + (int64_t)n * o.cs;  // rows are stepped through: 32 kept offsets would spill
         if (o.scale_r != nullptr) {
             const float sr = o.scale_r[r0 + c0 + min(lane, some - 1)];  // one row's per lane
 #pragma unroll
@@ -145,11 +152,12 @@ __device__ __forceinline__ void turned_any(const TurnedOut &o, uint32_t taddr, b
             for (int c = 0; c < 32; ++c) v[c] = an * __uint_as_float(r[c]);
         }
         if (o.beta != 0.f) {
+            const char *from = at;
 #pragma unroll
             for (int h = 0; h < 32; h += 8) {
                 float old[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) old[c] = n_ok && h + c < some ? ld_out<CD>(at + (h + c) * o.rs) : 0.f;
+                for (int c = 0; c < 8; ++c, from += o.rs) old[c] = n_ok && h + c < some ? ld_out<CD>(from) : 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[h + c] = fmaf(o.beta, old[c], v[h + c]);
             }
@@ -172,10 +180,10 @@ __device__ __forceinline__ void turned_rows_d(const TurnedOut &o, uint32_t stage
                                               int rows, int n0, int lane, int first, int step) {
     if (o.dtype == DG_F32) {
         turned_any<DG_F32, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
-    } else if (o.vec && o.beta == 0.f && n0 + 32 <= o.N) {
+    } else if (o.vec && o.beta == 0.f && n0 + 32 <= o.N && !empty) {
         if (o.dtype == DG_BF16)
-            turned_fast16<DG_BF16, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
-        else turned_fast16<DG_F16, FUSED, ACT>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+            turned_fast16<DG_BF16, FUSED, ACT>(o, stage, taddr, r0, rows, n0, lane, first, step);
+        else turned_fast16<DG_F16, FUSED, ACT>(o, stage, taddr, r0, rows, n0, lane, first, step);
     } else if (o.dtype == DG_BF16) {
         turned_any<DG_BF16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
     } else {

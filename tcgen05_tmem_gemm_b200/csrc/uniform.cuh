@@ -31,4 +31,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
 }
 
+// Arrive on an mbarrier of another CTA of the cluster once this thread's TMEM
+// loads are done (tcgen05.wait::ld, then the fence).  Not a release to the
+// cluster (mbar_arrive_cluster): nothing in memory is handed over, and one would
+// wait for every store of C before it, 3000 cycles at the end of a tile.
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 }  // namespace dg
