@@ -20,9 +20,9 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // The byte of a block's scale from the largest magnitude's bits (NaN and
-// infinities compare above every finite one), and the factor pair (s, r) with
-// which mx4_unit makes x / s: for E8M0 the exact 1 / s, for E4M3 s and its
-// rounded reciprocal.  A block with a NaN or an infinity has the scale NaN and
+// infinities compare above every finite one), and the pair (s, r) with which
+// mx4_unit makes x / s: for E8M0 the exact 1 / s, for E4M3 s and its rounded
+// reciprocal.  A block with a NaN or an infinity has the scale NaN and
 // codes of zero.
 template <int BLOCK>
 __device__ __forceinline__ uint32_t mx4_scale(uint32_t top, float &s, float &r) {
@@ -40,26 +40,53 @@ __device__ __forceinline__ uint32_t mx4_scale(uint32_t top, float &s, float &r) 
         s = r = 0.f;
         return 0x7f;
     }
-    const float want = __fdiv_rn(__uint_as_float(top), 6.f);
+    // top / 6, rounded once (as quotient2 does; where the remainder underflows the scale is 0 in any case)
+    const float x = __uint_as_float(top), sixth = 1.f / 6.f, y = x * sixth;
+    const float want = fmaf(fmaf(-y, 6.f, x), sixth, y);
     const uint32_t code = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
     s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
     r = s > 0.f ? __frcp_rn(s) : 0.f;
     return code;
 }
 
-// x / s.  For E4M3, x times the rounded reciprocal and one correction by the
-// remainder, which the fused multiply-add gives exactly: the result differs
-// from the exact quotient by little more than half an ulp, is exact where the
-// quotient is an FP32 number, and so lies on E2M1's rounding borders exactly
-// where the quotient does (s has four significant bits: no other quotient comes
-// within half an ulp of a border).
+// Two FP32 values in one register pair, and the instructions that take two at
+// a time.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
+// x / s but for the sign of a zero, from the rounded reciprocal r of s and -s:
+// one correction of x r by the remainder, which the fused multiply-add gives
+// exactly.  The result differs from the exact quotient by little more than half
+// an ulp and is exact where the quotient is an FP32 number.
+__device__ __forceinline__ Two quotient2(Two x, Two minus_s, Two r) {
+    const Two y = mul2(x, r);
+    return fma2(fma2(y, minus_s, x), r, y);
+}
+
+// Two values under their block's scale.  The quotient by an E4M3 number lies on
+// E2M1's rounding borders exactly where the exact quotient does: with four
+// significant bits in s no other comes within half an ulp of a border.
 template <int BLOCK>
-__device__ __forceinline__ float mx4_unit(float x, float s, float r) {
-    if (BLOCK == 32) return r == 0.f ? 0.f : x * r;
-    if (r == 0.f) return 0.f;
-    const float y = x * r;
-    // a zero keeps its sign
-    return __uint_as_float(__float_as_uint(fmaf(fmaf(-y, s, x), r, y)) | (__float_as_uint(x) & 0x80000000u));
+__device__ __forceinline__ Two mx4_unit(Two x, Two minus_s, Two r) {
+    return BLOCK == 32 ? mul2(x, r) : quotient2(x, minus_s, r);
+}
+
+__device__ __forceinline__ float with_sign(float v, float x) {
+    return __uint_as_float((__float_as_uint(v) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u));
 }
 
 // Eight values to eight codes, the first in the lowest four bits.
@@ -103,25 +130,27 @@ __device__ __forceinline__ float mx4_scale_value(uint32_t code) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(code & 0x7f), __NV_E4M3)));
 }
 
+// A division out of line: inlined at every use its code no longer fits the
+// instruction cache.
+__device__ __noinline__ float divided(float x, float t) { return __fdiv_rn(x, t); }
+
 // The division by the matrix's factor: u = x / t, rounded once.
 struct Factor {
-    float t, r;
-    bool divide, plain;  // plain: t is of a size for which quotient() holds
+    float t, size, r;       // t, |t| and its rounded reciprocal
+    uint32_t flip;          // the codes' sign bits where t is negative
+    bool divide, plain;     // plain: t is of a size for which quotient() holds
     __device__ explicit Factor(const float *scale) {
         divide = scale != nullptr;
         t = divide ? *scale : 1.f;
-        const float a = fabsf(t);
-        plain = a >= 0x1p-60f && a <= 0x1p60f;
-        r = plain ? __frcp_rn(t) : 0.f;
+        size = fabsf(t);
+        flip = t < 0.f ? 0x88888888u : 0u;
+        plain = size >= 0x1p-60f && size <= 0x1p60f;
+        r = plain ? __frcp_rn(size) : 0.f;
     }
-    // x / t from the rounded reciprocal and the exact remainder of a first
-    // quotient: correctly rounded (Markstein 1990, theorem 6.2 of "Computation
-    // of elementary functions on the IBM RISC System/6000 processor") while
-    // the remainder does not underflow.
-    __device__ __forceinline__ float quotient(float x) const {
-        const float y = x * r;
-        return fmaf(fmaf(-y, t, x), r, y);
-    }
+    // x / |t|, but for the sign of a zero: correctly rounded (Markstein 1990,
+    // "Computation of elementary functions on the IBM RISC System/6000
+    // processor") while the remainder does not underflow.
+    __device__ __forceinline__ Two quotient(Two x) const { return quotient2(x, Two(-size, -size), Two(r, r)); }
 };
 
 // Below this magnitude of a block's largest value its quotients are divided
@@ -151,7 +180,8 @@ struct Lot {
             return m;
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) m = __vmaxu2(m, w[b * N + i] & 0x7fff7fffu);
+            for (int i = 0; i < N; ++i)
+                asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[b * N + i] & 0x7fff7fffu));
             m = max(m & 0xffffu, m >> 16);
             if (DT == DG_BF16) return m << 16;
             return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) & 0x7fffffffu;
@@ -169,28 +199,59 @@ __device__ __forceinline__ uint32_t encode(const Lot<DT> &x, int n, const Factor
         const uint32_t top = x.template top<BLOCK>(b);
         float s, r;
         // the largest |x / t| is that of the largest |x|: rounding keeps the order
-        const uint32_t code = mx4_scale<BLOCK>(f.divide ? abs_bits(__fdiv_rn(__uint_as_float(top), f.t)) : top, s, r);
+        const uint32_t code = mx4_scale<BLOCK>(f.divide ? abs_bits(divided(__uint_as_float(top), f.t)) : top, s, r);
         if (b * BLOCK < n) scales |= code << (8 * b);
         const bool plain = f.plain && __uint_as_float(top) >= kLeastPlain;
+        const Two ms(-s, -s), rr(r, r);
+        // each way a loop of its own: a branch per pair costs as much as the arithmetic
+        if (!f.divide) {
 #pragma unroll
-        for (int j = 0; j < BLOCK / 8; ++j) {
-            float u[8];
-            const int at = b * BLOCK + 8 * j;
-            if (!f.divide) {
+            for (int j = 0; j < BLOCK / 8; ++j) {
+                float u[8];
+                const int at = b * BLOCK + 8 * j;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = mx4_unit<BLOCK>(x[at + i], s, r);
-            } else if (plain) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // a zero has the quotient's sign (a block with a NaN has r = 0 and codes of 0)
-                    const float q = f.quotient(x[at + i]);
-                    u[i] = mx4_unit<BLOCK>(x[at + i] == 0.f ? x[at + i] * f.r : q, s, r);
+                for (int i = 0; i < 8; i += 2) {
+                    const float x0 = x[at + i], x1 = x[at + i + 1];
+                    mx4_unit<BLOCK>(Two(x0, x1), ms, rr).get(u[i], u[i + 1]);
+                    if (BLOCK == 16) {
+                        u[i] = with_sign(u[i], x0);
+                        u[i + 1] = with_sign(u[i + 1], x1);
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = mx4_unit<BLOCK>(__fdiv_rn(x[at + i], f.t), s, r);
+                e[at / 8] = e2m1x8(u);
             }
-            e[at / 8] = e2m1x8(u);
+        } else if (plain) {
+#pragma unroll
+            for (int j = 0; j < BLOCK / 8; ++j) {
+                float u[8];
+                const int at = b * BLOCK + 8 * j;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float x0 = x[at + i], x1 = x[at + i + 1];
+                    mx4_unit<BLOCK>(f.quotient(Two(x0, x1)), ms, rr).get(u[i], u[i + 1]);
+                    u[i] = with_sign(u[i], x0);
+                    u[i + 1] = with_sign(u[i + 1], x1);
+                }
+                e[at / 8] = e2m1x8(u) ^ f.flip;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < BLOCK / 8; ++j) {
+                float u[8];
+                const int at = b * BLOCK + 8 * j;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float x0 = x[at + i], x1 = x[at + i + 1];
+                    mx4_unit<BLOCK>(Two(divided(x0, f.size), divided(x1, f.size)), ms, rr).get(u[i], u[i + 1]);
+                    u[i] = with_sign(u[i], x0);
+                    u[i + 1] = with_sign(u[i + 1], x1);
+                }
+                e[at / 8] = e2m1x8(u) ^ f.flip;
+            }
+        }
+        if (r == 0.f) {
+#pragma unroll
+            for (int j = 0; j < BLOCK / 8; ++j) e[b * BLOCK / 8 + j] = 0u;
         }
     }
     if (n < 32) {
@@ -239,95 +300,136 @@ constexpr int kSpan = 1024;  // k per warp
 template <int DT>
 constexpr int kStageWords = (DT == DG_F32 ? kSpan : kSpan / 2) + 33 + 4;
 
-// A warp takes 1024 k of a row, a lane 32 of them: one block of 32 or two of
-// 16, so that no maximum crosses lanes.  VEC: a lane loads its own 64 (or 128)
-// bytes, 16 at a time; the warp's four loads share their lines in L1.
-// Otherwise (rows at any address) the warp copies the row's words, whole
-// 128-byte lines per load, through shared memory.
-template <int DT, int BLOCK, bool VEC>
-__global__ void __launch_bounds__(32 * kQuantWarps) quantize_rows_kernel(const QuantParams p) {
-    pdl_wait_then_release();
-    constexpr int ES = Lot<DT>::ES, W = Lot<DT>::W;
-    __shared__ uint32_t stage[VEC ? 1 : kQuantWarps * kStageWords<DT>];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Factor f(p.q.scale);
-    const int K = (int)p.q.K, k0 = (int)blockIdx.x * kSpan, k = k0 + lane * 32, n = K - k;
-    const uint32_t tile = blockIdx.x * (uint32_t)(kSpan / BLOCK / 4) + (uint32_t)lane / (BLOCK / 8);  // of scales, along k
-    for (int64_t row = (int64_t)blockIdx.y * kQuantWarps + warp; row < p.q.rows; row += (int64_t)gridDim.y * kQuantWarps) {
-        const char *x = p.x.ptr + axis_offset(p.x.row, row) + (int64_t)k0 * ES;
-        Lot<DT> v;
-        if (VEC) {
-            const uint4 *from = reinterpret_cast<const uint4 *>(x + lane * 32 * ES);
-            if (n >= 32) {
+// The words of a row's 1024 k that start at x, whatever the address: whole
+// 128-byte lines per load, kept in registers; then, through a warp's part of
+// shared memory, lane l's 32 elements, from element 32 l on.
+template <int DT>
+struct Raw {
+    static constexpr int W = Lot<DT>::W, N = DT == DG_F32 ? W : W + 1, per = 4 / Lot<DT>::ES;  // elements per word
+    uint32_t w[N];
+    uint32_t odd;  // the first word's lower half is not the row's
+    __device__ __forceinline__ void load(const char *x, int elems, int lane) {
+        odd = DT == DG_F32 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(x) >> 1) & 1u;
+        const char *at = x - 2 * odd + 4 * lane;
+        const int count = (elems + (int)odd + per - 1) / per;
 #pragma unroll
-                for (int i = 0; i < W / 4; ++i) *reinterpret_cast<uint4 *>(v.w + 4 * i) = from[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const char *at = reinterpret_cast<const char *>(from) + 4 * i;
-                    if (DT == DG_F32) {
-                        v.w[i] = i < n ? *reinterpret_cast<const uint32_t *>(at) : 0u;
-                    } else {
-                        const uint32_t lo = 2 * i < n ? *reinterpret_cast<const uint16_t *>(at) : 0u;
-                        const uint32_t hi = 2 * i + 1 < n ? *reinterpret_cast<const uint16_t *>(at + 2) : 0u;
-                        v.w[i] = lo | hi << 16;
-                    }
-                }
-            }
-        } else {
-            uint32_t *const mine = stage + warp * kStageWords<DT>;
-            const uint32_t odd = DT == DG_F32 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(x) >> 1) & 1u;
-            const char *const words = x - 2 * odd;
-            const int elems = min(kSpan, K - k0), per = 4 / ES;  // elements per word
-            const int count = (elems + (int)odd + per - 1) / per;
-            __syncwarp();
-#pragma unroll 4
-            for (int j = lane; j < count; j += 32) {
-                uint32_t b;
-                const char *at = words + (int64_t)j * 4;
-                if (DT == DG_F32 || (!(odd && j == 0) && per * j + 1 - (int)odd < elems)) {
-                    b = *reinterpret_cast<const uint32_t *>(at);
-                } else {  // a word that is half the row's
-                    const bool low = !(odd && j == 0);
-                    b = (uint32_t)*reinterpret_cast<const uint16_t *>(at + (low ? 0 : 2)) << (low ? 0 : 16);
-                }
-                mine[j + j / W] = b;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const uint32_t b = mine[lane * (W + 1) + i];
-                v.w[i] = DT == DG_F32 ? b
-                                      : __funnelshift_r(b, mine[i + 1 < W ? lane * (W + 1) + i + 1 : (lane + 1) * (W + 1)],
-                                                        16u * odd);
-            }
-            if (n < 32) {
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    v.w[i] &= per * i >= n ? 0u : (per == 2 && 2 * i + 1 >= n) ? 0xffffu : 0xffffffffu;
+        for (int i = 0; i < N; ++i, at += 128) {
+            const int j = 32 * i + lane;
+            w[i] = 0;
+            if (j >= count) continue;
+            if (DT == DG_F32 || (!(odd && j == 0) && per * j + 1 - (int)odd < elems)) {
+                w[i] = *reinterpret_cast<const uint32_t *>(at);
+            } else {  // a word that is half the row's
+                const bool low = !(odd && j == 0);
+                w[i] = (uint32_t)*reinterpret_cast<const uint16_t *>(at + (low ? 0 : 2)) << (low ? 0 : 16);
             }
         }
-        uint32_t e[4];
-        uint32_t scales = encode<DT, BLOCK>(v, max(n, 0), f, e);
-        // four blocks' scales are one word
-        if (BLOCK == 32) {
-            scales <<= 8 * (lane & 3);
-            scales |= __shfl_xor_sync(0xffffffffu, scales, 1);
-            scales |= __shfl_xor_sync(0xffffffffu, scales, 2);
-        } else {
-            scales <<= 16 * (lane & 1);
-            scales |= __shfl_xor_sync(0xffffffffu, scales, 1);
+    }
+    __device__ __forceinline__ void turn(Lot<DT> &v, uint32_t *mine, int lane) const {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int j = 32 * i + lane;
+            if (i < W || j < 32 * W + 1) mine[j + j / W] = w[i];
         }
-        if (n <= 0) continue;
-        if ((lane & (BLOCK / 8 - 1)) == 0)
-            *reinterpret_cast<uint32_t *>(p.q.scales + (row / 128 * p.q.k_tiles + tile) * 512 + row % 32 * 16 +
-                                          row % 128 / 32 * 4) = scales;
-        store_codes(p.q.codes + row * p.q.code_stride + k / 2, p.q.align, e, n);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const uint32_t b = mine[lane * (W + 1) + i];
+            v.w[i] = DT == DG_F32
+                         ? b
+                         : __funnelshift_r(b, mine[i + 1 < W ? lane * (W + 1) + i + 1 : (lane + 1) * (W + 1)], 16u * odd);
+        }
+    }
+};
+
+// A lane's 32 elements at an address that is a multiple of 16, n of which exist.
+template <int DT>
+__device__ __forceinline__ void load_lot(Lot<DT> &v, const char *x, int n) {
+    constexpr int W = Lot<DT>::W;
+    if (n >= 32) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            *reinterpret_cast<uint4 *>(v.w + 4 * i) = *reinterpret_cast<const uint4 *>(x + 16 * i);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const char *at = x + 4 * i;
+        if (DT == DG_F32) {
+            v.w[i] = i < n ? *reinterpret_cast<const uint32_t *>(at) : 0u;
+        } else {
+            const uint32_t lo = 2 * i < n ? *reinterpret_cast<const uint16_t *>(at) : 0u;
+            const uint32_t hi = 2 * i + 1 < n ? *reinterpret_cast<const uint16_t *>(at + 2) : 0u;
+            v.w[i] = lo | hi << 16;
+        }
     }
 }
 
-// A warp reads 1024 k of a row back, a lane eight at a time: its stores are
-// whole 512-byte runs.  Rows at any address go through shared memory, as above.
+// A warp takes 1024 k of four rows that are 32 apart, whose scales are
+// neighbours; a lane has 32 k of each: one block of 32 or two of 16, so that no
+// maximum crosses lanes.  VEC: a lane loads its own 64 (or 128) bytes, 16 at a
+// time (the warp's four loads share their lines in L1), a row ahead of the one
+// it works on.  Otherwise (rows at any address) the warp copies the row through
+// shared memory.
+template <int DT, int BLOCK, bool VEC>
+__global__ void __launch_bounds__(32 * kQuantWarps) quantize_rows_kernel(const QuantParams p) {
+    pdl_wait_then_release();
+    constexpr int ES = Lot<DT>::ES;
+    __shared__ uint32_t stage[VEC ? 1 : kQuantWarps * kStageWords<DT>];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Factor f(p.q.scale);
+    const int K = (int)p.q.K, k0 = (int)blockIdx.x * kSpan, k = k0 + lane * 32, n = max(0, K - k);
+    const uint32_t tile = blockIdx.x * (uint32_t)(kSpan / BLOCK / 4) + (uint32_t)lane / (BLOCK / 8);  // of scales, along k
+    const int64_t quarters = (p.q.rows + 127) / 128 * 4;
+    for (int64_t quarter = blockIdx.y; quarter < quarters; quarter += gridDim.y) {
+        const int64_t row0 = quarter / 4 * 128 + quarter % 4 * 8 + warp;
+        const int rows = (int)min((int64_t)4, (p.q.rows - row0 + 31) / 32);
+        if (rows <= 0) continue;
+        Lot<DT> v, next;
+        Raw<DT> raw;
+        auto load = [&](int i) {
+            const char *x = p.x.ptr + axis_offset(p.x.row, row0 + 32 * i) + (int64_t)k0 * ES;
+            if (VEC) load_lot(next, x + lane * 32 * ES, n);
+            else raw.load(x, min(kSpan, K - k0), lane);
+        };
+        load(0);
+        uint4 scales = make_uint4(0, 0, 0, 0);
+        uint8_t *codes = p.q.codes + row0 * p.q.code_stride + k / 2;
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i) {
+            if (VEC) v = next;
+            else raw.turn(v, stage + warp * kStageWords<DT>, lane);
+            if (i + 1 < rows) load(i + 1);
+            uint32_t e[4];
+            uint32_t s = encode<DT, BLOCK>(v, n, f, e);
+            // four blocks' scales are one word
+            if (BLOCK == 32) {
+                s <<= 8 * (lane & 3);
+                s |= __shfl_xor_sync(0xffffffffu, s, 1);
+                s |= __shfl_xor_sync(0xffffffffu, s, 2);
+            } else {
+                s <<= 16 * (lane & 1);
+                s |= __shfl_xor_sync(0xffffffffu, s, 1);
+            }
+            scales = make_uint4(scales.y, scales.z, scales.w, s);  // the last four
+            if (n > 0) store_codes(codes + 32 * i * p.q.code_stride, p.q.align, e, n);
+        }
+        if (n == 0 || (lane & (BLOCK / 8 - 1)) != 0) continue;
+        uint32_t *const out = reinterpret_cast<uint32_t *>(p.q.scales + (row0 / 128 * p.q.k_tiles + tile) * 512 + row0 % 32 * 16);
+        if (rows == 4) {
+            *reinterpret_cast<uint4 *>(out) = scales;
+        } else {
+            if (rows == 3) out[rows - 3] = scales.y;
+            if (rows >= 2) out[rows - 2] = scales.z;
+            out[rows - 1] = scales.w;
+        }
+    }
+}
+
+// A warp reads 1024 k of four rows back that are 32 apart, a lane eight k at a
+// time: its stores are whole 512-byte runs.  Rows at any address go through
+// shared memory, as above.
 template <int DT, int BLOCK, bool VEC>
 __global__ void __launch_bounds__(32 * kQuantWarps) dequantize_rows_kernel(const QuantParams p) {
     pdl_wait_then_release();
@@ -337,63 +439,79 @@ __global__ void __launch_bounds__(32 * kQuantWarps) dequantize_rows_kernel(const
     const float factor = p.q.scale != nullptr ? *p.q.scale : 1.f;
     const int K = (int)p.q.K, k0 = (int)blockIdx.x * kSpan, n0 = K - k0 - lane * 8;
     const int block = lane * 8 / BLOCK;  // of the first chunk
-    for (int64_t row = (int64_t)blockIdx.y * kQuantWarps + warp; row < p.q.rows; row += (int64_t)gridDim.y * kQuantWarps) {
-        char *const y = const_cast<char *>(p.x.ptr) + axis_offset(p.x.row, row) + (int64_t)k0 * ES;
-        const uint8_t *codes = p.q.codes + row * p.q.code_stride + k0 / 2 + lane * 4;
-        const uint8_t *scales = p.q.scales + (row / 128 * p.q.k_tiles + blockIdx.x * (uint32_t)(kSpan / BLOCK / 4)) * 512 +
-                                row % 32 * 16 + row % 128 / 32 * 4 + block / 4 * 512 + block % 4;
+    const int64_t quarters = (p.q.rows + 127) / 128 * 4;
+    for (int64_t quarter = blockIdx.y; quarter < quarters; quarter += gridDim.y) {
+        const int64_t row0 = quarter / 4 * 128 + quarter % 4 * 8 + warp;
+        const int rows = (int)min((int64_t)4, (p.q.rows - row0 + 31) / 32);
+        if (rows <= 0) continue;
+        // the scales of all four rows are 16 bytes
+        const uint8_t *scales = p.q.scales + row0 % 32 * 16 +
+                                (row0 / 128 * p.q.k_tiles + blockIdx.x * (uint32_t)(kSpan / BLOCK / 4) + block / 4) * 512;
+        uint4 s[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            s[c] = n0 > c * 256 ? *reinterpret_cast<const uint4 *>(scales + c * (64 / BLOCK) * 512) : make_uint4(0, 0, 0, 0);
+        const uint8_t *codes = p.q.codes + row0 * p.q.code_stride + k0 / 2 + lane * 4;
         uint32_t *const mine = stage + warp * kStageWords<DT>;
-        uint32_t e[4], s[4];
+        uint32_t e[4][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int n = n0 - c * 256;
-            e[c] = n > 0 ? load_codes8(codes + c * 128, p.q.align, n) : 0u;
-            s[c] = n > 0 ? scales[c * (64 / BLOCK) * 512] : 0u;
-        }
-        if (!VEC) __syncwarp();  // the last row's words have been stored
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int n = n0 - c * 256;
-            if (n <= 0) continue;
-            const float unit = mx4_scale_value<BLOCK>(s[c]) * factor;
-            float v[8];
-            e2m1x8_values(e[c], v);
-            uint32_t w[W];
+            for (int c = 0; c < 4; ++c)
+                e[i][c] = i < rows && n0 > c * 256
+                              ? load_codes8(codes + 32 * i * p.q.code_stride + c * 128, p.q.align, n0 - c * 256)
+                              : 0u;
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                w[i] = DT == DG_F32 ? __float_as_uint(v[i] * unit)
-                                    : pack2<DT == DG_BF16>(v[2 * i & 7] * unit, v[(2 * i + 1) & 7] * unit);
-            char *const at = y + (c * 256 + lane * 8) * ES;
-            if (VEC && n >= 8) {
+        for (int i = 0; i < 4; ++i) {
+            if (i >= rows) break;
+            char *const y = const_cast<char *>(p.x.ptr) + axis_offset(p.x.row, row0 + 32 * i) + (int64_t)k0 * ES;
+            if (!VEC) __syncwarp();  // the last row's words have been stored
 #pragma unroll
-                for (int i = 0; i < W / 4; ++i)
-                    *reinterpret_cast<uint4 *>(at + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            } else if (VEC) {
+            for (int c = 0; c < 4; ++c) {
+                const int n = n0 - c * 256;
+                if (n <= 0) continue;
+                const uint32_t word = i == 0 ? s[c].x : i == 1 ? s[c].y : i == 2 ? s[c].z : s[c].w;
+                const float unit = mx4_scale_value<BLOCK>(word >> (8 * (block & 3)) & 0xff) * factor;
+                float v[8];
+                e2m1x8_values(e[i][c], v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < n) {
-                        if (DT == DG_F32) *reinterpret_cast<uint32_t *>(at + 4 * i) = w[i & (W - 1)];
-                        else *reinterpret_cast<uint16_t *>(at + 2 * i) = (uint16_t)(w[i / 2 & (W - 1)] >> (i & 1 ? 16 : 0));
-                    }
-            } else {
+                for (int j = 0; j < 8; j += 2) mul2(Two(v[j], v[j + 1]), Two(unit, unit)).get(v[j], v[j + 1]);
+                uint32_t w[W];
 #pragma unroll
-                for (int i = 0; i < W; ++i) mine[(c * 32 + lane) * W + i] = w[i];
+                for (int j = 0; j < W; ++j)
+                    w[j] = DT == DG_F32 ? __float_as_uint(v[j]) : pack2<DT == DG_BF16>(v[2 * j & 7], v[(2 * j + 1) & 7]);
+                char *const at = y + (c * 256 + lane * 8) * ES;
+                if (VEC && n >= 8) {
+#pragma unroll
+                    for (int j = 0; j < W / 4; ++j)
+                        *reinterpret_cast<uint4 *>(at + 16 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                } else if (VEC) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < n) {
+                            if (DT == DG_F32) *reinterpret_cast<uint32_t *>(at + 4 * j) = w[j & (W - 1)];
+                            else *reinterpret_cast<uint16_t *>(at + 2 * j) = (uint16_t)(w[j / 2 & (W - 1)] >> (j & 1 ? 16 : 0));
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) mine[(c * 32 + lane) * W + j] = w[j];
+                }
             }
-        }
-        if (VEC) continue;
-        __syncwarp();
-        const uint32_t odd = DT == DG_F32 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(y) >> 1) & 1u;
-        char *const words = y - 2 * odd;
-        const int elems = min(kSpan, K - k0), per = 4 / ES, count = (elems + (int)odd + per - 1) / per;
+            if (VEC) continue;
+            __syncwarp();
+            const uint32_t odd = DT == DG_F32 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(y) >> 1) & 1u;
+            char *const words = y - 2 * odd;
+            const int elems = min(kSpan, K - k0), per = 4 / ES, count = (elems + (int)odd + per - 1) / per;
 #pragma unroll 4
-        for (int j = lane; j < count; j += 32) {
-            char *at = words + (int64_t)j * 4;
-            const uint32_t here = mine[j], b = odd ? __funnelshift_r(j > 0 ? mine[j - 1] : 0u, here, 16) : here;
-            if (DT == DG_F32 || (!(odd && j == 0) && per * j + 1 - (int)odd < elems)) {
-                *reinterpret_cast<uint32_t *>(at) = b;
-            } else {
-                const bool low = !(odd && j == 0);
-                *reinterpret_cast<uint16_t *>(at + (low ? 0 : 2)) = (uint16_t)(b >> (low ? 0 : 16));
+            for (int j = lane; j < count; j += 32) {
+                char *at = words + (int64_t)j * 4;
+                const uint32_t here = mine[j], b = odd ? __funnelshift_r(j > 0 ? mine[j - 1] : 0u, here, 16) : here;
+                if (DT == DG_F32 || (!(odd && j == 0) && per * j + 1 - (int)odd < elems)) {
+                    *reinterpret_cast<uint32_t *>(at) = b;
+                } else {
+                    const bool low = !(odd && j == 0);
+                    *reinterpret_cast<uint16_t *>(at + (low ? 0 : 2)) = (uint16_t)(b >> (low ? 0 : 16));
+                }
             }
         }
     }
@@ -401,9 +519,9 @@ __global__ void __launch_bounds__(32 * kQuantWarps) dequantize_rows_kernel(const
 
 // ------------------------------------------------------------------ any view
 
-constexpr int kTurnK = 64;  // a thread takes 64 k of a row
+constexpr int kTurnK = 32;  // a thread takes 32 k of a row
 
-// Any view, a thread per row and 64 k: made for rows that are neighbours in
+// Any view, a thread per row and 32 k: made for rows that are neighbours in
 // memory (a weight along its other dim), whose loads are then whole sectors.
 // ONE: k is one dim.
 template <int DT, int BLOCK, bool ONE>
@@ -416,42 +534,39 @@ __global__ void __launch_bounds__(128) quantize_any_kernel(const QuantParams p) 
     const char *x = p.x.ptr + axis_offset(p.x.row, row);
     uint8_t *scales_row = p.q.scales + row / 128 * p.q.k_tiles * 512 + row % 32 * 16 + row % 128 / 32 * 4;
     for (int k0 = (int)blockIdx.y * kTurnK; k0 < K; k0 += (int)gridDim.y * kTurnK) {
-        uint32_t scales = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = k0 + 32 * h, n = K - k;
-            if (n <= 0) break;
-            Lot<DT> v;
-            auto put = [&](int i, const char *at) {
-                uint32_t b = 0;
-                if (i < n) {
-                    if (DT == DG_F32) b = *reinterpret_cast<const uint32_t *>(at);
-                    else b = *reinterpret_cast<const uint16_t *>(at);
-                }
-                if (DT == DG_F32) v.w[i & (Lot<DT>::W - 1)] = b;
-                else if (i & 1) v.w[i / 2] |= b << 16;
-                else v.w[i / 2] = b;
-            };
-            if (ONE) {
-                const char *at = x + k * p.col;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) put(i, at + i * p.col);
-            } else {
-#pragma unroll 1
-                for (int i = 0; i < 32; ++i) put(i, x + axis_offset(p.x.col, min(k + i, K - 1)));
+        const int n = K - k0;
+        Lot<DT> v;
+        auto put = [&](int i, const char *at) {
+            uint32_t b = 0;
+            if (i < n) {
+                if (DT == DG_F32) b = *reinterpret_cast<const uint32_t *>(at);
+                else b = *reinterpret_cast<const uint16_t *>(at);
             }
-            uint32_t e[4];
-            scales |= encode<DT, BLOCK>(v, n, f, e) << (h * (256 / BLOCK));
-            store_codes(p.q.codes + row * p.q.code_stride + k / 2, p.q.align, e, n);
+            if (DT == DG_F32) v.w[i & (Lot<DT>::W - 1)] = b;
+            else if (i & 1) v.w[i / 2] |= b << 16;
+            else v.w[i / 2] = b;
+        };
+        if (ONE) {
+            const char *at = x + k0 * p.col;
+#pragma unroll
+            for (int i = 0; i < 32; ++i, at += p.col) put(i, at);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 32; ++i) put(i, x + axis_offset(p.x.col, min(k0 + i, K - 1)));
         }
-        // blocks past the last one of their tile get a zero
+        uint32_t e[4];
+        const uint32_t scales = encode<DT, BLOCK>(v, n, f, e);
+        store_codes(p.q.codes + row * p.q.code_stride + k0 / 2, p.q.align, e, n);
+        // the blocks past the last one of their tile get a zero
         const int block = k0 / BLOCK;
         uint8_t *out = scales_row + (int64_t)(block / 4) * 512 + block % 4;
         if (BLOCK == 16) {
-            *reinterpret_cast<uint32_t *>(out) = scales;
-        } else {
             *reinterpret_cast<uint16_t *>(out) = (uint16_t)scales;
-            if (k0 + kTurnK >= K && block % 4 == 0) *reinterpret_cast<uint16_t *>(out + 2) = 0;
+            if (n <= 32 && block % 4 == 0) *reinterpret_cast<uint16_t *>(out + 2) = 0;
+        } else {
+            *out = (uint8_t)scales;
+            if (n <= 32)
+                for (int i = block % 4 + 1; i < 4; ++i) out[i - block % 4] = 0;
         }
     }
 }
@@ -490,7 +605,7 @@ cudaError_t run(const QuantParams &p, bool back, cudaStream_t s) {
     // neighbours in a row go to neighbouring lanes; otherwise neighbouring rows do
     if (p.x.col.n == 0 || (p.x.col.n == 1 && p.col == Lot<DT>::ES)) {
         const dim3 grid((unsigned)((p.q.K + kSpan - 1) / kSpan),
-                        (unsigned)std::min<int64_t>((p.q.rows + kQuantWarps - 1) / kQuantWarps, 65535));
+                        (unsigned)std::min<int64_t>((p.q.rows + 127) / 128 * 4, 65532));
         auto kern = back ? (p.vec ? dequantize_rows_kernel<DT, BLOCK, true> : dequantize_rows_kernel<DT, BLOCK, false>)
                          : (p.vec ? quantize_rows_kernel<DT, BLOCK, true> : quantize_rows_kernel<DT, BLOCK, false>);
         return launch_ex(kern, grid, dim3(32 * kQuantWarps), 0, s, dim3(1, 1, 1), p.pdl, p);
