@@ -441,14 +441,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                 if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)(local >> 1) & 1u, wc)) break;
                 tc_fence_after();
             }
-            turned_rows(o, turn, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256), x.k == 0, x.r0,
-                        x.rows, n0, lane, half, 2);
-            if (x.k > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_tmem(dsmem_map(bar_tempty + 8 * b, 0));
-                ++local;
-            }
+            turned_rows<FP8>(o, turn, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 256), x.k == 0, x.r0,
+                        x.rows, n0, lane, half, [&] {
+                            if (x.k == 0) return;
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_tmem(dsmem_map(bar_tempty + 8 * b, 0));
+                        });
+            if (x.k > 0) ++local;
         }
     }
 

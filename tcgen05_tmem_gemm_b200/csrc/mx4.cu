@@ -69,20 +69,21 @@ dg_status quant_call(const dg_view *x, const dg_mx4 *q, bool back, cudaStream_t 
     return DG_OK;
 }
 
-template <int BLOCK>
-cudaError_t launch_mx4(Mx4Params p, const CUtensorMap (&m)[4], int num_sms, cudaStream_t s) {
+template <int BLOCK, bool PAIR>
+cudaError_t launch_mx4(Mx4Params p, const CUtensorMap (&m)[4], int q_rows, int num_sms, cudaStream_t s) {
     static SmemLimit limit;
-    const int q_rows = std::min(p.tile_w, (p.M + 15) / 16 * 16);
     const int most = 256 / mx4_scale_cols(BLOCK, p.tile_w);  // stages that TMEM has scale columns for
     int stages = 2;
     while (stages < most && mx4_layout(stages + 1, BLOCK, p.tile_w, q_rows).total <= 227 * 1024) ++stages;
     p.stages = stages;
     const size_t smem = mx4_layout(stages, BLOCK, p.tile_w, q_rows).total;
-    const cudaError_t e = limit.ensure(mx4_kernel<BLOCK>, smem);
+    auto kern = mx4_kernel<BLOCK, PAIR>;
+    const cudaError_t e = limit.ensure(kern, smem);
     if (e != cudaSuccess) return e;
-    const int grid = (int)std::min<int64_t>(num_sms, (int64_t)p.tiles_m * p.tiles_n);
-    return launch_ex(mx4_kernel<BLOCK>, dim3(grid), dim3(kMx4Threads), smem, s, dim3(1, 1, 1), p.pdl, m[0], m[1], m[2], m[3],
-                     p, q_rows);
+    const int64_t units = (int64_t)p.tiles_m * p.tiles_n;
+    const int grid = PAIR ? (int)std::min<int64_t>(num_sms & ~1, 2 * units) : (int)std::min<int64_t>(num_sms, units);
+    return launch_ex(kern, dim3(grid), dim3(kMx4Threads), smem, s, dim3(PAIR ? 2 : 1, 1, 1), p.pdl, m[0], m[1], m[2],
+                     m[3], p, q_rows);
 }
 
 bool codes_map(CUtensorMap *m, const dg_mx4 *q, int box_rows) {
@@ -152,17 +153,20 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     p.M = (int32_t)A->rows;
     p.N = (int32_t)B->rows;
     p.K = product ? (int32_t)A->K : 0;
-    p.tiles_n = (p.N + 127) / 128;
-    // 256 rows a tile where that leaves no SM without one
-    p.tile_w = p.M > 128 && (int64_t)p.tiles_n * ((p.M + 255) / 256) >= num_sms ? 256 : 128;
+    // 256 rows a tile where that leaves no SM without one, and then in pairs of CTAs
+    const bool pair = num_sms >= 2 && p.M > 128 &&
+                      (int64_t)((p.N + 255) / 256) * ((p.M + 255) / 256) * 2 >= num_sms;
+    p.tile_w = pair ? 256 : 128;
+    p.tiles_n = pair ? (p.N + 255) / 256 : (p.N + 127) / 128;
     p.tiles_m = (p.M + p.tile_w - 1) / p.tile_w;
+    const int q_rows = pair ? 128 : std::min(128, (p.M + 15) / 16 * 16);  // per CTA
     if ((int64_t)p.tiles_m * p.tiles_n > INT32_MAX / 2) return DG_ERR_UNSUPPORTED;
     p.k_tiles = (int32_t)scale_tiles(A->K, A->block);
     p.sa = static_cast<const uint8_t *>(A->scales);
     p.sb = static_cast<const uint8_t *>(B->scales);
     p.fa = product ? A->scale : nullptr;
     p.fb = product ? B->scale : nullptr;
-    p.idesc = 1u << 7 | 1u << 10 | (A->block == 32 ? 1u << 23 : 0u) | (128u >> 7) << 27;  // E2M1 twice, M = 128
+    p.idesc = 1u << 7 | 1u << 10 | (A->block == 32 ? 1u << 23 : 0u) | (pair ? 2u : 1u) << 27;  // E2M1 twice, M / 128
     p.out.c = static_cast<char *>(C->ptr);
     p.out.rs = ci.row.n ? ci.row.stride[0] : 0;
     p.out.cs = ci.col.n ? ci.col.stride[0] : ci.es;
@@ -178,11 +182,13 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     p.stall_loader = test_stall();
     p.pdl = early_launch_mode() != 0;
     CUtensorMap m[4] = {};
-    if (product && (!codes_map(&m[0], B, 128) || !codes_map(&m[1], A, std::min(p.tile_w, (p.M + 15) / 16 * 16)) ||
+    if (product && (!codes_map(&m[0], B, 128) || !codes_map(&m[1], A, q_rows) ||
                     !scales_map(&m[2], B, 1) || !scales_map(&m[3], A, p.tile_w / 128)))
         return DG_ERR_UNSUPPORTED;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = A->block == 32 ? launch_mx4<32>(p, m, num_sms, s) : launch_mx4<16>(p, m, num_sms, s);
+    const cudaError_t e =
+        A->block == 32 ? (pair ? launch_mx4<32, true>(p, m, q_rows, num_sms, s) : launch_mx4<32, false>(p, m, q_rows, num_sms, s))
+                       : (pair ? launch_mx4<16, true>(p, m, q_rows, num_sms, s) : launch_mx4<16, false>(p, m, q_rows, num_sms, s));
     if (e != cudaSuccess) return DG_ERR_CUDA;
     count_launch();
     return DG_OK;

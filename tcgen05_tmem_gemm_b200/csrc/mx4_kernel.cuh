@@ -1,9 +1,13 @@
 // C = A B^T of 4-bit floats with block scales: tcgen05.mma .block_scale,
 // scales in TMEM.
 //
-// A tile is 128 columns of C by up to 256 of its rows, computed as C^T: the
-// tensor core's M side (P) holds rows of B, its N side (Q) rows of A, so that
-// a single token costs an N of 16.  A stage of the ring is 256 k: 128 bytes of
+// A tile is 128 columns of C (256 for a pair of CTAs) by up to 256 of its rows,
+// computed as C^T: the tensor core's M side (P) holds rows of B, its N side (Q)
+// rows of A, so that a single token costs an N of 16.  In a pair (cta_group::2)
+// each CTA has its own 128 rows of P and half of Q's rows; what a stage copies
+// per product then falls from 48 to 32 KB per SM, which is what bounds large
+// products.  Q's scales are in both CTAs' TMEM, each copied from its own shared
+// memory by the same instruction.  A stage of the ring is 256 k: 128 bytes of
 // codes per row (tensor copies, 128-byte swizzle) and the scales' tiles as
 // they lie in memory (128 rows by 4 blocks, 512 bytes), which one tcgen05.cp
 // each spreads over the lanes of TMEM.  Every stage has scale columns of its
@@ -73,7 +77,44 @@ __host__ __device__ inline int mx4_scale_cols(int block, int tile_w) {
     return kMx4K / (4 * block) * (4 + 4 * ((tile_w + 127) / 128));
 }
 
-template <int BLOCK>
+template <int BLOCK, bool PAIR>
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+    if constexpr (!PAIR) {
+        umma_mx4<BLOCK>(d_tmem, a_desc, b_desc, idesc, sfa, sfb, accumulate);
+    } else if constexpr (BLOCK == 32) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else tmem_cp_scales(taddr, desc);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mx4_commit(uint32_t bar) {
+    if constexpr (PAIR) tc_commit_pair_mc(bar, 0x3);
+    else tc_commit(bar);
+}
+
+template <int BLOCK, bool PAIR>
 __global__ void __launch_bounds__(kMx4Threads, 1)
     mx4_kernel(const __grid_constant__ CUtensorMap tmap_p, const __grid_constant__ CUtensorMap tmap_q,
                const __grid_constant__ CUtensorMap tmap_sp, const __grid_constant__ CUtensorMap tmap_sq,
@@ -99,6 +140,9 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const WaitCtl wc{abort_flag, p.err_word, p.timeout_ns};
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
     const int units = p.tiles_m * p.tiles_n;
     const int buffers = p.tile_w <= 128 ? 2 : 1;  // accumulators
     const int q_tiles = (p.tile_w + 127) / 128;   // scale tiles along a tile's rows of C
@@ -110,7 +154,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, kTurnWarps);
+            mbar_init(bar_tempty + 8 * b, (PAIR ? 2 : 1) * kTurnWarps);  // in a pair the even CTA's counts both
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -118,11 +162,17 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         fence_proxy_async_smem();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), 512u);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(tmem_slot), 512u);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), 512u);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers exist before either signals the other's
     tc_fence_after();
     const uint32_t tmem_base = uniform(*tmem_slot);
     pdl_wait();  // what comes before touches this CTA's own memory only
@@ -131,7 +181,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
     auto tile_rows = [&](int u, int &m0, int &n0) {
         const int tn = u / p.tiles_m;
         m0 = (u - tn * p.tiles_m) * p.tile_w;
-        n0 = tn * 128;
+        n0 = tn * (PAIR ? 256 : 128);
         return min(p.tile_w, p.M - m0);
     };
 
@@ -142,23 +192,33 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         int it = 0, s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int u = first; ok && u < units; u += stride) {
             int m0, n0;
-            tile_rows(u, m0, n0);
+            const int rows = tile_rows(u, m0, n0), h = ((rows + 31) & ~31) / 2;  // a pair: Q's rows per CTA
+            n0 += (int)rank * 128;
             for (int k = 0; k < p.K; k += kMx4K, ++it) {
                 if (!warp_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
                     ok = false;
                     break;
                 }
                 if (!stall && elect_one()) {
-                    const uint32_t full = bar_full + 8 * s, ps = sbase + s * L.stage_bytes, qs = ps + L.p_bytes;
+                    const uint32_t full = PAIR ? dsmem_map(bar_full + 8 * s, 0) : bar_full + 8 * s;
+                    const uint32_t ps = sbase + s * L.stage_bytes, qs = ps + L.p_bytes;
                     const uint32_t sp = qs + L.q_bytes, sq = sp + L.sp_bytes;
                     const int t0 = k / (4 * BLOCK);
-                    mbar_arrive_expect_tx(full, L.p_bytes + L.q_bytes + L.sp_bytes + L.sq_bytes);
-                    tma_load_2d(ps, &tmap_p, full, k / 2, n0);
-                    tma_load_2d(qs, &tmap_q, full, k / 2, m0);
-                    tma_load_3d(sp, &tmap_sp, full, 0, t0, n0 / 128);
-                    tma_load_3d(sq, &tmap_sq, full, 0, t0, m0 / 128);
+                    const uint32_t bytes = L.p_bytes + L.q_bytes + L.sp_bytes + L.sq_bytes;
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * s, PAIR ? 2u * bytes : bytes);
+                    if (PAIR) {
+                        tma_load_2d_pair(ps, &tmap_p, full, k / 2, n0);
+                        tma_load_2d_pair(qs, &tmap_q, full, k / 2, m0 + (int)rank * h);
+                        tma_load_3d_pair(sp, &tmap_sp, full, 0, t0, n0 / 128);
+                        tma_load_3d_pair(sq, &tmap_sq, full, 0, t0, m0 / 128);
+                    } else {
+                        tma_load_2d(ps, &tmap_p, full, k / 2, n0);
+                        tma_load_2d(qs, &tmap_q, full, k / 2, m0);
+                        tma_load_3d(sp, &tmap_sp, full, 0, t0, n0 / 128);
+                        tma_load_3d(sq, &tmap_sq, full, 0, t0, m0 / 128);
+                    }
                 }
                 if (++s == stages) {
                     s = 0;
@@ -166,13 +226,16 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 }
             }
         }
-        if (!stall)
+        if (!leader) pdl_release();
+        // full[] of a pair's even CTA counts both CTAs' bytes
+        if (leader && !stall)
             for (int d = 1; d <= stages && it - d >= 0; ++d) {
                 const int j = it - d;
                 mbar_wait_drain(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u, p.timeout_ns);
             }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer
+        if (leader) {
         const int stages = p.stages;
         const uint32_t scale_cols = (uint32_t)mx4_scale_cols(BLOCK, p.tile_w);
         const uint64_t da0 = make_sw128_desc(sbase, 16u, 1024);
@@ -181,9 +244,9 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         int local = 0, s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && p.K > 0 && u < units; u += gridDim.x, ++local) {
+        for (int u = first; ok && p.K > 0 && u < units; u += stride, ++local) {
             int m0, n0;
-            const int rows = tile_rows(u, m0, n0), w = (rows + 15) & ~15;
+            const int rows = tile_rows(u, m0, n0), w = PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15;
             const bool two = rows > 128;  // tiles of Q's scales
             const uint32_t idesc = p.idesc | (uint32_t)(w >> 3) << 17;
             const int b = buffers == 2 ? local & 1 : 0, turn = buffers == 2 ? local >> 1 : local;
@@ -205,9 +268,9 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                         if (t * 4 * BLOCK >= left) continue;
                         const uint64_t ds = ds0 + soff + (uint64_t)((t * kScaleTile) >> 4);
                         const uint32_t to = sfb + (uint32_t)(4 * t * q_tiles);
-                        tmem_cp_scales(sfa + 4u * t, ds);
-                        tmem_cp_scales(to, ds + (uint64_t)((T * kScaleTile) >> 4));
-                        if (two) tmem_cp_scales(to + 4u, ds + (uint64_t)((2 * T * kScaleTile) >> 4));
+                        cp_scales<PAIR>(sfa + 4u * t, ds);
+                        cp_scales<PAIR>(to, ds + (uint64_t)((T * kScaleTile) >> 4));
+                        if (two) cp_scales<PAIR>(to + 4u, ds + (uint64_t)((2 * T * kScaleTile) >> 4));
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {  // 64 k each
@@ -216,10 +279,10 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                         const int t = BLOCK == 16 ? kk : kk >> 1;
                         const uint32_t id = BLOCK == 16 ? 0u : 2u * (uint32_t)(kk & 1);
                         const uint64_t off = soff + (uint64_t)((kk * 32) >> 4);
-                        umma_mx4<BLOCK>(d_tmem, da0 + off, db0 + off, idesc | id << 4 | id << 29, sfa + 4u * t,
-                                        sfb + (uint32_t)(4 * t * q_tiles), k > 0 || kk > 0 ? 1u : 0u);
+                        mma_mx4<BLOCK, PAIR>(d_tmem, da0 + off, db0 + off, idesc | id << 4 | id << 29, sfa + 4u * t,
+                                             sfb + (uint32_t)(4 * t * q_tiles), k > 0 || kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(bar_empty + 8 * s);
+                    mx4_commit<PAIR>(bar_empty + 8 * s);
                 }
                 if (++s == stages) {
                     s = 0;
@@ -227,11 +290,15 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 }
             }
             if (!ok) break;
-            if (elect_one()) tc_commit(bar_tfull + 8 * b);
+            if (elect_one()) mx4_commit<PAIR>(bar_tfull + 8 * b);
         }
         pdl_release();
-        if (elect_one()) tc_commit(bar_drain);
+        if (elect_one()) {
+            if (PAIR) tc_commit_pair_mc(bar_drain, 0x1);
+            else tc_commit(bar_drain);
+        }
         mbar_wait_drain(bar_drain, 0, p.timeout_ns);
+        }
     } else {
         // ------------------------------------------------------ epilogue
         const int quarter = warp & 3, half = warp >= 6 ? 1 : 0;  // the two warps of a quarter take turns
@@ -240,7 +307,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
         if (p.fa != nullptr) o.alpha *= *p.fa;
         if (p.fb != nullptr) o.alpha *= *p.fb;
         int local = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++local) {
+        for (int u = first; u < units; u += stride, ++local) {
             int m0, n0;
             const int rows = tile_rows(u, m0, n0);
             const int b = buffers == 2 ? local & 1 : 0, turn = buffers == 2 ? local >> 1 : local;
@@ -248,23 +315,27 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)turn & 1u, wc)) break;
                 tc_fence_after();
             }
-            turned_rows(o, turn_at, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 128), p.K == 0, m0,
-                        rows, n0 + quarter * 32, lane, half, 2);
-            if (p.K > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_tempty + 8 * b);
-            }
+            turned_rows<false>(o, turn_at, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 128), p.K == 0, m0,
+                        rows, n0 + (int)rank * 128 + quarter * 32, lane, half, [&] {
+                            if (p.K == 0) return;
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane != 0) return;
+                            if (PAIR) mbar_arrive_tmem(dsmem_map(bar_tempty + 8 * b, 0));
+                            else mbar_arrive(bar_tempty + 8 * b);
+                        });
         }
     }
 
     // ---------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // neither CTA frees TMEM or exits while the pair still uses it
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, 512u);
+        if (PAIR) tmem_dealloc_pair(tmem_base, 512u);
+        else tmem_dealloc(tmem_base, 512u);
     }
 }
 

@@ -55,11 +55,16 @@ __device__ __forceinline__ void stmatrix_turned(uint32_t addr, uint32_t a, uint3
                  : "memory");
 }
 
-// Blocks c0 = 32 first, 32 (first + step), ... of a tile: 16-bit C, beta = 0,
-// columns n0 .. n0 + 31 all inside C.
-template <int CD, bool FUSED, int ACT>
-__device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage, uint32_t taddr, int64_t r0, int rows,
-                                              int n0, int lane, int first, int step) {
+constexpr int kTurnBlocks = 4;  // a warp's blocks of 32 rows: every other one of a tile of 256
+using TurnedWords = uint32_t[kTurnBlocks][4][4];
+
+// Blocks c0 = 32 half, 32 (half + 2), ... of a tile, 16-bit C, beta = 0, columns
+// n0 .. n0 + 31 all inside C: read, scaled and packed into registers.
+// SR: with a scale per row (a template argument: its registers would spill where
+// no call has them).
+template <bool SR, bool B16, bool FUSED, int ACT>
+__device__ __forceinline__ void turned_read(TurnedWords &w, const TurnedOut &o, uint32_t taddr, int64_t r0, int rows,
+                                            int n0, int lane, int half) {
     const int col = 2 * (lane & 3), sub = lane >> 2;
     float an[4], bn[4];
 #pragma unroll
@@ -67,48 +72,56 @@ __device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage
         an[q] = o.alpha * (o.scale_n != nullptr ? o.scale_n[n0 + 8 * q + sub] : 1.f);
         bn[q] = FUSED && o.bias_n != nullptr ? o.bias_n[n0 + 8 * q + sub] : 0.f;
     }
-    // unit u of row r lies at unit u ^ (r / 2 % 4): neither side has bank conflicts
-    const uint32_t put = stage + (uint32_t)lane * 64u, swz = (uint32_t)(lane >> 1) & 3u;
-    if (32 * first >= rows) return;
-    uint32_t r[2][16];
-    __syncwarp();
-    tmem_ld_frag(taddr + 32u * first, r[0]);
-    tmem_ld_frag(taddr + (16u << 16) + 32u * first, r[1]);
-    char *at = o.c + (r0 + 32 * first + sub) * o.rs + (int64_t)n0 * 2 + (lane & 3) * 16;
-    const int64_t eight = 8 * o.rs, ahead = (int64_t)(32 * step - 32) * o.rs;
-#pragma unroll 1
-    for (int c0 = 32 * first; c0 < rows; c0 += 32 * step) {
-        tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < kTurnBlocks; ++k) {
+        const int c0 = 32 * half + 64 * k;
+        if (c0 >= rows) continue;
         float sr[8];
-        if (o.scale_r != nullptr) {
+        if (SR) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)  // rows past the last are not stored: any row's scale will do
                 sr[j] = o.scale_r[r0 + min(c0 + 8 * (j >> 1) + col + (j & 1), rows - 1)];
         }
-        uint32_t w[4][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // n 8 q .. 8 q + 7
+        for (int h = 0; h < 2; ++h) {  // 16 lanes at a time: 32 more registers would spill
+            uint32_t r[16];
+            __syncwarp();
+            tmem_ld_frag(taddr + ((uint32_t)h << 20) + (uint32_t)c0, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v[2];
+            for (int q = 2 * h; q < 2 * h + 2; ++q) {  // n 8 q .. 8 q + 7
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float a = o.scale_r != nullptr ? an[q] * sr[2 * j + i] : an[q];
-                    v[i] = a * __uint_as_float(r[q >> 1][4 * j + 2 * (q & 1) + i]);
-                    if (FUSED) v[i] = act_fn<ACT, true>(v[i] + bn[q]);
+                for (int j = 0; j < 4; ++j) {
+                    float v[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = SR ? an[q] * sr[2 * j + i] : an[q];
+                        v[i] = a * __uint_as_float(r[4 * j + 2 * (q & 1) + i]);
+                        if (FUSED) v[i] = act_fn<ACT, true>(v[i] + bn[q]);
+                    }
+                    w[k][q][j] = pack2<B16>(v[0], v[1]);
                 }
-                w[q][j] = pack2<CD == DG_BF16>(v[0], v[1]);
             }
         }
-        if (c0 + 32 * step < rows) {  // the next block's, beside the rest of this one
-            __syncwarp();
-            tmem_ld_frag(taddr + (uint32_t)(c0 + 32 * step), r[0]);
-            tmem_ld_frag(taddr + (16u << 16) + (uint32_t)(c0 + 32 * step), r[1]);
-        }
+    }
+}
+
+// And turned on their way to C.
+__device__ __forceinline__ void turned_write(const TurnedWords &w, const TurnedOut &o, uint32_t stage, int64_t r0, int rows,
+                                             int n0, int lane, int half) {
+    // unit u of row r lies at unit u ^ (r / 2 % 4): neither side has bank conflicts
+    const int sub = lane >> 2;
+    const uint32_t put = stage + (uint32_t)lane * 64u, swz = (uint32_t)(lane >> 1) & 3u;
+    char *at = o.c + (r0 + 32 * half + sub) * o.rs + (int64_t)n0 * 2 + (lane & 3) * 16;
+    const int64_t eight = 8 * o.rs;
+#pragma unroll
+    for (int k = 0; k < kTurnBlocks; ++k) {
+        const int c0 = 32 * half + 64 * k;
+        if (c0 >= rows) continue;
         __syncwarp();  // the last block has left the staging block
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            stmatrix_turned(put + ((uint32_t)q ^ swz) * 16u, w[q][0], w[q][1], w[q][2], w[q][3]);
+            stmatrix_turned(put + ((uint32_t)q ^ swz) * 16u, w[k][q][0], w[k][q][1], w[k][q][2], w[k][q][3]);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i, at += eight) {
@@ -116,20 +129,20 @@ __device__ __forceinline__ void turned_fast16(const TurnedOut &o, uint32_t stage
             const float4 t = ld_shared_v4(stage + (uint32_t)row * 64u + (((uint32_t)lane ^ (uint32_t)(row >> 1)) & 3u) * 16u);
             if (c0 + row < rows) *reinterpret_cast<float4 *>(at) = t;
         }
-        at += ahead;
+        at += 4 * eight;
     }
 }
 
 // The same for any C: a thread holds column n0 + lane and 32 rows.
 template <int CD, bool FUSED, int ACT>
 __device__ __forceinline__ void turned_any(const TurnedOut &o, uint32_t taddr, bool empty, int64_t r0, int rows, int n0,
-                                           int lane, int first, int step) {
+                                           int lane, int half) {
     const int n = n0 + lane;
     const bool n_ok = n < o.N;
     const float an = o.alpha * (o.scale_n != nullptr && n_ok ? o.scale_n[n] : 1.f);
     const float bn = FUSED && o.bias_n != nullptr && n_ok ? o.bias_n[n] : 0.f;
 #pragma unroll 1
-    for (int c0 = 32 * first; c0 < rows; c0 += 32 * step) {
+    for (int c0 = 32 * half; c0 < rows; c0 += 64) {
         const int some = min(32, rows - c0);
         uint32_t r[32];
         if (empty) {
@@ -175,36 +188,48 @@ __device__ __forceinline__ void turned_any(const TurnedOut &o, uint32_t taddr, b
     }
 }
 
-template <bool FUSED, int ACT>
-__device__ __forceinline__ void turned_rows_d(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty, int64_t r0,
-                                              int rows, int n0, int lane, int first, int step) {
-    if (o.dtype == DG_F32) {
-        turned_any<DG_F32, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
-    } else if (o.vec && o.beta == 0.f && n0 + 32 <= o.N && !empty) {
-        if (o.dtype == DG_BF16)
-            turned_fast16<DG_BF16, FUSED, ACT>(o, stage, taddr, r0, rows, n0, lane, first, step);
-        else turned_fast16<DG_F16, FUSED, ACT>(o, stage, taddr, r0, rows, n0, lane, first, step);
-    } else if (o.dtype == DG_BF16) {
-        turned_any<DG_BF16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
-    } else {
-        turned_any<DG_F16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, first, step);
-    }
+template <bool SR, bool FUSED, int ACT>
+__device__ __forceinline__ void turned_read_d(TurnedWords &w, const TurnedOut &o, uint32_t taddr, int64_t r0, int rows,
+                                              int n0, int lane, int half) {
+    if (o.dtype == DG_BF16) turned_read<SR, true, FUSED, ACT>(w, o, taddr, r0, rows, n0, lane, half);
+    else turned_read<SR, false, FUSED, ACT>(w, o, taddr, r0, rows, n0, lane, half);
 }
 
-// Rows [r0, r0 + rows) of C, whose accumulators are the TMEM columns from
-// `taddr` (lane quarter included) on, and columns n0 .. n0 + 31: the blocks of
-// 32 rows first, first + step, ...  `empty`: the sums are zero and TMEM is not
-// read.  r0 indexes scale_r and C's rows.  stage: kTurnBytes of the warp's own.
+template <bool FUSED, int ACT>
+__device__ __forceinline__ void turned_any_d(const TurnedOut &o, uint32_t taddr, bool empty, int64_t r0, int rows, int n0,
+                                             int lane, int half) {
+    if (o.dtype == DG_F32) turned_any<DG_F32, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, half);
+    else if (o.dtype == DG_BF16) turned_any<DG_BF16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, half);
+    else turned_any<DG_F16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, half);
+}
+
+// Rows [r0, r0 + rows) of C (256 at most), whose accumulators are the TMEM
+// columns from `taddr` (lane quarter included) on, and columns n0 .. n0 + 31:
+// every other block of 32 rows, from block `half` on.  `empty`: the sums are zero
+// and TMEM is not read.  r0 indexes scale_r and C's rows.  stage: kTurnBytes of
+// the warp's own.  release() is called once, by the whole warp, when the warp has
+// done with TMEM.  SR: scales per row take the fast way too.
+template <bool SR, typename Release>
 __device__ __forceinline__ void turned_rows(const TurnedOut &o, uint32_t stage, uint32_t taddr, bool empty, int64_t r0,
-                                            int rows, int n0, int lane, int first, int step) {
-    if (n0 >= o.N) return;
-    if (o.act == DG_ACT_GELU_TANH)
-        turned_rows_d<true, DG_ACT_GELU_TANH>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
-    else if (o.act == DG_ACT_RELU)
-        turned_rows_d<true, DG_ACT_RELU>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
-    else if (o.bias_n != nullptr)
-        turned_rows_d<true, DG_ACT_NONE>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
-    else turned_rows_d<false, DG_ACT_NONE>(o, stage, taddr, empty, r0, rows, n0, lane, first, step);
+                                            int rows, int n0, int lane, int half, Release release) {
+    const bool fused = o.bias_n != nullptr;
+    if (n0 >= o.N) {
+        release();
+    } else if (o.dtype != DG_F32 && o.vec && o.beta == 0.f && n0 + 32 <= o.N && !empty && SR == (o.scale_r != nullptr)) {
+        TurnedWords w;
+        if (o.act == DG_ACT_GELU_TANH) turned_read_d<SR, true, DG_ACT_GELU_TANH>(w, o, taddr, r0, rows, n0, lane, half);
+        else if (o.act == DG_ACT_RELU) turned_read_d<SR, true, DG_ACT_RELU>(w, o, taddr, r0, rows, n0, lane, half);
+        else if (fused) turned_read_d<SR, true, DG_ACT_NONE>(w, o, taddr, r0, rows, n0, lane, half);
+        else turned_read_d<SR, false, DG_ACT_NONE>(w, o, taddr, r0, rows, n0, lane, half);
+        release();
+        turned_write(w, o, stage, r0, rows, n0, lane, half);
+    } else {
+        if (o.act == DG_ACT_GELU_TANH) turned_any_d<true, DG_ACT_GELU_TANH>(o, taddr, empty, r0, rows, n0, lane, half);
+        else if (o.act == DG_ACT_RELU) turned_any_d<true, DG_ACT_RELU>(o, taddr, empty, r0, rows, n0, lane, half);
+        else if (fused) turned_any_d<true, DG_ACT_NONE>(o, taddr, empty, r0, rows, n0, lane, half);
+        else turned_any_d<false, DG_ACT_NONE>(o, taddr, empty, r0, rows, n0, lane, half);
+        release();
+    }
 }
 
 }  // namespace dg
