@@ -71,9 +71,9 @@ typedef enum {
                                C has two elements at one address                 */
     DG_ERR_ALIGN = 6,       /* pointer or stride not a multiple of the element    */
     DG_ERR_POINTER = 7,     /* pointer is not device-accessible                   */
-    DG_ERR_VALUE = 8,       /* alpha or beta not finite; a bad activation, group or
-                               reserved field; a target out of range (reported by
-                               dg_sync_status)                                   */
+    DG_ERR_VALUE = 8,       /* alpha or beta not finite; a bad activation, group, block
+                               or reserved field; a target or offsets out of range
+                               (reported by dg_sync_status)                      */
     DG_ERR_UNSUPPORTED = 9, /* valid request this build does not implement        */
     DG_ERR_CUDA = 10,       /* a CUDA runtime call failed                          */
     DG_ERR_TIMEOUT = 11     /* a device-side wait gave up (see dg_sync_status)    */
@@ -363,7 +363,10 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W,
  * scale_a device float32[R], scale_b and the epilogue's bias device
  * float32[groups * N], each or NULL.
  * alpha == 0 or K == 0 reads neither A nor B; beta == 0 does not read C.
- * Errors: as dg_gemm_ex; DG_ERR_NDIM for a B that is not [groups, K, N] with
+ * 16-bit C of contiguous columns and rows at multiples of 16 bytes, and F32 C,
+ * are stored fastest, and with beta == 0.
+ * Errors: as dg_gemm_ex; DG_ERR_ALIGN for a scale or bias off multiples of 4;
+ * DG_ERR_NDIM for a B that is not [groups, K, N] with
  * row_dims 2; DG_ERR_UNSUPPORTED for more than 1024 groups or a size of 2^31 -
  * 2^13 and more.
  */
@@ -456,7 +459,9 @@ dg_status dg_dequantize_mx4(const dg_mx4 *q, const dg_view *y, void *stream);
  * (or column) of C NaN.  C's rows and columns are one dim each, of any stride.
  * alpha == 0 or K == 0 reads neither A nor B.
  * Errors: as dg_gemm_ex; DG_ERR_VALUE for different blocks; DG_ERR_ALIGN for
- * codes whose rows do not start at multiples of 16 bytes.
+ * codes whose rows do not start at multiples of 16 bytes; DG_ERR_UNSUPPORTED for
+ * rows that share their codes (a stride of 0) and for a C of several row or
+ * column dims.
  */
 dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C,
                       float alpha, float beta, const dg_epilogue *epilogue,
@@ -469,7 +474,7 @@ const char *dg_status_string(dg_status s);
  * dg_sync_status — synchronise `stream`, then return and clear the device
  * error word of the current device: DG_ERR_TIMEOUT if a kernel's bounded wait
  * gave up since the last check (its output is then undefined), DG_ERR_VALUE if
- * a target of dg_linear_ce was out of range, DG_ERR_CUDA if the
+ * a target of dg_linear_ce or a group's offsets were out of range, DG_ERR_CUDA if the
  * synchronisation failed, DG_OK otherwise.
  */
 dg_status dg_sync_status(void *stream);

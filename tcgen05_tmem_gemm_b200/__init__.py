@@ -622,16 +622,17 @@ def _groups(offsets, stack) -> int:
 def gemm_grouped(a, b, c, offsets, scale_a=None, scale_b=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
                  act="none", stream=None):
     """dg_gemm_grouped on torch tensors: c[r] = act(alpha * scale_a[r] * scale_b[g] * (a[r] b[g]) + beta * c[r] +
-    bias[g]) for the rows r of each group g, offsets[g] <= r < offsets[g + 1].  a is [R, K], b [groups, K, N] (a
-    [groups, N, K] weight is passed as weight.transpose(1, 2)), c [R, N], offsets int64 [groups + 1] on the device;
-    scale_a float32 [R], scale_b and bias float32 [groups, N].  Raises DgError on a bad status; returns c."""
+    bias[g]) for the rows r of each group g, offsets[g] <= r < offsets[g + 1].  a is [..., K] (R rows in all), b
+    [groups, K, N] (a [groups, N, K] weight is passed as weight.transpose(1, 2)), c [..., N], offsets int64
+    [groups + 1] on the device; scale_a float32 [R], scale_b and bias float32 [groups, N].  Raises DgError on a bad
+    status; returns c."""
     groups = _groups(offsets, b)
     if scale_a is not None:
-        _vector(scale_a, "scale_a", _torch.float32, a.shape[0])
+        _vector(scale_a, "scale_a", _torch.float32, a.shape[:-1].numel())
     for name, t in (("scale_b", scale_b), ("bias", bias)):
         if t is not None:
             _vector(t, name, _torch.float32, groups * b.shape[2])
-    av, bv, cv = view(a), view(b, 2), view(c)
+    av, bv, cv = view(a, a.dim() - 1), view(b, 2), view(c, c.dim() - 1)
     epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
     st = lib.dg_gemm_grouped(ctypes.byref(av), ctypes.byref(bv), ctypes.byref(cv), offsets.data_ptr(), groups, alpha,
                              beta, _ptr(scale_a), _ptr(scale_b), epi, _stream_ptr(stream))
@@ -642,10 +643,10 @@ def gemm_grouped(a, b, c, offsets, scale_a=None, scale_b=None, alpha: float = 1.
 
 def gemm_grouped_dw(x, dy, dw, offsets, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """dg_gemm_grouped_dw on torch tensors: dw[g] = alpha * x^T dy over the rows of group g + beta * dw[g].  x is
-    [R, K], dy [R, N], dw [groups, K, N] (that of a [groups, N, K] weight is passed as dweight.transpose(1, 2)).
+    [..., K], dy [..., N], dw [groups, K, N] (that of a [groups, N, K] weight is passed as dweight.transpose(1, 2)).
     Raises DgError on a bad status; returns dw."""
     groups = _groups(offsets, dw)
-    xv, dyv, dwv = view(x), view(dy), view(dw, 2)
+    xv, dyv, dwv = view(x, x.dim() - 1), view(dy, dy.dim() - 1), view(dw, 2)
     st = lib.dg_gemm_grouped_dw(ctypes.byref(xv), ctypes.byref(dyv), ctypes.byref(dwv), offsets.data_ptr(), groups,
                                 alpha, beta, _stream_ptr(stream))
     if st != DG_OK:
@@ -680,9 +681,9 @@ def mx4(codes, scales, K: int | None = None, block: int = 32, scale=None) -> dg_
 
 
 def quantize_mx4(x, codes, scales, block: int = 32, scale=None, stream=None):
-    """dg_quantize_mx4 on torch tensors: the codes and block scales (see mx4) of x [rows, K] / scale, written in
+    """dg_quantize_mx4 on torch tensors: the codes and block scales (see mx4) of x [..., K] / scale, written in
     place.  Raises DgError on a bad status; returns (codes, scales)."""
-    xv, q = view(x), mx4(codes, scales, x.shape[-1], block, scale)
+    xv, q = view(x, x.dim() - 1), mx4(codes, scales, x.shape[-1], block, scale)
     st = lib.dg_quantize_mx4(ctypes.byref(xv), ctypes.byref(q), _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_quantize_mx4")
@@ -690,9 +691,9 @@ def quantize_mx4(x, codes, scales, block: int = 32, scale=None, stream=None):
 
 
 def dequantize_mx4(codes, scales, y, block: int = 32, scale=None, stream=None):
-    """dg_dequantize_mx4 on torch tensors: y [rows, K] = the values of codes and scales (see mx4).  Raises DgError on
+    """dg_dequantize_mx4 on torch tensors: y [..., K] = the values of codes and scales (see mx4).  Raises DgError on
     a bad status; returns y."""
-    yv, q = view(y), mx4(codes, scales, y.shape[-1], block, scale)
+    yv, q = view(y, y.dim() - 1), mx4(codes, scales, y.shape[-1], block, scale)
     st = lib.dg_dequantize_mx4(ctypes.byref(q), ctypes.byref(yv), _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_dequantize_mx4")

@@ -372,6 +372,8 @@ dg_status dg_gemm_grouped(const dg_view *A, const dg_view *B, const dg_view *C, 
     if (!in_type(A->dtype) || A->dtype != B->dtype || C->dtype == DG_E4M3) return DG_ERR_DTYPE;
     if (!std::isfinite(alpha) || !std::isfinite(beta)) return DG_ERR_VALUE;
     if ((st = offsets_ok(offsets, groups)) != DG_OK) return st;
+    for (const float *f : {scale_a, scale_b, epilogue ? epilogue->bias : nullptr})
+        if (reinterpret_cast<uintptr_t>(f) % 4) return DG_ERR_ALIGN;
     c.a = A;
     c.b = B;
     c.c = C;

@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(128) quantize_any_kernel(const QuantParams p) 
     const Factor f(p.q.scale);
     const char *x = p.x.ptr + axis_offset(p.x.row, row);
     uint8_t *scales_row = p.q.scales + row / 128 * p.q.k_tiles * 512 + row % 32 * 16 + row % 128 / 32 * 4;
-    for (int k0 = (int)blockIdx.y * kTurnK; k0 < K; k0 += (int)gridDim.y * kTurnK) {
+    for (int64_t k64 = (int64_t)blockIdx.y * kTurnK; k64 < K; k64 += (int64_t)gridDim.y * kTurnK) {
+        const int k0 = (int)k64;
         const int n = K - k0;
         Lot<DT> v;
         auto put = [&](int i, const char *at) {
@@ -581,7 +582,8 @@ __global__ void __launch_bounds__(128) dequantize_any_kernel(const QuantParams p
     char *y = const_cast<char *>(p.x.ptr) + axis_offset(p.x.row, row);
     const uint8_t *codes = p.q.codes + row * p.q.code_stride;
     const uint8_t *scales_row = p.q.scales + row / 128 * p.q.k_tiles * 512 + row % 32 * 16 + row % 128 / 32 * 4;
-    for (int k0 = (int)blockIdx.y * kTurnK; k0 < K; k0 += (int)gridDim.y * kTurnK) {
+    for (int64_t k64 = (int64_t)blockIdx.y * kTurnK; k64 < K; k64 += (int64_t)gridDim.y * kTurnK) {
+        const int k0 = (int)k64;
         uint32_t e[kTurnK / 8];
 #pragma unroll
         for (int j = 0; j < kTurnK / 8; ++j)
