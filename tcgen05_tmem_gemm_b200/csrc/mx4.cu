@@ -81,8 +81,9 @@ cudaError_t launch_mx4(Mx4Params p, const CUtensorMap (&m)[4], int q_rows, int n
     const cudaError_t e = limit.ensure(kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)p.tiles_m * p.tiles_n;
-    const int grid = PAIR ? (int)std::min<int64_t>(num_sms & ~1, 2 * units) : (int)std::min<int64_t>(num_sms, units);
-    return launch_ex(kern, dim3(grid), dim3(kMx4Threads), smem, s, dim3(PAIR ? 2 : 1, 1, 1), p.pdl, m[0], m[1], m[2],
+    const int grid = PAIR ? (int)std::min<int64_t>(num_sms & ~1, 2 * units)
+                          : (int)std::min<int64_t>(num_sms, units) * p.split;
+    return launch_ex(kern, dim3(grid), dim3(kMx4Threads), smem, s, dim3(PAIR ? 2 : p.split, 1, 1), p.pdl, m[0], m[1], m[2],
                      m[3], p, q_rows);
 }
 
@@ -161,6 +162,25 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     p.tiles_m = (p.M + p.tile_w - 1) / p.tile_w;
     const int q_rows = pair ? 128 : std::min(128, (p.M + 15) / 16 * 16);  // per CTA
     if ((int64_t)p.tiles_m * p.tiles_n > INT32_MAX / 2) return DG_ERR_UNSUPPORTED;
+    // Few tiles: k over a cluster of f CTAs.  In microseconds, a stage costs 0.33 and the exchange 0.7 and
+    // a tile's rows times (0.02 + 0.09 / f); clusters of eight do not fill every group of SMs.  (B200, f = 1
+    // and the chosen one: 8x4096x14336 19.2 -> 10.1, 1x512x2048 4.6 -> 3.6, 128x1024x16384 25.1 -> 9.8;
+    // 128x4096x4096 stays at one, 8.6 against 10.3.)
+    const int steps = (p.K + kMx4K - 1) / kMx4K;
+    p.split = 1;
+    double least = 0.33 * steps;
+    if (!pair)
+        for (int f = 2; f <= 8; f *= 2) {
+            const int per = (steps + f - 1) / f;
+            const double room = (f == 8 ? 0.7 : 0.9) * num_sms;
+            if ((double)p.tiles_m * p.tiles_n * f > room || (f - 1) * per >= steps) break;
+            const double cost = 0.33 * per + 0.7 + std::min(p.M, 128) * (0.02 + 0.09 / f);
+            if (cost < least) {
+                least = cost;
+                p.split = f;
+            }
+        }
+    p.k_split = (steps + p.split - 1) / p.split * kMx4K;
     p.k_tiles = (int32_t)scale_tiles(A->K, A->block);
     p.sa = static_cast<const uint8_t *>(A->scales);
     p.sb = static_cast<const uint8_t *>(B->scales);

@@ -12,6 +12,10 @@
 // they lie in memory (128 rows by 4 blocks, 512 bytes), which one tcgen05.cp
 // each spreads over the lanes of TMEM.  Every stage has scale columns of its
 // own in TMEM, so a stage's release (its MMAs done) also frees its scales.
+//
+// Few tiles and a long k: the CTAs of a cluster take a part of k each, leave
+// their sums in their rings, and every CTA adds its share of the tile's rows, in
+// rank order, from all of them through distributed shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -25,6 +29,8 @@ struct Mx4Params {
     int32_t tile_w;          // rows of C per tile: 128 or 256 (fewer in the last)
     int32_t tiles_m, tiles_n;
     int32_t stages;
+    int32_t split;           // CTAs of a cluster that share a tile's k (not in pairs; each has one tile)
+    int32_t k_split;         // k per such CTA, a multiple of a stage's
     int32_t k_tiles;         // tiles of scales along k
     const uint8_t *sa, *sb;  // scales of A and of B
     const float *fa, *fb;    // their tensors' factors, or null
@@ -142,7 +148,11 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
     const WaitCtl wc{abort_flag, p.err_word, p.timeout_ns};
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
-    const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const int split = PAIR ? 1 : p.split;
+    const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x / split;
+    const int stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x / split;
+    const int part = split > 1 ? (int)cluster_ctarank() : 0;
+    const int kb = part * p.k_split, ke = split > 1 ? min(p.K, kb + p.k_split) : p.K;  // this CTA's k
     const int units = p.tiles_m * p.tiles_n;
     const int buffers = p.tile_w <= 128 ? 2 : 1;  // accumulators
     const int q_tiles = (p.tile_w + 127) / 128;   // scale tiles along a tile's rows of C
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
             int m0, n0;
             const int rows = tile_rows(u, m0, n0), h = ((rows + 31) & ~31) / 2;  // a pair: Q's rows per CTA
             n0 += (int)rank * 128;
-            for (int k = 0; k < p.K; k += kMx4K, ++it) {
+            for (int k = kb; k < ke; k += kMx4K, ++it) {
                 if (!warp_wait(bar_empty + 8 * s, ph ^ 1u, wc)) {
                     ok = false;
                     break;
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
             if (!warp_wait(bar_tempty + 8 * b, ((uint32_t)turn & 1u) ^ 1u, wc)) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(b * 128);
-            for (int k = 0; k < p.K; k += kMx4K) {
+            for (int k = kb; k < ke; k += kMx4K) {
                 if (!warp_wait(bar_full + 8 * s, ph, wc)) {
                     ok = false;
                     break;
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 tc_fence_after();
                 const uint64_t soff = (uint64_t)((s * L.stage_bytes) >> 4);
                 const uint32_t sfa = tmem_base + 256u + (uint32_t)s * scale_cols, sfb = sfa + 4u * T;
-                const int left = p.K - k;
+                const int left = ke - k;
                 if (elect_one()) {
 #pragma unroll
                     for (int t = 0; t < T; ++t) {
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                         const uint32_t id = BLOCK == 16 ? 0u : 2u * (uint32_t)(kk & 1);
                         const uint64_t off = soff + (uint64_t)((kk * 32) >> 4);
                         mma_mx4<BLOCK, PAIR>(d_tmem, da0 + off, db0 + off, idesc | id << 4 | id << 29, sfa + 4u * t,
-                                             sfb + (uint32_t)(4 * t * q_tiles), k > 0 || kk > 0 ? 1u : 0u);
+                                             sfb + (uint32_t)(4 * t * q_tiles), k > kb || kk > 0 ? 1u : 0u);
                     }
                     mx4_commit<PAIR>(bar_empty + 8 * s);
                 }
@@ -315,8 +325,23 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
                 if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)turn & 1u, wc)) break;
                 tc_fence_after();
             }
-            turned_rows<false>(o, turn_at, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 128), p.K == 0, m0,
-                        rows, n0 + (int)rank * 128 + quarter * 32, lane, half, [&] {
+            const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * 128);
+            if (split > 1) {  // [row][128 columns] of sums, over the idle ring
+                for (int c0 = 32 * half; c0 < rows; c0 += 64) {
+                    uint32_t r[32];
+                    __syncwarp();
+                    tmem_ld16(lanes + (uint32_t)c0, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                    tmem_ld16(lanes + (uint32_t)c0 + 16u, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (c0 + c < rows)
+                            st_shared_f32(sbase + (uint32_t)(c0 + c) * 512u + (uint32_t)(quarter * 32 + lane) * 4u,
+                                          __uint_as_float(r[c]));
+                }
+                continue;
+            }
+            turned_rows<false>(o, turn_at, lanes, p.K == 0, m0, rows, n0 + (int)rank * 128 + quarter * 32, lane, half, [&] {
                             if (p.K == 0) return;
                             tc_fence_before();
                             __syncwarp();
@@ -328,6 +353,29 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
     }
 
     // ---------------------------------------------------------- teardown
+    if (!PAIR && split > 1) {
+        __syncwarp();
+        cluster_sync();  // every part's sums are there
+        int m0, n0;
+        const int rows = tile_rows(first, m0, n0);
+        TurnedOut o = p.out;
+        if (p.fa != nullptr) o.alpha *= *p.fa;
+        if (p.fb != nullptr) o.alpha *= *p.fb;
+        // a warp takes 32 columns of a row at a time
+        for (int i = part * (kMx4Threads / 32) + warp; i < rows * 4; i += split * (kMx4Threads / 32)) {
+            const int row = i >> 2, c = (i & 3) * 32 + lane, n = n0 + c;
+            const uint32_t at = sbase + (uint32_t)row * 512u + (uint32_t)c * 4u;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = q < split ? dsmem_ld_f32(dsmem_map(at, (uint32_t)q)) : 0.f;
+            float sum = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) sum += v[q];
+            if (n < o.N) turned_store(o, sum, m0 + row, n);
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while others read its sums
+    }
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();  // neither CTA frees TMEM or exits while the pair still uses it

@@ -236,6 +236,25 @@ def test_rows_weight_layouts():
     rows_case([10, 20], 128, 96, b=big[1:4:2, 2:98, 8:].transpose(1, 2))  # slices of a larger stack
 
 
+def test_rows_of_several_dims():
+    # [batch, positions] of tokens, one of them sliced away; the CUDA cores on demand
+    x = values((4, 9, 128), "bf16", 1)
+    w, offsets = values((3, 96, 128), "bf16", 2), offsets_of([10, 0, 22])
+    want = torch.empty(32, 96, device="cuda")
+    dg.gemm_grouped(x[:, 1:].reshape(32, 128), w.transpose(1, 2), want, offsets)
+    c = torch.empty(4, 8, 96, device="cuda")
+    dg.gemm_grouped(x[:, 1:], w.transpose(1, 2), c, offsets)
+    z = steps(128, torch.bfloat16) * 2 * (x[:, 1:].double().abs().sum(2).max() * w.double().abs().max())
+    assert bool(((c.view(32, 96) - want).abs() <= z).all())
+    dg.dg_set_option(dg.DG_OPT_FORCE_KIND, dg.DG_KIND_SIMT)
+    try:
+        rows_case([10, 0, 22], 128, 96, out="f32")
+        dw_case([10, 0, 22], 128, 96)
+    finally:
+        dg.dg_set_option(dg.DG_OPT_FORCE_KIND, 0)
+    assert dg.dg_sync_status() == dg.DG_OK
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("rows", [[2], [1, 1], [3, 0, 2, 1, 0, 0, 1, 1]])
 def test_rows_single_tokens(rows, dtype):
@@ -245,6 +264,27 @@ def test_rows_single_tokens(rows, dtype):
 def test_rows_deep():
     rows_case([300, 20], 8192, 256, out="f32")
     rows_case([5], 16384, 128, out="f32", weight="kn")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_long_sums_keep_their_precision(dtype):
+    """F32 sums of many products.  A step of 16 truncates to 2^-23, 2^-24 of the sum on average, always towards zero:
+    128 steps of an accumulator lose 128 * 2^-24 = 7.6e-6 of it at most, in the norm over many sums; 14336 products in
+    one accumulator would lose seven times that."""
+    x, w = values((200, 14336), dtype, 1), values((1, 300, 14336), dtype, 2, 2.0 ** -6)
+    c = torch.empty(200, 300, device="cuda")
+    dg.gemm_grouped(x, w.transpose(1, 2), c, offsets_of([200]))
+    want = x.double() @ w[0].double().t()
+    assert float((c.double() - want).norm() / want.norm()) <= 7.6e-6
+    x, dy = values((16000, 300), dtype, 3), values((16000, 260), dtype, 4)
+    x, dy = padded(x, 4), padded(dy, 4)
+    dw = torch.empty(3, 300, 260, device="cuda")
+    sizes = [12000, 100, 3900]
+    dg.gemm_grouped_dw(x, dy, dw, offsets_of(sizes))
+    assert dg.dg_sync_status() == dg.DG_OK
+    for g, (a, b) in enumerate([(0, 12000), (12000, 12100), (12100, 16000)]):
+        want = x[a:b].double().t() @ dy[a:b].double()
+        assert float((dw[g].double() - want).norm() / want.norm()) <= 7.6e-6
 
 
 def test_rows_most_groups():

@@ -332,6 +332,17 @@ def test_product_wide_tiles(M, N, K, block):
 
 
 @pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,N,K", [(1, 128, 16384), (1, 4096, 14336), (8, 1000, 5000), (33, 40, 4100), (128, 256, 8192),
+                                   (200, 100, 4096), (127, 2300, 2304), (3, 18000, 4096)])
+def test_product_split(M, N, K, block):
+    """Few tiles and a long k, which the CTAs of a cluster share; the same sums every time."""
+    a, b = random_operand(M, K, block, 1), random_operand(N, K, block, 2)
+    c = check_product(M, N, K, block, a=a, b=b)
+    assert torch.equal(c, check_product(M, N, K, block, a=a, b=b))
+    check_product(M, N, K, block, "bf16", alpha=0.01, beta=0.5, bias=True, act="gelu_tanh", factors=True)
+
+
+@pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh"])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("beta", [0.0, -0.5])
