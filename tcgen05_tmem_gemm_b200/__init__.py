@@ -149,18 +149,19 @@ def _load():
     L.dg_linear_ce_grad_workspace.argtypes = [V, V, V, V, P(I64), P(I64)]
     L.dg_linear_ce_grad_workspace.restype = ctypes.c_int
     I32, F = ctypes.c_int32, ctypes.c_float
-    L.dg_gemm_grouped.argtypes = [V, V, V, ctypes.c_void_p, I32, F, F, ctypes.c_void_p, ctypes.c_void_p,
+    A = ctypes.c_void_p  # a structure by address: byref() or packed bytes
+    L.dg_gemm_grouped.argtypes = [A, A, A, ctypes.c_void_p, I32, F, F, ctypes.c_void_p, ctypes.c_void_p,
                                   P(dg_epilogue), ctypes.c_void_p]
     L.dg_gemm_grouped.restype = ctypes.c_int
-    L.dg_gemm_grouped_dw.argtypes = [V, V, V, ctypes.c_void_p, I32, F, F, ctypes.c_void_p]
+    L.dg_gemm_grouped_dw.argtypes = [A, A, A, ctypes.c_void_p, I32, F, F, ctypes.c_void_p]
     L.dg_gemm_grouped_dw.restype = ctypes.c_int
     L.dg_mx4_scale_bytes.argtypes = [I64, I64, I32]
     L.dg_mx4_scale_bytes.restype = I64
-    L.dg_quantize_mx4.argtypes = [V, P(dg_mx4), ctypes.c_void_p]
+    L.dg_quantize_mx4.argtypes = [A, A, ctypes.c_void_p]
     L.dg_quantize_mx4.restype = ctypes.c_int
-    L.dg_dequantize_mx4.argtypes = [P(dg_mx4), V, ctypes.c_void_p]
+    L.dg_dequantize_mx4.argtypes = [A, A, ctypes.c_void_p]
     L.dg_dequantize_mx4.restype = ctypes.c_int
-    L.dg_gemm_mx4.argtypes = [P(dg_mx4), P(dg_mx4), V, F, F, P(dg_epilogue), ctypes.c_void_p]
+    L.dg_gemm_mx4.argtypes = [A, A, A, F, F, P(dg_epilogue), ctypes.c_void_p]
     L.dg_gemm_mx4.restype = ctypes.c_int
     L.dg_status_string.argtypes = [ctypes.c_int]
     L.dg_status_string.restype = ctypes.c_char_p
@@ -222,33 +223,38 @@ _TORCH_DT = None
 
 def _torch_dtype_code(t) -> int:
     global _TORCH_DT
-    import torch
-
     if _TORCH_DT is None:
+        import torch
+
         _TORCH_DT = {torch.float32: DG_F32, torch.float16: DG_F16, torch.bfloat16: DG_BF16,
                      torch.float8_e4m3fn: DG_E4M3}
-    if t.dtype not in _TORCH_DT:
+    code = _TORCH_DT.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported tensor dtype {t.dtype}")
-    return _TORCH_DT[t.dtype]
+    return code
 
 
 def view(t, row_dims: int = 1) -> dg_view:
     """A dg_view of a torch tensor in place (its strides, in bytes, as they are)."""
+    return dg_view.from_buffer_copy(_packed_view(t, row_dims))
+
+
+def _packed_view(t, row_dims: int) -> bytes:
     code = _torch_dtype_code(t)
     es = ELEM_SIZE[code]
     shape, stride = t.shape, t.stride()
     n = len(shape)
-    if n == 3:
-        return dg_view.from_buffer_copy(_VIEW.pack(t.data_ptr(), 3, row_dims, *shape, 1, stride[0] * es,
-                                                   stride[1] * es, stride[2] * es, 0, code, 0))
     if n == 2:
-        return dg_view.from_buffer_copy(_VIEW.pack(t.data_ptr(), 2, row_dims, shape[0], shape[1], 1, 1,
-                                                   stride[0] * es, stride[1] * es, 0, 0, code, 0))
+        return _VIEW.pack(t.data_ptr(), 2, row_dims, shape[0], shape[1], 1, 1, stride[0] * es, stride[1] * es, 0, 0,
+                          code, 0)
+    if n == 3:
+        return _VIEW.pack(t.data_ptr(), 3, row_dims, *shape, 1, stride[0] * es, stride[1] * es, stride[2] * es, 0,
+                          code, 0)
     if n > 4:
         raise ValueError("views have at most 4 dims")
     if n == 0:
         shape, stride = (1,), (1,)
-    return make_view(t.data_ptr(), shape, [s * es for s in stride], row_dims, code)
+    return bytes(make_view(t.data_ptr(), shape, [s * es for s in stride], row_dims, code))
 
 
 def _as_view(x, row_dims=1):
@@ -612,11 +618,12 @@ def linear_ce_grad(x, w, target, lse, dloss, dx=None, dw=None, alpha: float = 1.
 
 def _groups(offsets, stack) -> int:
     """The number of groups, from int64 offsets [groups + 1] and a [groups, K, N] tensor."""
-    if offsets.dtype != _torch.int64 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+    size, shape = offsets.shape, stack.shape
+    if len(size) != 1 or size[0] < 1 or offsets.dtype != _torch.int64 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int64 tensor of groups + 1 elements")
-    if stack.dim() != 3 or stack.shape[0] != offsets.shape[0] - 1:
-        raise ValueError(f"expected [{offsets.shape[0] - 1}, K, N], got {tuple(stack.shape)}")
-    return stack.shape[0]
+    if len(shape) != 3 or shape[0] != size[0] - 1:
+        raise ValueError(f"expected [{size[0] - 1}, K, N], got {tuple(shape)}")
+    return shape[0]
 
 
 def gemm_grouped(a, b, c, offsets, scale_a=None, scale_b=None, alpha: float = 1.0, beta: float = 0.0, bias=None,
@@ -632,10 +639,10 @@ def gemm_grouped(a, b, c, offsets, scale_a=None, scale_b=None, alpha: float = 1.
     for name, t in (("scale_b", scale_b), ("bias", bias)):
         if t is not None:
             _vector(t, name, _torch.float32, groups * b.shape[2])
-    av, bv, cv = view(a, a.dim() - 1), view(b, 2), view(c, c.dim() - 1)
     epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
-    st = lib.dg_gemm_grouped(ctypes.byref(av), ctypes.byref(bv), ctypes.byref(cv), offsets.data_ptr(), groups, alpha,
-                             beta, _ptr(scale_a), _ptr(scale_b), epi, _stream_ptr(stream))
+    st = lib.dg_gemm_grouped(_packed_view(a, a.dim() - 1), _packed_view(b, 2), _packed_view(c, c.dim() - 1),
+                             offsets.data_ptr(), groups, alpha, beta, _ptr(scale_a), _ptr(scale_b), epi,
+                             _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_gemm_grouped")
     return c
@@ -646,9 +653,8 @@ def gemm_grouped_dw(x, dy, dw, offsets, alpha: float = 1.0, beta: float = 0.0, s
     [..., K], dy [..., N], dw [groups, K, N] (that of a [groups, N, K] weight is passed as dweight.transpose(1, 2)).
     Raises DgError on a bad status; returns dw."""
     groups = _groups(offsets, dw)
-    xv, dyv, dwv = view(x, x.dim() - 1), view(dy, dy.dim() - 1), view(dw, 2)
-    st = lib.dg_gemm_grouped_dw(ctypes.byref(xv), ctypes.byref(dyv), ctypes.byref(dwv), offsets.data_ptr(), groups,
-                                alpha, beta, _stream_ptr(stream))
+    st = lib.dg_gemm_grouped_dw(_packed_view(x, x.dim() - 1), _packed_view(dy, dy.dim() - 1), _packed_view(dw, 2),
+                                offsets.data_ptr(), groups, alpha, beta, _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_gemm_grouped_dw")
     return dw
@@ -665,6 +671,10 @@ def mx4(codes, scales, K: int | None = None, block: int = 32, scale=None) -> dg_
     """A dg_mx4 of torch tensors in place: codes uint8 [rows, ceil(K / 2)], two E2M1 codes per byte along k (even k in
     the low four bits), scales uint8 in tiles (dg_mx4_scale_bytes of them), scale a float32 of one element on the
     device or None.  K defaults to two per byte."""
+    return dg_mx4.from_buffer_copy(_packed_mx4(codes, scales, K, block, scale))
+
+
+def _packed_mx4(codes, scales, K, block, scale) -> bytes:
     rows, nbytes = codes.shape
     K = 2 * nbytes if K is None else int(K)
     stride = codes.stride()
@@ -672,19 +682,22 @@ def mx4(codes, scales, K: int | None = None, block: int = 32, scale=None) -> dg_
         raise TypeError("codes and scales must be uint8")
     if nbytes != (K + 1) // 2 or (nbytes > 1 and stride[1] != 1):
         raise ValueError(f"codes must have ceil(K / 2) = {(K + 1) // 2} contiguous bytes a row")
-    if scales.numel() != lib.dg_mx4_scale_bytes(rows, K, block) or not scales.is_contiguous():
-        raise ValueError(f"scales must be {lib.dg_mx4_scale_bytes(rows, K, block)} contiguous bytes (block {block})")
+    if block not in (16, 32):
+        raise ValueError("block must be 16 or 32")
+    need = -(-rows // 128) * -(-K // (4 * block)) * 512  # dg_mx4_scale_bytes
+    if scales.numel() != need or not scales.is_contiguous():
+        raise ValueError(f"scales must be {need} contiguous bytes (block {block})")
     if scale is not None:
         _vector(scale, "scale", _torch.float32, 1)
-    return dg_mx4.from_buffer_copy(_MX4.pack(codes.data_ptr(), scales.data_ptr(),
-                                             0 if scale is None else scale.data_ptr(), rows, K, stride[0], block, 0))
+    return _MX4.pack(codes.data_ptr(), scales.data_ptr(), 0 if scale is None else scale.data_ptr(), rows, K, stride[0],
+                     block, 0)
 
 
 def quantize_mx4(x, codes, scales, block: int = 32, scale=None, stream=None):
     """dg_quantize_mx4 on torch tensors: the codes and block scales (see mx4) of x [..., K] / scale, written in
     place.  Raises DgError on a bad status; returns (codes, scales)."""
-    xv, q = view(x, x.dim() - 1), mx4(codes, scales, x.shape[-1], block, scale)
-    st = lib.dg_quantize_mx4(ctypes.byref(xv), ctypes.byref(q), _stream_ptr(stream))
+    st = lib.dg_quantize_mx4(_packed_view(x, x.dim() - 1), _packed_mx4(codes, scales, x.shape[-1], block, scale),
+                             _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_quantize_mx4")
     return codes, scales
@@ -693,8 +706,8 @@ def quantize_mx4(x, codes, scales, block: int = 32, scale=None, stream=None):
 def dequantize_mx4(codes, scales, y, block: int = 32, scale=None, stream=None):
     """dg_dequantize_mx4 on torch tensors: y [..., K] = the values of codes and scales (see mx4).  Raises DgError on
     a bad status; returns y."""
-    yv, q = view(y, y.dim() - 1), mx4(codes, scales, y.shape[-1], block, scale)
-    st = lib.dg_dequantize_mx4(ctypes.byref(q), ctypes.byref(yv), _stream_ptr(stream))
+    st = lib.dg_dequantize_mx4(_packed_mx4(codes, scales, y.shape[-1], block, scale), _packed_view(y, y.dim() - 1),
+                               _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_dequantize_mx4")
     return y
@@ -703,9 +716,9 @@ def dequantize_mx4(codes, scales, y, block: int = 32, scale=None, stream=None):
 def gemm_mx4(a: dg_mx4, b: dg_mx4, c, alpha: float = 1.0, beta: float = 0.0, bias=None, act="none", stream=None):
     """dg_gemm_mx4: c [M, N] = act(alpha * a b^T + beta * c + bias) of a [M, K] and b [N, K] in 4-bit floats (see
     mx4), c a torch tensor or dg_view.  Raises DgError on a bad status; returns c."""
-    cv = _as_view(c)
+    cv = ctypes.byref(c) if isinstance(c, dg_view) else _packed_view(c, 1)
     epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
-    st = lib.dg_gemm_mx4(ctypes.byref(a), ctypes.byref(b), ctypes.byref(cv), alpha, beta, epi, _stream_ptr(stream))
+    st = lib.dg_gemm_mx4(ctypes.byref(a), ctypes.byref(b), cv, alpha, beta, epi, _stream_ptr(stream))
     if st != DG_OK:
         raise DgError(st, "dg_gemm_mx4")
     return c
