@@ -240,7 +240,10 @@ bool tensor_call(const GroupedCall &c, GroupedParams p, int num_sms, cudaStream_
         p.out.N = (int32_t)c.N;
         p.out.rs = one_stride(c.ci.row);
         p.out.cs = c.ci.col.n ? c.ci.col.stride[0] : c.ci.es;
-        p.tile_w = (int32_t)std::min<int64_t>(256, (c.R + 31) / 32 * 32);
+        // four times the average group, as the most: what a narrower tile saves of the ring holds more stages
+        int64_t most = 64;
+        while (most < 256 && most * c.groups < 4 * c.R) most *= 2;
+        p.tile_w = (int32_t)std::min<int64_t>(most, (c.R + 31) / 32 * 32);
         p.q_rows = p.tile_w <= 32 ? 16 : p.tile_w <= 64 ? 32 : p.tile_w <= 128 ? 64 : 128;
         bool mn = false;
         if (!none) {
