@@ -371,9 +371,11 @@ __device__ __forceinline__ void load_lot(Lot<DT> &v, const char *x, int n) {
 // maximum crosses lanes.  VEC: a lane loads its own 64 (or 128) bytes, 16 at a
 // time (the warp's four loads share their lines in L1), a row ahead of the one
 // it works on.  Otherwise (rows at any address) the warp copies the row through
-// shared memory.
+// shared memory; there a third block per SM is worth a few spilled registers
+// (8192 x 14337 BF16 119 -> 100 us), while the compiler's own choice, three as
+// well, is best for the rest.
 template <int DT, int BLOCK, bool VEC>
-__global__ void __launch_bounds__(32 * kQuantWarps) quantize_rows_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(32 * kQuantWarps, VEC || DT == DG_F32 ? 0 : 3) quantize_rows_kernel(const QuantParams p) {
     pdl_wait_then_release();
     constexpr int ES = Lot<DT>::ES;
     __shared__ uint32_t stage[VEC ? 1 : kQuantWarps * kStageWords<DT>];
