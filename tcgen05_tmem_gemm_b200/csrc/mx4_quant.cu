@@ -147,16 +147,21 @@ struct Factor {
         plain = size >= 0x1p-60f && size <= 0x1p60f;
         r = plain ? __frcp_rn(size) : 0.f;
     }
-    // x / |t|, but for the sign of a zero: correctly rounded (Markstein 1990,
-    // "Computation of elementary functions on the IBM RISC System/6000
-    // processor") while the remainder does not underflow.
-    __device__ __forceinline__ Two quotient(Two x) const { return quotient2(x, Two(-size, -size), Two(r, r)); }
+    // x / |t|, but for the sign of a zero: correctly rounded, while nothing
+    // underflows, because a second correction starts from a quotient within an
+    // ulp (Markstein 1990, "Computation of elementary functions on the IBM RISC
+    // System/6000 processor").
+    __device__ __forceinline__ Two quotient(Two x) const {
+        const Two ms(-size, -size), rr(r, r), q = quotient2(x, ms, rr);
+        return fma2(fma2(q, ms, x), rr, q);
+    }
 };
 
-// Below this magnitude of a block's largest value its quotients are divided
-// one by one; above it a value whose remainder underflows is so small a part
-// of the largest that its code is 0 in any case.
+// Below this magnitude of a block's largest value, or of its quotient, the
+// quotients are divided one by one; above it a value whose remainder or quotient
+// underflows is so small a part of the largest that its code is 0 in any case.
 constexpr float kLeastPlain = 0x1p-90f;
+constexpr float kMostPlain = 0x1p126f;  // and no quotient of the block is near the end of FP32
 
 // 32 neighbouring k of a row as they lie in memory (zeros past K).
 template <int DT>
@@ -197,11 +202,19 @@ __device__ __forceinline__ uint32_t encode(const Lot<DT> &x, int n, const Factor
 #pragma unroll
     for (int b = 0; b < 32 / BLOCK; ++b) {
         const uint32_t top = x.template top<BLOCK>(b);
-        float s, r;
+        const float most = __uint_as_float(top);
+        const bool plain = f.plain && most >= kLeastPlain && most * f.r >= kLeastPlain && most * f.r <= kMostPlain;
         // the largest |x / t| is that of the largest |x|: rounding keeps the order
-        const uint32_t code = mx4_scale<BLOCK>(f.divide ? abs_bits(divided(__uint_as_float(top), f.t)) : top, s, r);
+        uint32_t under = top;
+        if (f.divide) {
+            float q, unused;
+            if (plain) f.quotient(Two(most, 0.f)).get(q, unused);
+            else q = divided(most, f.size);
+            under = abs_bits(q);
+        }
+        float s, r;
+        const uint32_t code = mx4_scale<BLOCK>(under, s, r);
         if (b * BLOCK < n) scales |= code << (8 * b);
-        const bool plain = f.plain && __uint_as_float(top) >= kLeastPlain;
         const Two ms(-s, -s), rr(r, r);
         // each way a loop of its own: a branch per pair costs as much as the arithmetic
         if (!f.divide) {

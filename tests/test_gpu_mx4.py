@@ -212,6 +212,29 @@ def test_quantise_with_a_factor(block, factor):
 
 
 @pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("exponent", [-126, -61, -60, -31, 31, 60, 61, 126])
+def test_quantise_with_far_factors(exponent, block):
+    """Quotients at the ends of FP32, subnormal and infinite ones among them, and values that are far apart."""
+    scale = torch.full((1,), 1.375 * 2.0 ** exponent, device="cuda")
+    x = normal((64, 256), "f32", 7) * torch.pow(2.0, torch.arange(-124, 4, 2, device="cuda").float())[:, None]
+    check_quantised(x, block, scale)
+    check_quantised(x * 2.0 ** 60, block, -scale)
+    check_quantised((normal((64, 256), "f32", 8) * torch.logspace(-30, 30, 256, device="cuda")).bfloat16(), block, scale)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_quantise_quotients_are_rounded_once(block):
+    """Factors of any significand: quotients next to FP32's own rounding borders."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for i in range(12):
+        scale = torch.rand(1, generator=g, device="cuda") + 0.5
+        u = torch.randn(512, 512, generator=g, device="cuda") + 3
+        # FP32 numbers whose quotient is within an ulp of a midpoint of two others
+        x = ((u.double() + u.double() * 2.0 ** -24) * scale.double()).float()
+        check_quantised(x, block, scale)
+
+
+@pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("R,K", [(1, 1), (3, 33), (128, 64), (200, 1000), (5, 4097)])
 def test_read_back(R, K, dtype, block):
