@@ -154,9 +154,16 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     p.M = (int32_t)A->rows;
     p.N = (int32_t)B->rows;
     p.K = product ? (int32_t)A->K : 0;
-    // 256 rows a tile where that leaves no SM without one, and then in pairs of CTAs
+    // Tiles of 128 x 128 per CTA, or of 256 x 256 per pair of CTAs: whichever takes less time by a model in
+    // microseconds per round of the grid, 0.38 a stage and 1 a tile of a CTA, 0.42 and 2.6 of a pair (B200, CTAs
+    // and pairs: 777x1000x5003 7.7 and 12.3, 300x512x20000 8.5 and 12.0, 1024x14336x4096 44.5 and 28.9,
+    // 2048^3 9.7 and 9.2).
+    const int steps = (p.K + kMx4K - 1) / kMx4K;
+    auto rounds = [&](int64_t side, int64_t slots) {
+        return (double)((((p.N + side - 1) / side) * ((p.M + side - 1) / side) + slots - 1) / slots);
+    };
     const bool pair = num_sms >= 2 && p.M > 128 &&
-                      (int64_t)((p.N + 255) / 256) * ((p.M + 255) / 256) * 2 >= num_sms;
+                      rounds(256, num_sms / 2) * (0.42 * steps + 2.6) < rounds(128, num_sms) * (0.38 * steps + 1);
     p.tile_w = pair ? 256 : 128;
     p.tiles_n = pair ? (p.N + 255) / 256 : (p.N + 127) / 128;
     p.tiles_m = (p.M + p.tile_w - 1) / p.tile_w;
@@ -166,7 +173,6 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     // a tile's rows times (0.02 + 0.09 / f); clusters of eight do not fill every group of SMs.  (B200, f = 1
     // and the chosen one: 8x4096x14336 19.2 -> 10.1, 1x512x2048 4.6 -> 3.6, 128x1024x16384 25.1 -> 9.8;
     // 128x4096x4096 stays at one, 8.6 against 10.3.)
-    const int steps = (p.K + kMx4K - 1) / kMx4K;
     p.split = 1;
     double least = 0.33 * steps;
     if (!pair)

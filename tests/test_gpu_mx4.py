@@ -349,9 +349,18 @@ def test_product_columns(N, out, block):
 
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("M,N,K", [(700, 20000, 256), (1000, 9000, 160), (257, 19000, 96), (384, 40000, 64)])
-def test_product_wide_tiles(M, N, K, block):
-    """Enough tiles for every SM: those of 256 rows, several per SM."""
+def test_product_many_tiles(M, N, K, block):
+    """More tiles than SMs, several for each."""
     check_product(M, N, K, block, "bf16")
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,N,K", [(1000, 9000, 2048), (777, 15000, 2562), (257, 20000, 4100), (2048, 2048, 2048),
+                                   (129, 40000, 4096), (520, 9001, 6000)])
+def test_product_pairs(M, N, K, block):
+    """A longer k and more tiles: those of 256 rows and columns that pairs of CTAs take, whole and partial ones."""
+    check_product(M, N, K, block, "bf16")
+    check_product(M, N, K, block, "f32", alpha=0.01, beta=0.5, bias=True, act="relu", factors=True)
 
 
 @pytest.mark.parametrize("block", [16, 32])
