@@ -16,6 +16,11 @@
 // Few tiles and a long k: the CTAs of a cluster take a part of k each, leave
 // their sums in their rings, and every CTA adds its share of the tile's rows, in
 // rank order, from all of them through distributed shared memory.
+//
+// What bounds it (B200): the copies, about 740 cycles per stage and SM against
+// 512 of MMAs, then the power cap (8192 x 4096 x 14336 in blocks of 16: 207 us
+// with a cold cache, 243 back to back; 4096^3: 41 us, 3.4 PFLOP/s); for one row
+// the four copies of a stage, 0.3 us (1 x 4096 x 14336: 8 us).
 #pragma once
 
 #include "common.cuh"

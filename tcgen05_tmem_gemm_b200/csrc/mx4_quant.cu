@@ -5,6 +5,11 @@
 // largest to [4, 8) (above 6 it is cut); a block of 16 an E4M3 scale, a sixth
 // of the largest.  Everything is rounded to nearest, ties to even, and every
 // division by a block's scale decides as the exact quotient would.
+//
+// They should be bound by HBM and are bound by instructions (8192 x 14336 BF16 on
+// B200, 300 MB: quantised in blocks of 32 in 59 us, of 16 in 70, with a factor 88;
+// read back in 53; the bytes take 46): about 8 to 16 per value, at a third of the
+// warps an SM holds.
 #include <algorithm>
 
 #include "mx4_quant.h"

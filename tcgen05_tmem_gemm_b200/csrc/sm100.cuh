@@ -375,14 +375,6 @@ __device__ __forceinline__ uint64_t make_scales_desc(uint32_t smem_addr) {
     return d;
 }
 
-// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from
-// global to this CTA's shared memory; the bytes complete on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
 // 32 lanes x 32 bits, 16 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

@@ -203,11 +203,10 @@ __device__ __forceinline__ void turned_any_d(const TurnedOut &o, uint32_t taddr,
     else turned_any<DG_F16, FUSED, ACT>(o, taddr, empty, r0, rows, n0, lane, half);
 }
 
-// One element, from its sum.
+// One element of a C without scales, from its sum.
 __device__ __forceinline__ void turned_store(const TurnedOut &o, float sum, int64_t r, int n) {
     char *const at = o.c + r * o.rs + (int64_t)n * o.cs;
-    float v = epi_value(sum, o.alpha * (o.scale_n != nullptr ? o.scale_n[n] : 1.f),
-                        o.scale_r != nullptr ? o.scale_r[r] : 1.f, o.beta, at, o.dtype);
+    float v = epi_value(sum, o.alpha, 1.f, o.beta, at, o.dtype);
     if (o.bias_n != nullptr || o.act != DG_ACT_NONE) v = epi_fuse(v, o.bias_n, n, o.act, o.dtype != DG_F32);
     store_elem(at, o.dtype, v);
 }
