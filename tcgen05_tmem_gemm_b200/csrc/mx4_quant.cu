@@ -208,7 +208,8 @@ __device__ __forceinline__ uint32_t encode(const Lot<DT> &x, int n, const Factor
     for (int b = 0; b < 32 / BLOCK; ++b) {
         const uint32_t top = x.template top<BLOCK>(b);
         const float most = __uint_as_float(top);
-        const bool plain = f.plain && most >= kLeastPlain && most * f.r >= kLeastPlain && most * f.r <= kMostPlain;
+        const bool plain = f.plain && (top == 0 || (most >= kLeastPlain && most * f.r >= kLeastPlain &&
+                                                    most * f.r <= kMostPlain));  // zeros: lanes past K among them
         // the largest |x / t| is that of the largest |x|: rounding keeps the order
         uint32_t under = top;
         if (f.divide) {

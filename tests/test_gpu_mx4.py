@@ -223,6 +223,17 @@ def test_quantise_with_far_factors(exponent, block):
 
 
 @pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("factor", [0.01, -3.0, 2.0 ** -70, math.inf])
+def test_quantise_zeros_with_a_factor(factor, block):
+    scale = torch.full((1,), factor, device="cuda")
+    for dtype in ("bf16", "f16", "f32"):
+        x = normal((70, 1100), dtype, 12)
+        x[3], x[5, 16:64], x[9, ::2], x[11] = 0, 0, -0.0, -0.0
+        check_quantised(x, block, scale)
+        check_quantised(x.t(), block, scale)
+
+
+@pytest.mark.parametrize("block", [16, 32])
 def test_quantise_quotients_are_rounded_once(block):
     """Factors of any significand: quotients next to FP32's own rounding borders."""
     g = torch.Generator(device="cuda").manual_seed(11)
