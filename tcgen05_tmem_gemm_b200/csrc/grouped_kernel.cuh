@@ -35,9 +35,12 @@
 // 1024 of MMAs).
 //
 // The tensor core truncates when it adds to an accumulator: a sum of 14336
-// products of BF16 normal values came out 1.6e-5 low, of 4096 4.4e-6.  For 16-bit
-// operands and F32 C a sum therefore starts a fresh accumulator every 2048 k; the
-// epilogue adds them up in the other accumulator's place in TMEM.
+// products of BF16 normal values came out 1.6e-5 low, of 4096 4.4e-6, and 65536
+// positive products of F16 4.3e-4, twice F16's own rounding.  A sum therefore
+// starts a fresh accumulator every 2048 k, whatever the type of C, and the
+// epilogue adds them up: the first part's accumulator holds the sum, the others
+// are made in the other one, one after the other (the first two without a pause;
+// later ones wait some 1000 cycles of their 16 thousand for the epilogue's read).
 #pragma once
 
 #include <climits>
@@ -395,18 +398,23 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                     continue;
                 }
                 const uint32_t idesc = p.idesc | (uint32_t)(x.w >> 3) << 17;
-                const uint32_t d_tmem = tmem_base + (uint32_t)(b * 256);
+                int at = b;  // a sum's first part is made in this accumulator, the others in the other one
+                uint32_t d_tmem = tmem_base;
                 for (int k = 0, kc = 0; k < x.k; k += KD, kc += KD) {
-                    if (kc == p.k_chunk) kc = 0;
+                    if (kc == p.k_chunk) {
+                        if (elect_one()) tc_commit_pair_mc(bar_tfull + 8 * at, 0x3);
+                        at = b ^ 1;
+                        kc = 0;
+                    }
                     if (kc == 0) {
-                        if (k > 0 && elect_one()) tc_commit_pair_mc(bar_tfull + 8 * b, 0x3);
-                        if (!warp_wait(bar_tempty + 8 * b, ((uint32_t)(b ? uses[1] : uses[0]) & 1u) ^ 1u, wc)) {
+                        if (!warp_wait(bar_tempty + 8 * at, ((uint32_t)(at ? uses[1] : uses[0]) & 1u) ^ 1u, wc)) {
                             ok = false;
                             break;
                         }
-                        if (b) ++uses[1];
+                        if (at) ++uses[1];
                         else ++uses[0];
                         tc_fence_after();
+                        d_tmem = tmem_base + (uint32_t)(at * 256);
                     }
                     if (!warp_wait(bar_full + 8 * s, ph, wc)) {
                         ok = false;
@@ -437,8 +445,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                     if (k == 0) more = warp_unit<BYK>(p, tables, u += pairs, next);  // beside the first MMAs
                 }
                 if (!ok) break;
-                if (elect_one()) tc_commit_pair_mc(bar_tfull + 8 * b, 0x3);
-                if (x.k <= p.k_chunk) b ^= 1;  // a sum of several parts has the other accumulator's place too
+                if (elect_one()) tc_commit_pair_mc(bar_tfull + 8 * at, 0x3);
+                b ^= 1;  // free before the sum is, if that had several parts
             }
             pdl_release();
             if (elect_one()) tc_commit_pair_mc(bar_drain, 0x1);
@@ -458,42 +466,26 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
             if (o.bias_n != nullptr) o.bias_n += gs;
             const int n0 = x.n0 + (int)rank * kPRows + quarter * 32;
             const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
-            const uint32_t acc = lanes + (uint32_t)(b * 256), other = lanes + (uint32_t)((b ^ 1) * 256);
-            const uint32_t empty_bar = dsmem_map(bar_tempty + 8 * b, 0);
+            const uint32_t acc = lanes + (uint32_t)(b * 256), part = lanes + (uint32_t)((b ^ 1) * 256);
+            const uint32_t empty_bar = dsmem_map(bar_tempty + 8 * b, 0), part_empty = dsmem_map(bar_tempty + 8 * (b ^ 1), 0);
             bool ok = true;
             for (int k = 0; k < x.k; k += min(p.k_chunk, x.k - k)) {
-                if (!mbar_wait(bar_tfull + 8 * b, (uint32_t)(b ? uses[1] : uses[0]) & 1u, wc)) {
+                const int at = k > 0 ? b ^ 1 : b;
+                if (!mbar_wait(bar_tfull + 8 * at, (uint32_t)(at ? uses[1] : uses[0]) & 1u, wc)) {
                     ok = false;
                     break;
                 }
-                if (b) ++uses[1];
+                if (at) ++uses[1];
                 else ++uses[0];
                 tc_fence_after();
                 if (x.k <= p.k_chunk) break;
-                // one part of several: added to those before, in the other accumulator's place, or, the
-                // last one, back in its own
-                const bool last = x.k - k <= p.k_chunk;
-                for (int c0 = 32 * half; c0 < x.rows; c0 += 64) {
-#pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        uint32_t r[16], t[16];
-                        __syncwarp();
-                        tmem_ld16(acc + (uint32_t)(c0 + h), r);
-                        if (k > 0) tmem_ld16(other + (uint32_t)(c0 + h), t);
-                        tmem_ld_wait();
-                        if (k > 0) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                r[i] = __float_as_uint(__uint_as_float(t[i]) + __uint_as_float(r[i]));
-                        }
-                        tmem_st16((last ? acc : other) + (uint32_t)(c0 + h), r);
-                    }
-                }
-                tmem_st_wait();
-                if (last) break;
+                if (k == 0) continue;
+                // a further part: added to the first one's accumulator
+                for (int c0 = 32 * half; c0 < x.rows; c0 += 64) turned_add(acc + (uint32_t)c0, part + (uint32_t)c0);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_tmem(empty_bar);
+                if (lane == 0) mbar_arrive_tmem(part_empty);
+                tmem_st_wait();
             }
             if (!ok) break;
             turned_rows<FP8>(o, turn, acc, x.k == 0, x.r0, x.rows, n0, lane, half, [&] {
@@ -502,7 +494,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_tmem(empty_bar);
             });
-            if (x.k > 0 && x.k <= p.k_chunk) b ^= 1;
+            if (x.k > 0) b ^= 1;
         }
     }
 

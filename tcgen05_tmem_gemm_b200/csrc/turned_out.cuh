@@ -106,6 +106,22 @@ __device__ __forceinline__ void turned_read(TurnedWords &w, const TurnedOut &o, 
     }
 }
 
+// 32 columns of TMEM (FP32) added to others, which are there after a tmem_st_wait.
+__device__ __forceinline__ void turned_add(uint32_t to, uint32_t from) {
+    uint32_t r[32], t[32];
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        tmem_ld16(from + (uint32_t)h, *reinterpret_cast<uint32_t(*)[16]>(&r[h]));
+        tmem_ld16(to + (uint32_t)h, *reinterpret_cast<uint32_t(*)[16]>(&t[h]));
+    }
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t[i] = __float_as_uint(__uint_as_float(t[i]) + __uint_as_float(r[i]));
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) tmem_st16(to + (uint32_t)h, *reinterpret_cast<uint32_t(*)[16]>(&t[h]));
+}
+
 // And turned on their way to C.
 __device__ __forceinline__ void turned_write(const TurnedWords &w, const TurnedOut &o, uint32_t stage, int64_t r0, int rows,
                                              int n0, int lane, int half) {
