@@ -344,8 +344,9 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W,
  *  groups   at most 1024.
  * One launch each, whatever the sizes; no workspace.  Sums are FP32 and in a
  * fixed order: runs are bit-identical.  The tensor core truncates as it adds:
- * sums of F16 and BF16 products are made in parts of 2048, each low by at most
- * 2e-5 of its magnitudes, and the parts are added with rounding to nearest.
+ * sums of F16 and BF16 products are made in parts of 2048, of E4M3 products in
+ * parts of 4096, each low by at most 2e-5 of its magnitudes, and the parts are
+ * added with rounding to nearest.
  * F16, BF16 and E4M3 (both operands alike) run on the tensor cores where every
  * row, or column, of an operand that is contiguous starts at a multiple of 16
  * bytes; F32, and any other view, on the CUDA cores (correct, and much slower).

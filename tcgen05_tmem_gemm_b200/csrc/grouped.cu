@@ -296,7 +296,7 @@ dg_status grouped_call(const GroupedCall &c, cudaStream_t s) {
     p.out.scale_n = product ? c.scale_n : nullptr;
     p.out.bias_n = c.bias;
     p.out.act = c.act;
-    p.k_chunk = c.a->dtype == DG_E4M3 ? INT32_MAX : 2048;
+    p.k_chunk = c.a->dtype == DG_E4M3 ? 4096 : 2048;  // 128 steps of the tensor core
     p.scale_n_gs = (int32_t)c.N;
     p.err_word = err_word;
     p.timeout_ns = wait_timeout_ns();

@@ -37,7 +37,8 @@
 // The tensor core truncates when it adds to an accumulator: a sum of 14336
 // products of BF16 normal values came out 1.6e-5 low, of 4096 4.4e-6, and 65536
 // positive products of F16 4.3e-4, twice F16's own rounding.  A sum therefore
-// starts a fresh accumulator every 2048 k, whatever the type of C, and the
+// starts a fresh accumulator every 2048 k (E4M3, whose steps are 32 k: 4096; 65536
+// positive products in one came out 5.9e-5 low), whatever the type of C, and the
 // epilogue adds them up: the first part's accumulator holds the sum, the others
 // are made in the other one, one after the other (the first two without a pause;
 // later ones wait some 1000 cycles of their 16 thousand for the epilogue's read).

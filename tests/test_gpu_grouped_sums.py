@@ -78,3 +78,18 @@ def test_sums_of_one_part_and_of_several_in_turn(out):
         tol = PART * S + 2.0 ** -22 * want.abs()
         tol = tol + torch.finfo(dw.dtype).eps / 2 * (want.abs() + tol)
         assert bool(((dw[g].double() - want).abs() <= tol).all()), g
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("weight", ["nk", "kn"])
+def test_rows_long_sums_of_e4m3(out, weight):
+    """Parts of 4096: as many steps, of 32 products each."""
+    K, sizes = 65536, [200, 0, 57]
+    x = positive((257, K), torch.float8_e4m3fn, 1, 0)
+    w = positive((3, 300, K) if weight == "nk" else (3, K, 304), torch.float8_e4m3fn, 2)
+    w = w.transpose(1, 2) if weight == "nk" else w
+    c = torch.empty(257, w.shape[2], device="cuda", dtype=DT[out])
+    dg.gemm_grouped(x, w, c, torch.tensor([0] + sizes, device="cuda").cumsum(0), alpha=2.0 ** -8)
+    assert dg.dg_sync_status() == dg.DG_OK
+    for r, g in ((slice(0, 200), 0), (slice(200, 257), 2)):
+        check_mean(c[r], 2.0 ** -8 * (x[r].double() @ w[g].double()))
