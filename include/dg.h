@@ -340,7 +340,8 @@ dg_status dg_linear_ce_grad_workspace(const dg_view *X, const dg_view *W,
  *    offsets[g + 1] - 1.  Groups may be empty; rows in front of offsets[0] and
  *    from offsets[groups] on belong to none.  A group whose offsets decrease or
  *    leave [0, R] counts as empty and is reported by dg_sync_status as
- *    DG_ERR_VALUE.
+ *    DG_ERR_VALUE; in dg_gemm_grouped a group that then begins in front of the
+ *    end of an earlier one counts as empty too (no row is computed twice).
  *  groups   at most 1024.
  * One launch each, whatever the sizes; no workspace.  Sums are FP32 and in a
  * fixed order: runs are bit-identical.  The tensor core truncates as it adds:

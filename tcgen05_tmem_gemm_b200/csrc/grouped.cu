@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(256) grouped_any_kernel(const GroupedAnyParams
     extern __shared__ int any_table[];
     int *start = any_table, *size = start + p.groups, *before = size + p.groups;
     __shared__ float As[kAnyK][kAnyTile + 4], Bs[kAnyK][kAnyTile + 4];
-    group_tables(p.offsets, p.groups, p.R, blockIdx.x == 0 && blockIdx.y == 0 ? p.err_word : nullptr, start, size);
-    __syncthreads();
+    const bool bad = __syncthreads_or(
+        group_tables(p.offsets, p.groups, p.R, blockIdx.x == 0 && blockIdx.y == 0 ? p.err_word : nullptr, start, size));
     int g, r0, rows, k0, K;
     if (BYK) {
         g = blockIdx.x / p.tiles_m;
@@ -44,7 +44,10 @@ __global__ void __launch_bounds__(256) grouped_any_kernel(const GroupedAnyParams
         k0 = start[g];
         K = p.K == 0 ? 0 : size[g];
     } else {
-        if (threadIdx.x < 32) group_scan(size, before, p.groups, kAnyTile, threadIdx.x);
+        if (threadIdx.x < 32) {
+            if (bad) group_disjoint(start, size, p.groups, threadIdx.x);
+            group_scan(size, before, p.groups, kAnyTile, threadIdx.x);
+        }
         __syncthreads();
         const int u = blockIdx.x;
         if (u >= before[p.groups]) return;

@@ -170,16 +170,41 @@ __device__ __forceinline__ bool warp_unit(const GroupedParams &p, const GroupTab
 }
 
 // The groups' rows from the offsets, checked: a group whose offsets decrease
-// or leave [0, R] has no rows and is reported.
-__device__ __forceinline__ void group_tables(const int64_t *offsets, int groups, int R, int *err_word, int *start,
+// or leave [0, R] has no rows and is reported.  Returns whether the calling
+// thread met one.
+__device__ __forceinline__ bool group_tables(const int64_t *offsets, int groups, int R, int *err_word, int *start,
                                              int *size) {
+    bool bad = false;
     for (int g = threadIdx.x; g < groups; g += blockDim.x) {
         const int64_t a = offsets[g], b = offsets[g + 1];
         const bool ok = a >= 0 && a <= b && b <= R;
         if (!ok && err_word) atomicExch(err_word, (int)DG_ERR_VALUE);
+        bad |= !ok;
         start[g] = ok ? (int)a : 0;
         size[g] = ok ? (int)(b - a) : 0;
     }
+    return bad;
+}
+
+// By rows, one warp, after a bad group: groups that begin in front of the end
+// of an earlier one have no rows either.  No row then belongs to two groups, and
+// all groups together have at most R rows, which the grid and the counts of tiles
+// rely on.  (Offsets that nowhere decrease have no such groups.)
+__device__ __forceinline__ void group_disjoint(const int *start, int *size, int groups, int lane) {
+    int end = 0;
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+        const int g = g0 + lane, n = g < groups ? size[g] : 0, from = g < groups ? start[g] : 0;
+        int m = n > 0 ? from + n : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, m, d);
+            if (lane >= d) m = max(m, v);
+        }
+        const int left = __shfl_up_sync(0xffffffffu, m, 1), before = lane > 0 ? max(end, left) : end;
+        if (n > 0 && from < before) size[g] = 0;
+        end = max(end, __shfl_sync(0xffffffffu, m, 31));
+    }
+    __syncwarp();
 }
 
 // One warp: the tiles of at most w rows before each group.
@@ -296,11 +321,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1)
     // everything above touches this pair's own memory only; what follows reads
     // what the previous kernel may have written
     pdl_wait();
-    group_tables(p.offsets, p.groups, p.R, p.err_word, start, size);
+    bool bad = group_tables(p.offsets, p.groups, p.R, p.err_word, start, size);
     tc_fence_before();
-    __syncthreads();
+    bad = __syncthreads_or(bad);
     if (!BYK) {
-        if (warp == 0) group_tiles(p, size, before, lane, pairs);
+        if (warp == 0) {
+            if (bad) group_disjoint(start, size, p.groups, lane);
+            group_tiles(p, size, before, lane, pairs);
+        }
         __syncthreads();
     }
     __syncwarp();
