@@ -459,7 +459,11 @@ dg_status dg_dequantize_mx4(const dg_mx4 *q, const dg_view *y, void *stream);
  * dg_gemm_mx4 — C = act(alpha * A B^T + beta * C + bias) for two such matrices
  * of one block size, A [M x K] and B [N x K] (a weight as it is stored), on the
  * tensor cores; epilogue as in dg_gemm_ex, or NULL.  Products are exact and
- * summed in FP32, in a fixed order.  A block whose scale is NaN makes its row
+ * summed in FP32, in a fixed order.  The tensor core truncates as it adds, at
+ * most 2^-23 of the sum for each 64 of K: for F32 C, sums of more than 16384 are
+ * made in pieces (of 16384 at least, one launch each) that are added in C with
+ * rounding to nearest; for 16-bit C they are not, and 65536 positive products
+ * have come out 2e-5 low.  A block whose scale is NaN makes its row
  * (or column) of C NaN.  C's rows and columns are one dim each, of any stride.
  * alpha == 0 or K == 0 reads neither A nor B.
  * Errors: as dg_gemm_ex; DG_ERR_VALUE for different blocks; DG_ERR_ALIGN for

@@ -186,7 +186,6 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
                 p.split = f;
             }
         }
-    p.k_split = (steps + p.split - 1) / p.split * kMx4K;
     p.k_tiles = (int32_t)scale_tiles(A->K, A->block);
     p.sa = static_cast<const uint8_t *>(A->scales);
     p.sb = static_cast<const uint8_t *>(B->scales);
@@ -212,11 +211,27 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
                     !scales_map(&m[2], B, 1) || !scales_map(&m[3], A, p.tile_w / 128)))
         return DG_ERR_UNSUPPORTED;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e =
-        A->block == 32 ? (pair ? launch_mx4<32, true>(p, m, q_rows, num_sms, s) : launch_mx4<32, false>(p, m, q_rows, num_sms, s))
-                       : (pair ? launch_mx4<16, true>(p, m, q_rows, num_sms, s) : launch_mx4<16, false>(p, m, q_rows, num_sms, s));
-    if (e != cudaSuccess) return DG_ERR_CUDA;
-    count_launch();
+    // F32 C: no accumulator takes more than kMx4Part of k (the tensor core truncates as it adds); the pieces of a
+    // longer sum are added in C, a launch each.  A 16-bit C could not hold them, and its own rounding is larger.
+    const TurnedOut out = p.out;
+    const int split = p.split;
+    const int64_t K = p.K, piece = C->dtype == DG_F32 ? (int64_t)kMx4Part * split : std::max<int64_t>(K, 1);
+    for (int64_t k = 0; k == 0 || k < K; k += piece) {
+        p.k_from = (int32_t)k;
+        p.K = (int32_t)std::min(K, k + piece);
+        const int some = (p.K - p.k_from + kMx4K - 1) / kMx4K;
+        // every CTA of a cluster has a part of the piece
+        for (p.split = split; p.split > 1 && (some + p.split - 1) / p.split * (p.split - 1) >= some;) p.split /= 2;
+        p.k_split = (some + p.split - 1) / p.split * kMx4K;
+        p.out.beta = k == 0 ? out.beta : 1.f;
+        p.out.bias_n = p.K == K ? out.bias_n : nullptr;
+        p.out.act = p.K == K ? out.act : DG_ACT_NONE;
+        const cudaError_t e =
+            A->block == 32 ? (pair ? launch_mx4<32, true>(p, m, q_rows, num_sms, s) : launch_mx4<32, false>(p, m, q_rows, num_sms, s))
+                           : (pair ? launch_mx4<16, true>(p, m, q_rows, num_sms, s) : launch_mx4<16, false>(p, m, q_rows, num_sms, s));
+        if (e != cudaSuccess) return DG_ERR_CUDA;
+        count_launch();
+    }
     return DG_OK;
 }
 

@@ -30,7 +30,8 @@
 namespace dg {
 
 struct Mx4Params {
-    int32_t M, N, K;
+    int32_t M, N;
+    int32_t k_from, K;       // the piece of k of this launch, from a multiple of a stage's k up to K
     int32_t tile_w;          // rows of C per tile: 128 or 256 (fewer in the last)
     int32_t tiles_m, tiles_n;
     int32_t stages;
@@ -61,6 +62,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
 
 constexpr int kMx4Threads = 64 + 32 * kTurnWarps;
 constexpr int kMx4K = 256;  // k per stage
+// The most k of an accumulator for F32 C: 256 steps of the tensor core, each of which truncates.  Positive products
+// under scales that differ came out 5e-6 low; 65536 of them in one accumulator 2.1e-5.
+constexpr int kMx4Part = 16384;
 constexpr uint32_t kScaleTile = 512;
 
 struct Mx4Layout {
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1)
     const int first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x / split;
     const int stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x / split;
     const int part = split > 1 ? (int)cluster_ctarank() : 0;
-    const int kb = part * p.k_split, ke = split > 1 ? min(p.K, kb + p.k_split) : p.K;  // this CTA's k
+    const int kb = p.k_from + part * p.k_split, ke = split > 1 ? min(p.K, kb + p.k_split) : p.K;  // this CTA's k
     const int units = p.tiles_m * p.tiles_n;
     const int buffers = p.tile_w <= 128 ? 2 : 1;  // accumulators
     const int q_tiles = (p.tile_w + 127) / 128;   // scale tiles along a tile's rows of C
