@@ -467,8 +467,8 @@ dg_status dg_dequantize_mx4(const dg_mx4 *q, const dg_view *y, void *stream);
  * (or column) of C NaN.  C's rows and columns are one dim each, of any stride.
  * alpha == 0 or K == 0 reads neither A nor B.
  * Errors: as dg_gemm_ex; DG_ERR_VALUE for different blocks; DG_ERR_ALIGN for
- * codes whose rows do not start at multiples of 16 bytes; DG_ERR_UNSUPPORTED for
- * rows that share their codes (a stride of 0) and for a C of several row or
+ * codes whose rows do not start at multiples of 16 bytes, or a bias off multiples
+ * of 4; DG_ERR_UNSUPPORTED for rows that share their codes (a stride of 0) and for a C of several row or
  * column dims.
  */
 dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C,

@@ -715,7 +715,9 @@ def dequantize_mx4(codes, scales, y, block: int = 32, scale=None, stream=None):
 
 def gemm_mx4(a: dg_mx4, b: dg_mx4, c, alpha: float = 1.0, beta: float = 0.0, bias=None, act="none", stream=None):
     """dg_gemm_mx4: c [M, N] = act(alpha * a b^T + beta * c + bias) of a [M, K] and b [N, K] in 4-bit floats (see
-    mx4), c a torch tensor or dg_view.  Raises DgError on a bad status; returns c."""
+    mx4), c a torch tensor or dg_view, bias float32 [N].  Raises DgError on a bad status; returns c."""
+    if bias is not None and not isinstance(bias, int):
+        _vector(bias, "bias", _torch.float32, b.rows)
     cv = ctypes.byref(c) if isinstance(c, dg_view) else _packed_view(c, 1)
     epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
     st = lib.dg_gemm_mx4(ctypes.byref(a), ctypes.byref(b), cv, alpha, beta, epi, _stream_ptr(stream))

@@ -135,6 +135,8 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     if (A->K != B->K || ci.rows != A->rows || ci.cols != B->rows) return DG_ERR_SHAPE;
     if (C->dtype == DG_E4M3) return DG_ERR_DTYPE;
     if (!std::isfinite(alpha) || !std::isfinite(beta)) return DG_ERR_VALUE;
+    const float *bias = epilogue ? epilogue->bias : nullptr;
+    if (reinterpret_cast<uintptr_t>(bias) % 4) return DG_ERR_ALIGN;
     if (ci.row.n > 1 || ci.col.n > 1) return DG_ERR_UNSUPPORTED;
     if (A->rows == 0 || B->rows == 0) return DG_OK;
     const bool product = alpha != 0.f && A->K > 0;
@@ -144,7 +146,6 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
     if (product)
         for (const dg_mx4 *q : {A, B})
             if (q->rows > 1 && (q->code_stride == 0 || q->code_stride >= int64_t(1) << 40)) return DG_ERR_UNSUPPORTED;
-    const float *bias = epilogue ? epilogue->bias : nullptr;
     if (!device_pointer(C->ptr) || (bias && !device_pointer(bias))) return DG_ERR_POINTER;
     if (product && (!mx4_pointers(A) || !mx4_pointers(B))) return DG_ERR_POINTER;
     int num_sms = 0;
