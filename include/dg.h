@@ -162,8 +162,9 @@ typedef struct {
  * path: the tensor-core kernels (single CTA, CTA pairs, split-K clusters,
  * gathered operands), the GEMVs, the CUDA-core kernel, and alpha == 0 or
  * K == 0, where C = act(beta * C + bias).  Errors as dg_gemm, plus
- * DG_ERR_VALUE for a bad activation or reserved field and DG_ERR_POINTER for
- * a bias that is not device memory of the current device.
+ * DG_ERR_VALUE for a bad activation or reserved field, DG_ERR_POINTER for
+ * a bias that is not device memory of the current device and DG_ERR_ALIGN for
+ * one (or a scale, in dg_gemm too) off multiples of 4 bytes.
  */
 dg_status dg_gemm_ex(const dg_view *A, const dg_view *B, const dg_view *C,
                      float alpha, float beta,
@@ -234,7 +235,7 @@ typedef struct {
  *  alpha == 0 or K == 0 reads neither x nor W.
  * Errors: DG_ERR_UNSUPPORTED if R > 8, DG_ERR_VALUE for a group that is not a
  * positive multiple of 32, a reserved field that is not 0 or a non-finite
- * alpha or beta, DG_ERR_SHAPE, DG_ERR_STRIDE, DG_ERR_ALIGN (scales),
+ * alpha or beta, DG_ERR_SHAPE, DG_ERR_STRIDE, DG_ERR_ALIGN (scales, bias),
  * DG_ERR_DTYPE and DG_ERR_POINTER as dg_gemm.
  */
 dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y,

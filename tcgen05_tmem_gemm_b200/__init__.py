@@ -12,6 +12,7 @@ or ``__graft_entry__.build()``); importing this package without it raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 
@@ -458,11 +459,33 @@ def dg_version() -> int:
 
 # ----------------------------------------------------------- conveniences
 
+def _extents(x, row_dims: int):
+    """Rows and columns of a torch tensor or dg_view."""
+    shape = x.shape[:x.ndim]
+    if isinstance(x, dg_view):
+        row_dims = x.row_dims
+    return math.prod(shape[:row_dims]), math.prod(shape[row_dims:])
+
+
+def _floats(t, name: str, n: int):
+    """A tensor that a kernel reads n floats of (an address is the caller's word for it)."""
+    if t is None or isinstance(t, int):
+        return
+    if t.dtype != _torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.float32 tensor of {n} elements")
+
+
 def gemm(A, B, C, alpha: float = 1.0, beta: float = 0.0, scale_a=None, scale_b=None,
          stream=None, a_row_dims: int = 1, b_row_dims: int = 1, c_row_dims: int = 1,
          bias=None, act="none"):
     """dg_gemm (dg_gemm_ex when a bias or activation is given) on torch tensors
-    or dg_view objects; raises DgError on a bad status."""
+    or dg_view objects; raises DgError on a bad status.  scale_a, scale_b and
+    bias are float32 of M, N and N elements at least."""
+    if scale_a is not None or scale_b is not None or bias is not None:
+        m, n = _extents(C, c_row_dims)
+        _floats(scale_a, "scale_a", m)
+        _floats(scale_b, "scale_b", n)
+        _floats(bias, "bias", n)
     if bias is None and act in ("none", DG_ACT_NONE):
         st = dg_gemm(_as_view(A, a_row_dims), _as_view(B, b_row_dims), _as_view(C, c_row_dims),
                      alpha, beta, scale_a, scale_b, stream)
@@ -515,6 +538,7 @@ def gemv_w4(x, codes, scales, y, zeros=None, group: int = 128, alpha: float = 1.
     xv = view(x, x.dim() - 1)
     yv = view(y, y.dim() - 1)
     W = w4(codes, scales, zeros, group, x.shape[-1])
+    _floats(bias, "bias", codes.shape[0])
     epi = None if bias is None and act in ("none", DG_ACT_NONE) else ctypes.byref(epilogue(bias, act))
     st = lib.dg_gemv_w4(ctypes.byref(xv), ctypes.byref(W), ctypes.byref(yv), alpha, beta, epi, _stream_ptr(stream))
     if st != DG_OK:

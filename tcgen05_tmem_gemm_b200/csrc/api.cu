@@ -1268,6 +1268,15 @@ dg_status gemm_tiles(const dg_view *A, const dg_view *B, const dg_view *C, float
 
 using namespace dg;
 
+namespace {
+
+// Scales and biases are read as floats: elsewhere a kernel would fault.
+bool floats_aligned(const float *a, const float *b, const float *c) {
+    return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) % 4 == 0;
+}
+
+}  // namespace
+
 extern "C" {
 
 dg_status dg_gemm_ex(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta,
@@ -1281,6 +1290,7 @@ dg_status dg_gemm_ex(const dg_view *A, const dg_view *B, const dg_view *C, float
         bias = epilogue->bias;
         act = epilogue->activation;
     }
+    if (!floats_aligned(scale_a, scale_b, bias)) return DG_ERR_ALIGN;
     return gemm_call(A, B, C, alpha, beta, scale_a, scale_b, bias, act, false, stream);
 }
 
@@ -1302,6 +1312,7 @@ dg_status dg_autotune(const dg_view *A, const dg_view *B, const dg_view *C, floa
         act = epilogue->activation;
     }
     if (reps < 1 || reps > 1000) return DG_ERR_VALUE;
+    if (!floats_aligned(scale_a, scale_b, bias)) return DG_ERR_ALIGN;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     Views v{A, B, C, {}, {}, {}};
     v.act = act;
@@ -1463,6 +1474,7 @@ extern "C" {
 dg_status dg_gemm_static(const dg_view *A, const dg_view *B, const dg_view *C, float alpha, float beta,
                          const float *scale_a, const float *scale_b, void *stream) {
     if (!A || !B || !C) return DG_ERR_NULL;
+    if (!floats_aligned(scale_a, scale_b, nullptr)) return DG_ERR_ALIGN;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     Views v{A, B, C, {}, {}, {}};
     Plan pl;
@@ -1540,6 +1552,7 @@ dg_status dg_gemv_w4(const dg_view *x, const dg_w4 *W, const dg_view *y, float a
     if (W->scale_dtype != DG_F32 && W->scale_dtype != DG_F16 && W->scale_dtype != DG_BF16) return DG_ERR_DTYPE;
     if (W->group <= 0 || W->group % 32 != 0) return DG_ERR_VALUE;
     if (!std::isfinite(alpha) || !std::isfinite(beta)) return DG_ERR_VALUE;
+    if (!floats_aligned(bias, nullptr, nullptr)) return DG_ERR_ALIGN;
     constexpr int64_t most = (int64_t(1) << 31) - (1 << 13);  // the kernel rounds k and n up to its tiles in 32 bits
     if (xi.rows > 8 || W->K > most || W->N > most) return DG_ERR_UNSUPPORTED;
     if (xi.rows == 0 || W->N == 0) return DG_OK;
