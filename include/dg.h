@@ -408,8 +408,8 @@ dg_status dg_gemm_grouped_dw(const dg_view *X, const dg_view *dY, const dg_view 
  *               ceil(K / 2) bytes (K odd: the last byte's high four bits are 0)
  *  scales       device uint8, one byte per block, 16-byte aligned,
  *               dg_mx4_scale_bytes bytes.  Of block 32 an E8M0 (2^(byte - 127),
- *               255 is NaN), of block 16 an E4M3 (127 is NaN; the sign is not
- *               used).  They lie in tiles of 128 rows by 4 blocks, 512 bytes
+ *               255 is NaN), of block 16 an E4M3 without a sign (127 is NaN;
+ *               bit 7 is 0).  They lie in tiles of 128 rows by 4 blocks, 512 bytes
  *               each, as the tensor cores read them: that of row r and block b
  *               is byte r % 32 * 16 + r % 128 / 32 * 4 + b % 4 of tile
  *               r / 128 * ceil(ceil(K / block) / 4) + b / 4.  Bytes of a tile
