@@ -187,9 +187,6 @@ dg_status dg_gemm_mx4(const dg_mx4 *A, const dg_mx4 *B, const dg_view *C, float 
                 p.split = f;
             }
         }
-    p.k_tiles = (int32_t)scale_tiles(A->K, A->block);
-    p.sa = static_cast<const uint8_t *>(A->scales);
-    p.sb = static_cast<const uint8_t *>(B->scales);
     p.fa = product ? A->scale : nullptr;
     p.fb = product ? B->scale : nullptr;
     p.idesc = 1u << 7 | 1u << 10 | (A->block == 32 ? 1u << 23 : 0u) | (pair ? 2u : 1u) << 27;  // E2M1 twice, M / 128

@@ -1,8 +1,8 @@
 // C = A B^T of 4-bit floats with block scales: tcgen05.mma .block_scale,
 // scales in TMEM.
 //
-// A tile is 128 columns of C (256 for a pair of CTAs) by up to 256 of its rows,
-// computed as C^T: the tensor core's M side (P) holds rows of B, its N side (Q)
+// A tile is 128 columns of C by up to 128 of its rows, of a pair of CTAs 256 by
+// up to 256, computed as C^T: the tensor core's M side (P) holds rows of B, its N side (Q)
 // rows of A, so that a single token costs an N of 16.  In a pair (cta_group::2)
 // each CTA has its own 128 rows of P and half of Q's rows; what a stage copies
 // per product then falls from 48 to 32 KB per SM, which is what bounds large
@@ -37,8 +37,6 @@ struct Mx4Params {
     int32_t stages;
     int32_t split;           // CTAs of a cluster that share a tile's k (not in pairs; each has one tile)
     int32_t k_split;         // k per such CTA, a multiple of a stage's
-    int32_t k_tiles;         // tiles of scales along k
-    const uint8_t *sa, *sb;  // scales of A and of B
     const float *fa, *fb;    // their tensors' factors, or null
     uint32_t idesc;          // instruction descriptor without N and scale ids
     TurnedOut out;
