@@ -28,11 +28,11 @@
 // (rows past the group are then asked for past the operand's end).
 //
 // What bounds it (B200): HBM where a weight meets few rows (64 rows over 8
-// groups of 4096 x 14336 BF16 in 151-161 us, 5.9-6.2 TB/s); the tensor core and
-// the power cap in large products (8192 rows, K = 14336, N = 4096: 789-865 us,
-// 1018 cycles per 1024 of MMAs); the copies by k, whose operands both arrive as
-// 128-byte columns (8192 rows, 8 dW of 4096 x 4096: 206-253 us, 1268 cycles per
-// 1024 of MMAs).
+// groups of 4096 x 14336 BF16 in 155-163 us, 5.8-6.1 TB/s); the tensor core and
+// the power cap in large products (8192 rows, K = 14336, N = 4096: 705 us with a
+// cold cache, 805-850 back to back); the copies by k, whose operands both arrive
+// as 128-byte columns (8192 rows, 8 dW of 4096 x 4096: 204 us cold, 207-245 back
+// to back, 1268 cycles per 1024 of MMAs).
 //
 // The tensor core truncates when it adds to an accumulator: a sum of 14336
 // products of BF16 normal values came out 1.6e-5 low, of 4096 4.4e-6, and 65536
@@ -40,8 +40,11 @@
 // starts a fresh accumulator every 2048 k (E4M3, whose steps are 32 k: 4096; 65536
 // positive products in one came out 5.9e-5 low), whatever the type of C, and the
 // epilogue adds them up: the first part's accumulator holds the sum, the others
-// are made in the other one, one after the other (the first two without a pause;
-// later ones wait some 1000 cycles of their 16 thousand for the epilogue's read).
+// are made in the other one, one after the other.  Each part after the first
+// costs a pause of some 1700 cycles, in which nothing is multiplied (2048 rows
+// over 4 groups with a cold cache, N = 4096, BF16: 75 -> 78 us at K = 4096, 217 ->
+// 231 at 14336; in calls back to back, at the power cap, up to 3.5 %).  Sums kept
+// in registers, which would need no pause, spilled and slowed every other call.
 #pragma once
 
 #include <climits>

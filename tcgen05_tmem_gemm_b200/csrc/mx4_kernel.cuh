@@ -2,8 +2,8 @@
 // scales in TMEM.
 //
 // A tile is 128 columns of C by up to 128 of its rows, of a pair of CTAs 256 by
-// up to 256, computed as C^T: the tensor core's M side (P) holds rows of B, its N side (Q)
-// rows of A, so that a single token costs an N of 16.  In a pair (cta_group::2)
+// up to 256, computed as C^T: the tensor core's M side (P) holds rows of B, its
+// N side (Q) rows of A, so that a single token costs an N of 16.  In a pair (cta_group::2)
 // each CTA has its own 128 rows of P and half of Q's rows; what a stage copies
 // per product then falls from 48 to 32 KB per SM, which is what bounds large
 // products.  Q's scales are in both CTAs' TMEM, each copied from its own shared
@@ -18,9 +18,10 @@
 // rank order, from all of them through distributed shared memory.
 //
 // What bounds it (B200): the copies, about 740 cycles per stage and SM against
-// 512 of MMAs, then the power cap (8192 x 4096 x 14336 in blocks of 16: 207 us
-// with a cold cache, 243 back to back; 4096^3: 41 us, 3.4 PFLOP/s); for one row
-// the four copies of a stage, 0.3 us (1 x 4096 x 14336: 8 us).
+// 512 of MMAs, then the power cap (8192 x 4096 x 14336 in blocks of 16: 203 us
+// with a cold cache, 222-248 back to back; 4096^3: 52 us cold, 43 from L2); for
+// one row the four copies of a stage, 0.3 us (1 x 4096 x 14336 in blocks of 32:
+// 7.3 us with its operands in L2, 16.4 from HBM).
 #pragma once
 
 #include "common.cuh"

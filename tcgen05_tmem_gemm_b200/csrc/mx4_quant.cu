@@ -6,10 +6,12 @@
 // of the largest.  Everything is rounded to nearest, ties to even, and every
 // division by a block's scale decides as the exact quotient would.
 //
-// They should be bound by HBM and are bound by instructions (8192 x 14336 BF16 on
-// B200, 300 MB: quantised in blocks of 32 in 59 us, of 16 in 70, with a factor 88;
-// read back in 53; the bytes take 46): about 8 to 16 per value, at a third of the
-// warps an SM holds.
+// They should be bound by HBM and no unit is full (8192 x 14336 BF16 on B200, 300
+// MB: quantised in blocks of 32 in 59 us, of 16 in 70, with a factor 88; read back
+// in 53; the bytes take 46).  With a factor 53 % of the issue slots and 32 % of
+// DRAM are used, reading back 46 % and 41 %, and waiting for loads is the largest
+// stall: 8 to 16 instructions per value, a third of the warps an SM holds, and
+// a row loaded one row ahead of its use.
 #include <algorithm>
 
 #include "mx4_quant.h"
