@@ -28,10 +28,10 @@
 // (rows past the group are then asked for past the operand's end).
 //
 // What bounds it (B200): HBM where a weight meets few rows (64 rows over 8
-// groups of 4096 x 14336 BF16 in 155-163 us, 5.8-6.1 TB/s); the tensor core and
+// groups of 4096 x 14336 BF16 in 155-165 us, 5.7-6.1 TB/s); the tensor core and
 // the power cap in large products (8192 rows, K = 14336, N = 4096: 705 us with a
-// cold cache, 805-850 back to back); the copies by k, whose operands both arrive
-// as 128-byte columns (8192 rows, 8 dW of 4096 x 4096: 204 us cold, 207-245 back
+// cold cache, 805-873 back to back); the copies by k, whose operands both arrive
+// as 128-byte columns (8192 rows, 8 dW of 4096 x 4096: 204 us cold, 207-250 back
 // to back, 1268 cycles per 1024 of MMAs).
 //
 // The tensor core truncates when it adds to an accumulator: a sum of 14336
@@ -44,7 +44,7 @@
 // costs a pause of some 1700 cycles, in which nothing is multiplied (2048 rows
 // over 4 groups with a cold cache, N = 4096, BF16: 75 -> 78 us at K = 4096, 217 ->
 // 231 at 14336; in calls back to back, at the power cap, up to 3.5 %).  Sums kept
-// in registers, which would need no pause, spilled and slowed every other call.
+// in registers, which would need no pause, spilled and slowed calls of one part.
 #pragma once
 
 #include <climits>

@@ -19,7 +19,7 @@
 //
 // What bounds it (B200): the copies, about 740 cycles per stage and SM against
 // 512 of MMAs, then the power cap (8192 x 4096 x 14336 in blocks of 16: 203 us
-// with a cold cache, 222-248 back to back; 4096^3: 52 us cold, 43 from L2); for
+// with a cold cache, 222-251 back to back; 4096^3: 52 us cold, 43 from L2); for
 // one row the four copies of a stage, 0.3 us (1 x 4096 x 14336 in blocks of 32:
 // 7.3 us with its operands in L2, 16.4 from HBM).
 #pragma once
